@@ -25,6 +25,16 @@ MOE_ACT_BF16 = 0
 MOE_ACT_MXFP4 = 1
 MOE_ACT_MXFP8 = 2
 
+MOE_F32 = 0
+MOE_BF16 = 1
+MOE_F16 = 2
+
+MOE_SCORE_SIGMOID = 0
+MOE_SCORE_SOFTMAX = 1
+
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2 = 1
+
 MOE_W_MXFP4 = 0
 MOE_W_NVFP4 = 1
 
@@ -36,6 +46,9 @@ EXPORTED = (
     "moe_combine_norm", "moe_layer_forward", "moe_layer_forward_host", "moe_layer_forward_norm", "moe_synth_weights", "moe_selftest_wait_timeout",
     "moe_dense_workspace_size", "moe_dense_linear", "moe_nvfp4_pack", "moe_nvfp4_unpack", "moe_workspace_routing",
     "moe_decode_pieces_bytes", "moe_decode_pieces", "moe_expert_ffn_decode",
+    "moe_route_logits", "moe_route_scores", "moe_route_scores_backward", "moe_combine_backward", "moe_nvfp4_operand_codes",
+    "moe_nvfp4_operand_scales", "moe_nvfp4_workspace_size", "moe_nvfp4_quantize", "moe_nvfp4_operand_values",
+    "moe_nvfp4_matmul", "moe_nvfp4_linear",
 )
 
 
@@ -59,12 +72,23 @@ class moe_mxfp4_matrix(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "s", "q_mma", "s_mma")]
 
 
+class moe_route_rule(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("score", "groups", "top_groups", "group_score", "renormalize")] + \
+               [("scale", ctypes.c_float)]
+
+
+class moe_nvfp4_operand(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "s", "gs")] + [("gs_rows", ctypes.c_int32)]
+
+
 _lib = None
 P = ctypes.c_void_p
 I32, I64, U32, U64 = ctypes.c_int, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64
 SZ = ctypes.c_size_t
 WP = ctypes.POINTER(moe_expert_weights)
 MP = ctypes.POINTER(moe_mxfp4_matrix)
+RP = ctypes.POINTER(moe_route_rule)
+OP = ctypes.POINTER(moe_nvfp4_operand)
 
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [I32]),
@@ -100,6 +124,17 @@ _SIGS = {
     "moe_expert_ffn_decode": (I32, [P, P, I32, P, P, P, P, I32, I32, I32, I32, I32, WP, P, P, P, SZ, P]),
     "moe_workspace_routing": (I32, [P, SZ, I32, I32, I32, I32, I32, I32, ctypes.POINTER(P), ctypes.POINTER(P),
                                     ctypes.POINTER(P), ctypes.POINTER(P)]),
+    "moe_route_logits": (I32, [P, P, P, I32, I32, I32, P, P]),
+    "moe_route_scores": (I32, [P, I32, I64, P, I32, I32, I32, RP, P, P, P, P, P]),
+    "moe_route_scores_backward": (I32, [P, I32, I64, I32, I32, I32, RP, P, P, P, P, I64, P]),
+    "moe_combine_backward": (I32, [P, P, P, P, I32, I32, I32, P, P, P]),
+    "moe_nvfp4_operand_codes": (SZ, [I64, I64]),
+    "moe_nvfp4_operand_scales": (SZ, [I64, I64]),
+    "moe_nvfp4_workspace_size": (SZ, [I64, I64, I64]),
+    "moe_nvfp4_quantize": (I32, [P, I32, I64, I64, I64, OP, OP, I32, P, SZ, P]),
+    "moe_nvfp4_operand_values": (I32, [OP, I64, I64, P, P]),
+    "moe_nvfp4_matmul": (I32, [OP, OP, I64, I64, I64, P, I32, I64, P, SZ, P]),
+    "moe_nvfp4_linear": (I32, [P, I32, I64, I64, I64, OP, I64, P, I32, I64, P, SZ, P]),
 }
 
 
@@ -345,3 +380,57 @@ def moe_synth_weights(seed, tensor_id, expert_first, n_experts, rows, K, c, out,
 def moe_selftest_wait_timeout(ws, limit_us, ws_bytes=None, stream=None):
     n = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
     _check("moe_selftest_wait_timeout", load().moe_selftest_wait_timeout(_p(ws), n, int(limit_us), _stream(stream)))
+
+
+# ------------------------------------------------------------------ routing rules, dense NVFP4 products
+
+def moe_route_logits(x, W_r, b, T, d, E, logits, stream=None):
+    _check("moe_route_logits", load().moe_route_logits(_p(x), _p(W_r), _p(b), T, d, E, _p(logits), _stream(stream)))
+
+
+def moe_route_scores(logits, dtype, ld, bias, T, E, k, rule: moe_route_rule, ids, w, scores=None, counts=None, stream=None):
+    _check("moe_route_scores", load().moe_route_scores(_p(logits), dtype, ld, _p(bias), T, E, k, rule, _p(ids), _p(w),
+                                                       _p(scores), _p(counts), _stream(stream)))
+
+
+def moe_route_scores_backward(logits, dtype, ld, T, E, k, rule: moe_route_rule, ids, dw, dscores, dlogits, ldd,
+                              stream=None):
+    _check("moe_route_scores_backward",
+           load().moe_route_scores_backward(_p(logits), dtype, ld, T, E, k, rule, _p(ids), _p(dw), _p(dscores),
+                                            _p(dlogits), ldd, _stream(stream)))
+
+
+def moe_combine_backward(dy, y_perm, inv_pos, w, T, k, d, dw, dy_perm, stream=None):
+    _check("moe_combine_backward", load().moe_combine_backward(_p(dy), _p(y_perm), _p(inv_pos), _p(w), T, k, d, _p(dw),
+                                                               _p(dy_perm), _stream(stream)))
+
+
+def moe_nvfp4_operand_codes(rows, K) -> int:
+    return int(load().moe_nvfp4_operand_codes(rows, K))
+
+
+def moe_nvfp4_operand_scales(rows, K) -> int:
+    return int(load().moe_nvfp4_operand_scales(rows, K))
+
+
+def moe_nvfp4_workspace_size(M, N, K) -> int:
+    return int(load().moe_nvfp4_workspace_size(M, N, K))
+
+
+def moe_nvfp4_quantize(x, dtype, R, C, ld, rows, cols, scales_given=0, ws=None, ws_bytes=None, stream=None):
+    _check("moe_nvfp4_quantize", load().moe_nvfp4_quantize(_p(x), dtype, R, C, ld, rows, cols, int(scales_given), _p(ws),
+                                                           _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_nvfp4_operand_values(op: moe_nvfp4_operand, rows, K, v, stream=None):
+    _check("moe_nvfp4_operand_values", load().moe_nvfp4_operand_values(op, rows, K, _p(v), _stream(stream)))
+
+
+def moe_nvfp4_matmul(A: moe_nvfp4_operand, B: moe_nvfp4_operand, M, N, K, y, dtype, ldy, ws, ws_bytes=None, stream=None):
+    _check("moe_nvfp4_matmul", load().moe_nvfp4_matmul(A, B, M, N, K, _p(y), dtype, ldy, _p(ws), _ws_bytes(ws, ws_bytes),
+                                                       _stream(stream)))
+
+
+def moe_nvfp4_linear(x, x_dtype, M, K, ldx, W: moe_nvfp4_operand, N, y, y_dtype, ldy, ws, ws_bytes=None, stream=None):
+    _check("moe_nvfp4_linear", load().moe_nvfp4_linear(_p(x), x_dtype, M, K, ldx, W, N, _p(y), y_dtype, ldy, _p(ws),
+                                                       _ws_bytes(ws, ws_bytes), _stream(stream)))

@@ -1,0 +1,490 @@
+// nvfp4_matmul.cu -- dense product of two NVFP4 operands on the tensor cores (kind::mxf4nvf4):
+//   y[m][n] = ga[m] gb[n] sum_k A[m][k] B[n][k],
+// A [M][K] the activations, B [N][K] the weights (or any two operands that contract along K), both in
+// the tensor-core layout of nvfp4_operand.cu: code tiles of 128 rows x 256 values with the 128-byte swizzle and
+// 512-byte scale atoms, so that every piece is one contiguous bulk copy and ragged sizes need no
+// masks before the store (padding along K holds zeros; padding rows only reach results that are not stored).
+// Products and sums are the tensor core's (fp32 accumulators); each result is scaled by ga and gb in fp32
+// and rounded once.
+//
+// Two kernels:
+//   rows    up to 128 activation rows per tile: the weights are the MMA's M side (128 weight rows), the
+//           activations its N side (8 .. 128 rows), so that few activation rows waste no tensor-core rows
+//           and each weight byte is read once.  Bound by the weight read; the K range of a tile is split
+//           over the CTAs of a cluster, whose partial sums are exchanged through distributed shared
+//           memory and added in rank order.
+//   square  128 activation rows x 256 weight rows per tile, persistent CTAs; bound by the FP4 rate and the
+//           shared-memory feed.
+// Every barrier wait is bounded: on expiry the CTA records MOE_ERR_TIMEOUT, waits (bounded) for its own
+// copies and MMAs, frees tensor memory and exits.
+#include "ops.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 128 * 128;  // code tile: 128 rows x 128 bytes (256 values)
+constexpr int kAtom = 512;        // scale atom: 128 rows x 4 scales
+constexpr int kAtoms = 4;         // scale atoms of 128 rows per K step of 256 values
+constexpr uint32_t kTmemCols = 512;
+
+struct MatmulArgs {
+    const uint8_t* qa;
+    const uint8_t* sa;
+    const float* ga;
+    int ga_rows;
+    const uint8_t* qb;
+    const uint8_t* sb;
+    const float* gb;
+    int gb_rows;
+    int64_t M, N;
+    int KT;  // K steps of 256 values
+    void* y;
+    int dtype;
+    int64_t ldy;
+    int* status;
+};
+
+__device__ __forceinline__ void store_one(void* y, int dtype, int64_t at, float v) {
+    if (dtype == MOE_F32) static_cast<float*>(y)[at] = v;
+    else if (dtype == MOE_BF16) static_cast<uint16_t*>(y)[at] = f32_to_bf16_bits(v);
+    else static_cast<__half*>(y)[at] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ uint32_t pack_two(int dtype, float a, float b) {
+    if (dtype == MOE_BF16) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&p);
+    }
+    const __half2 p = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// ------------------------------------------------------------------ rows kernel
+// One K step (256 values) of M = 128 weight rows x N activation rows: eight scale-atom copies, four MMAs,
+// the commit that frees the stage.  Scale columns of a stage: weights' atom i at sf + 4 i, activations' at
+// sf + 16 + 4 i.
+__device__ __forceinline__ void rows_stage_mma(uint32_t d, uint32_t sf, uint64_t a, uint64_t b, uint64_t asf, uint64_t bsf,
+                                               uint32_t idesc, uint32_t accumulate, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%2], %3;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%4], %5;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%6], %7;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%8], %9;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%10], %11;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%12], %13;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%14], %15;\n\t}" ::"r"(sf),
+        "l"(asf), "r"(sf + 4), "l"(asf + 32), "r"(sf + 8), "l"(asf + 64), "r"(sf + 12), "l"(asf + 96), "r"(sf + 16), "l"(bsf),
+        "r"(sf + 20), "l"(bsf + 32), "r"(sf + 24), "l"(bsf + 64), "r"(sf + 28), "l"(bsf + 96)
+        : "memory");
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 q, %4, %4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %7, %8, %3, [%9], [%10], q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %11, %12, %3, [%13], [%14], q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %15, %16, %3, [%17], [%18], q;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%19];\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sf), "r"(sf + 16), "l"(a + 2), "l"(b + 2), "r"(sf + 4), "r"(sf + 20),
+        "l"(a + 4), "l"(b + 4), "r"(sf + 8), "r"(sf + 24), "l"(a + 6), "l"(b + 6), "r"(sf + 12), "r"(sf + 28),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+constexpr int kRowsThreads = 192;  // copy warp, MMA warp, 4 epilogue warps
+
+template <int NT>
+__host__ __device__ constexpr int rows_stage_bytes() { return kTile + NT * 128 + 2 * kAtoms * kAtom; }
+template <int NT>
+__host__ __device__ constexpr int rows_stages() { return NT == 128 ? 6 : 8; }
+// (more than half of the SM's shared memory, so that one CTA per SM owns its tensor memory)
+template <int NT>
+constexpr size_t rows_smem() { return (size_t)rows_stages<NT>() * rows_stage_bytes<NT>() + 1024 + 256; }
+static_assert(rows_smem<8>() > 116 * 1024 && rows_smem<64>() <= 232448 && rows_smem<128>() <= 232448, "one CTA per SM");
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster_f32(const void* p, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// Grid: x = weight tile * splits + rank (a cluster of `splits` CTAs per tile), y = tile of NT activation rows.
+template <int NT>
+__global__ void __launch_bounds__(kRowsThreads, 1) nvfp4_rows_matmul_kernel(const MatmulArgs args, int splits) {
+    constexpr int kStages = rows_stages<NT>(), kStageBytes = rows_stage_bytes<NT>();
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = splits > 1 ? (int)cluster_rank() : 0;
+    const int64_t nt = blockIdx.x / splits, m0 = (int64_t)blockIdx.y * NT;
+    const int k0 = (int)((int64_t)args.KT * rank / splits), k1 = (int)((int64_t)args.KT * (rank + 1) / splits);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t kSfBase = NT;  // scale columns after the accumulator
+
+    // the weights and the activations of K step kt into stage s
+    auto load_w = [&](int s, int kt) {
+        unsigned char* p = smem + (size_t)s * kStageBytes;
+        const size_t at = (size_t)nt * args.KT + kt;
+        bulk_load(p, args.qb + at * kTile, kTile, &full[s]);
+        bulk_load(p + kTile + NT * 128, args.sb + at * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
+    };
+    auto load_x = [&](int s, int kt) {
+        unsigned char* p = smem + (size_t)s * kStageBytes;
+        const size_t at = (size_t)(m0 / 128) * args.KT + kt;
+        bulk_load(p + kTile, args.qa + at * kTile + (m0 % 128) * 128, NT * 128, &full[s]);
+        bulk_load(p + kTile + NT * 128 + kAtoms * kAtom, args.sa + at * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            const int head = min(kStages, k1 - k0);
+            for (; it < head; ++it) {  // the weights do not depend on the kernel before
+                mbar_arrive_expect_tx(&full[it], kStageBytes);
+                load_w(it, k0 + it);
+            }
+            pdl_wait();
+            for (int i = 0; i < head; ++i) load_x(i, k0 + i);
+            for (; it < k1 - k0; ++it) {
+                const int s = it % kStages;
+                if (!mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, abort_flag, args.status)) break;
+                mbar_arrive_expect_tx(&full[s], kStageBytes);
+                load_w(s, k0 + it);
+                load_x(s, k0 + it);
+            }
+            if (*abort_flag) {
+                volatile int never = 0;
+                for (int i = max(0, it - kStages); i < it; ++i)
+                    mbar_wait(&full[i % kStages], (i / kStages) & 1, &never, nullptr, 100000000LL);
+            }
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = idesc_mxf4nvf4_ue4m3(128, NT);
+        for (int it = 0; it < k1 - k0; ++it) {
+            const int s = it % kStages;
+            if (!mbar_wait_warp(&full[s], (it / kStages) & 1, abort_flag, args.status)) break;
+            tc_fence_after();
+            unsigned char* p = smem + (size_t)s * kStageBytes;
+            unsigned char* sf = p + kTile + NT * 128;
+            rows_stage_mma(tmem, tmem + kSfBase + s * 32, desc_sw128(p), desc_sw128(p + kTile), desc_sf(sf),
+                           desc_sf(sf + kAtoms * kAtom), idesc, it > 0 ? 1u : 0u, &empty[s]);
+        }
+        // fires once every MMA and scale copy of this warp has completed (also when aborting)
+        tc_commit(acc_full);
+    }
+    __syncwarp();
+    pdl_wait();  // ga comes from the kernel before
+    volatile int never = 0;
+    mbar_wait(acc_full, 0, &never, args.status);  // the commit always comes; bounded all the same
+    tc_fence_after();
+    __syncthreads();  // and no copy is in flight: every stage was consumed (or drained when aborting)
+
+    const int64_t n = nt * 128 + 32 * (warp & 3) + lane;
+    const bool owner = warp >= 2;
+    float* part = reinterpret_cast<float*>(smem);  // [NT][128] partial sums, on the stages
+    const float gb = owner && n < args.N ? args.gb[args.gb_rows ? n : 0] : 0.f;
+    auto store = [&](int64_t m, float acc) {
+        if (m < args.M && n < args.N) store_one(args.y, args.dtype, m * args.ldy + n, acc * args.ga[args.ga_rows ? m : 0] * gb);
+    };
+    if (owner) {
+        const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+#pragma unroll
+        for (int c = 0; c < NT; c += 8) {
+            uint32_t v[8];
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                         : "r"(acc + c));
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (splits > 1) part[(c + i) * 128 + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
+                else store(m0 + c + i, __uint_as_float(v[i]));
+            }
+        }
+    }
+    if (splits > 1) {
+        cluster_sync();
+        if (owner)
+            for (int c = rank; c < NT && m0 + c < args.M; c += splits) {  // this CTA's share of the activation rows
+                float sum = 0.f;
+                for (int r = 0; r < splits; ++r) sum += ld_cluster_f32(&part[c * 128 + 32 * (warp & 3) + lane], r);
+                store(m0 + c, sum);
+            }
+        cluster_sync();  // the partial sums stay until every CTA has read them
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ square kernel
+constexpr int kSqStages = 4;
+constexpr int kSqEpiWarps = 8;
+constexpr int kSqThreads = 64 + 32 * kSqEpiWarps;
+constexpr int kSqStageBytes = 3 * kTile + 12 * kAtom;
+constexpr int kSqSfCols = 48;
+constexpr uint32_t kSqSfBase = 256;  // scale columns after the accumulator
+constexpr size_t kSqSmem = (size_t)kSqStages * kSqStageBytes + 1024 + 256;
+static_assert(kSqStageBytes % 1024 == 0 && kSqSfBase + kSqStages * kSqSfCols <= kTmemCols, "stage alignment, tensor memory");
+
+__global__ void __launch_bounds__(kSqThreads, 1) nvfp4_square_matmul_kernel(const MatmulArgs args, int MT, int NT) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kSqStages * kSqStageBytes);
+    uint64_t* empty = full + kSqStages;
+    uint64_t* acc_full = empty + kSqStages;
+    uint64_t* acc_empty = acc_full + 1;
+    uint64_t* mma_done = acc_empty + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kSqStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, kSqEpiWarps);
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+
+    const int n_tiles = MT * NT, KT = args.KT;
+    const int64_t last_b = (args.N + 127) / 128 - 1;  // last 128-row block of B
+    auto stage = [&](int s) { return smem + (size_t)s * kSqStageBytes; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+                const int64_t mb = t / NT, b0 = 2 * (int64_t)(t % NT), b1 = min(b0 + 1, last_b);
+                for (int kt = 0; kt < KT; ++kt, ++it) {
+                    const int s = it % kSqStages;
+                    if (!mbar_wait(&empty[s], ((it / kSqStages) & 1) ^ 1, abort_flag, args.status)) {
+                        ok = false;
+                        break;
+                    }
+                    unsigned char* p = stage(s);
+                    const size_t ka = (size_t)mb * KT + kt, kb0 = (size_t)b0 * KT + kt, kb1 = (size_t)b1 * KT + kt;
+                    mbar_arrive_expect_tx(&full[s], kSqStageBytes);
+                    bulk_load(p, args.qa + ka * kTile, kTile, &full[s]);
+                    bulk_load(p + kTile, args.qb + kb0 * kTile, kTile, &full[s]);
+                    bulk_load(p + 2 * kTile, args.qb + kb1 * kTile, kTile, &full[s]);
+                    bulk_load(p + 3 * kTile, args.sa + ka * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
+                    bulk_load(p + 3 * kTile + 4 * kAtom, args.sb + kb0 * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
+                    bulk_load(p + 3 * kTile + 8 * kAtom, args.sb + kb1 * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
+                }
+            }
+            if (*abort_flag) {
+                volatile int never = 0;
+                for (int i = max(0, it - kSqStages); i < it; ++i)
+                    mbar_wait(&full[i % kSqStages], (i / kSqStages) & 1, &never, nullptr, 100000000LL);
+            }
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = idesc_mxf4nvf4_ue4m3(128, 256);
+        int it = 0, tile = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x, ++tile) {
+            if (!mbar_wait_warp(acc_empty, (tile & 1) ^ 1, abort_flag, args.status)) break;
+            tc_fence_after();
+            for (int kt = 0; kt < KT; ++kt, ++it) {
+                const int s = it % kSqStages;
+                if (!mbar_wait_warp(&full[s], (it / kSqStages) & 1, abort_flag, args.status)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                unsigned char* p = stage(s);
+                const uint32_t sf = tmem + kSqSfBase + s * kSqSfCols;
+                stage_scales_nv_to_tmem(sf, desc_sf(p + 3 * kTile), desc_sf(p + 3 * kTile + 4 * kAtom),
+                                        desc_sf(p + 3 * kTile + 8 * kAtom));
+                stage_mmas_nv_commit(tmem, desc_sw128(p), desc_sw128(p + kTile), idesc, sf, kt > 0 ? 1u : 0u, &empty[s]);
+            }
+            if (!ok) break;
+            tc_commit(acc_full);
+        }
+        tc_commit(mma_done);
+        volatile int never = 0;
+        mbar_wait_warp(mma_done, 0, &never, nullptr, 100000000LL);
+    } else {
+        const int q = warp & 3, half = (warp - 2) / 4;
+        const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
+        const int size = args.dtype == MOE_F32 ? 4 : 2;
+        const bool wide = reinterpret_cast<uintptr_t>(args.y) % 16 == 0 && (args.ldy * size) % 16 == 0;
+        int tile = 0;
+        for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, ++tile) {
+            const int64_t m0 = (int64_t)(t / NT) * 128 + 32 * q, n0 = (int64_t)(t % NT) * 256 + 128 * half;
+            const int64_t m = m0 + lane;
+            const float ga = m < args.M ? args.ga[args.ga_rows ? m : 0] : 0.f;
+            if (!mbar_wait(acc_full, tile & 1, abort_flag, args.status)) break;
+            tc_fence_after();
+            uint32_t v[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(acc + 32 * c, v[c]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int64_t nc = n0 + 32 * c;
+                if (nc >= args.N) break;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float gb = args.gb_rows ? __ldg(args.gb + min(nc + i, args.N - 1)) : __ldg(args.gb);
+                    v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * ga * gb);
+                }
+                if (wide && nc + 32 <= args.N) {
+                    // 16-byte pieces transposed inside groups of four lanes: a store writes 64 contiguous bytes of 8 rows
+                    const int rb = 4 * (lane >> 2), piece = lane & 3;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (size == 2 && h == 1) break;
+                        uint4 pc[4];
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            if (size == 2) {
+                                uint32_t o[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    o[i] = pack_two(args.dtype, __uint_as_float(v[c][8 * a + 2 * i]), __uint_as_float(v[c][8 * a + 2 * i + 1]));
+                                pc[a] = make_uint4(o[0], o[1], o[2], o[3]);
+                            } else {
+                                pc[a] = make_uint4(v[c][16 * h + 4 * a], v[c][16 * h + 4 * a + 1], v[c][16 * h + 4 * a + 2], v[c][16 * h + 4 * a + 3]);
+                            }
+                        }
+                        transpose4_pieces(pc, lane);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int64_t r = m0 + rb + j;
+                            if (r < args.M)
+                                *reinterpret_cast<uint4*>(static_cast<char*>(args.y) + (r * args.ldy + nc + 16 * h) * size + 16 * piece) = pc[j];
+                        }
+                    }
+                } else if (m < args.M) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (nc + i < args.N) store_one(args.y, args.dtype, m * args.ldy + nc + i, __uint_as_float(v[c][i]));
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ host side
+template <int NT>
+cudaError_t launch_rows(const MatmulArgs& a, cudaStream_t st, bool pdl) {
+    const int64_t wt = (a.N + 127) / 128, mt = (a.M + NT - 1) / NT;
+    // split K while the tiles leave SMs idle and every CTA keeps at least two K steps
+    int splits = 1;
+    while (splits < 8 && wt * mt * splits * 2 <= sm_count() && a.KT / (splits * 2) >= 2) splits *= 2;
+    const void* f = (const void*)nvfp4_rows_matmul_kernel<NT>;
+    cudaError_t e = ensure_dyn_smem(f, rows_smem<NT>());
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(wt * splits), (unsigned)mt);
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.dynamicSmemBytes = rows_smem<NT>();
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (splits > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)splits;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    void* args[] = {const_cast<MatmulArgs*>(&a), &splits};
+    return cudaLaunchKernelExC(&cfg, f, args);
+}
+
+}  // namespace
+
+cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_operand* B, int64_t M, int64_t N, int64_t K, void* y,
+                                moe_dtype dtype, int64_t ldy, int* status, cudaStream_t st, bool pdl) {
+    if (M == 0 || N == 0) return cudaSuccess;
+    MatmulArgs a = {A->q, A->s, A->gs, A->gs_rows, B->q, B->s, B->gs, B->gs_rows, M, N, (int)((K + 255) / 256), y, (int)dtype, ldy,
+                    status};
+    if (M <= 8) return launch_rows<8>(a, st, pdl);
+    if (M <= 16) return launch_rows<16>(a, st, pdl);
+    if (M <= 32) return launch_rows<32>(a, st, pdl);
+    if (M <= 64) return launch_rows<64>(a, st, pdl);
+    if (M <= 128) return launch_rows<128>(a, st, pdl);
+    int MT = (int)((M + 127) / 128), NT = (int)((N + 255) / 256);
+    const int64_t tiles = (int64_t)MT * NT;
+    const int sms = sm_count();
+    void* args[] = {&a, &MT, &NT};
+    return launch_kernel((const void*)nvfp4_square_matmul_kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kSqThreads), kSqSmem,
+                         st, pdl, args);
+}
+
+}  // namespace moe

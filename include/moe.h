@@ -128,7 +128,7 @@ typedef struct moe_expert_weights {
 /* Human-readable name of a status code (static string). */
 const char* moe_status_string(moe_status s);
 
-/* ABI version of this header (incremented on changes to the entry points or their structs);
+/* ABI version of this header (incremented on changes to existing entry points or their structs);
  * moe_abi_version() returns the library's, which a caller compares with MOE_ABI_VERSION. */
 #define MOE_ABI_VERSION 13
 int moe_abi_version(void);
@@ -428,6 +428,108 @@ typedef struct {
 size_t moe_dense_workspace_size(int T, int K, int N, moe_act_fmt fmt);  /* 0 for an unsupported shape */
 moe_status moe_dense_linear(const uint16_t* x, int T, int K, int N, const moe_mxfp4_matrix* W, moe_act_fmt fmt,
                             uint16_t* y, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- routing rules
+ * moe_route keeps the k largest logits and weighs them with their softmax.  The calls below take the logits and
+ * apply the other rules that sparse layers use: scores by sigmoid or softmax, a balance bias that takes
+ * part in the choice and not in the weights, experts in groups of which only the best are open to a
+ * token, renormalised weights.  Their ids and w go into moe_permute, the expert calls and moe_combine as
+ * moe_route's do. */
+
+typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
+typedef enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;
+/* Score of a group of experts: its largest ranking value, or the sum of its two largest. */
+typedef enum moe_group_score { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+
+typedef struct moe_route_rule {
+    int32_t score;       /* moe_score */
+    int32_t groups;      /* 1 .. 32, a divisor of E; group g holds experts g E/groups .. */
+    int32_t top_groups;  /* 1 .. groups: groups open to a token */
+    int32_t group_score; /* moe_group_score */
+    int32_t renormalize; /* nonzero: a token's weights are divided by their sum */
+    float scale;         /* factor of the weights (finite) */
+} moe_route_rule;
+
+/* The fixed-order fp32 logits of moe_route (same definition, all T*E of them): x bf16 [T][d], W_r fp32 [E][d],
+ * b fp32 [E] or NULL, logits fp32 [T][E].  d % 128 == 0, x and W_r 16-byte aligned. */
+moe_status moe_route_logits(const uint16_t* x, const float* W_r, const float* b, int T, int d, int E, float* logits,
+                            moe_stream_t stream);
+
+/* Scores s = sigmoid(l) or softmax(l) of logits [T][ld] (dtype; ld >= E); ranking values v = s + bias (bias fp32
+ * [E], finite, or NULL: then the logits are ranked, which is the order of the scores; sums of a group's
+ * two largest are then sums of scores).  The top_groups best groups stay, then the k largest v among their
+ * experts; ties go to the lower id.  The choice is the one that 64-bit arithmetic makes on the given logits
+ * and bias.  ids int32 [T][k]: the set in ascending order; w fp32 [T][k]: s of the picks (without bias), divided by
+ * their sum when the rule renormalises (0 when that sum is 0), times scale.
+ *   An expert whose logit is -inf or NaN is out of service: score 0, ranked below every other expert of the
+ * open groups, and picked (lowest id first, weight 0) only when fewer than k others are there; a group without
+ * an expert in service ranks last.  A logit of +inf scores like the largest finite number.
+ *   scores (optional) fp32 [T][E]: s.  counts (optional) int32 [E]: picks per expert, overwritten.
+ * T >= 0, 1 <= k <= 32, E <= 1024, k <= top_groups * E / groups. */
+moe_status moe_route_scores(const void* logits, moe_dtype dtype, int64_t ld, const float* bias, int T, int E, int k,
+                            const moe_route_rule* rule, int32_t* ids, float* w, float* scores, int32_t* counts,
+                            moe_stream_t stream);
+
+/* Gradient of the logits [T][ldd] (dtype, as the logits) from the gradient dw fp32 [T][k] of moe_route_scores'
+ * weights, and that of its scores, dscores fp32 [T][E] (optional, NULL: none; a balance loss on the scores, say).
+ * ids as that call chose them, which is held fixed; an id outside [0, E) takes no part.  Experts out of service
+ * get 0.  dlogits may not overlap the logits. */
+moe_status moe_route_scores_backward(const void* logits, moe_dtype dtype, int64_t ld, int T, int E, int k,
+                                     const moe_route_rule* rule, const int32_t* ids, const float* dw, const float* dscores,
+                                     void* dlogits, int64_t ldd, moe_stream_t stream);
+
+/* Gradients of moe_combine's weighted sum: dw[t][j] = sum_i dy[t][i] * y_perm[inv_pos[t*k+j]][i] (fp32) and
+ * dy_perm[inv_pos[t*k+j]] = w[t][j] * dy[t] (bf16).  dy bf16 [T][d]; y_perm, dy_perm bf16 [T*k][d]; w, dw fp32 [T][k].
+ * Either result may be NULL (not computed; y_perm is needed for dw only, w for dy_perm only).  inv_pos
+ * names each row at most once; an entry outside [0, T*k) gives dw 0.  d % 8 == 0, 1 <= k <= 32; 16-byte aligned. */
+moe_status moe_combine_backward(const uint16_t* dy, const uint16_t* y_perm, const int32_t* inv_pos, const float* w, int T,
+                                int k, int d, float* dw, uint16_t* dy_perm, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- dense NVFP4 products
+ * y = A B^T with both operands in NVFP4: the shared projections and shared experts beside NVFP4 expert weights
+ * (moe_dense_linear takes MXFP4 matrices), and the products of their gradients.
+ *   An operand is a matrix [rows][K] that contracts along K: E2M1 codes, one E4M3 scale per 16 elements, one
+ * fp32 scale per row or one for all.  q and s are in the tensor-core layout: with rows padded to 128 and
+ * K to 256, code tiles and scale atoms as moe_mxfp4_codes_to_mma and moe_mxfp4_scales_to_mma (K' = 2K) lay them
+ * out, so tensor-core copies of moe_nvfp4_pack's weights are operands as they are (gs_rows = 0, gs = the
+ * matrix's global scale) wherever rows % 128 == 0 and K % 256 == 0.  Padding along K holds zeros. */
+typedef struct moe_nvfp4_operand {
+    uint8_t* q;      /* moe_nvfp4_operand_codes(rows, K) bytes, 16-byte aligned */
+    uint8_t* s;      /* moe_nvfp4_operand_scales(rows, K) bytes, 16-byte aligned */
+    float* gs;       /* [rows] when gs_rows, else [1] */
+    int32_t gs_rows;
+} moe_nvfp4_operand;
+
+size_t moe_nvfp4_operand_codes(int64_t rows, int64_t K);  /* 0 for an unsupported shape */
+size_t moe_nvfp4_operand_scales(int64_t rows, int64_t K);
+
+/* Workspace for moe_nvfp4_linear at these sizes, for moe_nvfp4_matmul, and for moe_nvfp4_quantize of
+ * any of [M][K], [N][K], [M][N].  Initialise it once with moe_workspace_init; device-side timeouts are reported
+ * through it.  0 for an unsupported shape. */
+size_t moe_nvfp4_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/* Operands of x [R][C] (dtype, row stride ld >= C): `rows` is that of x ([R] rows contracting along C), `cols` that of
+ * its transpose ([C] rows contracting along R); either may be NULL.  The rule is moe_nvfp4_pack's with
+ * a global scale per operand row, computed from the row (scales_given = 0; gs_rows must be 1), so a row's operand
+ * does not depend on the others; or with the scales found in gs (scales_given != 0): values beyond their range
+ * saturate.  ws: used by cols with computed scales only (may be NULL otherwise). */
+moe_status moe_nvfp4_quantize(const void* x, moe_dtype dtype, int64_t R, int64_t C, int64_t ld,
+                              const moe_nvfp4_operand* rows, const moe_nvfp4_operand* cols, int scales_given, void* ws,
+                              size_t ws_bytes, moe_stream_t stream);
+
+/* The numbers an operand stands for, fp32 v [rows][K]: (E2M1 * E4M3) * gs, rounded once. */
+moe_status moe_nvfp4_operand_values(const moe_nvfp4_operand* op, int64_t rows, int64_t K, float* v, moe_stream_t stream);
+
+/* y [M][ldy] (dtype) = A [M][K] * B [N][K]^T: fp32 sums on the tensor cores, times the rows' scales, rounded
+ * once.  K >= 1, ldy >= N; y aligned to its element. */
+moe_status moe_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_operand* B, int64_t M, int64_t N, int64_t K, void* y,
+                            moe_dtype dtype, int64_t ldy, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* y [M][ldy] = Q(x) W^T: the rows of x [M][ldx] quantised (computed row scales) into the workspace, then the product
+ * with the operand W [N][K].  ws: moe_nvfp4_workspace_size(M, N, K) bytes. */
+moe_status moe_nvfp4_linear(const void* x, moe_dtype x_dtype, int64_t M, int64_t K, int64_t ldx, const moe_nvfp4_operand* W,
+                            int64_t N, void* y, moe_dtype y_dtype, int64_t ldy, void* ws, size_t ws_bytes,
+                            moe_stream_t stream);
 
 /* ---------------------------------------------------------------- failure-detection self-test
  * Not part of the layer.  Every barrier wait in the library's kernels is bounded: when it runs out

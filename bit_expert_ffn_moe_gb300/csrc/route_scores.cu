@@ -1,7 +1,7 @@
 // route_scores.cu -- routing rules on given logits (sigmoid or softmax scores, a balance bias that
 // takes part in the choice only, expert groups, top-k, renormalised weights) and their gradient.
 //
-// One warp per token; lane l holds the experts l + 32 i in registers (i < NV, E <= 32 NV <= 1024).
+// One warp per token; lane l holds the experts NV l .. NV l + NV - 1 in registers (E <= 32 NV <= 1024).
 //
 // The choice is the one that 64-bit arithmetic makes.  Without a bias the scores are monotone in the
 // logits, so the logits themselves are ranked and nothing is rounded.  With a bias (and for the sums of
@@ -117,14 +117,16 @@ struct Top2 {
 // 2^shift lanes share an expert group: as many as G groups leave to each.
 __device__ __forceinline__ int group_lane_shift(int G) { return G <= 1 ? 5 : G <= 2 ? 4 : G <= 4 ? 3 : G <= 8 ? 2 : G <= 16 ? 1 : 0; }
 
-// Score of group lane >> sh from values val[e] (-inf: out of service); every lane of the group gets it.
+// Score of group lane >> sh from values val[e] (-inf: out of service); every lane of the group gets it, and
+// in *least the smaller of the values it is made of.
 template <typename F>
-__device__ __forceinline__ F group_score(const F* val, int G, int S, int sh, bool top2) {
+__device__ __forceinline__ F group_score(const F* val, int G, int S, int sh, bool top2, F* least = nullptr) {
     const int lane = threadIdx.x & 31, g = lane >> sh, lp = 1 << sh;
     Top2<F> t{(F)-INFINITY, (F)-INFINITY};
     if (g < G)
         for (int j = lane & (lp - 1); j < S; j += lp) t.add(val[g * S + j]);
     for (int m = 1; m < lp; m <<= 1) t.merge(m);
+    if (least) *least = top2 && t.b > -INFINITY ? t.b : t.a;
     return t.score(top2);
 }
 
@@ -144,269 +146,528 @@ __device__ __forceinline__ uint32_t best_groups(F score, uint32_t cand, int G, i
     return mask;
 }
 
+// What a warp needs of a row: NV values per lane, lane l the experts NV l .. NV l + NV - 1.
 template <int NV, typename T>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(const RouteScoresArgs a) {
-    extern __shared__ double scratch[];  // per warp E values, where the rule has groups or a bias
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = blockIdx.x * kRouteWarps + warp;
-    if (t >= a.T) return;
-    const int E = a.E, k = a.k, G = a.rule.groups;
+__device__ __forceinline__ void load_chunk(const T* row, int E, bool wide, float (&l)[NV]) {
+    const int e0 = NV * (int)(threadIdx.x & 31);
+    constexpr int bytes = NV * (int)sizeof(T);
+    if (bytes >= 4 && wide && e0 + NV <= E) {
+        constexpr int words = bytes >= 4 ? bytes / 4 : 1;
+        uint32_t u[words];
+        const T* p = row + e0;
+        if constexpr (words % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < words / 4; ++i) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                u[4 * i] = q.x, u[4 * i + 1] = q.y, u[4 * i + 2] = q.z, u[4 * i + 3] = q.w;
+            }
+        } else if constexpr (words == 2) {
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+            u[0] = q.x, u[1] = q.y;
+        } else {
+            u[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        }
+        const T* v = reinterpret_cast<const T*>(u);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) l[i] = to_f32(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) l[i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
+    }
+}
+
+// Error bounds of differences of two fp32 ranking values.  Sigmoid s = 1 / (1 + e), e = exp2 of the rounded exponent
+// by the hardware's approximation (relative error 2^-22 + |l| 2^-24), 1 / by the hardware's (1 ulp): an error of
+// s (1 - s) (2^-22 + |l| 2^-24) + s (2^-24 + 2^-23) < 2.3 * 2^-23, as s (1 - s) <= 1/4 and s (1 - s) |l| < 0.23.
+// Softmax: the sum's NV + 5 roundings and the two exp, relative to the row's largest score.  The sum with
+// the bias rounds once more, 2^-24 of the value.
+constexpr float kSigmoidErr = 5.6e-7f;  // 2 * 2.3 * 2^-23
+__device__ __forceinline__ float softmax_err(int nv, float largest) { return (float)(nv + 16) * 1.1920929e-7f * largest; }
+constexpr float kSumErr = 1.8e-7f;  // 1.5 * 2^-23 of the largest value
+
+__device__ __forceinline__ float sigmoid_fast(float l) {
+    float e, s;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * l));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    return s;
+}
+
+// Exclusive prefix sum over lanes of a count of at most 32.
+__device__ __forceinline__ int lane_prefix(int count, int bits) {
+    const uint32_t below = (1u << (threadIdx.x & 31)) - 1;
+    int p = 0;
+    for (int b = 0; b < bits; ++b) p += __popc(__ballot_sync(kFull, (count >> b) & 1) & below) << b;
+    return p;
+}
+
+// ------------------------------------------------------------------ the careful choice
+// A 64-bit key in the order of doubles (no NaN).
+__device__ __forceinline__ unsigned long long key64(double v) {
+    const long long u = __double_as_longlong(v == 0.0 ? 0.0 : v);
+    return u < 0 ? ~(unsigned long long)u : (unsigned long long)u | 0x8000000000000000ull;
+}
+
+struct Scratch {  // of a warp, in shared memory
+    unsigned long long* v64;  // [E]
+    uint32_t* key;            // [E]
+    uint16_t* list;           // [E]
+    int* picks;               // [32]
+};
+constexpr int kScratchPerExpert = 14;
+__device__ __forceinline__ Scratch warp_scratch(void* smem, int E, int warps, int warp) {
+    Scratch s;
+    char* p = static_cast<char*>(smem);
+    s.v64 = reinterpret_cast<unsigned long long*>(p) + (size_t)warp * E;
+    p += (size_t)8 * warps * E;
+    s.picks = reinterpret_cast<int*>(p) + 32 * warp;
+    p += (size_t)128 * warps;
+    s.key = reinterpret_cast<uint32_t*>(p) + (size_t)warp * E;
+    p += (size_t)4 * warps * E;
+    s.list = reinterpret_cast<uint16_t*>(p) + (size_t)warp * E;
+    return s;
+}
+
+// The whole choice for one token by one warp from shared memory: experts out of service inside the
+// choice, and values closer than their error, of which those that could stand on either side of the border
+// (a few) are computed in 64 bits, one per lane.  Writes the k ids in ascending order to picks[].
+template <typename T>
+__device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const T* row, const Scratch sc) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t below = (1u << lane) - 1;
+    const int E = a.E, k = a.k, G = a.rule.groups, S = E / G, nv = (E + 31) / 32;
     const bool softmax = a.rule.score == MOE_SCORE_SOFTMAX, biased = a.bias != nullptr;
     const bool top2 = a.rule.group_score == MOE_GROUP_TOP2;
-    double* v64 = scratch + (size_t)warp * E;
-
-    float l[NV];
-    const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ld;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = lane + 32 * i < E ? to_f32(row[lane + 32 * i]) : -INFINITY;
-    RowNorm norm = {0.f, 0.f};
-    if (softmax) norm = softmax_norm<NV>(l);
-
-    // Ranking values and the bound on the error of a difference of two of them.  fp32 sigmoid: expf and
-    // a division are within 2^-22 of it; softmax: the sum's (NV + 16) roundings dominate, relative to the
-    // row's largest score; the sum with the bias rounds once more.
-    float v[NV];
-    float vmax = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        v[i] = l[i];
-        if (biased) {
-            v[i] = in_service(l[i]) ? score_f32(l[i], softmax, norm) + __ldg(a.bias + e) : -INFINITY;
-            if (in_service(l[i])) vmax = fmaxf(vmax, fabsf(v[i]));
-        }
-        if (e < E && a.scores) a.scores[(int64_t)t * E + e] = score_f32(l[i], softmax, norm);
+    float mx = -kMaxF32, inv_sum = 0.f;
+    if (softmax && (biased || top2)) {
+        for (int e = lane; e < E; e += 32)
+            if (in_service(to_f32(row[e]))) mx = fmaxf(mx, clamp_logit(to_f32(row[e])));
+        mx = warp_max_f32(mx);
+        float sum = 0.f;
+        for (int e = lane; e < E; e += 32)
+            if (in_service(to_f32(row[e]))) sum += expf(clamp_logit(to_f32(row[e])) - mx);
+        sum = warp_butterfly_sum(sum);
+        inv_sum = sum > 0.f ? 1.f / sum : 0.f;
     }
-    const float err_s = softmax ? (float)(NV + 16) * 1.1920929e-7f * norm.inv_sum : 9.5367432e-7f;
-    float err = 0.f;
-    if (biased) err = err_s + 4.7683716e-7f * warp_max_f32(vmax);
-
-    double norm64 = 0.0;  // 1 / sum exp(l - max) in 64 bits, computed when a choice needs it
-    auto exact_value = [&](float lv, int e) -> double {
-        double s = softmax ? exp((double)clamp_logit(lv) - (double)norm.max) * norm64 : sigmoid_f64(lv);
-        if (biased) s += (double)__ldg(a.bias + e);
-        return s;
-    };
-    auto need_exact = [&]() {
-        if (!softmax || norm64 != 0.0) return;
-        double sum = 0.0;
-#pragma unroll 1
-        for (int i = 0; i < NV; ++i) {
-            const float lv = lane + 32 * i < E ? to_f32(row[lane + 32 * i]) : -INFINITY;
-            if (in_service(lv)) sum += exp((double)clamp_logit(lv) - (double)norm.max);
+    const RowNorm norm = {mx, inv_sum};
+    const float err_s = softmax ? softmax_err(nv, inv_sum) : kSigmoidErr;
+    double inv64 = 0.0;
+    // 64-bit values of the n listed experts
+    auto exact_list = [&](int n) {
+        if (softmax && inv64 == 0.0) {
+            double sum = 0.0;
+            for (int e = lane; e < E; e += 32)
+                if (in_service(to_f32(row[e]))) sum += exp((double)clamp_logit(to_f32(row[e])) - (double)mx);
+            inv64 = 1.0 / warp_sum_f64(sum);
         }
-        norm64 = 1.0 / warp_sum_f64(sum);
+        for (int i = lane; i < n; i += 32) {
+            const int e = sc.list[i];
+            const float lv = to_f32(row[e]);
+            double s = softmax ? exp((double)clamp_logit(lv) - (double)mx) * inv64 : sigmoid_f64(lv);
+            if (biased) s += (double)__ldg(a.bias + e);
+            sc.v64[i] = __double_as_longlong(s);
+        }
+        __syncwarp();
     };
+    auto score32 = [&](float lv) { return softmax ? score_f32(lv, true, norm) : sigmoid_fast(clamp_logit(lv)); };
 
-    // ---------------------------------------------------------------- groups
-    uint32_t kept = 0xffffffffu;
-    const int S = E / G;
+    // keys of the ranking values; ranked values are the logits or scores + bias
+    float vmax = 0.f;
+    for (int e = lane; e < E; e += 32) {
+        const float lv = to_f32(row[e]);
+        float v = lv;
+        if (biased && in_service(lv)) {
+            v = score32(lv) + __ldg(a.bias + e);
+            vmax = fmaxf(vmax, fabsf(v));
+        }
+        // (a NaN value comes from a NaN bias: ranked like an expert out of service)
+        sc.key[e] = in_service(lv) && v == v ? logit_key(v) : kOutKey;
+    }
+    const float err = biased ? err_s + kSumErr * warp_max_f32(vmax) : 0.f;
+    __syncwarp();
+
+    uint32_t kept = kFull;
     const GroupOf group_of(S);
     if (G > 1 && a.rule.top_groups < G) {
-        const int sh = group_lane_shift(G), keep = a.rule.top_groups;
+        const int sh = group_lane_shift(G), keep = a.rule.top_groups, g = lane >> sh;
         const bool raw = !biased && !top2;  // the groups' best logits: exact
-        float* vs = reinterpret_cast<float*>(v64);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (lane + 32 * i < E)
-                vs[lane + 32 * i] = (biased || raw) ? v[i] : in_service(l[i]) ? score_f32(l[i], softmax, norm) : -INFINITY;
+        float* val = reinterpret_cast<float*>(sc.v64);
+        for (int e = lane; e < E; e += 32) {
+            const uint32_t q = sc.key[e];
+            val[e] = q == kOutKey ? -INFINITY : (biased || raw) ? key_logit(q) : score32(to_f32(row[e]));
+        }
         __syncwarp();
-        const float gs = group_score<float>(vs, G, S, sh, top2);
-        const uint32_t all = G == 32 ? kFull : (1u << G) - 1;
-        kept = best_groups<float>(gs, all, G, sh, keep);
+        float second;
+        const float gs = group_score<float>(val, G, S, sh, top2, &second);
+        kept = best_groups<float>(gs, G == 32 ? kFull : (1u << G) - 1, G, sh, keep);
         if (!raw) {
-            const int g = lane >> sh;
             const bool mine = g < G && gs > -INFINITY;
             const bool in = g < G && ((kept >> g) & 1);
             const float lo = warp_max_f32(mine && !in ? gs : -INFINITY);   // best left out
             const float hi = -warp_max_f32(mine && in ? -gs : -INFINITY);  // worst kept
-            const float gerr = 2.f * (biased ? err : err_s) + 4.7683716e-7f * fmaxf(fabsf(lo), fabsf(hi));
+            const float verr = biased ? err : err_s;
+            const float gerr = 2.f * verr + kSumErr * fmaxf(fabsf(lo), fabsf(hi));
             if (lo > -INFINITY && hi < INFINITY && hi - lo <= gerr) {
-                need_exact();
-                const uint32_t lanes = __ballot_sync(kFull, mine && gs >= hi - gerr && gs <= lo + gerr);
+                const bool is_open = mine && gs >= hi - gerr && gs <= lo + gerr;
+                const uint32_t lanes = __ballot_sync(kFull, is_open);
                 const uint32_t sure = __ballot_sync(kFull, mine && gs > lo + gerr);
                 uint32_t open = 0, in_mask = 0;
                 for (int j = 0; j < G; ++j) {
                     open |= ((lanes >> (j << sh)) & 1u) << j;
                     in_mask |= ((sure >> (j << sh)) & 1u) << j;
                 }
+                // of the open groups, the values that may be among a group's best one or two
+                if ((lane & ((1 << sh) - 1)) == 0) sc.picks[g] = __float_as_int(second - verr);
                 __syncwarp();
-#pragma unroll 1
-                for (int i = 0; i < NV; ++i) {
+                int n = 0;
+                for (int i = 0; i < nv; ++i) {
                     const int e = lane + 32 * i;
-                    if (e >= E || !((open >> group_of(e)) & 1)) continue;
-                    const float lv = to_f32(row[e]);
-                    v64[e] = in_service(lv) ? exact_value(lv, e) : -(double)INFINITY;
+                    bool take = e < E && ((open >> group_of(e < E ? e : 0)) & 1);
+                    if (take) take = val[e] > -INFINITY && val[e] >= __int_as_float(sc.picks[group_of(e)]);
+                    const uint32_t who = __ballot_sync(kFull, take);
+                    if (take) sc.list[n + __popc(who & below)] = (uint16_t)e;
+                    n += __popc(who);
                 }
                 __syncwarp();
-                const bool is_open = g < G && ((open >> g) & 1);
-                const double gx = group_score<double>(v64, is_open ? G : 0, S, sh, top2);
-                kept = in_mask | best_groups<double>(gx, open, G, sh, keep - __popc(in_mask));
+                exact_list(n);
+                double x = -(double)INFINITY, y = -(double)INFINITY;
+                if (is_open && (lane & ((1 << sh) - 1)) == 0)
+                    for (int i = 0; i < n; ++i) {
+                        if (group_of(sc.list[i]) != g) continue;
+                        const double v = __longlong_as_double(sc.v64[i]);
+                        if (v > x) y = x, x = v;
+                        else if (v > y) y = v;
+                    }
+                const double gx = top2 && y > -(double)INFINITY ? x + y : x;
+                kept = in_mask | best_groups<unsigned long long>(key64(gx), open, G, sh, keep - __popc(in_mask));
             }
         }
+        __syncwarp();
+        for (int e = lane; e < E; e += 32)
+            if (!((kept >> group_of(e)) & 1)) sc.key[e] = 0u;
+        __syncwarp();
     }
 
-    // ---------------------------------------------------------------- top-k: the k-th key and who ties with it
-    uint32_t key[NV];
-    uint32_t chosen = 0;  // bit i: expert lane + 32 i is picked
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        const bool cand = e < E && (G == 1 || ((kept >> group_of(e)) & 1));
-        // (a NaN value comes from a NaN bias: ranked like an expert out of service)
-        key[i] = !cand ? 0u : in_service(l[i]) && v[i] == v[i] ? logit_key(v[i]) : kOutKey;
-    }
-    uint32_t last = 0, next = 0;  // key of the pick that completes the k, largest key left out
-    int above = 0;                // picks with a larger key than `last`
-    {
-        uint32_t gone = 0;
-        int n = 0;
-        while (true) {
-            uint32_t lb = 0;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (!((gone >> i) & 1)) lb = max(lb, key[i]);
-            const uint32_t wb = __reduce_max_sync(kFull, lb);
-            if (n >= k) {
-                next = n > k ? last : wb;
-                break;
-            }
-            if (wb != last) above = n;
-            last = wb;
-            n += __popc(__ballot_sync(kFull, lb == wb));
-            if (lb == wb) {
-                bool done = false;
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-                    if (!done && !((gone >> i) & 1) && key[i] == wb) {
-                        gone |= 1u << i;
-                        done = true;
-                    }
+    // the k-th key and who ties with it
+    uint32_t gone = 0, chosen = 0;  // bit i: expert lane + 32 i
+    uint32_t last = 0, next = 0;    // key of the pick that completes the k, largest key left out
+    int above = 0, n = 0;           // picks with a larger key than `last`, picks so far
+    uint32_t lb = 0;
+    int li = -1;
+    while (true) {
+        if (li < 0) {
+            lb = 0;
+            for (int i = 0; i < nv; ++i) {
+                const uint32_t q = lane + 32 * i < E && !((gone >> i) & 1) ? sc.key[lane + 32 * i] : 0u;
+                if (q > lb) lb = q, li = i;
             }
         }
+        const uint32_t wb = __reduce_max_sync(kFull, lb);
+        if (n >= k) {
+            next = n > k ? last : wb;
+            break;
+        }
+        if (wb != last) above = n;
+        last = wb;
+        n += __popc(__ballot_sync(kFull, lb == wb));
+        if (lb == wb) gone |= 1u << (li & 31), li = -1;
     }
-    const bool close = biased && last > kOutKey && next > kOutKey && key_logit(last) - key_logit(next) <= err;
-    if (!close) {
+    if (!(biased && last > kOutKey && next > kOutKey && key_logit(last) - key_logit(next) <= err)) {
         int ties = k - above;  // how many of the experts at `last` are picked, lowest ids first
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (key[i] > last) chosen |= 1u << i;
-            const uint32_t tie = __ballot_sync(kFull, key[i] == last);
-            if (key[i] == last && __popc(tie & ((1u << lane) - 1)) < ties) chosen |= 1u << i;
+        for (int i = 0; i < nv; ++i) {
+            const uint32_t q = lane + 32 * i < E ? sc.key[lane + 32 * i] : 0u;
+            if (q > last) chosen |= 1u << i;
+            const uint32_t tie = __ballot_sync(kFull, q == last);
+            if (q == last && __popc(tie & below) < ties) chosen |= 1u << i;
             ties -= __popc(tie);
         }
     } else {
-        need_exact();
         const float top = key_logit(next) + err, bottom = key_logit(last) - err;
         uint32_t open = 0;
-        int sure = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (key[i] <= kOutKey) continue;
-            const float x = key_logit(key[i]);
-            if (x > top) {
-                chosen |= 1u << i;
-                ++sure;
-            } else if (x >= bottom) {
-                open |= 1u << i;
+        int sure = 0, m = 0;
+        for (int i = 0; i < nv; ++i) {
+            const int e = lane + 32 * i;
+            const uint32_t q = e < E ? sc.key[e] : 0u;
+            const bool up = q > kOutKey && key_logit(q) > top, take = q > kOutKey && !up && key_logit(q) >= bottom;
+            if (up) chosen |= 1u << i;
+            if (take) open |= 1u << i;
+            sure += __popc(__ballot_sync(kFull, up));
+            const uint32_t who = __ballot_sync(kFull, take);
+            if (take) sc.list[m + __popc(who & below)] = (uint16_t)e;
+            m += __popc(who);
+        }
+        __syncwarp();
+        exact_list(m);
+        // list entries are in id order: an equal value before an entry has the lower id
+        int at = 0;
+        for (int i = 0; i < nv; ++i) {
+            const uint32_t who = __ballot_sync(kFull, (open >> i) & 1);
+            if ((open >> i) & 1) {
+                const int me = at + __popc(who & below);
+                const unsigned long long mine = key64(__longlong_as_double(sc.v64[me]));
+                int before = sure;
+                for (int j = 0; j < m; ++j) {
+                    const unsigned long long o = key64(__longlong_as_double(sc.v64[j]));
+                    before += (o > mine || (o == mine && j < me)) ? 1 : 0;
+                }
+                if (before < k) chosen |= 1u << i;
             }
+            at += __popc(who);
         }
-        sure = __reduce_add_sync(kFull, sure);
-        __syncwarp();
-        // the open experts' values, in id order (NaN elsewhere: compares false)
-#pragma unroll 1
-        for (int i = 0; i < NV; ++i) {
-            const int e = lane + 32 * i;
-            if (e < E) v64[e] = ((open >> i) & 1) ? exact_value(to_f32(row[e]), e) : nan("");
-        }
-        __syncwarp();
-        uint32_t rest = open;
-        while (rest) {
-            const int i = __ffs(rest) - 1;
-            rest &= rest - 1;
-            const int e = lane + 32 * i;
-            const double mine = v64[e];
-            int before = sure;
-            for (int j = 0; j < E; ++j) before += (v64[j] > mine || (v64[j] == mine && j < e)) ? 1 : 0;
-            if (before < k) chosen |= 1u << i;
-        }
-        __syncwarp();
-    }
-
-    // ---------------------------------------------------------------- weights of the picks, in id order
-    const bool renorm = a.rule.renormalize != 0;
-    float ref = 0.f;
-    if (renorm) {
-        float m = -kMaxF32;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (((chosen >> i) & 1) && in_service(l[i])) m = fmaxf(m, clamp_logit(l[i]));
-        ref = warp_max_f32(m);
-        if (!softmax) ref = fminf(ref, 0.f);
-    }
-    float u[NV];
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        u[i] = 0.f;
-        if (!((chosen >> i) & 1)) continue;
-        u[i] = renorm ? score_ratio(l[i], softmax, ref) : score_f32(l[i], softmax, norm);
-        sum += u[i];
-    }
-    float scale = a.rule.scale;
-    if (renorm) {
-        sum = warp_butterfly_sum(sum);
-        scale = sum > 0.f ? scale / sum : 0.f;
     }
     int base = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const bool in = (chosen >> i) & 1;
-        const uint32_t who = __ballot_sync(kFull, in);
-        if (in) {
-            const int at = base + __popc(who & ((1u << lane) - 1));
-            a.ids[(int64_t)t * k + at] = lane + 32 * i;
-            a.w[(int64_t)t * k + at] = u[i] * scale;
-            if (a.counts) atomicAdd(a.counts + lane + 32 * i, 1);
-        }
+    for (int i = 0; i < nv; ++i) {
+        const uint32_t who = __ballot_sync(kFull, (chosen >> i) & 1);
+        const int at = base + __popc(who & below);
+        if (((chosen >> i) & 1) && at < k) sc.picks[at] = lane + 32 * i;
         base += __popc(who);
     }
 }
 
+// Descending sort of N registers: odd-even merge network (Batcher); 19 exchanges for 8.
+template <int N>
+__device__ __forceinline__ void sort_down(float* v) {
+#pragma unroll
+    for (int p = 1; p < N; p *= 2)
+#pragma unroll
+        for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+            for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const float x = v[i + j], y = v[i + j + q];
+                        v[i + j] = fmaxf(x, y);
+                        v[i + j + q] = fminf(x, y);
+                    }
+}
+
+// ------------------------------------------------------------------ the rules
+// Each lane sorts its NV values once (in runs of eight); a round of the choice is then a warp maximum of the lanes'
+// heads and a shift in the lane that held it.  The threshold separates the picks when the next value is
+// farther than the error bound (or, for exact values, ties are resolved in id order); everything else
+// goes to choose_careful.
+template <int NV, typename T>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(const RouteScoresArgs a, const bool wide) {
+    constexpr int kRun = NV < 8 ? NV : 8, kRuns = NV / kRun;
+    constexpr int kBits = NV == 1 ? 1 : NV == 2 ? 2 : NV == 4 ? 3 : NV == 8 ? 4 : NV == 16 ? 5 : 6;  // of a count up to NV
+    extern __shared__ double scratch[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * warps + warp;
+    if (t >= a.T) return;
+    const int E = a.E, k = a.k, G = a.rule.groups;
+    const bool softmax = a.rule.score == MOE_SCORE_SOFTMAX, biased = a.bias != nullptr, renorm = a.rule.renormalize != 0;
+    const bool grouped = G > 1 && a.rule.top_groups < G, top2 = a.rule.group_score == MOE_GROUP_TOP2;
+    const Scratch sc = warp_scratch(scratch, E, warps, warp);
+    int* picks = sc.picks;
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    const int e0 = NV * lane;
+
+    float l[NV];
+    load_chunk<NV>(row, E, wide, l);
+    const bool want_scores = biased || (grouped && top2);
+    RowNorm norm = {0.f, 0.f};
+    if (softmax && (want_scores || !renorm || a.scores)) norm = softmax_norm<NV>(l);
+    if (a.scores) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (e0 + i < E) a.scores[t * E + e0 + i] = score_f32(l[i], softmax, norm);
+    }
+
+    // ranking values: the logits, or scores (+ bias); -inf for experts out of service
+    float v[NV];
+    float vmax = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        v[i] = in_service(l[i]) ? l[i] : -INFINITY;  // (drops NaN)
+        if (!want_scores) continue;
+        if (in_service(l[i])) {
+            v[i] = softmax ? score_f32(l[i], true, norm) : sigmoid_fast(clamp_logit(l[i]));
+            if (biased) {
+                v[i] += __ldg(a.bias + e0 + i);
+                vmax = fmaxf(vmax, v[i] == v[i] ? fabsf(v[i]) : INFINITY);  // (NaN: a NaN bias)
+            }
+        }
+    }
+    const float err_s = softmax ? softmax_err(NV, norm.inv_sum) : kSigmoidErr;
+    const float err = biased ? err_s + kSumErr * warp_max_f32(vmax) : 0.f;
+    bool careful = biased && !(err < INFINITY);  // an infinite or NaN bias
+
+    if (grouped) {
+        const int S = E / G, lanes = S / NV;
+        const bool raw = !biased && !top2;
+        uint32_t kept = 0;
+        float hi, lo;
+        bool in = false;
+        if (S % NV == 0 && (lanes & (lanes - 1)) == 0) {  // whole lanes, a power of two of them, share a group
+            Top2<float> best{-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < NV; ++i) best.add(v[i]);
+            for (int m = 1; m < lanes; m <<= 1) best.merge(m);
+            const float gs = best.score(top2);
+            float left = gs;
+            hi = 0.f;
+            for (int r = 0; r < a.rule.top_groups; ++r) {  // the best group left, ties to the lower group
+                hi = warp_max_f32(left);
+                const int first = __ffs(__ballot_sync(kFull, left == hi && !in && e0 < E)) - 1;
+                if (first >= 0 && lane / lanes == first / lanes) in = true, left = -INFINITY;
+            }
+            lo = warp_max_f32(in ? -INFINITY : gs);
+        } else {  // through shared memory
+            float* val = reinterpret_cast<float*>(sc.v64);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (e0 + i < E) val[e0 + i] = v[i];
+            __syncwarp();
+            const int sh = group_lane_shift(G), g = lane >> sh;
+            const float gs = group_score<float>(val, G, S, sh, top2);
+            kept = best_groups<float>(gs, G == 32 ? kFull : (1u << G) - 1, G, sh, a.rule.top_groups);
+            const bool mine = g < G && ((kept >> g) & 1);
+            lo = warp_max_f32(g < G && !mine ? gs : -INFINITY);
+            hi = -warp_max_f32(mine ? -gs : -INFINITY);
+            __syncwarp();
+        }
+        const float gerr = raw ? 0.f : 2.f * (biased ? err : err_s) + kSumErr * fmaxf(fabsf(lo), fabsf(hi));
+        if (!raw && lo > -INFINITY && !(hi - lo > gerr)) careful = true;
+        const GroupOf group_of(S);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (kept) in = e0 + i < E && ((kept >> group_of(e0 + i < E ? e0 + i : 0)) & 1);
+            if (!in) v[i] = -INFINITY;
+            else if (!biased) v[i] = in_service(l[i]) ? l[i] : -INFINITY;
+        }
+    }
+
+    if (!careful) {
+        float h[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) h[i] = v[i];
+#pragma unroll
+        for (int r = 0; r < kRuns; ++r) sort_down<kRun>(h + kRun * r);
+        float last = 0.f, next = -INFINITY;
+        int n = 0, above = 0;
+        while (true) {
+            float head = h[0];
+#pragma unroll
+            for (int r = 1; r < kRuns; ++r) head = fmaxf(head, h[kRun * r]);
+            const float m = warp_max_f32(head);
+            if (n >= k) {
+                next = m;
+                break;
+            }
+            if (m == -INFINITY) {  // fewer than k experts in service
+                careful = true;
+                break;
+            }
+            if (m != last || n == 0) above = n;
+            last = m;
+            n += __popc(__ballot_sync(kFull, head == m));
+            bool open = head == m;
+#pragma unroll
+            for (int r = 0; r < kRuns; ++r) {
+                if (open && h[kRun * r] == m) {
+#pragma unroll
+                    for (int i = 0; i + 1 < kRun; ++i) h[kRun * r + i] = h[kRun * r + i + 1];
+                    h[kRun * r + kRun - 1] = -INFINITY;
+                    open = false;
+                }
+            }
+        }
+        const bool tie = n > k || next == last;
+        if (biased && (tie || last - next <= err)) careful = true;
+        if (!careful) {
+            uint32_t chosen = 0, ties = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (v[i] > last) chosen |= 1u << i;
+                if (v[i] == last) ties |= 1u << i;
+            }
+            if (tie) {  // the lowest ids among the experts at `last`
+                int room = k - above - lane_prefix(__popc(ties), kBits);
+                while (ties && room > 0) {
+                    chosen |= ties & -ties;
+                    ties &= ties - 1;
+                    --room;
+                }
+            } else {
+                chosen |= ties;
+            }
+            int at = lane_prefix(__popc(chosen), kBits);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if ((chosen >> i) & 1) picks[at++] = e0 + i;
+        }
+    }
+    if (careful) choose_careful<T>(a, row, sc);
+    __syncwarp();
+
+    // weights: lane j < k has pick j
+    const int id = lane < k ? picks[lane] : 0;
+    const float lp = lane < k ? to_f32(row[id]) : -INFINITY;
+    float u;
+    float scale = a.rule.scale;
+    if (renorm) {
+        float ref = warp_max_f32(in_service(lp) ? clamp_logit(lp) : -kMaxF32);
+        if (!softmax) ref = fminf(ref, 0.f);
+        u = score_ratio(lp, softmax, ref);
+        const float sum = warp_butterfly_sum(u);
+        scale = sum > 0.f ? scale / sum : 0.f;
+    } else {
+        u = score_f32(lp, softmax, norm);
+    }
+    if (lane < k) {
+        a.ids[t * k + lane] = id;
+        a.w[t * k + lane] = u * scale;
+        if (a.counts) atomicAdd(a.counts + id, 1);
+    }
+}
+
+// ------------------------------------------------------------------ gradient
 // Gradient of the logits from the gradient of the weights (and, optionally, of all the scores).
 // u_j: the picked scores, c the rule's factor.  Renormalised: du_j = c (dw_j - sum_i dw_i u_i / S) / S with
 // S = sum u (taken in ratios to the largest score, as above), else du_j = c dw_j.  Sigmoid: dl = ds s (1 - s), with
 // 1 - s = sigmoid(-l).  Softmax: dl = s (ds - sum ds s); with renormalised weights and no other gradient of
-// the scores that sum is zero by itself and only the picked experts get a gradient.
+// the scores that sum is zero by itself, so that, as for sigmoid scores, only the picked experts get a
+// gradient: the row is then written as zeros and the picks' values on top, and only the picked logits are read.
 template <int NV, typename T>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel(const RouteBackwardArgs a) {
-    extern __shared__ float rows[];  // per warp: the gradient of the scores [E], times the scores
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t = blockIdx.x * kRouteWarps + warp;
+__global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel(const RouteBackwardArgs a, const bool wide) {
+    extern __shared__ float rows[];  // per warp, dense gradients only: the gradient of the scores times the scores [E]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * warps + warp;
     if (t >= a.T) return;
-    const int E = a.E, k = a.k;
+    const int E = a.E, k = a.k, e0 = NV * lane;
     const bool softmax = a.rule.score == MOE_SCORE_SOFTMAX, renorm = a.rule.renormalize != 0;
-    float* ds = rows + (size_t)warp * E;
-    const T* row = static_cast<const T*>(a.logits) + (int64_t)t * a.ld;
-    T* out = static_cast<T*>(a.dlogits) + (int64_t)t * a.ldd;
+    const bool dense = a.dscores || (softmax && !renorm);
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
 
-    float l[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < E ? to_f32(row[e]) : -INFINITY;
-        if (e < E) ds[e] = 0.f;
-    }
-    RowNorm norm = {0.f, 0.f};
-    if (softmax) norm = softmax_norm<NV>(l);
-    __syncwarp();
-
-    // lane j < k: pick j; g = u_j du_j, the product that the logits' gradient needs
-    const int id = lane < k ? a.ids[(int64_t)t * k + lane] : -1;
+    // lane j < k: pick j
+    const int id = lane < k ? a.ids[t * k + lane] : -1;
     const bool valid = id >= 0 && id < E;
     const float lp = valid ? to_f32(row[id]) : -INFINITY;
-    const float dw = valid && in_service(lp) ? a.dw[(int64_t)t * k + lane] * a.rule.scale : 0.f;
-    float g = 0.f;
+    const float dw = valid && in_service(lp) ? a.dw[t * k + lane] * a.rule.scale : 0.f;
+    float l[NV];
+    RowNorm norm = {0.f, 0.f};
+    float* ds = rows + (size_t)warp * E;
+    if (dense) {
+        load_chunk<NV>(row, E, wide, l);
+        if (softmax) norm = softmax_norm<NV>(l);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (e0 + i < E) ds[e0 + i] = 0.f;
+        __syncwarp();
+    } else {  // zeros, over which the picks' values go
+        constexpr int bytes = NV * (int)sizeof(T);
+        if (wide && bytes % 16 == 0 && e0 + NV <= E) {
+#pragma unroll
+            for (int i = 0; i < bytes / 16; ++i) reinterpret_cast<uint4*>(out + e0)[i] = make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (e0 + i < E) out[e0 + i] = from_f32<T>(0.f);
+        }
+        __syncwarp();
+    }
+    float g;  // u_j du_j, the product that the logits' gradient needs
     if (renorm) {
         float ref = warp_max_f32(in_service(lp) ? clamp_logit(lp) : -kMaxF32);
         if (!softmax) ref = fminf(ref, 0.f);
@@ -417,30 +678,32 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel
     } else {
         g = dw * score_f32(lp, softmax, norm);
     }
+    if (!dense) {
+        if (valid) out[id] = from_f32<T>(in_service(lp) ? (softmax ? g : g * sigmoid_f32(-lp)) : 0.f);
+        return;
+    }
     if (valid) ds[id] = g;
     __syncwarp();
     float total = 0.f;  // softmax: sum of ds s over all experts
     float gs[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
         gs[i] = 0.f;
-        if (e >= E) continue;
-        gs[i] = ds[e];
+        if (e0 + i >= E) continue;
+        gs[i] = ds[e0 + i];
         float extra = 0.f;
-        if (a.dscores && in_service(l[i])) extra = a.dscores[(int64_t)t * E + e] * score_f32(l[i], softmax, norm);
+        if (a.dscores && in_service(l[i])) extra = a.dscores[t * E + e0 + i] * score_f32(l[i], softmax, norm);
         if (!renorm) total += gs[i];
         total += extra;
         gs[i] += extra;
     }
-    if (softmax && (!renorm || a.dscores)) total = warp_butterfly_sum(total);
+    if (softmax) total = warp_butterfly_sum(total);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        if (e >= E) continue;
+        if (e0 + i >= E) continue;
         float dl = 0.f;
         if (in_service(l[i])) dl = softmax ? gs[i] - score_f32(l[i], true, norm) * total : gs[i] * sigmoid_f32(-l[i]);
-        out[e] = from_f32<T>(dl);
+        out[e0 + i] = from_f32<T>(dl);
     }
 }
 
@@ -468,14 +731,21 @@ const void* backward_kernel(int E) {
 
 }  // namespace
 
+// Rows start on 16-byte boundaries: lanes read their experts in wide pieces.
+static bool rows_wide(const void* p, int64_t ld, moe_dtype dtype) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (dtype == MOE_F32 ? 4 : 2) % 16 == 0;
+}
+
 cudaError_t launch_route_scores(const RouteScoresArgs& a, moe_dtype dtype, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     const void* f = dtype == MOE_F32    ? scores_kernel<float>(a.E)
                     : dtype == MOE_BF16 ? scores_kernel<__nv_bfloat16>(a.E)
                                         : scores_kernel<__half>(a.E);
-    const size_t smem = a.bias || a.rule.groups > 1 ? sizeof(double) * kRouteWarps * (size_t)a.E : 0;
-    void* args[] = {const_cast<RouteScoresArgs*>(&a)};
-    return launch_kernel(f, dim3((a.T + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps), smem, st, false, args);
+    bool wide = rows_wide(a.logits, a.ld, dtype);
+    const int warps = a.E > 512 ? kRouteWarps / 2 : kRouteWarps;  // (less than 60 KB of scratch)
+    const size_t smem = (size_t)warps * (kScratchPerExpert * (size_t)a.E + 128);
+    void* args[] = {const_cast<RouteScoresArgs*>(&a), &wide};
+    return launch_kernel(f, dim3((a.T + warps - 1) / warps), dim3(32 * warps), smem, st, false, args);
 }
 
 cudaError_t launch_route_scores_backward(const RouteBackwardArgs& a, moe_dtype dtype, cudaStream_t st) {
@@ -483,9 +753,11 @@ cudaError_t launch_route_scores_backward(const RouteBackwardArgs& a, moe_dtype d
     const void* f = dtype == MOE_F32    ? backward_kernel<float>(a.E)
                     : dtype == MOE_BF16 ? backward_kernel<__nv_bfloat16>(a.E)
                                         : backward_kernel<__half>(a.E);
-    void* args[] = {const_cast<RouteBackwardArgs*>(&a)};
+    bool wide = rows_wide(a.logits, a.ld, dtype) && rows_wide(a.dlogits, a.ldd, dtype);
+    void* args[] = {const_cast<RouteBackwardArgs*>(&a), &wide};
+    const bool dense = a.dscores || (a.rule.score == MOE_SCORE_SOFTMAX && !a.rule.renormalize);
     return launch_kernel(f, dim3((a.T + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps),
-                         sizeof(float) * kRouteWarps * (size_t)a.E, st, false, args);
+                         dense ? sizeof(float) * kRouteWarps * (size_t)a.E : 0, st, false, args);
 }
 
 }  // namespace moe

@@ -30,19 +30,24 @@ def _need(cond: bool, what: str) -> None:
 
 
 def _matrix(t: torch.Tensor, what: str) -> int:
-    """Row stride of a 2-D CUDA tensor whose rows are contiguous."""
-    _need(t.dim() == 2 and t.is_cuda, "%s: a CUDA matrix expected" % what)
+    """Row stride of a 2-D CUDA tensor whose rows are contiguous and do not overlap."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError("%s: a CUDA matrix expected" % what)
     rows, cols = t.shape
-    _need(cols <= 1 or t.stride(1) == 1, "%s: contiguous rows expected" % what)
-    ld = t.stride(0) if rows > 1 else cols
-    _need(ld >= cols, "%s: rows may not overlap" % what)
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError("%s: contiguous rows expected" % what)
+    if rows <= 1:
+        return cols
+    if ld < cols:
+        raise ValueError("%s: rows may not overlap" % what)
     return ld
 
 
-def _plain(t: torch.Tensor, shape, dtype, like: torch.Tensor, what: str) -> None:
+def _plain(t: torch.Tensor, shape: tuple, dtype: torch.dtype, like: torch.Tensor, what: str) -> None:
     """A contiguous tensor of this shape and type on `like`'s device."""
-    _need(tuple(t.shape) == tuple(shape) and t.dtype == dtype and t.device == like.device and t.is_contiguous(),
-          "%s: contiguous %s of %s on %s expected" % (what, tuple(shape), dtype, like.device))
+    if t.shape != shape or t.dtype != dtype or t.get_device() != like.get_device() or not t.is_contiguous():
+        raise ValueError("%s: contiguous %s of %s on %s expected" % (what, shape, dtype, like.device))
 
 
 # ------------------------------------------------------------------ routing rules
@@ -172,7 +177,7 @@ def nvfp4_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
 
 def _on(op: Nvfp4Operand, rows: int, K: int, t: torch.Tensor, what: str) -> None:
     _need((op.rows, op.K) == (rows, K), "%s: an operand [%d, %d] expected, got [%d, %d]" % (what, rows, K, op.rows, op.K))
-    _need(op.q.device == t.device, "%s: on %s, the others on %s" % (what, op.q.device, t.device))
+    _need(op.q.get_device() == t.get_device(), "%s: on %s, the others on %s" % (what, op.q.device, t.device))
 
 
 def nvfp4_quantize(x: torch.Tensor, rows: Optional[Nvfp4Operand] = None, cols: Optional[Nvfp4Operand] = None,
@@ -196,7 +201,7 @@ def nvfp4_matmul(a: Nvfp4Operand, b: Nvfp4Operand, dtype: torch.dtype, workspace
     _on(b, b.rows, a.K, a.q, "b")
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.q.device)
-    _need(tuple(out.shape) == (a.rows, b.rows) and out.dtype == dtype and out.device == a.q.device, "out: [M, N] of dtype expected")
+    _need(out.shape == (a.rows, b.rows) and out.dtype == dtype and out.get_device() == a.q.get_device(), "out: [M, N] of dtype expected")
     B.moe_nvfp4_matmul(a.struct, b.struct, a.rows, b.rows, a.K, out, _dtype(out, "out"), _matrix(out, "out"), workspace)
     return out
 
@@ -208,6 +213,6 @@ def nvfp4_linear(x: torch.Tensor, W: Nvfp4Operand, workspace: torch.Tensor, out:
     _on(W, W.rows, K, x, "W")
     if out is None:
         out = torch.empty((M, W.rows), dtype=x.dtype, device=x.device)
-    _need(tuple(out.shape) == (M, W.rows) and out.device == x.device, "out: [M, N] expected")
+    _need(out.shape == (M, W.rows) and out.get_device() == x.get_device(), "out: [M, N] expected")
     B.moe_nvfp4_linear(x, code, M, K, ld, W.struct, W.rows, out, _dtype(out, "out"), _matrix(out, "out"), workspace)
     return out

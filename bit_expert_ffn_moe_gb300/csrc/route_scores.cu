@@ -51,7 +51,12 @@ __device__ __forceinline__ double warp_sum_f64(double v) {
     for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(kFull, v, m);
     return v;
 }
-__device__ __forceinline__ float warp_max_f32(float v) { return key_logit(__reduce_max_sync(kFull, logit_key(v))); }
+// Largest value of the warp (NaN ignored unless every lane has one).
+__device__ __forceinline__ float warp_max_f32(float v) {
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
 
 // The softmax of a row needs its largest logit and the sum of exp(l - max); unused for sigmoid scores.
 struct RowNorm {
@@ -80,35 +85,37 @@ __device__ __forceinline__ float score_f32(float l, bool softmax, const RowNorm&
 
 // A picked score as a ratio to exp(ref), for renormalised weights: ref is the largest picked logit
 // (sigmoid: at most 0, where exp(l) and the score part), so that a row of tiny scores keeps its ratios.
+// Sigmoid: exp(min(l, 0) - ref) / (1 + exp(-|l|)), for ref = 0 wherever l > 0.
 __device__ __forceinline__ float score_ratio(float l, bool softmax, float ref) {
     if (!in_service(l)) return 0.f;
     if (softmax) return expf(clamp_logit(l) - ref);
-    return l > 0.f ? sigmoid_f32(l) : expf(l - ref) / (1.f + expf(l));
+    return __fdividef(expf(fminf(l, 0.f) - ref), 1.f + expf(-fabsf(l)));
 }
 
-// Group of an expert: e / S as a product, exact for e < 1024 (its error e / 2^20 stays below 1 / S).
+// Group of an expert: e / S as a product with mul = ceil(2^20 / S), exact for e < 1024 (its error e / 2^20 stays
+// below 1 / S).
 struct GroupOf {
     uint32_t mul;
-    __device__ explicit GroupOf(int S) : mul(((1u << 20) + S - 1) / S) {}
     __device__ __forceinline__ int operator()(int e) const { return (int)(((uint32_t)e * mul) >> 20); }
 };
+
+__device__ __forceinline__ float larger(float x, float y) { return fmaxf(x, y); }
+__device__ __forceinline__ float smaller(float x, float y) { return fminf(x, y); }
+__device__ __forceinline__ double larger(double x, double y) { return x > y ? x : y; }
+__device__ __forceinline__ double smaller(double x, double y) { return x > y ? y : x; }
 
 // The two largest of a stream of values.
 template <typename F>
 struct Top2 {
     F a, b;
     __device__ __forceinline__ void add(F v) {
-        if (v > a) {
-            b = a;
-            a = v;
-        } else if (v > b) {
-            b = v;
-        }
+        b = larger(b, smaller(a, v));
+        a = larger(a, v);
     }
     __device__ __forceinline__ void merge(int xor_lane) {
         const F oa = __shfl_xor_sync(kFull, a, xor_lane), ob = __shfl_xor_sync(kFull, b, xor_lane);
-        add(oa);
-        add(ob);
+        b = larger(larger(b, ob), smaller(a, oa));
+        a = larger(a, oa);
     }
     // sum of the (up to) two best, or the best alone
     __device__ __forceinline__ F score(bool top2) const { return (top2 && b > -INFINITY) ? a + b : a; }
@@ -192,20 +199,21 @@ __device__ __forceinline__ float sigmoid_fast(float l) {
     return s;
 }
 
-// Exclusive prefix sum over lanes of a count of at most 32.
-__device__ __forceinline__ int lane_prefix(int count, int bits) {
-    const uint32_t below = (1u << (threadIdx.x & 31)) - 1;
-    int p = 0;
-    for (int b = 0; b < bits; ++b) p += __popc(__ballot_sync(kFull, (count >> b) & 1) & below) << b;
-    return p;
-}
-
 // ------------------------------------------------------------------ the careful choice
 // A 64-bit key in the order of doubles (no NaN).
 __device__ __forceinline__ unsigned long long key64(double v) {
     const long long u = __double_as_longlong(v == 0.0 ? 0.0 : v);
     return u < 0 ? ~(unsigned long long)u : (unsigned long long)u | 0x8000000000000000ull;
 }
+
+// What the launcher works out once: experts per group, ceil(2^20 / that), whether rows and bias may be read in wide
+// pieces, and how many lanes (2^lane_shift) hold exactly one group (-1: groups and lanes do not match).
+struct RoutePlan {
+    int S;
+    uint32_t group_mul;
+    int lane_shift;
+    bool wide, wide_bias;
+};
 
 struct Scratch {  // of a warp, in shared memory
     unsigned long long* v64;  // [E]
@@ -231,10 +239,10 @@ __device__ __forceinline__ Scratch warp_scratch(void* smem, int E, int warps, in
 // choice, and values closer than their error, of which those that could stand on either side of the border
 // (a few) are computed in 64 bits, one per lane.  Writes the k ids in ascending order to picks[].
 template <typename T>
-__device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const T* row, const Scratch sc) {
+__device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const RoutePlan& plan, const T* row, const Scratch sc) {
     const int lane = threadIdx.x & 31;
     const uint32_t below = (1u << lane) - 1;
-    const int E = a.E, k = a.k, G = a.rule.groups, S = E / G, nv = (E + 31) / 32;
+    const int E = a.E, k = a.k, G = a.rule.groups, S = plan.S, nv = (E + 31) / 32;
     const bool softmax = a.rule.score == MOE_SCORE_SOFTMAX, biased = a.bias != nullptr;
     const bool top2 = a.rule.group_score == MOE_GROUP_TOP2;
     float mx = -kMaxF32, inv_sum = 0.f;
@@ -286,7 +294,7 @@ __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const T* r
     __syncwarp();
 
     uint32_t kept = kFull;
-    const GroupOf group_of(S);
+    const GroupOf group_of{plan.group_mul};
     if (G > 1 && a.rule.top_groups < G) {
         const int sh = group_lane_shift(G), keep = a.rule.top_groups, g = lane >> sh;
         const bool raw = !biased && !top2;  // the groups' best logits: exact
@@ -423,47 +431,65 @@ __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const T* r
     }
 }
 
-// Descending sort of N registers: odd-even merge network (Batcher); 19 exchanges for 8.
-template <int N>
-__device__ __forceinline__ void sort_down(float* v) {
+// The lanes' values in descending order: bitonic sort, 15 exchanges.
+__device__ __forceinline__ float sort_lanes_down(float v) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int p = 1; p < N; p *= 2)
+    for (int n = 2; n <= 32; n *= 2)
 #pragma unroll
-        for (int q = p; q >= 1; q /= 2)
-#pragma unroll
-            for (int j = q % p; j + q < N; j += 2 * q)
-#pragma unroll
-                for (int i = 0; i < q; ++i)
-                    if (i + j + q < N && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-                        const float x = v[i + j], y = v[i + j + q];
-                        v[i + j] = fmaxf(x, y);
-                        v[i + j + q] = fminf(x, y);
-                    }
+        for (int j = n / 2; j >= 1; j /= 2) {
+            const float o = __shfl_xor_sync(kFull, v, j);
+            v = ((lane & n) == 0) == ((lane & j) == 0) ? fmaxf(v, o) : fminf(v, o);
+        }
+    return v;
+}
+
+// ------------------------------------------------------------------ the few at a border
+// For sigmoid scores, whose 64-bit value depends on one logit: the common case of two values (or two groups) on
+// either side of a border needs no pass over the row.  Kept small: this code runs for one token in some
+// thousands, so its time is mostly that of fetching it.
+__device__ __noinline__ double exact_sigmoid(float l, const float* bias) {
+    const double s = sigmoid_f64(clamp_logit(l));
+    return bias ? s + (double)__ldg(bias) : s;
+}
+
+// Lanes of `set` with a larger value than this lane's, or an equal one in a lower lane.
+__device__ __forceinline__ int lanes_before(uint32_t set, double v) {
+    const unsigned long long mine = key64(v);
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (uint32_t rest = set; rest; rest &= rest - 1) {
+        const int j = __ffs(rest) - 1;
+        const unsigned long long o = __shfl_sync(kFull, mine, j);
+        before += (o > mine || (o == mine && j < lane)) ? 1 : 0;
+    }
+    return before;
 }
 
 // ------------------------------------------------------------------ the rules
-// Each lane sorts its NV values once (in runs of eight); a round of the choice is then a warp maximum of the lanes'
-// heads and a shift in the lane that held it.  The threshold separates the picks when the next value is
-// farther than the error bound (or, for exact values, ties are resolved in id order); everything else
-// goes to choose_careful.
+// The k-th largest of the lanes' maxima is a lower bound of the k-th largest value, and few values beyond k pass it
+// (about k^2 / 64 at random): those go to lanes of their own, in id order, and the smallest are dropped one
+// by one until k are left.  With fp32 ranking values the bound is lowered by their error, so that every value
+// which might belong to the picks is among these; what is too close to the border is settled in 64 bits.
+// Issue-bound, hence the care for instructions: 16384 tokens of 256 fp32 logits are 2.5 us of reading.
 template <int NV, typename T>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(const RouteScoresArgs a, const bool wide) {
-    constexpr int kRun = NV < 8 ? NV : 8, kRuns = NV / kRun;
+__global__ void __launch_bounds__(32 * kRouteWarps)
+    route_scores_kernel(const __grid_constant__ RouteScoresArgs a, const __grid_constant__ RoutePlan plan) {
     constexpr int kBits = NV == 1 ? 1 : NV == 2 ? 2 : NV == 4 ? 3 : NV == 8 ? 4 : NV == 16 ? 5 : 6;  // of a count up to NV
     extern __shared__ double scratch[];
+    __shared__ float2 slots[kRouteWarps][32];  // id (bits) and ranking value of the values that pass
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * warps + warp;
     if (t >= a.T) return;
+    const uint32_t below = (1u << lane) - 1;
     const int E = a.E, k = a.k, G = a.rule.groups;
     const bool softmax = a.rule.score == MOE_SCORE_SOFTMAX, biased = a.bias != nullptr, renorm = a.rule.renormalize != 0;
     const bool grouped = G > 1 && a.rule.top_groups < G, top2 = a.rule.group_score == MOE_GROUP_TOP2;
-    const Scratch sc = warp_scratch(scratch, E, warps, warp);
-    int* picks = sc.picks;
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
     const int e0 = NV * lane;
 
     float l[NV];
-    load_chunk<NV>(row, E, wide, l);
+    load_chunk<NV>(row, E, plan.wide, l);
     const bool want_scores = biased || (grouped && top2);
     RowNorm norm = {0.f, 0.f};
     if (softmax && (want_scores || !renorm || a.scores)) norm = softmax_norm<NV>(l);
@@ -473,150 +499,193 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(const Ro
             if (e0 + i < E) a.scores[t * E + e0 + i] = score_f32(l[i], softmax, norm);
     }
 
-    // ranking values: the logits, or scores (+ bias); -inf for experts out of service
+    // ranking values: the logits, or scores (+ bias).  An expert out of service has -inf (NaN logits: NaN, which no
+    // comparison below lets pass; sigmoid_fast(-inf) is 0 and needs the test)
     float v[NV];
-    float vmax = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        v[i] = in_service(l[i]) ? l[i] : -INFINITY;  // (drops NaN)
-        if (!want_scores) continue;
-        if (in_service(l[i])) {
-            v[i] = softmax ? score_f32(l[i], true, norm) : sigmoid_fast(clamp_logit(l[i]));
-            if (biased) {
-                v[i] += __ldg(a.bias + e0 + i);
-                vmax = fmaxf(vmax, v[i] == v[i] ? fabsf(v[i]) : INFINITY);  // (NaN: a NaN bias)
-            }
+    for (int i = 0; i < NV; ++i) v[i] = l[i];
+    if (want_scores) {
+        float b[NV];
+        if (biased) load_chunk<NV>(a.bias, E, plan.wide_bias, b);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const float s = softmax ? score_f32(l[i], true, norm) : sigmoid_fast(clamp_logit(l[i]));
+            v[i] = in_service(l[i]) ? (biased ? s + b[i] : s) : -INFINITY;
         }
     }
     const float err_s = softmax ? softmax_err(NV, norm.inv_sum) : kSigmoidErr;
-    const float err = biased ? err_s + kSumErr * warp_max_f32(vmax) : 0.f;
-    bool careful = biased && !(err < INFINITY);  // an infinite or NaN bias
+    bool careful = false;
 
     if (grouped) {
-        const int S = E / G, lanes = S / NV;
-        const bool raw = !biased && !top2;
+        const int S = plan.S, sh = plan.lane_shift, lanes = 1 << (sh & 31);
+        const bool raw = !want_scores;
+        float hi, lo;  // worst group kept, best left out
+        bool in = false, decided = false;
         uint32_t kept = 0;
-        float hi, lo;
-        bool in = false;
-        if (S % NV == 0 && (lanes & (lanes - 1)) == 0) {  // whole lanes, a power of two of them, share a group
+        if (sh >= 0) {  // 2^sh whole lanes share a group
             Top2<float> best{-INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < NV; ++i) best.add(v[i]);
             for (int m = 1; m < lanes; m <<= 1) best.merge(m);
             const float gs = best.score(top2);
-            float left = gs;
+            float left = e0 < E ? gs : NAN;
             hi = 0.f;
             for (int r = 0; r < a.rule.top_groups; ++r) {  // the best group left, ties to the lower group
                 hi = warp_max_f32(left);
-                const int first = __ffs(__ballot_sync(kFull, left == hi && !in && e0 < E)) - 1;
-                if (first >= 0 && lane / lanes == first / lanes) in = true, left = -INFINITY;
+                const int first = __ffs(__ballot_sync(kFull, left == hi)) - 1;
+                if (lane >> sh == first >> sh) in = true, left = NAN;
             }
-            lo = warp_max_f32(in ? -INFINITY : gs);
+            lo = warp_max_f32(left == left ? left : -INFINITY);
+            const float verr = err_s + (biased ? kSumErr * fmaxf(fabsf(lo), fabsf(hi)) : 0.f);
+            const float gerr = 2.f * verr + kSumErr * fmaxf(fabsf(lo), fabsf(hi));
+            if (!raw && !softmax && lo > -INFINITY && hi - lo <= gerr) {
+                // the open groups' scores in 64 bits, from the values that may be among a group's best
+                const bool live = e0 < E && gs > -INFINITY, open = live && gs >= hi - gerr && gs <= lo + gerr;
+                const float least = (top2 && best.b > -INFINITY ? best.b : best.a) - verr;
+                uint32_t take = 0;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (open && v[i] > -INFINITY && v[i] >= least) take |= 1u << i;
+                Top2<double> x{-(double)INFINITY, -(double)INFINITY};
+                for (; take; take &= take - 1) {
+                    const int e = e0 + __ffs(take) - 1;
+                    x.add(exact_sigmoid(to_f32(row[e]), biased ? a.bias + e : nullptr));
+                }
+                __syncwarp();
+                for (int m = 1; m < lanes; m <<= 1) x.merge(m);
+                const bool head = (lane & (lanes - 1)) == 0;
+                const uint32_t set = __ballot_sync(kFull, open && head), sure = __ballot_sync(kFull, live && head && gs > lo + gerr);
+                int before = lanes_before(set, x.score(top2));
+                before = __shfl_sync(kFull, before, lane & ~(lanes - 1));
+                in = live && (gs > lo + gerr || (open && before + __popc(sure) < a.rule.top_groups));
+                decided = true;
+            }
         } else {  // through shared memory
-            float* val = reinterpret_cast<float*>(sc.v64);
+            float* val = reinterpret_cast<float*>(warp_scratch(scratch, E, warps, warp).v64);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (e0 + i < E) val[e0 + i] = v[i];
             __syncwarp();
-            const int sh = group_lane_shift(G), g = lane >> sh;
-            const float gs = group_score<float>(val, G, S, sh, top2);
-            kept = best_groups<float>(gs, G == 32 ? kFull : (1u << G) - 1, G, sh, a.rule.top_groups);
+            const int gsh = group_lane_shift(G), g = lane >> gsh;
+            const float gs = group_score<float>(val, G, S, gsh, top2);
+            kept = best_groups<float>(gs, G == 32 ? kFull : (1u << G) - 1, G, gsh, a.rule.top_groups);
             const bool mine = g < G && ((kept >> g) & 1);
             lo = warp_max_f32(g < G && !mine ? gs : -INFINITY);
             hi = -warp_max_f32(mine ? -gs : -INFINITY);
             __syncwarp();
         }
-        const float gerr = raw ? 0.f : 2.f * (biased ? err : err_s) + kSumErr * fmaxf(fabsf(lo), fabsf(hi));
-        if (!raw && lo > -INFINITY && !(hi - lo > gerr)) careful = true;
-        const GroupOf group_of(S);
+        if (!raw && !decided && lo > -INFINITY) {
+            const float verr = err_s + (biased ? kSumErr * fmaxf(fabsf(lo), fabsf(hi)) : 0.f);
+            if (!(hi - lo > 2.f * verr + kSumErr * fmaxf(fabsf(lo), fabsf(hi)))) careful = true;
+        }
+        const GroupOf group_of{plan.group_mul};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (kept) in = e0 + i < E && ((kept >> group_of(e0 + i < E ? e0 + i : 0)) & 1);
-            if (!in) v[i] = -INFINITY;
-            else if (!biased) v[i] = in_service(l[i]) ? l[i] : -INFINITY;
+            const float w = biased ? v[i] : l[i];
+            v[i] = in ? w : -INFINITY;
         }
     }
 
+    // candidates: every value that might be among the k largest, one per lane in id order
+    float head = v[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) head = fmaxf(head, v[i]);
+    head = fmaxf(head, -INFINITY);  // (a NaN sorts nowhere)
+    const float bound = __shfl_sync(kFull, sort_lanes_down(head), k - 1);
+    float floor_v = biased ? bound - (err_s + kSumErr * fabsf(bound)) : bound;
+    int at = 0, m = 0;
+    uint32_t take = 0;
+    auto count = [&](float least) {
+        take = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (v[i] >= least && v[i] > -INFINITY) take |= 1u << i;
+        const int c = __popc(take);
+        at = m = 0;
+#pragma unroll
+        for (int b = 0; b < kBits; ++b) {
+            const uint32_t lanes = __ballot_sync(kFull, (c >> b) & 1);
+            at += __popc(lanes & below) << b;
+            m += __popc(lanes) << b;
+        }
+    };
+    count(floor_v);
+    if (m > 32) {
+        // fewer lanes than k hold the open groups' experts: search a bound that 32 lanes take
+        uint32_t few = logit_key(INFINITY), many = logit_key(floor_v);  // (the key of -inf is above 0)
+        for (int r = 0; r < 32 && few - many > 1 && (m > 32 || m < k); ++r) {
+            const uint32_t mid = many + (few - many) / 2;
+            floor_v = key_logit(mid);
+            count(floor_v);
+            if (m > 32) many = mid;
+            else few = mid;
+        }
+        if (biased && m >= k && m <= 32) count(floor_v - (err_s + kSumErr * fabsf(floor_v)));
+    }
+    careful = careful || m < k || m > 32;
+
+    bool pick = false;
+    int id = 0;
     if (!careful) {
-        float h[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) h[i] = v[i];
-#pragma unroll
-        for (int r = 0; r < kRuns; ++r) sort_down<kRun>(h + kRun * r);
-        float last = 0.f, next = -INFINITY;
-        int n = 0, above = 0;
-        while (true) {
-            float head = h[0];
-#pragma unroll
-            for (int r = 1; r < kRuns; ++r) head = fmaxf(head, h[kRun * r]);
-            const float m = warp_max_f32(head);
-            if (n >= k) {
-                next = m;
-                break;
-            }
-            if (m == -INFINITY) {  // fewer than k experts in service
-                careful = true;
-                break;
-            }
-            if (m != last || n == 0) above = n;
-            last = m;
-            n += __popc(__ballot_sync(kFull, head == m));
-            bool open = head == m;
-#pragma unroll
-            for (int r = 0; r < kRuns; ++r) {
-                if (open && h[kRun * r] == m) {
-#pragma unroll
-                    for (int i = 0; i + 1 < kRun; ++i) h[kRun * r + i] = h[kRun * r + i + 1];
-                    h[kRun * r + kRun - 1] = -INFINITY;
-                    open = false;
+        for (int i = 0; i < NV; ++i)
+            if ((take >> i) & 1) slots[warp][at++] = make_float2(__int_as_float(e0 + i), v[i]);
+        __syncwarp();
+        const float2 mine = slots[warp][lane < m ? lane : 0];
+        id = __float_as_int(mine.x);
+        const float x = lane < m ? mine.y : INFINITY;
+        uint32_t alive = m == 32 ? kFull : (1u << m) - 1;
+        float next = -INFINITY;  // largest value dropped
+        for (int r = m; r > k; --r) {  // the smallest left, ties to the higher id
+            next = -warp_max_f32((alive >> lane) & 1 ? -x : -INFINITY);
+            const uint32_t who = __ballot_sync(kFull, x == next) & alive;
+            alive &= ~(0x80000000u >> __clz(who));
+        }
+        const float last = -warp_max_f32((alive >> lane) & 1 ? -x : -INFINITY);
+        if (biased) {
+            const float err = err_s + kSumErr * fabsf(last);
+            if (!(last - next > err)) {  // settled in 64 bits
+                if (softmax || !(err < INFINITY)) {
+                    careful = true;
+                } else {
+                    const bool in_play = lane < m && x >= last - err;
+                    const bool open = in_play && x <= next + err;
+                    const uint32_t set = __ballot_sync(kFull, open), sure = __ballot_sync(kFull, in_play && !open);
+                    double v64 = 0.0;
+                    if (open) v64 = exact_sigmoid(to_f32(row[id]), a.bias + id);
+                    __syncwarp();
+                    const bool wins = lanes_before(set, v64) + __popc(sure) < k;
+                    alive = sure | __ballot_sync(kFull, open && wins);
                 }
             }
         }
-        const bool tie = n > k || next == last;
-        if (biased && (tie || last - next <= err)) careful = true;
-        if (!careful) {
-            uint32_t chosen = 0, ties = 0;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (v[i] > last) chosen |= 1u << i;
-                if (v[i] == last) ties |= 1u << i;
-            }
-            if (tie) {  // the lowest ids among the experts at `last`
-                int room = k - above - lane_prefix(__popc(ties), kBits);
-                while (ties && room > 0) {
-                    chosen |= ties & -ties;
-                    ties &= ties - 1;
-                    --room;
-                }
-            } else {
-                chosen |= ties;
-            }
-            int at = lane_prefix(__popc(chosen), kBits);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if ((chosen >> i) & 1) picks[at++] = e0 + i;
-        }
+        pick = (alive >> lane) & 1;
     }
-    if (careful) choose_careful<T>(a, row, sc);
-    __syncwarp();
+    if (careful) {
+        const Scratch sc = warp_scratch(scratch, E, warps, warp);
+        choose_careful<T>(a, plan, row, sc);
+        __syncwarp();
+        pick = lane < k;
+        id = pick ? sc.picks[lane] : 0;
+    }
 
-    // weights: lane j < k has pick j
-    const int id = lane < k ? picks[lane] : 0;
-    const float lp = lane < k ? to_f32(row[id]) : -INFINITY;
-    float u;
-    float scale = a.rule.scale;
+    // weights of the picks, in lane order, which is id order
+    const float lp = pick ? to_f32(row[id]) : -INFINITY;
+    float u, scale = a.rule.scale;
     if (renorm) {
         float ref = warp_max_f32(in_service(lp) ? clamp_logit(lp) : -kMaxF32);
         if (!softmax) ref = fminf(ref, 0.f);
         u = score_ratio(lp, softmax, ref);
         const float sum = warp_butterfly_sum(u);
-        scale = sum > 0.f ? scale / sum : 0.f;
+        scale = sum > 0.f ? __fdividef(scale, sum) : 0.f;
     } else {
         u = score_f32(lp, softmax, norm);
     }
-    if (lane < k) {
-        a.ids[t * k + lane] = id;
-        a.w[t * k + lane] = u * scale;
+    const int rank = __popc(__ballot_sync(kFull, pick) & below);
+    if (pick && rank < k) {
+        a.ids[t * k + rank] = id;
+        a.w[t * k + rank] = u * scale;
         if (a.counts) atomicAdd(a.counts + id, 1);
     }
 }
@@ -629,7 +698,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_kernel(const Ro
 // the scores that sum is zero by itself, so that, as for sigmoid scores, only the picked experts get a
 // gradient: the row is then written as zeros and the picks' values on top, and only the picked logits are read.
 template <int NV, typename T>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel(const RouteBackwardArgs a, const bool wide) {
+__global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel(const __grid_constant__ RouteBackwardArgs a, const bool wide) {
     extern __shared__ float rows[];  // per warp, dense gradients only: the gradient of the scores times the scores [E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * warps + warp;
@@ -741,10 +810,19 @@ cudaError_t launch_route_scores(const RouteScoresArgs& a, moe_dtype dtype, cudaS
     const void* f = dtype == MOE_F32    ? scores_kernel<float>(a.E)
                     : dtype == MOE_BF16 ? scores_kernel<__nv_bfloat16>(a.E)
                                         : scores_kernel<__half>(a.E);
-    bool wide = rows_wide(a.logits, a.ld, dtype);
+    int nv = 1;  // experts per lane, as the kernel's
+    while (32 * nv < a.E) nv *= 2;
+    RoutePlan plan;
+    plan.S = a.E / a.rule.groups;
+    plan.group_mul = ((1u << 20) + plan.S - 1) / plan.S;
+    plan.lane_shift = -1;
+    for (int sh = 0; sh <= 5; ++sh)
+        if (plan.S == nv << sh) plan.lane_shift = sh;
+    plan.wide = rows_wide(a.logits, a.ld, dtype);
+    plan.wide_bias = reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
     const int warps = a.E > 512 ? kRouteWarps / 2 : kRouteWarps;  // (less than 60 KB of scratch)
     const size_t smem = (size_t)warps * (kScratchPerExpert * (size_t)a.E + 128);
-    void* args[] = {const_cast<RouteScoresArgs*>(&a), &wide};
+    void* args[] = {const_cast<RouteScoresArgs*>(&a), &plan};
     return launch_kernel(f, dim3((a.T + warps - 1) / warps), dim3(32 * warps), smem, st, false, args);
 }
 

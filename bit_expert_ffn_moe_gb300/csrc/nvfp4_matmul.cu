@@ -51,13 +51,29 @@ __device__ __forceinline__ void store_one(void* y, int dtype, int64_t at, float 
     else static_cast<__half*>(y)[at] = __float2half_rn(v);
 }
 
-__device__ __forceinline__ uint32_t pack_two(int dtype, float a, float b) {
-    if (dtype == MOE_BF16) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&p);
+template <typename T>
+__device__ __forceinline__ T out_value(float v);
+template <>
+__device__ __forceinline__ float out_value<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 out_value<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half out_value<__half>(float v) { return __float2half_rn(v); }
+
+// 16 bytes of results from consecutive fp32 values.
+template <typename T>
+__device__ __forceinline__ uint4 out_piece(const uint32_t* v) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            o[i] = v[i];
+        } else {
+            const T lo = out_value<T>(__uint_as_float(v[2 * i])), hi = out_value<T>(__uint_as_float(v[2 * i + 1]));
+            o[i] = (uint32_t)*reinterpret_cast<const uint16_t*>(&lo) | ((uint32_t)*reinterpret_cast<const uint16_t*>(&hi) << 16);
+        }
     }
-    const __half2 p = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&p);
+    return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // ------------------------------------------------------------------ rows kernel
@@ -266,13 +282,17 @@ constexpr int kSqThreads = 64 + 32 * kSqEpiWarps;
 constexpr int kSqStageBytes = 3 * kTile + 12 * kAtom;
 constexpr int kSqSfCols = 48;
 constexpr uint32_t kSqSfBase = 256;  // scale columns after the accumulator
-constexpr size_t kSqSmem = (size_t)kSqStages * kSqStageBytes + 1024 + 256;
+constexpr size_t kSqSmem = (size_t)kSqStages * kSqStageBytes + 512 * kSqEpiWarps + 1024 + 256;
 static_assert(kSqStageBytes % 1024 == 0 && kSqSfBase + kSqStages * kSqSfCols <= kTmemCols, "stage alignment, tensor memory");
+static_assert(kSqSmem <= 232448, "shared memory");
 
-__global__ void __launch_bounds__(kSqThreads, 1) nvfp4_square_matmul_kernel(const MatmulArgs args, int MT, int NT) {
+template <typename T>
+__global__ void __launch_bounds__(kSqThreads, 1)
+    nvfp4_square_matmul_kernel(const __grid_constant__ MatmulArgs args, const int MT, const int NT) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kSqStages * kSqStageBytes);
+    float* gb_smem = reinterpret_cast<float*>(smem + kSqStages * kSqStageBytes);  // [epilogue warp][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(gb_smem + 128 * kSqEpiWarps);
     uint64_t* empty = full + kSqStages;
     uint64_t* acc_full = empty + kSqStages;
     uint64_t* acc_empty = acc_full + 1;
@@ -365,13 +385,19 @@ __global__ void __launch_bounds__(kSqThreads, 1) nvfp4_square_matmul_kernel(cons
     } else {
         const int q = warp & 3, half = (warp - 2) / 4;
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
-        const int size = args.dtype == MOE_F32 ? 4 : 2;
-        const bool wide = reinterpret_cast<uintptr_t>(args.y) % 16 == 0 && (args.ldy * size) % 16 == 0;
+        const bool wide = reinterpret_cast<uintptr_t>(args.y) % 16 == 0 && (args.ldy * (int64_t)sizeof(T)) % 16 == 0;
+        float* gb = gb_smem + 128 * (warp - 2);
+        T* y = static_cast<T*>(args.y);
         int tile = 0;
         for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, ++tile) {
             const int64_t m0 = (int64_t)(t / NT) * 128 + 32 * q, n0 = (int64_t)(t % NT) * 256 + 128 * half;
             const int64_t m = m0 + lane;
             const float ga = m < args.M ? args.ga[args.ga_rows ? m : 0] : 0.f;
+            const int live = (int)min((int64_t)128, args.N - n0);  // columns of this warp's half (may be negative)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (32 * c + lane < live) gb[32 * c + lane] = args.gb[args.gb_rows ? n0 + 32 * c + lane : 0];
+            __syncwarp();
             if (!mbar_wait(acc_full, tile & 1, abort_flag, args.status)) break;
             tc_fence_after();
             uint32_t v[4][32];
@@ -381,48 +407,40 @@ __global__ void __launch_bounds__(kSqThreads, 1) nvfp4_square_matmul_kernel(cons
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty);
+            // 16-byte pieces transposed inside groups of four lanes: a store writes 64 contiguous bytes of 8 rows
+            const int64_t r0 = m0 + 4 * (lane >> 2);
+            T* out = y + r0 * args.ldy + n0 + (lane & 3) * (16 / (int)sizeof(T));
+            const int rows = (int)min((int64_t)4, args.M - r0);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const int64_t nc = n0 + 32 * c;
-                if (nc >= args.N) break;
+                if (32 * c >= live) break;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float gb = args.gb_rows ? __ldg(args.gb + min(nc + i, args.N - 1)) : __ldg(args.gb);
-                    v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * ga * gb);
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 g = *reinterpret_cast<const float4*>(gb + 32 * c + i);
+                    v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) * ga * g.x);
+                    v[c][i + 1] = __float_as_uint(__uint_as_float(v[c][i + 1]) * ga * g.y);
+                    v[c][i + 2] = __float_as_uint(__uint_as_float(v[c][i + 2]) * ga * g.z);
+                    v[c][i + 3] = __float_as_uint(__uint_as_float(v[c][i + 3]) * ga * g.w);
                 }
-                if (wide && nc + 32 <= args.N) {
-                    // 16-byte pieces transposed inside groups of four lanes: a store writes 64 contiguous bytes of 8 rows
-                    const int rb = 4 * (lane >> 2), piece = lane & 3;
+                if (wide && 32 * c + 32 <= live) {
+                    constexpr int kHalves = (int)sizeof(T) / 2;  // 32 columns: one or two times 64 bytes
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (size == 2 && h == 1) break;
+                    for (int h = 0; h < kHalves; ++h) {
                         uint4 pc[4];
 #pragma unroll
-                        for (int a = 0; a < 4; ++a) {
-                            if (size == 2) {
-                                uint32_t o[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    o[i] = pack_two(args.dtype, __uint_as_float(v[c][8 * a + 2 * i]), __uint_as_float(v[c][8 * a + 2 * i + 1]));
-                                pc[a] = make_uint4(o[0], o[1], o[2], o[3]);
-                            } else {
-                                pc[a] = make_uint4(v[c][16 * h + 4 * a], v[c][16 * h + 4 * a + 1], v[c][16 * h + 4 * a + 2], v[c][16 * h + 4 * a + 3]);
-                            }
-                        }
+                        for (int p = 0; p < 4; ++p) pc[p] = out_piece<T>(&v[c][(32 / kHalves) * h + (16 / (int)sizeof(T)) * p]);
                         transpose4_pieces(pc, lane);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int64_t r = m0 + rb + j;
-                            if (r < args.M)
-                                *reinterpret_cast<uint4*>(static_cast<char*>(args.y) + (r * args.ldy + nc + 16 * h) * size + 16 * piece) = pc[j];
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            if (j < rows) *reinterpret_cast<uint4*>(out + j * args.ldy + 32 * c + (32 / kHalves) * h) = pc[j];
                     }
                 } else if (m < args.M) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (nc + i < args.N) store_one(args.y, args.dtype, m * args.ldy + nc + i, __uint_as_float(v[c][i]));
+                        if (32 * c + i < live) y[m * args.ldy + n0 + 32 * c + i] = out_value<T>(__uint_as_float(v[c][i]));
                 }
             }
+            __syncwarp();  // gb is rewritten for the next tile
         }
     }
     tc_fence_before();
@@ -483,7 +501,10 @@ cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_oper
     const int64_t tiles = (int64_t)MT * NT;
     const int sms = sm_count();
     void* args[] = {&a, &MT, &NT};
-    return launch_kernel((const void*)nvfp4_square_matmul_kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kSqThreads), kSqSmem,
+    const void* f = dtype == MOE_F32    ? (const void*)nvfp4_square_matmul_kernel<float>
+                    : dtype == MOE_BF16 ? (const void*)nvfp4_square_matmul_kernel<__nv_bfloat16>
+                                        : (const void*)nvfp4_square_matmul_kernel<__half>;
+    return launch_kernel(f, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kSqThreads), kSqSmem,
                          st, pdl, args);
 }
 

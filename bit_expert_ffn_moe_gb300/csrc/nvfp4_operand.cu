@@ -13,11 +13,14 @@
 // without the correction 4% of those decisions differ), and farther away one ulp cannot change a
 // code.  D outside 2^-60 .. 2^60 takes the division.
 //
-// Row form: the threads of a row read it once (K <= 8192: 32 elements each in registers), reduce its maximum and
-// encode.  Both forms at once: two passes over x, the first for the row and column maxima (integer
-// maxima of the bits: the order of the atomics does not matter), the second over tiles of 64 x 128
-// elements, encoded along their rows from registers and along their columns through shared memory.
-// HBM bounds both: (2 or 4) R C bytes in, 9/16 R C out per form.
+// A thread encodes a block of 16: its maximum is taken on the packed bits (two 16-bit elements per
+// instruction), few enough registers keep most of an SM's warps resident, which hides the loads.
+//   rows only   the threads of a row hold it in registers (up to 8192 elements), reduce its maximum, encode.
+//   with columns  two passes over x: the row and column maxima (integer maxima of the bits: the order of the
+//               atomics does not matter), then tiles of 128 x 128 elements through shared memory, encoded
+//               along their rows and along their columns, two columns per thread.
+// HBM bounds both: (2 or 4) R C bytes in, 9/16 R C out per form; the second pass of the two-form kernel
+// finds x in L2 while it fits there.
 #include <type_traits>
 
 #include "ops.cuh"
@@ -26,45 +29,87 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTileR = 64, kTileC = 128;  // elements of a tile of the two-form kernel
+constexpr int kTileDim = 128;  // rows and columns of a tile of the two-form kernel
 
 __host__ __device__ inline int64_t pad_to(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-__device__ __forceinline__ float elem(float v) { return v; }
-__device__ __forceinline__ float elem(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float elem(__half v) { return __half2float(v); }
+// 16 consecutive elements as they are in memory.
+template <typename T>
+struct Block {
+    static constexpr int kWords = 4 * (int)sizeof(T);
+    uint32_t w[kWords];
 
-// N consecutive elements from p as fp32; those at or past `live` are zero.  wide: p is 16-byte aligned.
-template <int N, typename T>
-__device__ __forceinline__ void load_row(const T* p, int64_t live, bool wide, float (&v)[N]) {
-    constexpr int per = 16 / (int)sizeof(T);
-    if (wide && live >= N) {
+    // those at or past `live` are zero; wide: p is 16-byte aligned
+    __device__ __forceinline__ void load(const T* p, int64_t live, bool wide) {
+        if (wide && live >= 16) {
 #pragma unroll
-        for (int i = 0; i < N / per; ++i) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
-            const T* e = reinterpret_cast<const T*>(&u);
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            }
+        } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int j = 0; j < per; ++j) v[per * i + j] = elem(e[j]);
+            for (int i = 0; i < 16; ++i) w[i] = i < live ? __float_as_uint(p[i]) : 0u;
+        } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = (2 * i < live ? (uint32_t)h[2 * i] : 0u) | (2 * i + 1 < live ? (uint32_t)h[2 * i + 1] << 16 : 0u);
         }
-    } else {
+    }
+    __device__ __forceinline__ void values(float (&v)[16]) const {
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = i < live ? elem(p[i]) : 0.f;
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                    v[2 * i] = __uint_as_float(w[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                } else {
+                    const float2 f = h2_to_f2(w[i]);
+                    v[2 * i] = f.x;
+                    v[2 * i + 1] = f.y;
+                }
+            }
+        }
+    }
+};
+
+// Magnitudes compare as integers: a word of one fp32 or two 16-bit elements.
+template <typename T>
+__device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b) {
+    return sizeof(T) == 4 ? max(a, b & 0x7fffffffu) : __vmaxu2(a, b & 0x7fff7fffu);
+}
+// A maximum of magnitudes as fp32 bits.
+template <typename T>
+__device__ __forceinline__ uint32_t mag_f32(uint32_t m) {
+    if constexpr (sizeof(T) == 4) return m;
+    else if constexpr (std::is_same<T, __nv_bfloat16>::value) return max(m << 16, m & 0xffff0000u);
+    else {
+        const float2 f = h2_to_f2(m);
+        return max(__float_as_uint(f.x), __float_as_uint(f.y));
     }
 }
+template <typename T>
+__device__ __forceinline__ uint32_t block_mag(const Block<T>& b) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < Block<T>::kWords; ++i) m = mag_max<T>(m, b.w[i]);
+    return mag_f32<T>(m);
+}
 
-__device__ __forceinline__ float row_scale(float amax) {
-    const float g = __fdiv_rn(amax, 2688.f);
+__device__ __forceinline__ float row_scale(uint32_t mag) {
+    const float g = __fdiv_rn(__uint_as_float(mag), 2688.f);
     return g == 0.f ? 1.f : g;
 }
 
-// One block of 16 elements under the row scale g: two words of codes; returns the scale byte.
-__device__ __forceinline__ uint32_t encode_block(float* v, float g, bool given, uint32_t& c0, uint32_t& c1) {
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(v[i]));
+// One block of 16 elements of largest magnitude amax under the row scale g: 8 bytes of codes; returns the scale byte.
+__device__ __forceinline__ uint32_t encode_block(float (&v)[16], float amax, float g, bool given, uint2& codes) {
     const uint32_t sb = f32_to_e4m3_sat(__fdiv_rn(__fdiv_rn(amax, g), 6.f));
     const float D = __fmul_rn(e4m3x2_to_f2(sb).x, g);
-    c0 = c1 = 0u;
+    codes = make_uint2(0u, 0u);
     if (D == 0.f) return sb;
     if (given) {  // a row scale that is not the row's own may leave quotients far above 6: they saturate
         const float lim = 8.f * D;
@@ -82,155 +127,244 @@ __device__ __forceinline__ uint32_t encode_block(float* v, float g, bool given, 
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], D);
     }
-    c0 = e2m1x8_encode(v);
-    c1 = e2m1x8_encode(v + 8);
+    codes = make_uint2(e2m1x8_encode(v), e2m1x8_encode(v + 8));
     return sb;
 }
 
-// 32 elements (two blocks): 16 bytes of codes, two scale bytes.
-__device__ __forceinline__ uint32_t encode_unit(float (&v)[32], float g, bool given, uint4& codes) {
-    const uint32_t s0 = encode_block(v, g, given, codes.x, codes.y);
-    const uint32_t s1 = encode_block(v + 16, g, given, codes.z, codes.w);
-    return s0 | (s1 << 8);
+// Codes and scale of block b (16 elements) of operand row r, rows of Kp elements.  Four lanes with four
+// consecutive blocks (b % 4 = lane % 4) of one row store their scales as one word.
+__device__ __forceinline__ void store_block(uint8_t* q, uint8_t* s, int64_t r, int64_t b, int64_t Kp, uint2 codes, uint32_t sb,
+                                            bool live) {
+    if (live) *reinterpret_cast<uint2*>(q + mma_tile_offset(r, b >> 1, Kp) + 8 * (b & 1)) = codes;
+    uint32_t word = sb << (8 * (b & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, 1);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2);
+    if (live && (b & 3) == 0) *reinterpret_cast<uint32_t*>(s + mma_scale_offset(r, b, 2 * Kp)) = word;
 }
 
-// ------------------------------------------------------------------ row form
-// `tpr` threads (32 .. 256) share a row; thread c of them the 32-element units c, c + tpr, ...
+// ------------------------------------------------------------------ rows only
+// `tpr` threads (32 .. 256) share a row; thread c of them the blocks c, c + tpr, ...; the first two stay in registers.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     nvfp4_rows_kernel(const T* __restrict__ x, int64_t R, int64_t K, int64_t ld, bool wide, int tpr, uint8_t* __restrict__ q,
                       uint8_t* __restrict__ s, float* __restrict__ gs, bool given, bool gs_rows) {
-    __shared__ float part[kThreads / 32];
+    __shared__ uint32_t part[kThreads / 32];
     pdl_launch_dependents();  // a product launched behind this call fetches its weights meanwhile
-    const int in_row = threadIdx.x % tpr, rows = kThreads / tpr;
+    const int in_row = threadIdx.x & (tpr - 1), rows = kThreads / tpr;
     const int64_t r = (int64_t)blockIdx.x * rows + threadIdx.x / tpr;
     const int64_t Kp = pad_to(K, 256);
-    const int units = (int)(Kp / 32);
+    const int blocks = (int)(Kp / 16);  // a multiple of 16
     const bool live = r < R;
     const T* row = x + (live ? r : 0) * ld;
-    float v[32];
+    Block<T> kept[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int64_t b = in_row + j * tpr;
+        kept[j].load(row + 16 * b, live && b < blocks ? K - 16 * b : 0, wide);
+    }
+    uint32_t mag[2] = {block_mag(kept[0]), block_mag(kept[1])};
     float g = 1.f;
-    const int64_t u0 = in_row;
-    if (live && u0 < units) load_row<32>(row + 32 * u0, K - 32 * u0, wide, v);
     if (!given) {
-        float amax = 0.f;
-        if (live && u0 < units) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
-            float o[32];
-            for (int64_t u = u0 + tpr; u < units; u += tpr) {
-                load_row<32>(row + 32 * u, K - 32 * u, wide, o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(o[i]));
-            }
+        uint32_t m = max(mag[0], mag[1]);
+        for (int64_t b = in_row + 2 * tpr; b < blocks; b += tpr) {
+            Block<T> more;
+            more.load(row + 16 * b, live ? K - 16 * b : 0, wide);
+            m = max(m, block_mag(more));
         }
-        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+        m = __reduce_max_sync(0xffffffffu, m);
         if (tpr > 32) {
-            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
             __syncthreads();
             const int w0 = (threadIdx.x / tpr) * (tpr / 32);
-            for (int w = 0; w < tpr / 32; ++w) amax = fmaxf(amax, part[w0 + w]);
+            for (int w = 0; w < tpr / 32; ++w) m = max(m, part[w0 + w]);
         }
-        g = row_scale(amax);
+        g = row_scale(m);
         if (live && in_row == 0) gs[r] = g;
     } else if (live) {
         g = gs[gs_rows ? r : 0];
     }
-    for (int64_t u = u0; live && u < units; u += tpr) {
-        if (u != u0) load_row<32>(row + 32 * u, K - 32 * u, wide, v);
-        uint4 codes;
-        const uint32_t sb = encode_unit(v, g, given, codes);
-        *reinterpret_cast<uint4*>(q + mma_tile_offset(r, u, Kp)) = codes;
-        *reinterpret_cast<uint16_t*>(s + mma_scale_offset(r, 2 * u, 2 * Kp)) = (uint16_t)sb;
+    // (lanes of four consecutive blocks leave together: blocks and tpr are multiples of 16)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int64_t b = in_row + j * tpr;
+        const bool mine = live && b < blocks;
+        float v[16];
+        uint2 codes;
+        kept[j].values(v);
+        const uint32_t sb = encode_block(v, __uint_as_float(mag[j]), g, given, codes);
+        store_block(q, s, r, b, Kp, codes, sb, mine);
+    }
+    for (int b0 = 2 * tpr; b0 < blocks; b0 += tpr) {
+        const int64_t b = in_row + b0;
+        const bool mine = live && b < blocks;
+        Block<T> more;
+        more.load(row + 16 * b, mine ? K - 16 * b : 0, wide);
+        float v[16];
+        uint2 codes;
+        more.values(v);
+        const uint32_t sb = encode_block(v, __uint_as_float(block_mag(more)), g, given, codes);
+        store_block(q, s, r, b, Kp, codes, sb, mine);
     }
 }
 
-// ------------------------------------------------------------------ both forms
-// Maxima of |x| over rows and columns as fp32 bits in row_max[R] and col_max[C] (zeroed before).  A CTA
-// takes 256 columns x 256 rows: warp w the rows 32 w ..., lane l the columns 8 l ...
+// ------------------------------------------------------------------ with columns
+// Maxima of |x| over rows and columns as fp32 bits in row_max[R] and col_max[C] (zeroed before).  A warp takes
+// 32 rows of 16 bytes per lane; the 8 warps of a CTA 256 rows of the same columns.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     nvfp4_maxima_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld, bool wide, int col_tiles,
                         unsigned* __restrict__ row_max, unsigned* __restrict__ col_max) {
-    __shared__ float part[kThreads / 32][256];
+    constexpr int kPer = 16 / (int)sizeof(T), kWarpCols = 32 * kPer;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
-    const int64_t c0 = ct * 256 + 8 * lane, r0 = rt * 256 + 32 * warp;
-    float cm[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cm[i] = 0.f;
+    __shared__ uint32_t part[kThreads / 32][kWarpCols];
+    const int64_t col0 = (blockIdx.x % col_tiles) * (int64_t)kWarpCols;
+    const int64_t c0 = col0 + kPer * lane, r0 = (int64_t)(blockIdx.x / col_tiles) * kThreads + 32 * warp;
+    uint32_t cm[4] = {0u, 0u, 0u, 0u};
     unsigned mine = 0;
-#pragma unroll 4
-    for (int j = 0; j < 32; ++j) {
-        float v[8];
-        float m = 0.f;
-        if (r0 + j < R && c0 < C) {
-            load_row<8>(x + (r0 + j) * ld + c0, C - c0, wide, v);
+    const int rows = (int)max((int64_t)0, min((int64_t)32, R - r0));
+    for (int j0 = 0; j0 < rows; j0 += 8) {
+        uint4 u[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                cm[i] = fmaxf(cm[i], fabsf(v[i]));
-                m = fmaxf(m, fabsf(v[i]));
+        for (int j = 0; j < 8; ++j) {
+            u[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (j0 + j >= rows || c0 >= C) continue;
+            const T* p = x + (r0 + j0 + j) * ld + c0;
+            if (wide && c0 + kPer <= C) {
+                u[j] = __ldg(reinterpret_cast<const uint4*>(p));
+            } else {
+                __align__(16) T e[kPer];
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) e[i] = c0 + i < C ? p[i] : T(0.f);
+                u[j] = *reinterpret_cast<const uint4*>(e);
             }
         }
-        const unsigned rm = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-        if (lane == j) mine = rm;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            cm[0] = mag_max<T>(cm[0], u[j].x);
+            cm[1] = mag_max<T>(cm[1], u[j].y);
+            cm[2] = mag_max<T>(cm[2], u[j].z);
+            cm[3] = mag_max<T>(cm[3], u[j].w);
+            const uint32_t m = mag_max<T>(mag_max<T>(mag_max<T>(mag_max<T>(0u, u[j].x), u[j].y), u[j].z), u[j].w);
+            const unsigned rm = __reduce_max_sync(0xffffffffu, mag_f32<T>(m));
+            if (lane == j0 + j) mine = rm;
+        }
     }
-    if (row_max && r0 + lane < R) atomicMax(row_max + r0 + lane, mine);
+    if (row_max && lane < rows) atomicMax(row_max + r0 + lane, mine);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[warp][8 * lane + i] = cm[i];
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            part[warp][kPer * lane + i] = cm[i];
+        } else {
+            part[warp][kPer * lane + 2 * i] = mag_f32<T>(cm[i] & 0xffffu);
+            part[warp][kPer * lane + 2 * i + 1] = mag_f32<T>(cm[i] >> 16);
+        }
+    }
     __syncthreads();
-    float m = 0.f;
+    if (threadIdx.x >= kWarpCols || col0 + threadIdx.x >= C) return;
+    uint32_t m = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, part[w][threadIdx.x]);
-    const int64_t c = ct * 256 + threadIdx.x;
-    if (c < C) atomicMax(col_max + c, __float_as_uint(m));
+    for (int w = 0; w < kThreads / 32; ++w) m = max(m, part[w][threadIdx.x]);
+    atomicMax(col_max + col0 + threadIdx.x, m);
 }
 
-// A tile of 64 rows x 128 columns of x: thread (r, j) encodes 32 elements of row r for the row form, and
-// thread (c, j) 32 elements of column c, through shared memory, for the column form.  Tiles cover the
-// padded contractions (256 multiples), whose padding is written as zeros.
+// A tile of 128 x 128 elements of x in shared memory, encoded along its rows (a thread: 4 blocks) and along its
+// columns (a thread: 2 columns x 32 rows).  Tiles cover the padded contractions (256 multiples), whose
+// padding is written as zeros.
+template <typename T>
+__host__ __device__ constexpr int tile_pitch() { return kTileDim * (int)sizeof(T) + 16; }  // bytes
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
     nvfp4_both_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld, bool wide, int col_tiles,
-                      const unsigned* __restrict__ row_max, const unsigned* __restrict__ col_max, moe_nvfp4_operand rows,
-                      moe_nvfp4_operand cols, bool given) {
-    __shared__ T tile[kTileR][kTileC + 16 / sizeof(T)];
-    const int64_t r0 = (int64_t)(blockIdx.x / col_tiles) * kTileR, c0 = (int64_t)(blockIdx.x % col_tiles) * kTileC;
+                      const unsigned* __restrict__ row_max, const unsigned* __restrict__ col_max, const moe_nvfp4_operand rows,
+                      const moe_nvfp4_operand cols, bool given) {
+    extern __shared__ __align__(16) unsigned char tile[];
+    constexpr int kPitch = tile_pitch<T>(), kPer = 16 / (int)sizeof(T), kPieces = kTileDim / kPer;
+    const int64_t r0 = (int64_t)(blockIdx.x / col_tiles) * kTileDim, c0 = (int64_t)(blockIdx.x % col_tiles) * kTileDim;
     const int64_t Cp = pad_to(C, 256), Rp = pad_to(R, 256);
-    {
-        const int i = threadIdx.x >> 2, j = threadIdx.x & 3;
-        const int64_t r = r0 + i, c = c0 + 32 * j;
-        float v[32];
-        load_row<32>(x + (r < R ? r : 0) * ld + c, r < R ? C - c : 0, wide, v);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < kTileDim * kPieces; i += kThreads) {
+        const int rr = i / kPieces, pc = i % kPieces;
+        const int64_t r = r0 + rr, c = c0 + pc * kPer;
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (r < R && c < C) {
+            const T* p = x + r * ld + c;
+            if (wide && c + kPer <= C) {
+                u = __ldg(reinterpret_cast<const uint4*>(p));
+            } else {
+                __align__(16) T e[kPer];
 #pragma unroll
-        for (int m = 0; m < 32; ++m) {  // exact: v came from a T
-            if constexpr (std::is_same<T, float>::value) tile[i][32 * j + m] = v[m];
-            else if constexpr (std::is_same<T, __half>::value) tile[i][32 * j + m] = __float2half_rn(v[m]);
-            else tile[i][32 * j + m] = __float2bfloat16_rn(v[m]);
+                for (int j = 0; j < kPer; ++j) e[j] = c + j < C ? p[j] : T(0.f);
+                u = *reinterpret_cast<const uint4*>(e);
+            }
         }
-        if (rows.q && r < R && c < Cp) {
-            const float g = given ? rows.gs[rows.gs_rows ? r : 0] : row_scale(__uint_as_float(__ldg(row_max + r)));
-            if (!given && c == 0) rows.gs[r] = g;
-            uint4 codes;
-            const uint32_t sb = encode_unit(v, g, given, codes);
-            *reinterpret_cast<uint4*>(rows.q + mma_tile_offset(r, c / 32, Cp)) = codes;
-            *reinterpret_cast<uint16_t*>(rows.s + mma_scale_offset(r, c / 16, 2 * Cp)) = (uint16_t)sb;
-        }
+        *reinterpret_cast<uint4*>(tile + rr * kPitch + pc * 16) = u;
     }
     __syncthreads();
-    {
-        const int i = threadIdx.x & 127, j = threadIdx.x >> 7;
-        const int64_t c = c0 + i, r = r0 + 32 * j;
-        if (c >= C || r >= Rp) return;
-        float v[32];
+    if (rows.q) {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const int rr = 32 * i + (threadIdx.x >> 3), blk = threadIdx.x & 7;
+            const int64_t r = r0 + rr, b = c0 / 16 + blk;
+            const bool live = r < R && 16 * b < Cp;
+            Block<T> k;
 #pragma unroll
-        for (int m = 0; m < 32; ++m) v[m] = elem(tile[32 * j + m][i]);
-        const float g = given ? cols.gs[cols.gs_rows ? c : 0] : row_scale(__uint_as_float(__ldg(col_max + c)));
-        if (!given && r == 0) cols.gs[c] = g;
-        uint4 codes;
-        const uint32_t sb = encode_unit(v, g, given, codes);
-        *reinterpret_cast<uint4*>(cols.q + mma_tile_offset(c, r / 32, Rp)) = codes;
-        *reinterpret_cast<uint16_t*>(cols.s + mma_scale_offset(c, r / 16, 2 * Rp)) = (uint16_t)sb;
+            for (int j = 0; j < Block<T>::kWords / 4; ++j) {
+                const uint4 u = *reinterpret_cast<const uint4*>(tile + rr * kPitch + blk * 16 * (int)sizeof(T) + 16 * j);
+                k.w[4 * j] = u.x, k.w[4 * j + 1] = u.y, k.w[4 * j + 2] = u.z, k.w[4 * j + 3] = u.w;
+            }
+            const float g = !live ? 1.f : given ? rows.gs[rows.gs_rows ? r : 0] : row_scale(__ldg(row_max + r));
+            if (live && !given && b == 0) rows.gs[r] = g;
+            float v[16];
+            uint2 codes;
+            k.values(v);
+            const uint32_t sb = encode_block(v, __uint_as_float(block_mag(k)), g, given, codes);
+            store_block(rows.q, rows.s, r, b, Cp, codes, sb, live);
+        }
+    }
+    const int pair = threadIdx.x & 63, quarter = threadIdx.x >> 6;  // columns 2 pair, 2 pair + 1; rows 32 quarter ..
+    const int64_t c = c0 + 2 * pair, r = r0 + 32 * quarter;
+    if (c >= C || r >= Rp) return;
+    const bool two = c + 1 < C;
+    float g[2];
+    g[0] = given ? cols.gs[cols.gs_rows ? c : 0] : row_scale(__ldg(col_max + c));
+    g[1] = !two ? 1.f : given ? cols.gs[cols.gs_rows ? c + 1 : 0] : row_scale(__ldg(col_max + c + 1));
+    if (!given && r == 0) {
+        cols.gs[c] = g[0];
+        if (two) cols.gs[c + 1] = g[1];
+    }
+    uint2 codes[2][2];
+    uint32_t sb[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float v[2][16];
+        uint32_t m[2] = {0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const unsigned char* p = tile + (32 * quarter + 16 * h + j) * kPitch + 2 * pair * (int)sizeof(T);
+            if constexpr (sizeof(T) == 4) {
+                const float2 f = *reinterpret_cast<const float2*>(p);
+                v[0][j] = f.x, v[1][j] = f.y;
+            } else {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                    v[0][j] = __uint_as_float(w << 16), v[1][j] = __uint_as_float(w & 0xffff0000u);
+                } else {
+                    const float2 f = h2_to_f2(w);
+                    v[0][j] = f.x, v[1][j] = f.y;
+                }
+            }
+            m[0] = max(m[0], __float_as_uint(v[0][j]) & 0x7fffffffu);
+            m[1] = max(m[1], __float_as_uint(v[1][j]) & 0x7fffffffu);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sb[e][h] = encode_block(v[e], __uint_as_float(m[e]), g[e], given, codes[e][h]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (e == 1 && !two) break;
+        *reinterpret_cast<uint4*>(cols.q + mma_tile_offset(c + e, r / 32, Rp)) =
+            make_uint4(codes[e][0].x, codes[e][0].y, codes[e][1].x, codes[e][1].y);
+        *reinterpret_cast<uint16_t*>(cols.s + mma_scale_offset(c + e, r / 16, 2 * Rp)) = (uint16_t)(sb[e][0] | (sb[e][1] << 8));
     }
 }
 
@@ -239,33 +373,35 @@ cudaError_t quantize(const T* x, int64_t R, int64_t C, int64_t ld, const moe_nvf
                      const moe_nvfp4_operand* cols, bool given, unsigned* maxima, cudaStream_t st, bool pdl) {
     bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
     if (!cols) {
-        const int64_t units = pad_to(C, 256) / 32;
-        int tpr = 32;
-        while (tpr < kThreads && tpr < units) tpr *= 2;
-        const int64_t per = kThreads / tpr, blocks = (R + per - 1) / per;
+        const int64_t blocks = pad_to(C, 256) / 16;
+        int tpr = 32;  // the fewest threads that hold a row in two blocks each
+        while (tpr < kThreads && 2 * tpr < blocks) tpr *= 2;
+        const int64_t per = kThreads / tpr, grid = (R + per - 1) / per;
         bool gr = rows->gs_rows != 0;
         uint8_t *q = rows->q, *s = rows->s;
         float* gs = rows->gs;
         void* args[] = {&x, &R, &C, &ld, &wide, &tpr, &q, &s, &gs, &given, &gr};
-        return launch_kernel((const void*)nvfp4_rows_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), 0, st, pdl, args);
+        return launch_kernel((const void*)nvfp4_rows_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, pdl, args);
     }
     unsigned* row_max = rows ? maxima : nullptr;
     unsigned* col_max = maxima + (rows ? R : 0);
     if (!given) {
         cudaError_t e = cudaMemsetAsync(maxima, 0, sizeof(unsigned) * (size_t)((rows ? R : 0) + C), st);
         if (e != cudaSuccess) return e;
-        int ct = (int)((C + 255) / 256);
+        const int warp_cols = 32 * 16 / (int)sizeof(T);
+        int ct = (int)((C + warp_cols - 1) / warp_cols);
+        const int64_t grid = ct * ((R + kThreads - 1) / kThreads);
         void* args[] = {&x, &R, &C, &ld, &wide, &ct, &row_max, &col_max};
-        e = launch_kernel((const void*)nvfp4_maxima_kernel<T>, dim3((unsigned)(ct * ((R + 255) / 256))), dim3(kThreads), 0, st,
-                          false, args);
+        e = launch_kernel((const void*)nvfp4_maxima_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, false, args);
         if (e != cudaSuccess) return e;
     }
     // the padded contractions: columns to 256 for the row form, rows to 256 for the column form
-    int ct = (int)(pad_to(C, rows ? 256 : kTileC) / kTileC);
-    const int64_t rt = pad_to(R, 256) / kTileR;
+    int ct = (int)(pad_to(C, rows ? 256 : kTileDim) / kTileDim);
+    const int64_t rt = pad_to(R, 256) / kTileDim;
     moe_nvfp4_operand a = rows ? *rows : moe_nvfp4_operand{nullptr, nullptr, nullptr, 0}, b = *cols;
     void* args[] = {&x, &R, &C, &ld, &wide, &ct, &row_max, &col_max, &a, &b, &given};
-    return launch_kernel((const void*)nvfp4_both_kernel<T>, dim3((unsigned)(ct * rt)), dim3(kThreads), 0, st, false, args);
+    return launch_kernel((const void*)nvfp4_both_kernel<T>, dim3((unsigned)(ct * rt)), dim3(kThreads),
+                         (size_t)kTileDim * tile_pitch<T>(), st, false, args);
 }
 
 // Values of an operand: (E2M1 * E4M3) * row scale, the exact product of the first two rounded once.

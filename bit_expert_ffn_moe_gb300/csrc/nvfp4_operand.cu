@@ -7,29 +7,32 @@
 // in fp32, rounded to nearest even.  A row's own scale keeps a token's operand independent of the other
 // tokens of its batch.
 //
-// v / D costs three fp32 operations: q0 = v y, q = q0 + (v - q0 D) y with y = 1 / D rounded (Markstein's
-// correction, IBM J. Res. Dev. 34, 1990).  Over all 2^23 mantissas of D and all v within six ulps of the seven
-// values where the code changes, q decides as the rounded quotient does (checked exhaustively on a CPU;
-// without the correction 4% of those decisions differ), and farther away one ulp cannot change a
-// code.  D outside 2^-60 .. 2^60 takes the division.
+// Quotients cost three fp32 operations each: q0 = a y, q = q0 + (a - q0 b) y with y = 1 / b rounded (Markstein's
+// correction, IBM J. Res. Dev. 34, 1990).  Checked exhaustively on a CPU: for v / D, over all 2^23 mantissas of D and all
+// v within six ulps of the seven values where the code changes, q decides as the rounded quotient does
+// (without the correction 4% of those decisions differ, and farther away one ulp cannot change a code);
+// for max|block| / g with a 16-bit numerator and for t / 6, q is the rounded quotient.  fp32 maxima, and D or g outside
+// 2^-60 .. 2^60, take the division.
 //
 // A thread encodes a block of 16: its maximum is taken on the packed bits (two 16-bit elements per
 // instruction), few enough registers keep most of an SM's warps resident, which hides the loads.
 //   rows only   the threads of a row hold it in registers (up to 8192 elements), reduce its maximum, encode.
 //   with columns  two passes over x: the row and column maxima (integer maxima of the bits: the order of the
-//               atomics does not matter), then tiles of 128 x 128 elements through shared memory, encoded
-//               along their rows and along their columns, two columns per thread.
+//               atomics does not matter), then tiles of 256 rows x 64 columns through shared memory, encoded
+//               along their rows and along their columns, two columns per thread; 256 rows are a whole
+//               128-byte row of a column operand's code tile.
 // HBM bounds both: (2 or 4) R C bytes in, 9/16 R C out per form; the second pass of the two-form kernel
 // finds x in L2 while it fits there.
 #include <type_traits>
 
 #include "ops.cuh"
+#include "route_common.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTileDim = 128;  // rows and columns of a tile of the two-form kernel
+constexpr int kTileR = 256, kTileC = 64;  // rows and columns of a tile of the two-form kernel
 
 __host__ __device__ inline int64_t pad_to(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
@@ -105,10 +108,26 @@ __device__ __forceinline__ float row_scale(uint32_t mag) {
     return g == 0.f ? 1.f : g;
 }
 
-// One block of 16 elements of largest magnitude amax under the row scale g: 8 bytes of codes; returns the scale byte.
-__device__ __forceinline__ uint32_t encode_block(float (&v)[16], float amax, float g, bool given, uint2& codes) {
-    const uint32_t sb = f32_to_e4m3_sat(__fdiv_rn(__fdiv_rn(amax, g), 6.f));
-    const float D = __fmul_rn(e4m3x2_to_f2(sb).x, g);
+__device__ __forceinline__ bool mid_range(float v) { return v >= 8.6736174e-19f && v <= 1.1529215e18f; }
+__device__ __forceinline__ float quotient(float a, float b, float y) {  // y = 1 / b rounded
+    const float q0 = __fmul_rn(a, y);
+    return __fmaf_rn(__fmaf_rn(-q0, b, a), y, q0);
+}
+
+// A row scale and its reciprocal (0: outside the range in which quotients go by it).
+struct RowScale {
+    float g, y;
+};
+__device__ __forceinline__ RowScale with_reciprocal(float g) { return {g, mid_range(g) ? __frcp_rn(g) : 0.f}; }
+
+// One block of 16 elements of largest magnitude amax under the row scale: 8 bytes of codes; returns the scale byte.
+template <typename T>
+__device__ __forceinline__ uint32_t encode_block(float (&v)[16], float amax, RowScale rs, bool given, uint2& codes) {
+    float t;
+    if (sizeof(T) == 2 && rs.y != 0.f) t = quotient(quotient(amax, rs.g, rs.y), 6.f, 0.166666672f);
+    else t = __fdiv_rn(__fdiv_rn(amax, rs.g), 6.f);
+    const uint32_t sb = f32_to_e4m3_sat(t);
+    const float D = __fmul_rn(e4m3x2_to_f2(sb).x, rs.g);
     codes = make_uint2(0u, 0u);
     if (D == 0.f) return sb;
     if (given) {  // a row scale that is not the row's own may leave quotients far above 6: they saturate
@@ -116,12 +135,15 @@ __device__ __forceinline__ uint32_t encode_block(float (&v)[16], float amax, flo
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = fminf(fmaxf(v[i], -lim), lim);
     }
-    if (D >= 8.6736174e-19f && D <= 1.1529215e18f) {
+    if (mid_range(D)) {
         const float y = __frcp_rn(D);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float q0 = __fmul_rn(v[i], y);
-            v[i] = __fmaf_rn(__fmaf_rn(-q0, D, v[i]), y, q0);
+        for (int i = 0; i < 16; i += 2) {  // quotient() on pairs (q0 = a y + (-0): the rounded product)
+            const float2 a = make_float2(v[i], v[i + 1]), y2 = make_float2(y, y);
+            const float2 q0 = fma2(a, y2, make_float2(-0.f, -0.f));
+            const float2 q = fma2(fma2(q0, make_float2(-D, -D), a), y2, q0);
+            v[i] = q.x;
+            v[i + 1] = q.y;
         }
     } else {
 #pragma unroll
@@ -131,27 +153,43 @@ __device__ __forceinline__ uint32_t encode_block(float (&v)[16], float amax, flo
     return sb;
 }
 
-// Codes and scale of block b (16 elements) of operand row r, rows of Kp elements.  Four lanes with four
-// consecutive blocks (b % 4 = lane % 4) of one row store their scales as one word.
-__device__ __forceinline__ void store_block(uint8_t* q, uint8_t* s, int64_t r, int64_t b, int64_t Kp, uint2 codes, uint32_t sb,
-                                            bool live) {
-    if (live) *reinterpret_cast<uint2*>(q + mma_tile_offset(r, b >> 1, Kp) + 8 * (b & 1)) = codes;
+// Where a row of an operand of Kp elements lies: code block b (16 elements) at q + code_at(b), scale b at s + scale_at(b).
+struct RowPlace {
+    uint8_t* q;
+    uint8_t* s;
+    uint32_t swizzle;
+    __device__ __forceinline__ RowPlace(uint8_t* q_, uint8_t* s_, int64_t r, int64_t Kp) {
+        const int64_t rb = r >> 7;
+        const uint32_t in = (uint32_t)(r & 127);
+        q = q_ + rb * (Kp / 256) * 16384 + in * 128;
+        s = s_ + rb * (Kp / 64) * 512 + (in & 31) * 16 + (in >> 5) * 4;
+        swizzle = (in & 7) * 16;
+    }
+    __device__ __forceinline__ uint8_t* code_at(uint32_t b) const {
+        return q + (size_t)(b >> 4) * 16384 + ((((b >> 1) & 7) * 16) ^ swizzle) + 8 * (b & 1);
+    }
+    __device__ __forceinline__ uint8_t* scale_at(uint32_t b) const { return s + (size_t)(b >> 2) * 512 + (b & 3); }
+};
+
+// Block b of a row.  Four lanes with four consecutive blocks (b % 4 = lane % 4) of one row store their scales as one word.
+__device__ __forceinline__ void store_block(const RowPlace& at, uint32_t b, uint2 codes, uint32_t sb, bool live) {
+    if (live) *reinterpret_cast<uint2*>(at.code_at(b)) = codes;
     uint32_t word = sb << (8 * (b & 3));
     word |= __shfl_xor_sync(0xffffffffu, word, 1);
     word |= __shfl_xor_sync(0xffffffffu, word, 2);
-    if (live && (b & 3) == 0) *reinterpret_cast<uint32_t*>(s + mma_scale_offset(r, b, 2 * Kp)) = word;
+    if (live && (b & 3) == 0) *reinterpret_cast<uint32_t*>(at.scale_at(b)) = word;
 }
 
 // ------------------------------------------------------------------ rows only
-// `tpr` threads (32 .. 256) share a row; thread c of them the blocks c, c + tpr, ...; the first two stay in registers.
+// tpr = 2^tpr_log threads (32 .. 256) share a row; thread c of them the blocks c, c + tpr, ...; the first two stay in registers.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    nvfp4_rows_kernel(const T* __restrict__ x, int64_t R, int64_t K, int64_t ld, bool wide, int tpr, uint8_t* __restrict__ q,
+__global__ void __launch_bounds__(kThreads, 5)
+    nvfp4_rows_kernel(const T* __restrict__ x, int64_t R, int64_t K, int64_t ld, bool wide, int tpr_log, uint8_t* __restrict__ q,
                       uint8_t* __restrict__ s, float* __restrict__ gs, bool given, bool gs_rows) {
     __shared__ uint32_t part[kThreads / 32];
     pdl_launch_dependents();  // a product launched behind this call fetches its weights meanwhile
-    const int in_row = threadIdx.x & (tpr - 1), rows = kThreads / tpr;
-    const int64_t r = (int64_t)blockIdx.x * rows + threadIdx.x / tpr;
+    const int in_row = threadIdx.x & ((1 << tpr_log) - 1), tpr = 1 << tpr_log;
+    const int64_t r = (int64_t)blockIdx.x * (kThreads >> tpr_log) + (threadIdx.x >> tpr_log);
     const int64_t Kp = pad_to(K, 256);
     const int blocks = (int)(Kp / 16);  // a multiple of 16
     const bool live = r < R;
@@ -159,51 +197,52 @@ __global__ void __launch_bounds__(kThreads)
     Block<T> kept[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int64_t b = in_row + j * tpr;
-        kept[j].load(row + 16 * b, live && b < blocks ? K - 16 * b : 0, wide);
+        const int b = in_row + j * tpr;
+        kept[j].load(row + 16 * (int64_t)b, live && b < blocks ? K - 16 * (int64_t)b : 0, wide);
     }
-    uint32_t mag[2] = {block_mag(kept[0]), block_mag(kept[1])};
-    float g = 1.f;
+    const uint32_t mag[2] = {block_mag(kept[0]), block_mag(kept[1])};
+    RowScale rs = {1.f, 0.f};
     if (!given) {
         uint32_t m = max(mag[0], mag[1]);
-        for (int64_t b = in_row + 2 * tpr; b < blocks; b += tpr) {
+        for (int b = in_row + 2 * tpr; b < blocks; b += tpr) {
             Block<T> more;
-            more.load(row + 16 * b, live ? K - 16 * b : 0, wide);
+            more.load(row + 16 * (int64_t)b, live ? K - 16 * (int64_t)b : 0, wide);
             m = max(m, block_mag(more));
         }
         m = __reduce_max_sync(0xffffffffu, m);
         if (tpr > 32) {
             if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
             __syncthreads();
-            const int w0 = (threadIdx.x / tpr) * (tpr / 32);
-            for (int w = 0; w < tpr / 32; ++w) m = max(m, part[w0 + w]);
+            const int w0 = (threadIdx.x >> tpr_log) << (tpr_log - 5);
+            for (int w = 0; w < tpr >> 5; ++w) m = max(m, part[w0 + w]);
         }
-        g = row_scale(m);
-        if (live && in_row == 0) gs[r] = g;
+        rs = with_reciprocal(row_scale(m));
+        if (live && in_row == 0) gs[r] = rs.g;
     } else if (live) {
-        g = gs[gs_rows ? r : 0];
+        rs = with_reciprocal(gs[gs_rows ? r : 0]);
     }
+    const RowPlace at(q, s, live ? r : 0, Kp);
     // (lanes of four consecutive blocks leave together: blocks and tpr are multiples of 16)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int64_t b = in_row + j * tpr;
-        const bool mine = live && b < blocks;
+        const int b = in_row + j * tpr;
+        if (j == 1 && tpr >= blocks) break;
         float v[16];
         uint2 codes;
         kept[j].values(v);
-        const uint32_t sb = encode_block(v, __uint_as_float(mag[j]), g, given, codes);
-        store_block(q, s, r, b, Kp, codes, sb, mine);
+        const uint32_t sb = encode_block<T>(v, __uint_as_float(mag[j]), rs, given, codes);
+        store_block(at, b, codes, sb, live && b < blocks);
     }
     for (int b0 = 2 * tpr; b0 < blocks; b0 += tpr) {
-        const int64_t b = in_row + b0;
+        const int b = in_row + b0;
         const bool mine = live && b < blocks;
         Block<T> more;
-        more.load(row + 16 * b, mine ? K - 16 * b : 0, wide);
+        more.load(row + 16 * (int64_t)b, mine ? K - 16 * (int64_t)b : 0, wide);
         float v[16];
         uint2 codes;
         more.values(v);
-        const uint32_t sb = encode_block(v, __uint_as_float(block_mag(more)), g, given, codes);
-        store_block(q, s, r, b, Kp, codes, sb, mine);
+        const uint32_t sb = encode_block<T>(v, __uint_as_float(block_mag(more)), rs, given, codes);
+        store_block(at, b, codes, sb, mine);
     }
 }
 
@@ -267,22 +306,23 @@ __global__ void __launch_bounds__(kThreads)
     atomicMax(col_max + col0 + threadIdx.x, m);
 }
 
-// A tile of 128 x 128 elements of x in shared memory, encoded along its rows (a thread: 4 blocks) and along its
-// columns (a thread: 2 columns x 32 rows).  Tiles cover the padded contractions (256 multiples), whose
-// padding is written as zeros.
+// A tile of 256 x 64 elements of x in shared memory, encoded along its rows (a thread: 4 blocks) and along its
+// columns (a thread: 2 columns x 32 rows; eight lanes hold the 256 rows of a column and write its 128 bytes of
+// codes).  The 16-byte pieces of a row are rotated by its group of 32 rows, so that lanes reading 8 groups x 4
+// words meet all banks.  Tiles cover the padded contractions (256 multiples), whose padding is written as zeros.
 template <typename T>
-__host__ __device__ constexpr int tile_pitch() { return kTileDim * (int)sizeof(T) + 16; }  // bytes
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     nvfp4_both_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld, bool wide, int col_tiles,
-                      const unsigned* __restrict__ row_max, const unsigned* __restrict__ col_max, const moe_nvfp4_operand rows,
-                      const moe_nvfp4_operand cols, bool given) {
+                      const unsigned* __restrict__ row_max, const unsigned* __restrict__ col_max,
+                      const __grid_constant__ moe_nvfp4_operand rows, const __grid_constant__ moe_nvfp4_operand cols, bool given) {
     extern __shared__ __align__(16) unsigned char tile[];
-    constexpr int kPitch = tile_pitch<T>(), kPer = 16 / (int)sizeof(T), kPieces = kTileDim / kPer;
-    const int64_t r0 = (int64_t)(blockIdx.x / col_tiles) * kTileDim, c0 = (int64_t)(blockIdx.x % col_tiles) * kTileDim;
+    __shared__ RowScale row_scales[kTileR], col_scales[kTileC];
+    constexpr int kPitch = kTileC * (int)sizeof(T), kPer = 16 / (int)sizeof(T), kPieces = kTileC / kPer, kTurn = kPieces / 8;
+    const int64_t r0 = (int64_t)(blockIdx.x / col_tiles) * kTileR, c0 = (int64_t)(blockIdx.x % col_tiles) * kTileC;
     const int64_t Cp = pad_to(C, 256), Rp = pad_to(R, 256);
+    auto piece_at = [&](int rr, int pc) { return tile + rr * kPitch + ((pc + kTurn * (rr >> 5)) & (kPieces - 1)) * 16; };
 #pragma unroll 8
-    for (int i = threadIdx.x; i < kTileDim * kPieces; i += kThreads) {
+    for (int i = threadIdx.x; i < kTileR * kPieces; i += kThreads) {
         const int rr = i / kPieces, pc = i % kPieces;
         const int64_t r = r0 + rr, c = c0 + pc * kPer;
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
@@ -297,41 +337,49 @@ __global__ void __launch_bounds__(kThreads)
                 u = *reinterpret_cast<const uint4*>(e);
             }
         }
-        *reinterpret_cast<uint4*>(tile + rr * kPitch + pc * 16) = u;
+        *reinterpret_cast<uint4*>(piece_at(rr, pc)) = u;
+    }
+    if (rows.q) {
+        const int64_t r = r0 + threadIdx.x;
+        RowScale rs = {1.f, 0.f};
+        if (r < R) {
+            rs = with_reciprocal(given ? rows.gs[rows.gs_rows ? r : 0] : row_scale(__ldg(row_max + r)));
+            if (!given && c0 == 0) rows.gs[r] = rs.g;
+        }
+        row_scales[threadIdx.x] = rs;
+    }
+    if (threadIdx.x < kTileC) {
+        const int64_t c = c0 + threadIdx.x;
+        RowScale rs = {1.f, 0.f};
+        if (c < C) {
+            rs = with_reciprocal(given ? cols.gs[cols.gs_rows ? c : 0] : row_scale(__ldg(col_max + c)));
+            if (!given && r0 == 0) cols.gs[c] = rs.g;
+        }
+        col_scales[threadIdx.x] = rs;
     }
     __syncthreads();
     if (rows.q) {
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-            const int rr = 32 * i + (threadIdx.x >> 3), blk = threadIdx.x & 7;
+            const int rr = 64 * i + (threadIdx.x >> 2), blk = threadIdx.x & 3;
             const int64_t r = r0 + rr, b = c0 / 16 + blk;
             const bool live = r < R && 16 * b < Cp;
             Block<T> k;
 #pragma unroll
             for (int j = 0; j < Block<T>::kWords / 4; ++j) {
-                const uint4 u = *reinterpret_cast<const uint4*>(tile + rr * kPitch + blk * 16 * (int)sizeof(T) + 16 * j);
+                const uint4 u = *reinterpret_cast<const uint4*>(piece_at(rr, blk * (Block<T>::kWords / 4) + j));
                 k.w[4 * j] = u.x, k.w[4 * j + 1] = u.y, k.w[4 * j + 2] = u.z, k.w[4 * j + 3] = u.w;
             }
-            const float g = !live ? 1.f : given ? rows.gs[rows.gs_rows ? r : 0] : row_scale(__ldg(row_max + r));
-            if (live && !given && b == 0) rows.gs[r] = g;
             float v[16];
             uint2 codes;
             k.values(v);
-            const uint32_t sb = encode_block(v, __uint_as_float(block_mag(k)), g, given, codes);
-            store_block(rows.q, rows.s, r, b, Cp, codes, sb, live);
+            const uint32_t sb = encode_block<T>(v, __uint_as_float(block_mag(k)), row_scales[rr], given, codes);
+            store_block(RowPlace(rows.q, rows.s, live ? r : 0, Cp), (uint32_t)b, codes, sb, live);
         }
     }
-    const int pair = threadIdx.x & 63, quarter = threadIdx.x >> 6;  // columns 2 pair, 2 pair + 1; rows 32 quarter ..
-    const int64_t c = c0 + 2 * pair, r = r0 + 32 * quarter;
-    if (c >= C || r >= Rp) return;
-    const bool two = c + 1 < C;
-    float g[2];
-    g[0] = given ? cols.gs[cols.gs_rows ? c : 0] : row_scale(__ldg(col_max + c));
-    g[1] = !two ? 1.f : given ? cols.gs[cols.gs_rows ? c + 1 : 0] : row_scale(__ldg(col_max + c + 1));
-    if (!given && r == 0) {
-        cols.gs[c] = g[0];
-        if (two) cols.gs[c + 1] = g[1];
-    }
+    // lane: group of 32 rows (lane % 8) and column pair (lane / 8 of the warp's four)
+    const int group = threadIdx.x & 7, pair = threadIdx.x >> 3;
+    const int64_t c = c0 + 2 * pair;
     uint2 codes[2][2];
     uint32_t sb[2][2];
 #pragma unroll
@@ -340,7 +388,7 @@ __global__ void __launch_bounds__(kThreads)
         uint32_t m[2] = {0u, 0u};
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            const unsigned char* p = tile + (32 * quarter + 16 * h + j) * kPitch + 2 * pair * (int)sizeof(T);
+            const unsigned char* p = piece_at(32 * group + 16 * h + j, 2 * pair / kPer) + (2 * pair % kPer) * (int)sizeof(T);
             if constexpr (sizeof(T) == 4) {
                 const float2 f = *reinterpret_cast<const float2*>(p);
                 v[0][j] = f.x, v[1][j] = f.y;
@@ -357,14 +405,18 @@ __global__ void __launch_bounds__(kThreads)
             m[1] = max(m[1], __float_as_uint(v[1][j]) & 0x7fffffffu);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) sb[e][h] = encode_block(v[e], __uint_as_float(m[e]), g[e], given, codes[e][h]);
+        for (int e = 0; e < 2; ++e)
+            sb[e][h] = encode_block<T>(v[e], __uint_as_float(m[e]), col_scales[2 * pair + e], given, codes[e][h]);
     }
+    const uint32_t b = (uint32_t)(r0 / 16) + 2 * group;  // (the tile's 256 rows lie in the padded contraction: Rp is a multiple)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        if (e == 1 && !two) break;
-        *reinterpret_cast<uint4*>(cols.q + mma_tile_offset(c + e, r / 32, Rp)) =
-            make_uint4(codes[e][0].x, codes[e][0].y, codes[e][1].x, codes[e][1].y);
-        *reinterpret_cast<uint16_t*>(cols.s + mma_scale_offset(c + e, r / 16, 2 * Rp)) = (uint16_t)(sb[e][0] | (sb[e][1] << 8));
+        uint32_t word = (sb[e][0] | (sb[e][1] << 8)) << (16 * (group & 1));  // two groups: the four scales of a word
+        word |= __shfl_xor_sync(0xffffffffu, word, 1);
+        if (c + e >= C) continue;
+        const RowPlace at(cols.q, cols.s, c + e, Rp);
+        *reinterpret_cast<uint4*>(at.code_at(b)) = make_uint4(codes[e][0].x, codes[e][0].y, codes[e][1].x, codes[e][1].y);
+        if ((group & 1) == 0) *reinterpret_cast<uint32_t*>(at.scale_at(b)) = word;
     }
 }
 
@@ -374,13 +426,13 @@ cudaError_t quantize(const T* x, int64_t R, int64_t C, int64_t ld, const moe_nvf
     bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
     if (!cols) {
         const int64_t blocks = pad_to(C, 256) / 16;
-        int tpr = 32;  // the fewest threads that hold a row in two blocks each
-        while (tpr < kThreads && 2 * tpr < blocks) tpr *= 2;
-        const int64_t per = kThreads / tpr, grid = (R + per - 1) / per;
+        int tpr_log = 5;  // the fewest threads that hold a row in two blocks each
+        while ((1 << tpr_log) < kThreads && (2 << tpr_log) < blocks) ++tpr_log;
+        const int64_t per = kThreads >> tpr_log, grid = (R + per - 1) / per;
         bool gr = rows->gs_rows != 0;
         uint8_t *q = rows->q, *s = rows->s;
         float* gs = rows->gs;
-        void* args[] = {&x, &R, &C, &ld, &wide, &tpr, &q, &s, &gs, &given, &gr};
+        void* args[] = {&x, &R, &C, &ld, &wide, &tpr_log, &q, &s, &gs, &given, &gr};
         return launch_kernel((const void*)nvfp4_rows_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, pdl, args);
     }
     unsigned* row_max = rows ? maxima : nullptr;
@@ -396,12 +448,12 @@ cudaError_t quantize(const T* x, int64_t R, int64_t C, int64_t ld, const moe_nvf
         if (e != cudaSuccess) return e;
     }
     // the padded contractions: columns to 256 for the row form, rows to 256 for the column form
-    int ct = (int)(pad_to(C, rows ? 256 : kTileDim) / kTileDim);
-    const int64_t rt = pad_to(R, 256) / kTileDim;
+    int ct = (int)(pad_to(C, rows ? 256 : kTileC) / kTileC);
+    const int64_t rt = pad_to(R, 256) / kTileR;
     moe_nvfp4_operand a = rows ? *rows : moe_nvfp4_operand{nullptr, nullptr, nullptr, 0}, b = *cols;
     void* args[] = {&x, &R, &C, &ld, &wide, &ct, &row_max, &col_max, &a, &b, &given};
     return launch_kernel((const void*)nvfp4_both_kernel<T>, dim3((unsigned)(ct * rt)), dim3(kThreads),
-                         (size_t)kTileDim * tile_pitch<T>(), st, false, args);
+                         (size_t)kTileR * kTileC * sizeof(T), st, false, args);
 }
 
 // Values of an operand: (E2M1 * E4M3) * row scale, the exact product of the first two rounded once.

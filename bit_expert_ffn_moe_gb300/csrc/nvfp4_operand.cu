@@ -11,8 +11,9 @@
 // correction, IBM J. Res. Dev. 34, 1990).  Checked exhaustively on a CPU: for v / D, over all 2^23 mantissas of D and all
 // v within six ulps of the seven values where the code changes, q decides as the rounded quotient does
 // (without the correction 4% of those decisions differ, and farther away one ulp cannot change a code);
-// for max|block| / g with a 16-bit numerator and for t / 6, q is the rounded quotient.  fp32 maxima, and D or g outside
-// 2^-60 .. 2^60, take the division.
+// for max|block| / g with a 16-bit numerator and for t / 6, q is the rounded quotient.  1 / D itself is the hardware's
+// reciprocal with one Newton step; a GPU test runs all mantissas of D against the division.  fp32 maxima, and
+// row scales outside 2^-50 .. 2^50, take the division.
 //
 // A thread encodes a block of 16: its maximum is taken on the packed bits (two 16-bit elements per
 // instruction), few enough registers keep most of an SM's warps resident, which hides the loads.
@@ -80,10 +81,20 @@ struct Block {
     }
 };
 
-// Magnitudes compare as integers: a word of one fp32 or two 16-bit elements.
+// The larger magnitudes of a word of one fp32 or two 16-bit elements (a: magnitudes already).
 template <typename T>
 __device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b) {
-    return sizeof(T) == 4 ? max(a, b & 0x7fffffffu) : __vmaxu2(a, b & 0x7fff7fffu);
+    if constexpr (sizeof(T) == 4) {
+        return max(a, b & 0x7fffffffu);
+    } else {
+        uint32_t r;
+        if constexpr (std::is_same<T, __half>::value) {
+            asm("{\n\t.reg .b32 m;\n\tabs.f16x2 m, %2;\n\tmax.f16x2 %0, %1, m;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+        } else {
+            asm("{\n\t.reg .b32 m;\n\tabs.bf16x2 m, %2;\n\tmax.bf16x2 %0, %1, m;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+        }
+        return r;
+    }
 }
 // A maximum of magnitudes as fp32 bits.
 template <typename T>
@@ -108,19 +119,22 @@ __device__ __forceinline__ float row_scale(uint32_t mag) {
     return g == 0.f ? 1.f : g;
 }
 
-__device__ __forceinline__ bool mid_range(float v) { return v >= 8.6736174e-19f && v <= 1.1529215e18f; }
 __device__ __forceinline__ float quotient(float a, float b, float y) {  // y = 1 / b rounded
     const float q0 = __fmul_rn(a, y);
     return __fmaf_rn(__fmaf_rn(-q0, b, a), y, q0);
 }
 
-// A row scale and its reciprocal (0: outside the range in which quotients go by it).
+// A row scale and its reciprocal (0: outside 2^-50 .. 2^50, where quotients take the division).  A block scale of at
+// least 2^-9 and at most 448 keeps D = scale * g inside the range where no step of a quotient loses bits.
 struct RowScale {
     float g, y;
 };
-__device__ __forceinline__ RowScale with_reciprocal(float g) { return {g, mid_range(g) ? __frcp_rn(g) : 0.f}; }
+__device__ __forceinline__ RowScale with_reciprocal(float g) {
+    return {g, g >= 8.8817842e-16f && g <= 1.1258999e15f ? __frcp_rn(g) : 0.f};
+}
 
 // One block of 16 elements of largest magnitude amax under the row scale: 8 bytes of codes; returns the scale byte.
+// given: the row scale is not the row's own and quotients may be far above 6: they saturate.
 template <typename T>
 __device__ __forceinline__ uint32_t encode_block(float (&v)[16], float amax, RowScale rs, bool given, uint2& codes) {
     float t;
@@ -128,26 +142,27 @@ __device__ __forceinline__ uint32_t encode_block(float (&v)[16], float amax, Row
     else t = __fdiv_rn(__fdiv_rn(amax, rs.g), 6.f);
     const uint32_t sb = f32_to_e4m3_sat(t);
     const float D = __fmul_rn(e4m3x2_to_f2(sb).x, rs.g);
-    codes = make_uint2(0u, 0u);
-    if (D == 0.f) return sb;
-    if (given) {  // a row scale that is not the row's own may leave quotients far above 6: they saturate
+    if (given) {
         const float lim = 8.f * D;
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = fminf(fmaxf(v[i], -lim), lim);
     }
-    if (mid_range(D)) {
-        const float y = __frcp_rn(D);
+    if (rs.y != 0.f) {
+        float y;  // 1 / D rounded (the hardware's reciprocal and a Newton step); a zero scale gives zero codes
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(D));
+        y = sb == 0 ? 0.f : fmaf(y, fmaf(-D, y, 1.f), y);
+        const float2 y2 = make_float2(y, y), d2 = make_float2(-D, -D);
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {  // quotient() on pairs (q0 = a y + (-0): the rounded product)
-            const float2 a = make_float2(v[i], v[i + 1]), y2 = make_float2(y, y);
+            const float2 a = make_float2(v[i], v[i + 1]);
             const float2 q0 = fma2(a, y2, make_float2(-0.f, -0.f));
-            const float2 q = fma2(fma2(q0, make_float2(-D, -D), a), y2, q0);
+            const float2 q = fma2(fma2(q0, d2, a), y2, q0);
             v[i] = q.x;
             v[i + 1] = q.y;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = __fdiv_rn(v[i], D);
+        for (int i = 0; i < 16; ++i) v[i] = D == 0.f ? 0.f : __fdiv_rn(v[i], D);
     }
     codes = make_uint2(e2m1x8_encode(v), e2m1x8_encode(v + 8));
     return sb;

@@ -119,6 +119,29 @@ def test_far_scales_take_the_division(scale):
     check_operand(op, x.numpy())
 
 
+def test_every_mantissa_of_the_scale_decides_as_the_division():
+    """Block scale D = g (an E4M3 scale of one) for all 2^23 mantissas of g, elements within two ulps of each value where the code
+    changes: the codes are those of the quotients rounded to fp32."""
+    mids = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64, device="cuda")
+    grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], device="cuda")
+    rows, K = 1 << 19, 16 * 5
+    for part in range(1 << 4):
+        g = (torch.arange(rows, device="cuda", dtype=torch.int32) + part * rows + 0x3F800000).view(torch.float32)
+        near = (mids[None, :] * g[:, None].double()).float()
+        x = torch.zeros(rows, K, device="cuda")
+        for j in range(5):
+            x[:, 16 * j] = 6.0 * g  # the block's largest: scale 1
+            x[:, 16 * j + 1:16 * j + 8] = (near.view(torch.int32) + (j - 2)).view(torch.float32)
+            x[:, 16 * j + 8:16 * j + 15] = -(near.view(torch.int32) + (j - 2)).view(torch.float32)
+        op = ops.nvfp4_operand(rows, K)
+        op.gs.copy_(g)
+        ops.nvfp4_quantize(x, op, scales_given=True)
+        q = (x.abs().double() / g[:, None].double()).float()  # rounded once more than the quotient in 64 bits: innocuous
+        code = sum(((q > m) if i % 2 == 0 else (q >= m)).int() for i, m in enumerate(mids.float().tolist()))
+        want = (grid[code.long()] * torch.sign(x) * g[:, None])
+        assert torch.equal(op.values(), want)
+
+
 def check_product(a, b, dtype, out=None):
     ws = ops.nvfp4_workspace(a.rows, b.rows, a.K)
     y = ops.nvfp4_matmul(a, b, TYPES[dtype], ws, out)

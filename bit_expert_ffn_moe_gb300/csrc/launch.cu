@@ -1,4 +1,5 @@
 // launch.cu -- host-side launch helpers shared by the kernel families.
+#include <atomic>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -23,9 +24,12 @@ cudaError_t ensure_dyn_smem(const void* func, size_t bytes) {
 }
 
 int sm_count() {
+    static std::atomic<int> known[64];  // per device, 0: not asked yet
     int dev = 0, n = 0;
     cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (n > 0 && dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n > 0 ? n : 148;
 }
 

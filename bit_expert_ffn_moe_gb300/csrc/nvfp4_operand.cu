@@ -168,61 +168,62 @@ __device__ __forceinline__ uint32_t encode_block(float (&v)[16], float amax, Row
     return sb;
 }
 
-// Where a row of an operand of Kp elements lies: code block b (16 elements) at q + code_at(b), scale b at s + scale_at(b).
-struct RowPlace {
-    uint8_t* q;
-    uint8_t* s;
-    uint32_t swizzle;
-    __device__ __forceinline__ RowPlace(uint8_t* q_, uint8_t* s_, int64_t r, int64_t Kp) {
-        const int64_t rb = r >> 7;
-        const uint32_t in = (uint32_t)(r & 127);
-        q = q_ + rb * (Kp / 256) * 16384 + in * 128;
-        s = s_ + rb * (Kp / 64) * 512 + (in & 31) * 16 + (in >> 5) * 4;
-        swizzle = (in & 7) * 16;
-    }
-    __device__ __forceinline__ uint8_t* code_at(uint32_t b) const {
-        return q + (size_t)(b >> 4) * 16384 + ((((b >> 1) & 7) * 16) ^ swizzle) + 8 * (b & 1);
-    }
-    __device__ __forceinline__ uint8_t* scale_at(uint32_t b) const { return s + (size_t)(b >> 2) * 512 + (b & 3); }
-};
+// Byte offsets inside a 128-row block of an operand of width Kp: of the 16 bytes of codes of unit u (32
+// elements: two blocks) of row `in`, and of its two scales.
+__device__ __forceinline__ uint32_t unit_codes(uint32_t in, uint32_t u) {
+    return (u >> 3) * 16384u + in * 128u + (((u & 7u) ^ (in & 7u)) * 16u);
+}
+__device__ __forceinline__ uint32_t unit_scales(uint32_t in, uint32_t u) {
+    return (u >> 1) * 512u + (in & 31u) * 16u + (in >> 5) * 4u + 2u * (u & 1u);
+}
 
-// Block b of a row.  Four lanes with four consecutive blocks (b % 4 = lane % 4) of one row store their scales as one word.
-__device__ __forceinline__ void store_block(const RowPlace& at, uint32_t b, uint2 codes, uint32_t sb, bool live) {
-    if (live) *reinterpret_cast<uint2*>(at.code_at(b)) = codes;
-    uint32_t word = sb << (8 * (b & 3));
-    word |= __shfl_xor_sync(0xffffffffu, word, 1);
-    word |= __shfl_xor_sync(0xffffffffu, word, 2);
-    if (live && (b & 3) == 0) *reinterpret_cast<uint32_t*>(at.scale_at(b)) = word;
+// Two adjacent blocks of a row: 16 bytes of codes; the lanes of two adjacent units (u even in the even lane) store their
+// four scales as one word.
+template <typename T>
+__device__ __forceinline__ void encode_unit(const Block<T>& a, const Block<T>& b, uint32_t mag_a, uint32_t mag_b, RowScale rs, bool given,
+                                            uint8_t* q, uint8_t* s, bool live) {
+    float v[16];
+    uint2 ca, cb;
+    a.values(v);
+    uint32_t word = encode_block<T>(v, __uint_as_float(mag_a), rs, given, ca);
+    b.values(v);
+    word |= encode_block<T>(v, __uint_as_float(mag_b), rs, given, cb) << 8;
+    if (live) *reinterpret_cast<uint4*>(q) = make_uint4(ca.x, ca.y, cb.x, cb.y);
+    word |= __shfl_down_sync(0xffffffffu, word, 1) << 16;
+    if (live && (threadIdx.x & 1) == 0) *reinterpret_cast<uint32_t*>(s) = word;
 }
 
 // ------------------------------------------------------------------ rows only
-// tpr = 2^tpr_log threads (32 .. 256) share a row; thread c of them the blocks c, c + tpr, ...; the first two stay in registers.
+// tpr = 2^tpr_log threads (32 .. 256) share a row; thread c of them the units (two blocks) c, c + tpr, ...; the
+// first stays in registers.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, 4)
     nvfp4_rows_kernel(const T* __restrict__ x, int64_t R, int64_t K, int64_t ld, bool wide, int tpr_log, uint8_t* __restrict__ q,
                       uint8_t* __restrict__ s, float* __restrict__ gs, bool given, bool gs_rows) {
     __shared__ uint32_t part[kThreads / 32];
     pdl_launch_dependents();  // a product launched behind this call fetches its weights meanwhile
-    const int in_row = threadIdx.x & ((1 << tpr_log) - 1), tpr = 1 << tpr_log;
+    const int tpr = 1 << tpr_log, u0 = threadIdx.x & (tpr - 1);
     const int64_t r = (int64_t)blockIdx.x * (kThreads >> tpr_log) + (threadIdx.x >> tpr_log);
-    const int64_t Kp = pad_to(K, 256);
-    const int blocks = (int)(Kp / 16);  // a multiple of 16
+    const int units = (int)((K + 255) >> 8) * 8;
     const bool live = r < R;
     const T* row = x + (live ? r : 0) * ld;
-    Block<T> kept[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int b = in_row + j * tpr;
-        kept[j].load(row + 16 * (int64_t)b, live && b < blocks ? K - 16 * (int64_t)b : 0, wide);
-    }
-    const uint32_t mag[2] = {block_mag(kept[0]), block_mag(kept[1])};
+    Block<T> a, b;
+    auto load = [&](int u, bool take) {
+        const int64_t left = take ? K - 32 * (int64_t)u : 0;
+        a.load(row + 32 * (int64_t)u, left, wide);
+        b.load(row + 32 * (int64_t)u + 16, left - 16, wide);
+    };
+    load(u0, live && u0 < units);
+    uint32_t mag_a = block_mag(a), mag_b = block_mag(b);
     RowScale rs = {1.f, 0.f};
     if (!given) {
-        uint32_t m = max(mag[0], mag[1]);
-        for (int b = in_row + 2 * tpr; b < blocks; b += tpr) {
-            Block<T> more;
-            more.load(row + 16 * (int64_t)b, live ? K - 16 * (int64_t)b : 0, wide);
-            m = max(m, block_mag(more));
+        uint32_t m = max(mag_a, mag_b);
+        if (units > tpr) {
+            for (int u = u0 + tpr; u < units; u += tpr) {
+                load(u, live);
+                m = max(m, max(block_mag(a), block_mag(b)));
+            }
+            load(u0, live);
         }
         m = __reduce_max_sync(0xffffffffu, m);
         if (tpr > 32) {
@@ -232,32 +233,22 @@ __global__ void __launch_bounds__(kThreads, 5)
             for (int w = 0; w < tpr >> 5; ++w) m = max(m, part[w0 + w]);
         }
         rs = with_reciprocal(row_scale(m));
-        if (live && in_row == 0) gs[r] = rs.g;
+        if (live && u0 == 0) gs[r] = rs.g;
     } else if (live) {
         rs = with_reciprocal(gs[gs_rows ? r : 0]);
     }
-    const RowPlace at(q, s, live ? r : 0, Kp);
-    // (lanes of four consecutive blocks leave together: blocks and tpr are multiples of 16)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int b = in_row + j * tpr;
-        if (j == 1 && tpr >= blocks) break;
-        float v[16];
-        uint2 codes;
-        kept[j].values(v);
-        const uint32_t sb = encode_block<T>(v, __uint_as_float(mag[j]), rs, given, codes);
-        store_block(at, b, codes, sb, live && b < blocks);
-    }
-    for (int b0 = 2 * tpr; b0 < blocks; b0 += tpr) {
-        const int b = in_row + b0;
-        const bool mine = live && b < blocks;
-        Block<T> more;
-        more.load(row + 16 * (int64_t)b, mine ? K - 16 * (int64_t)b : 0, wide);
-        float v[16];
-        uint2 codes;
-        more.values(v);
-        const uint32_t sb = encode_block<T>(v, __uint_as_float(block_mag(more)), rs, given, codes);
-        store_block(at, b, codes, sb, mine);
+    const uint32_t in = (uint32_t)r & 127u;  // row of its 128-row block
+    uint8_t* qr = q + (r >> 7) * (int64_t)units * 2048 + in * 128u;
+    uint8_t* sr = s + (r >> 7) * (int64_t)units * 256 + unit_scales(in, 0);
+    for (int base = 0; base < units; base += tpr) {
+        const int u = base + u0;
+        const bool mine = live && u < units;
+        if (base > 0) {
+            load(u, mine);
+            mag_a = block_mag(a), mag_b = block_mag(b);
+        }
+        encode_unit(a, b, mag_a, mag_b, rs, given, qr + (int64_t)(u >> 3) * 16384 + (((uint32_t)u ^ in) & 7u) * 16u,
+                    sr + (int64_t)(u >> 1) * 512, mine);
     }
 }
 
@@ -326,7 +317,7 @@ __global__ void __launch_bounds__(kThreads)
 // codes).  The 16-byte pieces of a row are rotated by its group of 32 rows, so that lanes reading 8 groups x 4
 // words meet all banks.  Tiles cover the padded contractions (256 multiples), whose padding is written as zeros.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
     nvfp4_both_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld, bool wide, int col_tiles,
                       const unsigned* __restrict__ row_max, const unsigned* __restrict__ col_max,
                       const __grid_constant__ moe_nvfp4_operand rows, const __grid_constant__ moe_nvfp4_operand cols, bool given) {
@@ -374,41 +365,50 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
     __syncthreads();
     if (rows.q) {
+        // thread: row threadIdx / 2 (+ 128), unit threadIdx % 2 of the tile's 64 columns
+        const uint32_t in = threadIdx.x >> 1, u = threadIdx.x & 1;
+        const int64_t units = Cp / 32;
+        uint8_t* q = rows.q + (r0 >> 7) * units * 2048 + unit_codes(in, (uint32_t)(c0 >> 5) & 7u | u) + (c0 >> 8) * 16384;
+        uint8_t* s = rows.s + (r0 >> 7) * units * 256 + unit_scales(in, u) + (c0 >> 6) * 512;
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            const int rr = 64 * i + (threadIdx.x >> 2), blk = threadIdx.x & 3;
-            const int64_t r = r0 + rr, b = c0 / 16 + blk;
-            const bool live = r < R && 16 * b < Cp;
-            Block<T> k;
+        for (int i = 0; i < 2; ++i, q += units * 2048, s += units * 256) {
+            const int rr = 128 * i + in;
+            Block<T> a, b;
+            constexpr int kBlockPieces = Block<T>::kWords / 4;
 #pragma unroll
-            for (int j = 0; j < Block<T>::kWords / 4; ++j) {
-                const uint4 u = *reinterpret_cast<const uint4*>(piece_at(rr, blk * (Block<T>::kWords / 4) + j));
-                k.w[4 * j] = u.x, k.w[4 * j + 1] = u.y, k.w[4 * j + 2] = u.z, k.w[4 * j + 3] = u.w;
+            for (int j = 0; j < kBlockPieces; ++j) {
+                const uint4 x0 = *reinterpret_cast<const uint4*>(piece_at(rr, 2 * u * kBlockPieces + j));
+                const uint4 x1 = *reinterpret_cast<const uint4*>(piece_at(rr, (2 * u + 1) * kBlockPieces + j));
+                a.w[4 * j] = x0.x, a.w[4 * j + 1] = x0.y, a.w[4 * j + 2] = x0.z, a.w[4 * j + 3] = x0.w;
+                b.w[4 * j] = x1.x, b.w[4 * j + 1] = x1.y, b.w[4 * j + 2] = x1.z, b.w[4 * j + 3] = x1.w;
             }
-            float v[16];
-            uint2 codes;
-            k.values(v);
-            const uint32_t sb = encode_block<T>(v, __uint_as_float(block_mag(k)), row_scales[rr], given, codes);
-            store_block(RowPlace(rows.q, rows.s, live ? r : 0, Cp), (uint32_t)b, codes, sb, live);
+            encode_unit(a, b, block_mag(a), block_mag(b), row_scales[rr], given, q, s, r0 + rr < R);
         }
     }
     // lane: group of 32 rows (lane % 8) and column pair (lane / 8 of the warp's four)
     const int group = threadIdx.x & 7, pair = threadIdx.x >> 3;
     const int64_t c = c0 + 2 * pair;
+    const unsigned char* column = piece_at(32 * group, 2 * pair / kPer) + (2 * pair % kPer) * (int)sizeof(T);
     uint2 codes[2][2];
     uint32_t sb[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float v[2][16];
         uint32_t m[2] = {0u, 0u};
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const unsigned char* p = piece_at(32 * group + 16 * h + j, 2 * pair / kPer) + (2 * pair % kPer) * (int)sizeof(T);
-            if constexpr (sizeof(T) == 4) {
-                const float2 f = *reinterpret_cast<const float2*>(p);
+            for (int j = 0; j < 16; ++j) {
+                const float2 f = *reinterpret_cast<const float2*>(column + (16 * h + j) * kPitch);
                 v[0][j] = f.x, v[1][j] = f.y;
-            } else {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+                m[0] = mag_max<T>(m[0], __float_as_uint(f.x));
+                m[1] = mag_max<T>(m[1], __float_as_uint(f.y));
+            }
+        } else {
+            uint32_t both = 0u;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(column + (16 * h + j) * kPitch);
+                both = mag_max<T>(both, w);
                 if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                     v[0][j] = __uint_as_float(w << 16), v[1][j] = __uint_as_float(w & 0xffff0000u);
                 } else {
@@ -416,22 +416,23 @@ __global__ void __launch_bounds__(kThreads, 4)
                     v[0][j] = f.x, v[1][j] = f.y;
                 }
             }
-            m[0] = max(m[0], __float_as_uint(v[0][j]) & 0x7fffffffu);
-            m[1] = max(m[1], __float_as_uint(v[1][j]) & 0x7fffffffu);
+            m[0] = mag_f32<T>(both & 0xffffu), m[1] = mag_f32<T>(both & 0xffff0000u);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
             sb[e][h] = encode_block<T>(v[e], __uint_as_float(m[e]), col_scales[2 * pair + e], given, codes[e][h]);
     }
-    const uint32_t b = (uint32_t)(r0 / 16) + 2 * group;  // (the tile's 256 rows lie in the padded contraction: Rp is a multiple)
+    // the tile's 64 columns lie in one 128-row block of the column operand, its 256 rows in one code tile
+    uint8_t* q = cols.q + ((c0 >> 7) * (Rp >> 8) + (r0 >> 8)) * 16384;
+    uint8_t* s = cols.s + ((c0 >> 7) * (Rp >> 6) + (r0 >> 6)) * 512;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        uint32_t word = (sb[e][0] | (sb[e][1] << 8)) << (16 * (group & 1));  // two groups: the four scales of a word
-        word |= __shfl_xor_sync(0xffffffffu, word, 1);
+        uint32_t word = sb[e][0] | (sb[e][1] << 8);
+        word |= __shfl_down_sync(0xffffffffu, word, 1) << 16;  // two groups: the four scales of a word
         if (c + e >= C) continue;
-        const RowPlace at(cols.q, cols.s, c + e, Rp);
-        *reinterpret_cast<uint4*>(at.code_at(b)) = make_uint4(codes[e][0].x, codes[e][0].y, codes[e][1].x, codes[e][1].y);
-        if ((group & 1) == 0) *reinterpret_cast<uint32_t*>(at.scale_at(b)) = word;
+        const uint32_t in = ((uint32_t)c0 & 64u) + 2 * pair + e;
+        *reinterpret_cast<uint4*>(q + unit_codes(in, group)) = make_uint4(codes[e][0].x, codes[e][0].y, codes[e][1].x, codes[e][1].y);
+        if ((group & 1) == 0) *reinterpret_cast<uint32_t*>(s + unit_scales(in, group)) = word;
     }
 }
 
@@ -440,9 +441,9 @@ cudaError_t quantize(const T* x, int64_t R, int64_t C, int64_t ld, const moe_nvf
                      const moe_nvfp4_operand* cols, bool given, unsigned* maxima, cudaStream_t st, bool pdl) {
     bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
     if (!cols) {
-        const int64_t blocks = pad_to(C, 256) / 16;
-        int tpr_log = 5;  // the fewest threads that hold a row in two blocks each
-        while ((1 << tpr_log) < kThreads && (2 << tpr_log) < blocks) ++tpr_log;
+        const int64_t units = pad_to(C, 256) / 32;
+        int tpr_log = 5;  // the fewest threads that hold a row, 32 elements each
+        while ((1 << tpr_log) < kThreads && (1 << tpr_log) < units) ++tpr_log;
         const int64_t per = kThreads >> tpr_log, grid = (R + per - 1) / per;
         bool gr = rows->gs_rows != 0;
         uint8_t *q = rows->q, *s = rows->s;

@@ -12,6 +12,18 @@ import torch
 
 from . import binding as B
 
+# Calls at decode sizes cost the host more than the GPU: the functions below test with few attribute reads and call the
+# library's functions directly (binding.py's wrappers would convert every tensor again).
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        _lib = B.load()
+    return _lib
+
+
 _DTYPES = {torch.float32: B.MOE_F32, torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_F16}
 _SCORES = {"sigmoid": B.MOE_SCORE_SIGMOID, "softmax": B.MOE_SCORE_SOFTMAX}
 _GROUP_SCORES = {"max": B.MOE_GROUP_MAX, "top2": B.MOE_GROUP_TOP2}
@@ -72,7 +84,10 @@ def route_logits(x: torch.Tensor, W_r: torch.Tensor, b: Optional[torch.Tensor] =
     if b is not None:
         _plain(b, (E,), torch.float32, x, "b")
     logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
-    B.moe_route_logits(x, W_r, b, T, d, E, logits)
+    status = _library().moe_route_logits(x.data_ptr(), W_r.data_ptr(), None if b is None else b.data_ptr(), T, d, E,
+                                         logits.data_ptr(), B._current_stream())
+    if status:
+        raise B.MoeError("moe_route_logits", status)
     return logits
 
 
@@ -82,17 +97,23 @@ def route_scores(logits: torch.Tensor, k: int, rule: B.moe_route_rule, bias: Opt
     """ids int32 [T, k] (ascending) and weights fp32 [T, k] of logits [T, E] under `rule`; `bias` fp32 [E] takes part in the
     choice only.  Logits of -inf take an expert out of service.  scores fp32 [T, E] and counts int32 [E], when given, receive
     all the scores and the picks per expert."""
-    ld, code = _matrix(logits, "logits"), _dtype(logits, "logits")
+    ld = _matrix(logits, "logits")
+    code = _dtype(logits, "logits")
     T, E = logits.shape
+    dev = logits.device
     if bias is not None:
         _plain(bias, (E,), torch.float32, logits, "bias")
     if scores is not None:
         _plain(scores, (T, E), torch.float32, logits, "scores")
     if counts is not None:
         _plain(counts, (E,), torch.int32, logits, "counts")
-    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    B.moe_route_scores(logits, code, ld, bias, T, E, k, rule, ids, w, scores, counts)
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    status = _library().moe_route_scores(logits.data_ptr(), code, ld, None if bias is None else bias.data_ptr(), T, E, k, rule,
+                                         ids.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr(),
+                                         None if counts is None else counts.data_ptr(), B._current_stream())
+    if status:
+        raise B.MoeError("moe_route_scores", status)
     return ids, w
 
 
@@ -109,7 +130,11 @@ def route_scores_backward(logits: torch.Tensor, ids: torch.Tensor, dw: torch.Ten
     if dscores is not None:
         _plain(dscores, (T, E), torch.float32, logits, "dscores")
     dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    B.moe_route_scores_backward(logits, code, ld, T, E, k, rule, ids, dw, dscores, dlogits, E)
+    status = _library().moe_route_scores_backward(logits.data_ptr(), code, ld, T, E, k, rule, ids.data_ptr(), dw.data_ptr(),
+                                                  None if dscores is None else dscores.data_ptr(), dlogits.data_ptr(), E,
+                                                  B._current_stream())
+    if status:
+        raise B.MoeError("moe_route_scores_backward", status)
     return dlogits
 
 
@@ -130,7 +155,11 @@ def combine_backward(dy: torch.Tensor, y_perm: Optional[torch.Tensor], inv_pos: 
     dw = torch.empty((T, k), dtype=torch.float32, device=dy.device) if need_dw else None
     dy_perm = torch.empty((T * k, d), dtype=torch.bfloat16, device=dy.device) if need_dy_perm else None
     if need_dw or need_dy_perm:
-        B.moe_combine_backward(dy, y_perm if need_dw else None, inv_pos, w, T, k, d, dw, dy_perm)
+        status = _library().moe_combine_backward(dy.data_ptr(), y_perm.data_ptr() if need_dw else None, inv_pos.data_ptr(),
+                                                 w.data_ptr(), T, k, d, None if dw is None else dw.data_ptr(),
+                                                 None if dy_perm is None else dy_perm.data_ptr(), B._current_stream())
+        if status:
+            raise B.MoeError("moe_combine_backward", status)
     return dw, dy_perm
 
 
@@ -149,6 +178,7 @@ class Nvfp4Operand:
         _need(gs.numel() in (1, rows), "gs: one scale per row, or one")
         _plain(gs, (gs.numel(),), torch.float32, q, "gs")
         self.rows, self.K, self.q, self.s, self.gs = rows, K, q, s, gs
+        self.device = q.get_device()
         self.struct = B.moe_nvfp4_operand(q.data_ptr(), s.data_ptr(), gs.data_ptr(), int(gs.numel() == rows))
 
     def values(self) -> torch.Tensor:
@@ -176,8 +206,18 @@ def nvfp4_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
 
 
 def _on(op: Nvfp4Operand, rows: int, K: int, t: torch.Tensor, what: str) -> None:
-    _need((op.rows, op.K) == (rows, K), "%s: an operand [%d, %d] expected, got [%d, %d]" % (what, rows, K, op.rows, op.K))
-    _need(op.q.get_device() == t.get_device(), "%s: on %s, the others on %s" % (what, op.q.device, t.device))
+    if op.rows != rows or op.K != K or op.device != t.get_device():
+        raise ValueError("%s: an operand [%d, %d] on %s expected, got [%d, %d] on %s" % (what, rows, K, t.device, op.rows, op.K,
+                                                                                        op.q.device))
+
+
+def _output(out: torch.Tensor, M: int, N: int, like: torch.Tensor) -> int:
+    _need(out.shape == (M, N) and out.get_device() == like.get_device(), "out: [%d, %d] on %s expected" % (M, N, like.device))
+    return _matrix(out, "out")
+
+
+def _space(ws: Optional[torch.Tensor]) -> tuple:
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
 
 
 def nvfp4_quantize(x: torch.Tensor, rows: Optional[Nvfp4Operand] = None, cols: Optional[Nvfp4Operand] = None,
@@ -191,18 +231,28 @@ def nvfp4_quantize(x: torch.Tensor, rows: Optional[Nvfp4Operand] = None, cols: O
         _on(rows, R, C, x, "rows")
     if cols is not None:
         _on(cols, C, R, x, "cols")
-    B.moe_nvfp4_quantize(x, code, R, C, ld, None if rows is None else rows.struct, None if cols is None else cols.struct,
-                         scales_given, workspace)
+    status = _library().moe_nvfp4_quantize(x.data_ptr(), code, R, C, ld, None if rows is None else rows.struct,
+                                           None if cols is None else cols.struct, int(scales_given),
+                                           *_space(workspace), B._current_stream())
+    if status:
+        raise B.MoeError("moe_nvfp4_quantize", status)
 
 
 def nvfp4_matmul(a: Nvfp4Operand, b: Nvfp4Operand, dtype: torch.dtype, workspace: torch.Tensor,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """a [M, K] times b [N, K] transposed: [M, N] of dtype (into `out` when given)."""
-    _on(b, b.rows, a.K, a.q, "b")
+    M, N = a.rows, b.rows
+    _on(b, N, a.K, a.q, "b")
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.q.device)
-    _need(out.shape == (a.rows, b.rows) and out.dtype == dtype and out.get_device() == a.q.get_device(), "out: [M, N] of dtype expected")
-    B.moe_nvfp4_matmul(a.struct, b.struct, a.rows, b.rows, a.K, out, _dtype(out, "out"), _matrix(out, "out"), workspace)
+        out = torch.empty((M, N), dtype=dtype, device=a.q.device)
+        ld = N
+    else:
+        ld = _output(out, M, N, a.q)
+        _need(out.dtype == dtype, "out: %s expected" % (dtype,))
+    status = _library().moe_nvfp4_matmul(a.struct, b.struct, M, N, a.K, out.data_ptr(), _dtype(out, "out"), ld,
+                                         *_space(workspace), B._current_stream())
+    if status:
+        raise B.MoeError("moe_nvfp4_matmul", status)
     return out
 
 
@@ -210,9 +260,14 @@ def nvfp4_linear(x: torch.Tensor, W: Nvfp4Operand, workspace: torch.Tensor, out:
     """x [M, K] times W [N, K] transposed, x quantised row by row: [M, N] of x's type (or of `out`'s)."""
     ld, code = _matrix(x, "x"), _dtype(x, "x")
     M, K = x.shape
-    _on(W, W.rows, K, x, "W")
+    N = W.rows
+    _on(W, N, K, x, "W")
     if out is None:
-        out = torch.empty((M, W.rows), dtype=x.dtype, device=x.device)
-    _need(out.shape == (M, W.rows) and out.get_device() == x.get_device(), "out: [M, N] expected")
-    B.moe_nvfp4_linear(x, code, M, K, ld, W.struct, W.rows, out, _dtype(out, "out"), _matrix(out, "out"), workspace)
+        out, ldy, ycode = torch.empty((M, N), dtype=x.dtype, device=x.device), N, code
+    else:
+        ldy, ycode = _output(out, M, N, x), _dtype(out, "out")
+    status = _library().moe_nvfp4_linear(x.data_ptr(), code, M, K, ld, W.struct, N, out.data_ptr(), ycode, ldy,
+                                         *_space(workspace), B._current_stream())
+    if status:
+        raise B.MoeError("moe_nvfp4_linear", status)
     return out

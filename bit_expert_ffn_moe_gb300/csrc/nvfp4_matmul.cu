@@ -13,8 +13,8 @@
 //           and each weight byte is read once.  Bound by the weight read; the K range of a tile is split
 //           over the CTAs of a cluster, whose partial sums are exchanged through distributed shared
 //           memory and added in rank order.
-//   square  128 activation rows x 256 weight rows per tile, persistent CTAs; bound by the FP4 rate and the
-//           shared-memory feed.
+//   pair    more rows: 256 x 256 tiles by pairs of CTAs, persistent; bound by the shared-memory feed and the
+//           FP4 rate.
 // Every barrier wait is bounded: on expiry the CTA records MOE_ERR_TIMEOUT, waits (bounded) for its own
 // copies and MMAs, frees tensor memory and exits.
 #include "ops.cuh"
@@ -275,113 +275,220 @@ __global__ void __launch_bounds__(kRowsThreads, 1) nvfp4_rows_matmul_kernel(cons
     }
 }
 
-// ------------------------------------------------------------------ square kernel
-constexpr int kSqStages = 4;
-constexpr int kSqEpiWarps = 8;
-constexpr int kSqThreads = 64 + 32 * kSqEpiWarps;
-constexpr int kSqStageBytes = 3 * kTile + 12 * kAtom;
-constexpr int kSqSfCols = 48;
-constexpr uint32_t kSqSfBase = 256;  // scale columns after the accumulator
-constexpr size_t kSqSmem = (size_t)kSqStages * kSqStageBytes + 512 * kSqEpiWarps + 1024 + 256;
-static_assert(kSqStageBytes % 1024 == 0 && kSqSfBase + kSqStages * kSqSfCols <= kTmemCols, "stage alignment, tensor memory");
-static_assert(kSqSmem <= 232448, "shared memory");
+// ------------------------------------------------------------------ pair kernel
+// Two CTAs (a cluster, two neighbouring SMs) share one 256 x 256 tile (cta_group::2): CTA r holds the tile's A rows
+// 128 r .. and B rows 128 r .. in shared memory and A rows' results (128 lanes x 256 columns) in its tensor
+// memory; the leader (rank 0) issues the MMAs of both.  Each CTA thus copies 32 KB of codes per K step for
+// 128 x 256 results instead of 48 KB.  The scales of all 256 B rows go to both CTAs' tensor memory.
+//   warp 0     copies this CTA's operands; its copies complete on its own `full` barrier
+//   warp 1     rank 0: waits for its own stage and for the peer's arrival, issues scale copies and MMAs, whose
+//              commit frees the stage in both CTAs; rank 1: forwards its full stages to the leader
+//   warps 2-9  epilogue: two warps per lane quarter, each half of the columns; registers first, so that the next
+//              tile's MMAs run while these values are scaled and stored
+constexpr int kPairStages = 5;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kPairStageBytes = 2 * kTile + 12 * kAtom;  // A, B, A's scales, both halves of B's scales
+constexpr int kPairSfCols = 48;
+constexpr uint32_t kPairSfBase = 256;  // scale columns after the accumulator
+constexpr size_t kPairSmem = (size_t)kPairStages * kPairStageBytes + 512 * kPairEpiWarps + 1024 + 256;
+static_assert(kPairStageBytes % 1024 == 0 && kPairSfBase + kPairStages * kPairSfCols <= kTmemCols, "stage alignment, tensor memory");
+static_assert(kPairSmem <= 232448, "shared memory");
+
+// As stage_scales_nv_to_tmem / stage_mmas_nv_commit (tcgen05.cuh) for a CTA pair: the copies run in both CTAs, the
+// commit arrives on the barrier at this offset in both.
+__device__ __forceinline__ void pair_scales_to_tmem(uint32_t sf, uint64_t a, uint64_t b0, uint64_t b1) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%2], %3;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%4], %5;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%6], %7;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%8], %9;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%10], %11;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%12], %13;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%14], %15;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%16], %17;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%18], %19;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%20], %21;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%22], %23;\n\t}" ::"r"(sf),
+        "l"(a), "r"(sf + 4), "l"(a + 32), "r"(sf + 8), "l"(a + 64), "r"(sf + 12), "l"(a + 96), "r"(sf + 16), "l"(b0),
+        "r"(sf + 20), "l"(b1), "r"(sf + 24), "l"(b0 + 32), "r"(sf + 28), "l"(b1 + 32), "r"(sf + 32), "l"(b0 + 64),
+        "r"(sf + 36), "l"(b1 + 64), "r"(sf + 40), "l"(b0 + 96), "r"(sf + 44), "l"(b1 + 96)
+        : "memory");
+}
+__device__ __forceinline__ void pair_mmas_commit(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sf,
+                                                 uint32_t accumulate, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t.reg .b16 both;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "mov.b16 both, 3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 q, %4, %4;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %7, %8, %3, [%9], [%10], q;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %11, %12, %3, [%13], [%14], q;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %15, %16, %3, [%17], [%18], q;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%19], both;\n\t}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(sf), "r"(sf + 16), "l"(ad + 2), "l"(bd + 2), "r"(sf + 4), "r"(sf + 24),
+        "l"(ad + 4), "l"(bd + 4), "r"(sf + 8), "r"(sf + 32), "l"(ad + 6), "l"(bd + 6), "r"(sf + 12), "r"(sf + 40),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b16 both;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "mov.b16 both, 3;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+// Arrive on the barrier at this offset in CTA 0 of the cluster.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %0, 0;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+// mbar_wait_warp for a barrier that the peer CTA arrives on: acquires at cluster scope.
+__device__ __forceinline__ bool cluster_try_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool cluster_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+    bool ok = cluster_try_wait(bar, parity);
+    const long long t0 = clock64();
+    while (!ok) {
+        if (*abort_flag) break;
+        if ((ok = cluster_try_wait(bar, parity))) break;
+        if (clock64() - t0 > kWaitCycles) {
+            set_status(status, MOE_ERR_TIMEOUT);
+            *abort_flag = 1;
+            break;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
 
 template <typename T>
-__global__ void __launch_bounds__(kSqThreads, 1)
-    nvfp4_square_matmul_kernel(const __grid_constant__ MatmulArgs args, const int MT, const int NT) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    nvfp4_pair_matmul_kernel(const __grid_constant__ MatmulArgs args, const int MT, const int NT) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    float* gb_smem = reinterpret_cast<float*>(smem + kSqStages * kSqStageBytes);  // [epilogue warp][128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(gb_smem + 128 * kSqEpiWarps);
-    uint64_t* empty = full + kSqStages;
-    uint64_t* acc_full = empty + kSqStages;
-    uint64_t* acc_empty = acc_full + 1;
+    float* gb_smem = reinterpret_cast<float*>(smem + kPairStages * kPairStageBytes);  // [epilogue warp][128]
+    uint64_t* full = reinterpret_cast<uint64_t*>(gb_smem + 128 * kPairEpiWarps);      // this CTA's copies (rank 0: and the peer)
+    uint64_t* empty = full + kPairStages;
+    uint64_t* acc_full = empty + kPairStages;
+    uint64_t* acc_empty = acc_full + 1;  // rank 0: the epilogue warps of both CTAs
     uint64_t* mma_done = acc_empty + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kSqStages; ++s) {
-            mbar_init(&full[s], 1);
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&full[s], rank == 0 ? 2 : 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
-        mbar_init(acc_empty, kSqEpiWarps);
+        mbar_init(acc_empty, 2 * kPairEpiWarps);
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(kTmemCols)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // both CTAs' barriers and tensor memory are ready
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
 
-    const int n_tiles = MT * NT, KT = args.KT;
-    const int64_t last_b = (args.N + 127) / 128 - 1;  // last 128-row block of B
-    auto stage = [&](int s) { return smem + (size_t)s * kSqStageBytes; };
+    const int n_tiles = MT * NT, KT = args.KT, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const int64_t last_a = (args.M + 127) / 128 - 1, last_b = (args.N + 127) / 128 - 1;  // last 128-row blocks
+    auto stage = [&](int s) { return smem + (size_t)s * kPairStageBytes; };
 
     if (warp == 0) {
         if (lane == 0) {
             int it = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-                const int64_t mb = t / NT, b0 = 2 * (int64_t)(t % NT), b1 = min(b0 + 1, last_b);
+            for (int t = first; t < n_tiles && ok; t += step) {
+                const int64_t ab = min(2 * (int64_t)(t / NT) + rank, last_a), b0 = 2 * (int64_t)(t % NT), b1 = min(b0 + 1, last_b);
+                const size_t ka = (size_t)ab * KT, kb0 = (size_t)b0 * KT, kb1 = (size_t)b1 * KT, kb = rank == 0 ? kb0 : kb1;
                 for (int kt = 0; kt < KT; ++kt, ++it) {
-                    const int s = it % kSqStages;
-                    if (!mbar_wait(&empty[s], ((it / kSqStages) & 1) ^ 1, abort_flag, args.status)) {
+                    const int s = it % kPairStages;
+                    if (!mbar_wait(&empty[s], ((it / kPairStages) & 1) ^ 1, abort_flag, args.status)) {
                         ok = false;
                         break;
                     }
                     unsigned char* p = stage(s);
-                    const size_t ka = (size_t)mb * KT + kt, kb0 = (size_t)b0 * KT + kt, kb1 = (size_t)b1 * KT + kt;
-                    mbar_arrive_expect_tx(&full[s], kSqStageBytes);
-                    bulk_load(p, args.qa + ka * kTile, kTile, &full[s]);
-                    bulk_load(p + kTile, args.qb + kb0 * kTile, kTile, &full[s]);
-                    bulk_load(p + 2 * kTile, args.qb + kb1 * kTile, kTile, &full[s]);
-                    bulk_load(p + 3 * kTile, args.sa + ka * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
-                    bulk_load(p + 3 * kTile + 4 * kAtom, args.sb + kb0 * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
-                    bulk_load(p + 3 * kTile + 8 * kAtom, args.sb + kb1 * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
+                    mbar_arrive_expect_tx(&full[s], kPairStageBytes);
+                    bulk_load(p, args.qa + (ka + kt) * kTile, kTile, &full[s]);
+                    bulk_load(p + kTile, args.qb + (kb + kt) * kTile, kTile, &full[s]);
+                    bulk_load(p + 2 * kTile, args.sa + (ka + kt) * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
+                    bulk_load(p + 2 * kTile + 4 * kAtom, args.sb + (kb0 + kt) * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
+                    bulk_load(p + 2 * kTile + 8 * kAtom, args.sb + (kb1 + kt) * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
                 }
             }
+            // Copies still in flight land before the CTA's shared memory goes: after the last commit every stage has
+            // been consumed; when aborting, the outstanding ones are given a bounded time (rank 0's barriers also
+            // count the peer, whose stages may never come: the wait then just runs out).
             if (*abort_flag) {
                 volatile int never = 0;
-                for (int i = max(0, it - kSqStages); i < it; ++i)
-                    mbar_wait(&full[i % kSqStages], (i / kSqStages) & 1, &never, nullptr, 100000000LL);
+                for (int i = max(0, it - kPairStages); i < it; ++i)
+                    mbar_wait(&full[i % kPairStages], (i / kPairStages) & 1, &never, nullptr, 100000000LL);
             }
         }
-    } else if (warp == 1) {
-        const uint32_t idesc = idesc_mxf4nvf4_ue4m3(128, 256);
+    } else if (warp == 1 && rank == 0) {
+        const uint32_t idesc = idesc_mxf4nvf4_ue4m3(256, 256);
         int it = 0, tile = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x, ++tile) {
-            if (!mbar_wait_warp(acc_empty, (tile & 1) ^ 1, abort_flag, args.status)) break;
+        for (int t = first; t < n_tiles && ok; t += step, ++tile) {
+            if (!cluster_wait_warp(acc_empty, (tile & 1) ^ 1, abort_flag, args.status)) break;
             tc_fence_after();
             for (int kt = 0; kt < KT; ++kt, ++it) {
-                const int s = it % kSqStages;
-                if (!mbar_wait_warp(&full[s], (it / kSqStages) & 1, abort_flag, args.status)) {
+                const int s = it % kPairStages;
+                if (!cluster_wait_warp(&full[s], (it / kPairStages) & 1, abort_flag, args.status)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 unsigned char* p = stage(s);
-                const uint32_t sf = tmem + kSqSfBase + s * kSqSfCols;
-                stage_scales_nv_to_tmem(sf, desc_sf(p + 3 * kTile), desc_sf(p + 3 * kTile + 4 * kAtom),
-                                        desc_sf(p + 3 * kTile + 8 * kAtom));
-                stage_mmas_nv_commit(tmem, desc_sw128(p), desc_sw128(p + kTile), idesc, sf, kt > 0 ? 1u : 0u, &empty[s]);
+                const uint32_t sf = tmem + kPairSfBase + s * kPairSfCols;
+                pair_scales_to_tmem(sf, desc_sf(p + 2 * kTile), desc_sf(p + 2 * kTile + 4 * kAtom), desc_sf(p + 2 * kTile + 8 * kAtom));
+                pair_mmas_commit(tmem, desc_sw128(p), desc_sw128(p + kTile), idesc, sf, kt > 0 ? 1u : 0u, &empty[s]);
             }
             if (!ok) break;
-            tc_commit(acc_full);
+            pair_commit(acc_full);
         }
-        tc_commit(mma_done);
-        volatile int never = 0;
-        mbar_wait_warp(mma_done, 0, &never, nullptr, 100000000LL);
+        pair_commit(mma_done);
+    } else if (warp == 1) {
+        int it = 0;
+        bool ok = true;
+        for (int t = first; t < n_tiles && ok; t += step)
+            for (int kt = 0; kt < KT; ++kt, ++it) {
+                const int s = it % kPairStages;
+                if (!mbar_wait_warp(&full[s], (it / kPairStages) & 1, abort_flag, args.status)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) arrive_leader(&full[s]);
+                __syncwarp();
+            }
     } else {
         const int q = warp & 3, half = (warp - 2) / 4;
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
@@ -389,11 +496,11 @@ __global__ void __launch_bounds__(kSqThreads, 1)
         float* gb = gb_smem + 128 * (warp - 2);
         T* y = static_cast<T*>(args.y);
         int tile = 0;
-        for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, ++tile) {
-            const int64_t m0 = (int64_t)(t / NT) * 128 + 32 * q, n0 = (int64_t)(t % NT) * 256 + 128 * half;
+        for (int t = first; t < n_tiles; t += step, ++tile) {
+            const int64_t m0 = (int64_t)(t / NT) * 256 + 128 * rank + 32 * q, n0 = (int64_t)(t % NT) * 256 + 128 * half;
             const int64_t m = m0 + lane;
             const float ga = m < args.M ? args.ga[args.ga_rows ? m : 0] : 0.f;
-            const int live = (int)min((int64_t)128, args.N - n0);  // columns of this warp's half (may be negative)
+            const int live = (int)max((int64_t)0, min((int64_t)128, args.N - n0));  // columns of this warp's half
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 if (32 * c + lane < live) gb[32 * c + lane] = args.gb[args.gb_rows ? n0 + 32 * c + lane : 0];
@@ -406,11 +513,11 @@ __global__ void __launch_bounds__(kSqThreads, 1)
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty);
+            if (lane == 0) arrive_leader(acc_empty);
             // 16-byte pieces transposed inside groups of four lanes: a store writes 64 contiguous bytes of 8 rows
             const int64_t r0 = m0 + 4 * (lane >> 2);
             T* out = y + r0 * args.ldy + n0 + (lane & 3) * (16 / (int)sizeof(T));
-            const int rows = (int)min((int64_t)4, args.M - r0);
+            const int rows = (int)max((int64_t)0, min((int64_t)4, args.M - r0));
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 if (32 * c >= live) break;
@@ -443,11 +550,18 @@ __global__ void __launch_bounds__(kSqThreads, 1)
             __syncwarp();  // gb is rewritten for the next tile
         }
     }
+    __syncwarp();
+    {
+        // every MMA and scale copy has completed: the leader commits mma_done last, aborting or not
+        volatile int never = 0;
+        mbar_wait(mma_done, 0, &never, nullptr);
+    }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();  // neither CTA's shared or tensor memory goes while the other may use it
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
 }
 
@@ -497,15 +611,13 @@ cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_oper
     if (M <= 32) return launch_rows<32>(a, st, pdl);
     if (M <= 64) return launch_rows<64>(a, st, pdl);
     if (M <= 128) return launch_rows<128>(a, st, pdl);
-    int MT = (int)((M + 127) / 128), NT = (int)((N + 255) / 256);
-    const int64_t tiles = (int64_t)MT * NT;
-    const int sms = sm_count();
+    int MT = (int)((M + 255) / 256), NT = (int)((N + 255) / 256);
+    const int64_t tiles = (int64_t)MT * NT, pairs = sm_count() / 2;
     void* args[] = {&a, &MT, &NT};
-    const void* f = dtype == MOE_F32    ? (const void*)nvfp4_square_matmul_kernel<float>
-                    : dtype == MOE_BF16 ? (const void*)nvfp4_square_matmul_kernel<__nv_bfloat16>
-                                        : (const void*)nvfp4_square_matmul_kernel<__half>;
-    return launch_kernel(f, dim3((unsigned)(tiles < sms ? tiles : sms)), dim3(kSqThreads), kSqSmem,
-                         st, pdl, args);
+    const void* f = dtype == MOE_F32    ? (const void*)nvfp4_pair_matmul_kernel<float>
+                    : dtype == MOE_BF16 ? (const void*)nvfp4_pair_matmul_kernel<__nv_bfloat16>
+                                        : (const void*)nvfp4_pair_matmul_kernel<__half>;
+    return launch_kernel(f, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPairThreads), kPairSmem, st, pdl, args);
 }
 
 }  // namespace moe

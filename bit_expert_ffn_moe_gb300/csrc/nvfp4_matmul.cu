@@ -349,36 +349,9 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\t"
         "mapa.shared::cluster.u32 a, %0, 0;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
-// mbar_wait_warp for a barrier that the peer CTA arrives on: acquires at cluster scope.
-__device__ __forceinline__ bool cluster_try_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool cluster_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-    bool ok = cluster_try_wait(bar, parity);
-    const long long t0 = clock64();
-    while (!ok) {
-        if (*abort_flag) break;
-        if ((ok = cluster_try_wait(bar, parity))) break;
-        if (clock64() - t0 > kWaitCycles) {
-            set_status(status, MOE_ERR_TIMEOUT);
-            *abort_flag = 1;
-            break;
-        }
-    }
-    return __all_sync(0xffffffffu, ok);
-}
-
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     nvfp4_pair_matmul_kernel(const __grid_constant__ MatmulArgs args, const int MT, const int NT) {
@@ -458,11 +431,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         int it = 0, tile = 0;
         bool ok = true;
         for (int t = first; t < n_tiles && ok; t += step, ++tile) {
-            if (!cluster_wait_warp(acc_empty, (tile & 1) ^ 1, abort_flag, args.status)) break;
+            if (!mbar_wait_warp(acc_empty, (tile & 1) ^ 1, abort_flag, args.status)) break;
             tc_fence_after();
             for (int kt = 0; kt < KT; ++kt, ++it) {
                 const int s = it % kPairStages;
-                if (!cluster_wait_warp(&full[s], (it / kPairStages) & 1, abort_flag, args.status)) {
+                if (!mbar_wait_warp(&full[s], (it / kPairStages) & 1, abort_flag, args.status)) {
                     ok = false;
                     break;
                 }

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 // Maxima of |x| over rows and columns as fp32 bits in row_max[R] and col_max[C] (zeroed before).  A warp takes
 // 32 rows of 16 bytes per lane; the 8 warps of a CTA 256 rows of the same columns.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     nvfp4_maxima_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld, bool wide, int col_tiles,
                         unsigned* __restrict__ row_max, unsigned* __restrict__ col_max) {
     constexpr int kPer = 16 / (int)sizeof(T), kWarpCols = 32 * kPer;
@@ -312,127 +312,139 @@ __global__ void __launch_bounds__(kThreads)
     atomicMax(col_max + col0 + threadIdx.x, m);
 }
 
-// A tile of 256 x 64 elements of x in shared memory, encoded along its rows (a thread: 4 blocks) and along its
+// Tiles of 256 x 64 elements of x in shared memory, encoded along their rows (a thread: 2 units) and along their
 // columns (a thread: 2 columns x 32 rows; eight lanes hold the 256 rows of a column and write its 128 bytes of
 // codes).  The 16-byte pieces of a row are rotated by its group of 32 rows, so that lanes reading 8 groups x 4
 // words meet all banks.  Tiles cover the padded contractions (256 multiples), whose padding is written as zeros.
+// Persistent CTAs: the next tile is fetched (cp.async, a second buffer) while this one is encoded.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 3 : 4)
-    nvfp4_both_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld, bool wide, int col_tiles,
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 3)
+    nvfp4_both_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld, bool wide, int col_tiles, int n_tiles,
                       const unsigned* __restrict__ row_max, const unsigned* __restrict__ col_max,
                       const __grid_constant__ moe_nvfp4_operand rows, const __grid_constant__ moe_nvfp4_operand cols, bool given) {
-    extern __shared__ __align__(16) unsigned char tile[];
+    extern __shared__ __align__(16) unsigned char tiles[];  // two buffers
     __shared__ RowScale row_scales[kTileR], col_scales[kTileC];
     constexpr int kPitch = kTileC * (int)sizeof(T), kPer = 16 / (int)sizeof(T), kPieces = kTileC / kPer, kTurn = kPieces / 8;
-    const int64_t r0 = (int64_t)(blockIdx.x / col_tiles) * kTileR, c0 = (int64_t)(blockIdx.x % col_tiles) * kTileC;
     const int64_t Cp = pad_to(C, 256), Rp = pad_to(R, 256);
-    auto piece_at = [&](int rr, int pc) { return tile + rr * kPitch + ((pc + kTurn * (rr >> 5)) & (kPieces - 1)) * 16; };
-#pragma unroll 8
-    for (int i = threadIdx.x; i < kTileR * kPieces; i += kThreads) {
-        const int rr = i / kPieces, pc = i % kPieces;
-        const int64_t r = r0 + rr, c = c0 + pc * kPer;
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (r < R && c < C) {
+    auto place = [&](int rr, int pc) { return rr * kPitch + ((pc + kTurn * (rr >> 5)) & (kPieces - 1)) * 16; };
+    // fetch tile t into a buffer, and this thread's row and column scale (or maximum) of it into registers
+    float row_v = 0.f, col_v = 0.f;
+    auto fetch = [&](int t, unsigned char* to) {
+        const int64_t r0 = (int64_t)(t / col_tiles) * kTileR, c0 = (int64_t)(t % col_tiles) * kTileC;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < kTileR * kPieces; i += kThreads) {
+            const int rr = i / kPieces, pc = i % kPieces;
+            const int64_t r = r0 + rr, c = c0 + pc * kPer;
             const T* p = x + r * ld + c;
-            if (wide && c + kPer <= C) {
-                u = __ldg(reinterpret_cast<const uint4*>(p));
+            unsigned char* q = to + place(rr, pc);
+            if (r < R && wide && c + kPer <= C) {
+                cp_async16(q, p);
             } else {
                 __align__(16) T e[kPer];
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) e[j] = c + j < C ? p[j] : T(0.f);
-                u = *reinterpret_cast<const uint4*>(e);
+                for (int j = 0; j < kPer; ++j) e[j] = r < R && c + j < C ? p[j] : T(0.f);
+                *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(e);
             }
         }
-        *reinterpret_cast<uint4*>(piece_at(rr, pc)) = u;
-    }
-    if (rows.q) {
-        const int64_t r = r0 + threadIdx.x;
-        RowScale rs = {1.f, 0.f};
-        if (r < R) {
-            rs = with_reciprocal(given ? rows.gs[rows.gs_rows ? r : 0] : row_scale(__ldg(row_max + r)));
-            if (!given && c0 == 0) rows.gs[r] = rs.g;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const int64_t r = r0 + threadIdx.x, c = c0 + threadIdx.x;
+        if (rows.q && r < R) row_v = given ? rows.gs[rows.gs_rows ? r : 0] : __uint_as_float(__ldg(row_max + r));
+        if (threadIdx.x < kTileC && c < C) col_v = given ? cols.gs[cols.gs_rows ? c : 0] : __uint_as_float(__ldg(col_max + c));
+    };
+    fetch(blockIdx.x, tiles);
+    int buf = 0;
+    for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, buf ^= 1) {
+        const int64_t r0 = (int64_t)(t / col_tiles) * kTileR, c0 = (int64_t)(t % col_tiles) * kTileC;
+        unsigned char* tile = tiles + buf * (kTileR * kPitch);
+        auto piece_at = [&](int rr, int pc) { return tile + place(rr, pc); };
+        if (rows.q) {
+            const RowScale rs = with_reciprocal(given ? row_v : row_scale(__float_as_uint(row_v)));
+            row_scales[threadIdx.x] = rs;
+            if (!given && c0 == 0 && r0 + threadIdx.x < R) rows.gs[r0 + threadIdx.x] = rs.g;
         }
-        row_scales[threadIdx.x] = rs;
-    }
-    if (threadIdx.x < kTileC) {
-        const int64_t c = c0 + threadIdx.x;
-        RowScale rs = {1.f, 0.f};
-        if (c < C) {
-            rs = with_reciprocal(given ? cols.gs[cols.gs_rows ? c : 0] : row_scale(__ldg(col_max + c)));
-            if (!given && r0 == 0) cols.gs[c] = rs.g;
+        if (threadIdx.x < kTileC) {
+            const RowScale rs = with_reciprocal(given ? col_v : row_scale(__float_as_uint(col_v)));
+            col_scales[threadIdx.x] = rs;
+            if (!given && r0 == 0 && c0 + threadIdx.x < C) cols.gs[c0 + threadIdx.x] = rs.g;
         }
-        col_scales[threadIdx.x] = rs;
-    }
-    __syncthreads();
-    if (rows.q) {
-        // thread: row threadIdx / 2 (+ 128), unit threadIdx % 2 of the tile's 64 columns
-        const uint32_t in = threadIdx.x >> 1, u = threadIdx.x & 1;
-        const int64_t units = Cp / 32;
-        uint8_t* q = rows.q + (r0 >> 7) * units * 2048 + unit_codes(in, (uint32_t)(c0 >> 5) & 7u | u) + (c0 >> 8) * 16384;
-        uint8_t* s = rows.s + (r0 >> 7) * units * 256 + unit_scales(in, u) + (c0 >> 6) * 512;
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i, q += units * 2048, s += units * 256) {
-            const int rr = 128 * i + in;
-            Block<T> a, b;
-            constexpr int kBlockPieces = Block<T>::kWords / 4;
-#pragma unroll
-            for (int j = 0; j < kBlockPieces; ++j) {
-                const uint4 x0 = *reinterpret_cast<const uint4*>(piece_at(rr, 2 * u * kBlockPieces + j));
-                const uint4 x1 = *reinterpret_cast<const uint4*>(piece_at(rr, (2 * u + 1) * kBlockPieces + j));
-                a.w[4 * j] = x0.x, a.w[4 * j + 1] = x0.y, a.w[4 * j + 2] = x0.z, a.w[4 * j + 3] = x0.w;
-                b.w[4 * j] = x1.x, b.w[4 * j + 1] = x1.y, b.w[4 * j + 2] = x1.z, b.w[4 * j + 3] = x1.w;
-            }
-            encode_unit(a, b, block_mag(a), block_mag(b), row_scales[rr], given, q, s, r0 + rr < R);
-        }
-    }
-    // lane: group of 32 rows (lane % 8) and column pair (lane / 8 of the warp's four)
-    const int group = threadIdx.x & 7, pair = threadIdx.x >> 3;
-    const int64_t c = c0 + 2 * pair;
-    const unsigned char* column = piece_at(32 * group, 2 * pair / kPer) + (2 * pair % kPer) * (int)sizeof(T);
-    uint2 codes[2][2];
-    uint32_t sb[2][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float v[2][16];
-        uint32_t m[2] = {0u, 0u};
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const float2 f = *reinterpret_cast<const float2*>(column + (16 * h + j) * kPitch);
-                v[0][j] = f.x, v[1][j] = f.y;
-                m[0] = mag_max<T>(m[0], __float_as_uint(f.x));
-                m[1] = mag_max<T>(m[1], __float_as_uint(f.y));
-            }
+        if (t + (int)gridDim.x < n_tiles) {
+            fetch(t + gridDim.x, tiles + (buf ^ 1) * (kTileR * kPitch));
+            cp_async_wait_group<1>();
         } else {
-            uint32_t both = 0u;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(column + (16 * h + j) * kPitch);
-                both = mag_max<T>(both, w);
-                if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                    v[0][j] = __uint_as_float(w << 16), v[1][j] = __uint_as_float(w & 0xffff0000u);
-                } else {
-                    const float2 f = h2_to_f2(w);
-                    v[0][j] = f.x, v[1][j] = f.y;
-                }
-            }
-            m[0] = mag_f32<T>(both & 0xffffu), m[1] = mag_f32<T>(both & 0xffff0000u);
+            cp_async_wait_group<0>();
         }
+        __syncthreads();
+        if (rows.q) {
+            // thread: row threadIdx / 2 (+ 128), unit threadIdx % 2 of the tile's 64 columns
+            const uint32_t in = threadIdx.x >> 1, u = threadIdx.x & 1;
+            const int64_t units = Cp / 32;
+            uint8_t* q = rows.q + (r0 >> 7) * units * 2048 + unit_codes(in, (uint32_t)(c0 >> 5) & 7u | u) + (c0 >> 8) * 16384;
+            uint8_t* s = rows.s + (r0 >> 7) * units * 256 + unit_scales(in, u) + (c0 >> 6) * 512;
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i, q += units * 2048, s += units * 256) {
+                const int rr = 128 * i + in;
+                Block<T> a, b;
+                constexpr int kBlockPieces = Block<T>::kWords / 4;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            sb[e][h] = encode_block<T>(v[e], __uint_as_float(m[e]), col_scales[2 * pair + e], given, codes[e][h]);
-    }
-    // the tile's 64 columns lie in one 128-row block of the column operand, its 256 rows in one code tile
-    uint8_t* q = cols.q + ((c0 >> 7) * (Rp >> 8) + (r0 >> 8)) * 16384;
-    uint8_t* s = cols.s + ((c0 >> 7) * (Rp >> 6) + (r0 >> 6)) * 512;
+                for (int j = 0; j < kBlockPieces; ++j) {
+                    const uint4 x0 = *reinterpret_cast<const uint4*>(piece_at(rr, 2 * u * kBlockPieces + j));
+                    const uint4 x1 = *reinterpret_cast<const uint4*>(piece_at(rr, (2 * u + 1) * kBlockPieces + j));
+                    a.w[4 * j] = x0.x, a.w[4 * j + 1] = x0.y, a.w[4 * j + 2] = x0.z, a.w[4 * j + 3] = x0.w;
+                    b.w[4 * j] = x1.x, b.w[4 * j + 1] = x1.y, b.w[4 * j + 2] = x1.z, b.w[4 * j + 3] = x1.w;
+                }
+                encode_unit(a, b, block_mag(a), block_mag(b), row_scales[rr], given, q, s, r0 + rr < R);
+            }
+        }
+        // lane: group of 32 rows (lane % 8) and column pair (lane / 8 of the warp's four)
+        const int group = threadIdx.x & 7, pair = threadIdx.x >> 3;
+        const int64_t c = c0 + 2 * pair;
+        const unsigned char* column = piece_at(32 * group, 2 * pair / kPer) + (2 * pair % kPer) * (int)sizeof(T);
+        uint2 codes[2][2];
+        uint32_t sb[2][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        uint32_t word = sb[e][0] | (sb[e][1] << 8);
-        word |= __shfl_down_sync(0xffffffffu, word, 1) << 16;  // two groups: the four scales of a word
-        if (c + e >= C) continue;
-        const uint32_t in = ((uint32_t)c0 & 64u) + 2 * pair + e;
-        *reinterpret_cast<uint4*>(q + unit_codes(in, group)) = make_uint4(codes[e][0].x, codes[e][0].y, codes[e][1].x, codes[e][1].y);
-        if ((group & 1) == 0) *reinterpret_cast<uint32_t*>(s + unit_scales(in, group)) = word;
+        for (int h = 0; h < 2; ++h) {
+            float v[2][16];
+            uint32_t m[2] = {0u, 0u};
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float2 f = *reinterpret_cast<const float2*>(column + (16 * h + j) * kPitch);
+                    v[0][j] = f.x, v[1][j] = f.y;
+                    m[0] = mag_max<T>(m[0], __float_as_uint(f.x));
+                    m[1] = mag_max<T>(m[1], __float_as_uint(f.y));
+                }
+            } else {
+                uint32_t both = 0u;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(column + (16 * h + j) * kPitch);
+                    both = mag_max<T>(both, w);
+                    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                        v[0][j] = __uint_as_float(w << 16), v[1][j] = __uint_as_float(w & 0xffff0000u);
+                    } else {
+                        const float2 f = h2_to_f2(w);
+                        v[0][j] = f.x, v[1][j] = f.y;
+                    }
+                }
+                m[0] = mag_f32<T>(both & 0xffffu), m[1] = mag_f32<T>(both & 0xffff0000u);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                sb[e][h] = encode_block<T>(v[e], __uint_as_float(m[e]), col_scales[2 * pair + e], given, codes[e][h]);
+        }
+        // the tile's 64 columns lie in one 128-row block of the column operand, its 256 rows in one code tile
+        uint8_t* q = cols.q + ((c0 >> 7) * (Rp >> 8) + (r0 >> 8)) * 16384;
+        uint8_t* s = cols.s + ((c0 >> 7) * (Rp >> 6) + (r0 >> 6)) * 512;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            uint32_t word = sb[e][0] | (sb[e][1] << 8);
+            word |= __shfl_down_sync(0xffffffffu, word, 1) << 16;  // two groups: the four scales of a word
+            if (c + e >= C) continue;
+            const uint32_t in = ((uint32_t)c0 & 64u) + 2 * pair + e;
+            *reinterpret_cast<uint4*>(q + unit_codes(in, group)) = make_uint4(codes[e][0].x, codes[e][0].y, codes[e][1].x, codes[e][1].y);
+            if ((group & 1) == 0) *reinterpret_cast<uint32_t*>(s + unit_scales(in, group)) = word;
+        }
+        __syncthreads();  // the buffer and the scales are free
     }
 }
 
@@ -467,9 +479,11 @@ cudaError_t quantize(const T* x, int64_t R, int64_t C, int64_t ld, const moe_nvf
     int ct = (int)(pad_to(C, rows ? 256 : kTileC) / kTileC);
     const int64_t rt = pad_to(R, 256) / kTileR;
     moe_nvfp4_operand a = rows ? *rows : moe_nvfp4_operand{nullptr, nullptr, nullptr, 0}, b = *cols;
-    void* args[] = {&x, &R, &C, &ld, &wide, &ct, &row_max, &col_max, &a, &b, &given};
-    return launch_kernel((const void*)nvfp4_both_kernel<T>, dim3((unsigned)(ct * rt)), dim3(kThreads),
-                         (size_t)kTileR * kTileC * sizeof(T), st, false, args);
+    int n_tiles = (int)(ct * rt);
+    const int resident = sm_count() * (sizeof(T) == 4 ? 1 : 3);
+    void* args[] = {&x, &R, &C, &ld, &wide, &ct, &n_tiles, &row_max, &col_max, &a, &b, &given};
+    return launch_kernel((const void*)nvfp4_both_kernel<T>, dim3((unsigned)(n_tiles < resident ? n_tiles : resident)), dim3(kThreads),
+                         (size_t)2 * kTileR * kTileC * sizeof(T), st, false, args);
 }
 
 // Values of an operand: (E2M1 * E4M3) * row scale, the exact product of the first two rounded once.

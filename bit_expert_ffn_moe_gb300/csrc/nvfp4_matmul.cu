@@ -45,12 +45,6 @@ struct MatmulArgs {
     int* status;
 };
 
-__device__ __forceinline__ void store_one(void* y, int dtype, int64_t at, float v) {
-    if (dtype == MOE_F32) static_cast<float*>(y)[at] = v;
-    else if (dtype == MOE_BF16) static_cast<uint16_t*>(y)[at] = f32_to_bf16_bits(v);
-    else static_cast<__half*>(y)[at] = __float2half_rn(v);
-}
-
 template <typename T>
 __device__ __forceinline__ T out_value(float v);
 template <>
@@ -131,17 +125,23 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ float ld_cluster_f32(const void* p, uint32_t rank) {
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+// Four floats at the place of p in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ float4 ld_peer_f4(const void* p, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(smem_u32(p)), "r"(rank)
+        : "memory");
     return v;
 }
 
 // Grid: x = weight tile * splits + rank (a cluster of `splits` CTAs per tile), y = tile of NT activation rows.
-template <int NT>
-__global__ void __launch_bounds__(kRowsThreads, 1) nvfp4_rows_matmul_kernel(const MatmulArgs args, int splits) {
+template <int NT, typename T>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+    nvfp4_rows_matmul_kernel(const __grid_constant__ MatmulArgs args, const int splits) {
     constexpr int kStages = rows_stages<NT>(), kStageBytes = rows_stage_bytes<NT>();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -234,37 +234,61 @@ __global__ void __launch_bounds__(kRowsThreads, 1) nvfp4_rows_matmul_kernel(cons
     tc_fence_after();
     __syncthreads();  // and no copy is in flight: every stage was consumed (or drained when aborting)
 
-    const int64_t n = nt * 128 + 32 * (warp & 3) + lane;
-    const bool owner = warp >= 2;
-    float* part = reinterpret_cast<float*>(smem);  // [NT][128] partial sums, on the stages
-    const float gb = owner && n < args.N ? args.gb[args.gb_rows ? n : 0] : 0.f;
-    auto store = [&](int64_t m, float acc) {
-        if (m < args.M && n < args.N) store_one(args.y, args.dtype, m * args.ldy + n, acc * args.ga[args.ga_rows ? m : 0] * gb);
-    };
-    if (owner) {
+    // Results go through shared memory, [activation row][128 weight rows], on the stages; activation row c of the tile is
+    // then summed over the cluster's CTAs, in rank order, scaled and stored by a warp of CTA c % splits.
+    float* part = reinterpret_cast<float*>(smem);
+    const int rows = (int)min((int64_t)NT, args.M - m0);
+    if (warp >= 2) {
         const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-#pragma unroll
-        for (int c = 0; c < NT; c += 8) {
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 8) {
             uint32_t v[8];
             asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                          : "r"(acc + c));
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (splits > 1) part[(c + i) * 128 + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
-                else store(m0 + c + i, __uint_as_float(v[i]));
-            }
+            for (int i = 0; i < 8; ++i) part[(c + i) * 128 + 32 * (warp & 3) + lane] = __uint_as_float(v[i]);
+        }
+    }
+    __syncwarp();
+    if (splits > 1) cluster_sync();
+    else __syncthreads();
+    const int64_t n = nt * 128 + 4 * lane;  // this lane's four weight rows
+    const int live = (int)max((int64_t)0, min((int64_t)4, args.N - n));
+    float gb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gb[i] = i < live ? args.gb[args.gb_rows ? n + i : 0] : 0.f;
+    const bool wide = reinterpret_cast<uintptr_t>(args.y) % 16 == 0 && args.ldy % 4 == 0;
+    constexpr int kWarps = kRowsThreads / 32;
+    const int c0 = rank + splits * warp;
+    float ga_lane = 0.f;  // lane i: the scale of this warp's i-th row (at most 22)
+    if (c0 + splits * kWarps * lane < rows) ga_lane = args.ga[args.ga_rows ? m0 + c0 + splits * kWarps * lane : 0];
+#pragma unroll 2
+    for (int i = 0; i < (NT + kWarps - 1) / kWarps; ++i) {
+        const int c = c0 + splits * kWarps * i;
+        const float ga = __shfl_sync(0xffffffffu, ga_lane, i);
+        if (c >= rows) break;
+        const float* p = part + c * 128 + 4 * lane;
+        float4 v = splits > 1 ? ld_peer_f4(p, 0) : *reinterpret_cast<const float4*>(p);
+        for (int r = 1; r < splits; ++r) {
+            const float4 o = ld_peer_f4(p, r);
+            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        }
+        const float f[4] = {v.x * ga * gb[0], v.y * ga * gb[1], v.z * ga * gb[2], v.w * ga * gb[3]};
+        T* y = static_cast<T*>(args.y) + (m0 + c) * args.ldy + n;
+        if (wide && live == 4) {
+            __align__(16) T o[4] = {out_value<T>(f[0]), out_value<T>(f[1]), out_value<T>(f[2]), out_value<T>(f[3])};
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(o);
+            else *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < live) y[j] = out_value<T>(f[j]);
         }
     }
     if (splits > 1) {
-        cluster_sync();
-        if (owner)
-            for (int c = rank; c < NT && m0 + c < args.M; c += splits) {  // this CTA's share of the activation rows
-                float sum = 0.f;
-                for (int r = 0; r < splits; ++r) sum += ld_cluster_f32(&part[c * 128 + 32 * (warp & 3) + lane], r);
-                store(m0 + c, sum);
-            }
+        __syncwarp();
         cluster_sync();  // the partial sums stay until every CTA has read them
     }
     tc_fence_before();
@@ -545,7 +569,9 @@ cudaError_t launch_rows(const MatmulArgs& a, cudaStream_t st, bool pdl) {
     // split K while the tiles leave SMs idle and every CTA keeps at least two K steps
     int splits = 1;
     while (splits < 8 && wt * mt * splits * 2 <= sm_count() && a.KT / (splits * 2) >= 2) splits *= 2;
-    const void* f = (const void*)nvfp4_rows_matmul_kernel<NT>;
+    const void* f = a.dtype == MOE_F32    ? (const void*)nvfp4_rows_matmul_kernel<NT, float>
+                    : a.dtype == MOE_BF16 ? (const void*)nvfp4_rows_matmul_kernel<NT, __nv_bfloat16>
+                                          : (const void*)nvfp4_rows_matmul_kernel<NT, __half>;
     cudaError_t e = ensure_dyn_smem(f, rows_smem<NT>());
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -583,7 +609,10 @@ cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_oper
     if (M <= 16) return launch_rows<16>(a, st, pdl);
     if (M <= 32) return launch_rows<32>(a, st, pdl);
     if (M <= 64) return launch_rows<64>(a, st, pdl);
-    if (M <= 128) return launch_rows<128>(a, st, pdl);
+    // Beyond 128 rows the pair kernel's tiles are few and large: with half the SMs or fewer in reach of 128 x 128 tiles, tiles
+    // with their K range split over a cluster finish sooner, unless there is little K to split (us, pair / rows: 256 x 4096
+    // x 8192 17.6 / 13.0, 512 x 4096 x 8192 18.0 / 18.1, 512 x 8192 x 1024 8.4 / 17.5, 1024^3 8.2 / 9.1).
+    if (M <= 128 || (((M + 127) / 128) * ((N + 127) / 128) * 2 <= sm_count() && a.KT >= 8)) return launch_rows<128>(a, st, pdl);
     int MT = (int)((M + 255) / 256), NT = (int)((N + 255) / 256);
     const int64_t tiles = (int64_t)MT * NT, pairs = sm_count() / 2;
     void* args[] = {&a, &MT, &NT};

@@ -315,7 +315,8 @@ constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
 constexpr int kPairStageBytes = 2 * kTile + 12 * kAtom;  // A, B, A's scales, both halves of B's scales
 constexpr int kPairSfCols = 48;
 constexpr uint32_t kPairSfBase = 256;  // scale columns after the accumulator
-constexpr size_t kPairSmem = (size_t)kPairStages * kPairStageBytes + 512 * kPairEpiWarps + 1024 + 256;
+constexpr int kTurnWords = 32 * 17;  // a warp's 32 rows of 64 bytes, one word of padding each
+constexpr size_t kPairSmem = (size_t)kPairStages * kPairStageBytes + (512 + 4 * kTurnWords) * kPairEpiWarps + 1024 + 256;
 static_assert(kPairStageBytes % 1024 == 0 && kPairSfBase + kPairStages * kPairSfCols <= kTmemCols, "stage alignment, tensor memory");
 static_assert(kPairSmem <= 232448, "shared memory");
 
@@ -382,7 +383,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* gb_smem = reinterpret_cast<float*>(smem + kPairStages * kPairStageBytes);  // [epilogue warp][128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(gb_smem + 128 * kPairEpiWarps);      // this CTA's copies (rank 0: and the peer)
+    uint32_t* turn_smem = reinterpret_cast<uint32_t*>(gb_smem + 128 * kPairEpiWarps);  // [epilogue warp][32][17]
+    uint64_t* full = reinterpret_cast<uint64_t*>(turn_smem + kTurnWords * kPairEpiWarps);  // this CTA's copies (rank 0: and the peer)
     uint64_t* empty = full + kPairStages;
     uint64_t* acc_full = empty + kPairStages;
     uint64_t* acc_empty = acc_full + 1;  // rank 0: the epilogue warps of both CTAs
@@ -491,6 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
         const bool wide = reinterpret_cast<uintptr_t>(args.y) % 16 == 0 && (args.ldy * (int64_t)sizeof(T)) % 16 == 0;
         float* gb = gb_smem + 128 * (warp - 2);
+        uint32_t* turn = turn_smem + kTurnWords * (warp - 2);
         T* y = static_cast<T*>(args.y);
         int tile = 0;
         for (int t = first; t < n_tiles; t += step, ++tile) {
@@ -538,10 +541,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         for (int j = 0; j < 4; ++j)
                             if (j < rows) *reinterpret_cast<uint4*>(out + j * args.ldy + 32 * c + (32 / kHalves) * h) = pc[j];
                     }
-                } else if (m < args.M) {
+                } else {
+                    // rows that do not start on 16 bytes, or the ragged last columns: 64 bytes of each of the warp's 32 rows
+                    // through shared memory, then stored row by row, a word per lane
+                    constexpr int kHalves = (int)sizeof(T) / 2, kPerWord = 4 / (int)sizeof(T);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * c + i < live) y[m * args.ldy + n0 + 32 * c + i] = out_value<T>(__uint_as_float(v[c][i]));
+                    for (int h = 0; h < kHalves; ++h) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const uint4 o = out_piece<T>(&v[c][(32 / kHalves) * h + (16 / (int)sizeof(T)) * p]);
+                            uint32_t* to = turn + 17 * lane + 4 * p;
+                            to[0] = o.x, to[1] = o.y, to[2] = o.z, to[3] = o.w;
+                        }
+                        __syncwarp();
+                        const int col = 32 * c + (32 / kHalves) * h + kPerWord * (lane & 15), left = live - col;
+                        T* at = y + (m0 + (lane >> 4)) * args.ldy + n0 + col;
+#pragma unroll 4
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t w = turn[17 * (2 * i + (lane >> 4)) + (lane & 15)];
+                            if (m0 + 2 * i + (lane >> 4) < args.M && left > 0) {
+                                T* to = at + 2 * i * args.ldy;
+                                if (sizeof(T) == 4 || (left > 1 && reinterpret_cast<uintptr_t>(to) % 4 == 0)) {
+                                    *reinterpret_cast<uint32_t*>(to) = w;
+                                } else {
+                                    reinterpret_cast<uint16_t*>(to)[0] = (uint16_t)w;
+                                    if (left > 1) reinterpret_cast<uint16_t*>(to)[1] = (uint16_t)(w >> 16);
+                                }
+                            }
+                        }
+                        __syncwarp();
+                    }
                 }
             }
             __syncwarp();  // gb is rewritten for the next tile
@@ -609,10 +638,11 @@ cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_oper
     if (M <= 16) return launch_rows<16>(a, st, pdl);
     if (M <= 32) return launch_rows<32>(a, st, pdl);
     if (M <= 64) return launch_rows<64>(a, st, pdl);
-    // Beyond 128 rows the pair kernel's tiles are few and large: with half the SMs or fewer in reach of 128 x 128 tiles, tiles
-    // with their K range split over a cluster finish sooner, unless there is little K to split (us, pair / rows: 256 x 4096
-    // x 8192 17.6 / 13.0, 512 x 4096 x 8192 18.0 / 18.1, 512 x 8192 x 1024 8.4 / 17.5, 1024^3 8.2 / 9.1).
-    if (M <= 128 || (((M + 127) / 128) * ((N + 127) / 128) * 2 <= sm_count() && a.KT >= 8)) return launch_rows<128>(a, st, pdl);
+    // Beyond 128 rows the pair kernel's tiles are few and large: while 128 x 128 tiles leave half the SMs idle, these, with their
+    // K range split over a cluster, finish sooner (us, pair / rows: 256 x 4096 x 8192 17.6 / 12.1, 777 x 1000 x 1544 9.5 / 8.9,
+    // 200 x 600 x 300 8.7 / 7.3, 1024^3 7.9 / 8.0; without half the SMs idle, 512 x 4096 x 8192 17.8 / 18.1, 512 x 8192 x 1024
+    // 8.4 / 17.5).
+    if (M <= 128 || ((M + 127) / 128) * ((N + 127) / 128) * 2 <= sm_count()) return launch_rows<128>(a, st, pdl);
     int MT = (int)((M + 255) / 256), NT = (int)((N + 255) / 256);
     const int64_t tiles = (int64_t)MT * NT, pairs = sm_count() / 2;
     void* args[] = {&a, &MT, &NT};

@@ -168,7 +168,9 @@ def operand(rows, K, seed, dtype="fp32"):
 
 SHAPES = [(1, 128, 256), (1, 4096, 8192), (3, 200, 300), (8, 1000, 2048), (9, 128, 16), (16, 8192, 4096), (17, 640, 1),
           (33, 264, 4096), (64, 512, 2000), (65, 1000, 1544), (128, 128, 8192), (100, 4100, 512), (129, 257, 256),
-          (300, 1000, 1544), (256, 256, 512), (777, 1000, 1544), (1000, 130, 4096), (2048, 2048, 2048)]
+          (300, 1000, 1544), (256, 256, 512), (777, 1000, 1544), (1000, 130, 4096), (2048, 2048, 2048),
+          # CTA pairs: ragged last tiles, rows that start on 2 and 4 bytes, a short K, an odd last 128-row block on either side
+          (1500, 1501, 300), (2100, 1100, 520), (1153, 2305, 16), (1300, 1298, 4096), (2944, 1152, 256)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
@@ -177,10 +179,11 @@ def test_products(M, N, K, dtype):
     check_product(operand(M, K, M + K), operand(N, K, N), dtype)
 
 
-@pytest.mark.parametrize("M", [1, 7, 16, 31, 64, 128, 130, 512])
-def test_exact_sums_come_out_exact(M):
+@pytest.mark.parametrize("M,N", [(1, 384), (7, 384), (16, 384), (31, 384), (64, 384), (128, 384), (130, 384), (512, 384), (1400, 1600),
+                                 (2050, 1111)])
+def test_exact_sums_come_out_exact(M, N):
     """Codes of whole numbers under scales of one: every partial sum is a small whole number."""
-    N, K = 384, 1024
+    K = 1024
     g = torch.Generator(device="cuda").manual_seed(M)
     vals = torch.tensor([0., 1, 2, 3, 4, 6, -1, -2, -3, -4, -6], device="cuda")
     x = vals[torch.randint(0, 11, (M, K), generator=g, device="cuda")]
@@ -196,7 +199,7 @@ def test_exact_sums_come_out_exact(M):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("M", [1, 5, 40, 200])
+@pytest.mark.parametrize("M", [1, 5, 40, 200, 2500])
 def test_linear_is_quantise_then_product(M, dtype):
     N, K = 520, 1100
     W = operand(N, K, 9)
@@ -225,7 +228,7 @@ def test_a_tokens_result_does_not_depend_on_its_batch():
 
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_outputs_with_row_strides(dtype):
-    for M, N, K, ld in ((4, 200, 256, 333), (200, 300, 256, 304), (200, 300, 512, 301)):
+    for M, N, K, ld in ((4, 200, 256, 333), (200, 300, 256, 304), (200, 300, 512, 301), (1300, 1400, 256, 1404), (1300, 1399, 256, 1401)):
         room = torch.full((M, ld), 7.0, dtype=TYPES[dtype], device="cuda")
         y = check_product(operand(M, K, 1), operand(N, K, 2), dtype, room[:, :N])
         assert y.data_ptr() == room.data_ptr() and (room[:, N:] == 7.0).all()

@@ -1,7 +1,7 @@
 """Routing rules, their gradients and dense NVFP4 products on torch tensors.
 
-Each function checks its tensors, allocates its results and makes one call of the library (binding.py); the work is the
-library's kernels, on torch's current stream.  None of them synchronises.
+Each function checks its tensors, allocates its results and makes one call of the library, in an extension module; the work is
+the library's kernels, on torch's current stream.  None of them synchronises.
 """
 from __future__ import annotations
 
@@ -10,56 +10,33 @@ from typing import Optional, Tuple
 
 import torch
 
+from . import _build
 from . import binding as B
 
-# Calls at decode sizes cost the host more than the GPU: the functions below test with few attribute reads and call the
-# library's functions directly (binding.py's wrappers would convert every tensor again).
-_lib = None
-
-
-def _library():
-    global _lib
-    if _lib is None:
-        _lib = B.load()
-    return _lib
-
-
-_DTYPES = {torch.float32: B.MOE_F32, torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_F16}
 _SCORES = {"sigmoid": B.MOE_SCORE_SIGMOID, "softmax": B.MOE_SCORE_SOFTMAX}
 _GROUP_SCORES = {"max": B.MOE_GROUP_MAX, "top2": B.MOE_GROUP_TOP2}
+_SCALAR_TYPES = {torch.float32: 6, torch.float16: 5, torch.bfloat16: 15}  # torch's own numbers of these types
+
+_module = None
 
 
-def _dtype(t: torch.Tensor, what: str) -> int:
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError("%s: fp32, bf16 or fp16 expected, got %s" % (what, t.dtype))
-    return code
+def _calls():
+    """The extension module (csrc/torch_ops.cpp), which checks the tensors, allocates the results and calls the library."""
+    global _module
+    if _module is None:
+        import importlib.util
+        B.load()  # builds both when needed
+        spec = importlib.util.spec_from_file_location("moe_torch_ops", _build.TORCH_OPS)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(B.MoeError)
+        _module = module
+    return _module
 
 
 def _need(cond: bool, what: str) -> None:
     if not cond:
         raise ValueError(what)
-
-
-def _matrix(t: torch.Tensor, what: str) -> int:
-    """Row stride of a 2-D CUDA tensor whose rows are contiguous and do not overlap."""
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError("%s: a CUDA matrix expected" % what)
-    rows, cols = t.shape
-    ld, step = t.stride()
-    if cols > 1 and step != 1:
-        raise ValueError("%s: contiguous rows expected" % what)
-    if rows <= 1:
-        return cols
-    if ld < cols:
-        raise ValueError("%s: rows may not overlap" % what)
-    return ld
-
-
-def _plain(t: torch.Tensor, shape: tuple, dtype: torch.dtype, like: torch.Tensor, what: str) -> None:
-    """A contiguous tensor of this shape and type on `like`'s device."""
-    if t.shape != shape or t.dtype != dtype or t.get_device() != like.get_device() or not t.is_contiguous():
-        raise ValueError("%s: contiguous %s of %s on %s expected" % (what, shape, dtype, like.device))
 
 
 # ------------------------------------------------------------------ routing rules
@@ -79,15 +56,13 @@ def route_logits(x: torch.Tensor, W_r: torch.Tensor, b: Optional[torch.Tensor] =
     """fp32 router logits [T, E] of bf16 x [T, d] and fp32 W_r [E, d] in the layer's fixed order, b added."""
     _need(x.dim() == 2 and x.is_cuda and x.dtype == torch.bfloat16 and x.is_contiguous(), "x: contiguous bf16 [T, d] expected")
     T, d = x.shape
+    _need(W_r.dim() == 2 and W_r.shape[1] == d and W_r.dtype == torch.float32 and W_r.device == x.device and W_r.is_contiguous(),
+          "W_r: contiguous fp32 [E, d] expected")
     E = W_r.shape[0]
-    _plain(W_r, (E, d), torch.float32, x, "W_r")
-    if b is not None:
-        _plain(b, (E,), torch.float32, x, "b")
+    _need(b is None or (b.shape == (E,) and b.dtype == torch.float32 and b.device == x.device and b.is_contiguous()),
+          "b: contiguous fp32 [E] expected")
     logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
-    status = _library().moe_route_logits(x.data_ptr(), W_r.data_ptr(), None if b is None else b.data_ptr(), T, d, E,
-                                         logits.data_ptr(), B._current_stream())
-    if status:
-        raise B.MoeError("moe_route_logits", status)
+    B.moe_route_logits(x, W_r, b, T, d, E, logits)
     return logits
 
 
@@ -97,45 +72,14 @@ def route_scores(logits: torch.Tensor, k: int, rule: B.moe_route_rule, bias: Opt
     """ids int32 [T, k] (ascending) and weights fp32 [T, k] of logits [T, E] under `rule`; `bias` fp32 [E] takes part in the
     choice only.  Logits of -inf take an expert out of service.  scores fp32 [T, E] and counts int32 [E], when given, receive
     all the scores and the picks per expert."""
-    ld = _matrix(logits, "logits")
-    code = _dtype(logits, "logits")
-    T, E = logits.shape
-    dev = logits.device
-    if bias is not None:
-        _plain(bias, (E,), torch.float32, logits, "bias")
-    if scores is not None:
-        _plain(scores, (T, E), torch.float32, logits, "scores")
-    if counts is not None:
-        _plain(counts, (E,), torch.int32, logits, "counts")
-    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
-    w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    status = _library().moe_route_scores(logits.data_ptr(), code, ld, None if bias is None else bias.data_ptr(), T, E, k, rule,
-                                         ids.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr(),
-                                         None if counts is None else counts.data_ptr(), B._current_stream())
-    if status:
-        raise B.MoeError("moe_route_scores", status)
-    return ids, w
+    return (_module or _calls()).route_scores(logits, k, rule, bias, scores, counts)
 
 
 def route_scores_backward(logits: torch.Tensor, ids: torch.Tensor, dw: torch.Tensor, rule: B.moe_route_rule,
                           dscores: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of the logits (their type) from that of the weights, dw fp32 [T, k], and of the scores, dscores fp32 [T, E];
     the choice `ids` is held fixed."""
-    ld, code = _matrix(logits, "logits"), _dtype(logits, "logits")
-    T, E = logits.shape
-    _need(ids.dim() == 2, "ids: [T, k] expected")
-    k = ids.shape[1]
-    _plain(ids, (T, k), torch.int32, logits, "ids")
-    _plain(dw, (T, k), torch.float32, logits, "dw")
-    if dscores is not None:
-        _plain(dscores, (T, E), torch.float32, logits, "dscores")
-    dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    status = _library().moe_route_scores_backward(logits.data_ptr(), code, ld, T, E, k, rule, ids.data_ptr(), dw.data_ptr(),
-                                                  None if dscores is None else dscores.data_ptr(), dlogits.data_ptr(), E,
-                                                  B._current_stream())
-    if status:
-        raise B.MoeError("moe_route_scores_backward", status)
-    return dlogits
+    return (_module or _calls()).route_scores_backward(logits, ids, dw, rule, dscores)
 
 
 def combine_backward(dy: torch.Tensor, y_perm: Optional[torch.Tensor], inv_pos: torch.Tensor, w: torch.Tensor,
@@ -143,24 +87,7 @@ def combine_backward(dy: torch.Tensor, y_perm: Optional[torch.Tensor], inv_pos: 
                      ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
     """Gradients of the weighted sum y[t] = sum_j w[t, j] y_perm[inv_pos[t k + j]]: dw fp32 [T, k] and dy_perm bf16 [T k, d]
     (None where not needed) from dy bf16 [T, d]."""
-    _need(dy.dim() == 2 and dy.is_cuda and dy.dtype == torch.bfloat16 and dy.is_contiguous(), "dy: contiguous bf16 [T, d] expected")
-    _need(w.dim() == 2, "w: [T, k] expected")
-    T, d = dy.shape
-    k = w.shape[1]
-    _plain(w, (T, k), torch.float32, dy, "w")
-    _plain(inv_pos, (T * k,), torch.int32, dy, "inv_pos")
-    if need_dw:
-        _need(y_perm is not None, "y_perm: needed for dw")
-        _plain(y_perm, (T * k, d), torch.bfloat16, dy, "y_perm")
-    dw = torch.empty((T, k), dtype=torch.float32, device=dy.device) if need_dw else None
-    dy_perm = torch.empty((T * k, d), dtype=torch.bfloat16, device=dy.device) if need_dy_perm else None
-    if need_dw or need_dy_perm:
-        status = _library().moe_combine_backward(dy.data_ptr(), y_perm.data_ptr() if need_dw else None, inv_pos.data_ptr(),
-                                                 w.data_ptr(), T, k, d, None if dw is None else dw.data_ptr(),
-                                                 None if dy_perm is None else dy_perm.data_ptr(), B._current_stream())
-        if status:
-            raise B.MoeError("moe_combine_backward", status)
-    return dw, dy_perm
+    return (_module or _calls()).combine_backward(dy, y_perm, inv_pos, w, need_dw, need_dy_perm)
 
 
 # ------------------------------------------------------------------ dense NVFP4 products
@@ -172,11 +99,10 @@ class Nvfp4Operand:
     def __init__(self, rows: int, K: int, q: torch.Tensor, s: torch.Tensor, gs: torch.Tensor):
         nq, ns = B.moe_nvfp4_operand_codes(rows, K), B.moe_nvfp4_operand_scales(rows, K)
         _need(rows >= 0 and K >= 1 and (nq > 0 or rows == 0), "unsupported operand shape [%d, %d]" % (rows, K))
-        _plain(q, (nq,), torch.uint8, q, "q")
-        _plain(s, (ns,), torch.uint8, q, "s")
-        _need(q.is_cuda, "q: a CUDA tensor expected")
+        for t, n, dtype, what in ((q, nq, torch.uint8, "q"), (s, ns, torch.uint8, "s"), (gs, gs.numel(), torch.float32, "gs")):
+            _need(t.is_cuda and t.shape == (n,) and t.dtype == dtype and t.device == q.device and t.is_contiguous(),
+                  "%s: contiguous CUDA %s [%d] expected" % (what, dtype, n))
         _need(gs.numel() in (1, rows), "gs: one scale per row, or one")
-        _plain(gs, (gs.numel(),), torch.float32, q, "gs")
         self.rows, self.K, self.q, self.s, self.gs = rows, K, q, s, gs
         self.device = q.get_device()
         self.struct = B.moe_nvfp4_operand(q.data_ptr(), s.data_ptr(), gs.data_ptr(), int(gs.numel() == rows))
@@ -205,69 +131,24 @@ def nvfp4_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
     return ws
 
 
-def _on(op: Nvfp4Operand, rows: int, K: int, t: torch.Tensor, what: str) -> None:
-    if op.rows != rows or op.K != K or op.device != t.get_device():
-        raise ValueError("%s: an operand [%d, %d] on %s expected, got [%d, %d] on %s" % (what, rows, K, t.device, op.rows, op.K,
-                                                                                        op.q.device))
-
-
-def _output(out: torch.Tensor, M: int, N: int, like: torch.Tensor) -> int:
-    _need(out.shape == (M, N) and out.get_device() == like.get_device(), "out: [%d, %d] on %s expected" % (M, N, like.device))
-    return _matrix(out, "out")
-
-
-def _space(ws: Optional[torch.Tensor]) -> tuple:
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
-
-
 def nvfp4_quantize(x: torch.Tensor, rows: Optional[Nvfp4Operand] = None, cols: Optional[Nvfp4Operand] = None,
                    workspace: Optional[torch.Tensor] = None, scales_given: bool = False) -> None:
     """Operands of x [R, C]: `rows` [R, C] receives that of x, `cols` [C, R] that of its transpose; both from one call when both are
     given.  The row scales are computed from the rows, or taken from the operands (scales_given)."""
-    ld, code = _matrix(x, "x"), _dtype(x, "x")
-    R, C = x.shape
-    _need(rows is not None or cols is not None, "rows or cols: an operand to fill")
-    if rows is not None:
-        _on(rows, R, C, x, "rows")
-    if cols is not None:
-        _on(cols, C, R, x, "cols")
-    status = _library().moe_nvfp4_quantize(x.data_ptr(), code, R, C, ld, None if rows is None else rows.struct,
-                                           None if cols is None else cols.struct, int(scales_given),
-                                           *_space(workspace), B._current_stream())
-    if status:
-        raise B.MoeError("moe_nvfp4_quantize", status)
+    r = (None, 0, 0, 0) if rows is None else (rows.struct, rows.rows, rows.K, rows.device)
+    c = (None, 0, 0, 0) if cols is None else (cols.struct, cols.rows, cols.K, cols.device)
+    (_module or _calls()).nvfp4_quantize(x, *r, *c, workspace, scales_given)
 
 
 def nvfp4_matmul(a: Nvfp4Operand, b: Nvfp4Operand, dtype: torch.dtype, workspace: torch.Tensor,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """a [M, K] times b [N, K] transposed: [M, N] of dtype (into `out` when given)."""
-    M, N = a.rows, b.rows
-    _on(b, N, a.K, a.q, "b")
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=a.q.device)
-        ld = N
-    else:
-        ld = _output(out, M, N, a.q)
-        _need(out.dtype == dtype, "out: %s expected" % (dtype,))
-    status = _library().moe_nvfp4_matmul(a.struct, b.struct, M, N, a.K, out.data_ptr(), _dtype(out, "out"), ld,
-                                         *_space(workspace), B._current_stream())
-    if status:
-        raise B.MoeError("moe_nvfp4_matmul", status)
-    return out
+    code = _SCALAR_TYPES.get(dtype)
+    if code is None:
+        raise TypeError("fp32, bf16 or fp16 expected, got %s" % (dtype,))
+    return (_module or _calls()).nvfp4_matmul(a.struct, a.rows, a.K, a.device, b.struct, b.rows, b.K, b.device, a.q, code, workspace, out)
 
 
 def nvfp4_linear(x: torch.Tensor, W: Nvfp4Operand, workspace: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [M, K] times W [N, K] transposed, x quantised row by row: [M, N] of x's type (or of `out`'s)."""
-    ld, code = _matrix(x, "x"), _dtype(x, "x")
-    M, K = x.shape
-    N = W.rows
-    _on(W, N, K, x, "W")
-    if out is None:
-        out, ldy, ycode = torch.empty((M, N), dtype=x.dtype, device=x.device), N, code
-    else:
-        ldy, ycode = _output(out, M, N, x), _dtype(out, "out")
-    status = _library().moe_nvfp4_linear(x.data_ptr(), code, M, K, ld, W.struct, N, out.data_ptr(), ycode, ldy,
-                                         *_space(workspace), B._current_stream())
-    if status:
-        raise B.MoeError("moe_nvfp4_linear", status)
-    return out
+    return (_module or _calls()).nvfp4_linear(x, W.struct, W.rows, W.K, W.device, workspace, out)

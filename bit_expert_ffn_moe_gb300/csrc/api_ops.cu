@@ -203,9 +203,10 @@ moe_status moe_nvfp4_linear(const void* x, moe_dtype x_dtype, int64_t M, int64_t
         const moe_nvfp4_operand A = {reinterpret_cast<uint8_t*>(base + L.q), reinterpret_cast<uint8_t*>(base + L.s),
                                      reinterpret_cast<float*>(base + L.gs), 1};
         cudaStream_t st = (cudaStream_t)stream;
+        int* status = &static_cast<Ctrl*>(ws)->status;
         cudaError_t e = launch_nvfp4_quantize(x, x_dtype, M, K, ldx, &A, nullptr, false, nullptr, st, false);
         if (e != cudaSuccess) return e;
-        return launch_nvfp4_matmul(&A, W, M, N, K, y, y_dtype, ldy, &static_cast<Ctrl*>(ws)->status, st, true);
+        return launch_nvfp4_matmul(&A, W, M, N, K, y, y_dtype, ldy, status, st, true);
     });
 }
 

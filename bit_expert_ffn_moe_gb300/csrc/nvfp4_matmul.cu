@@ -138,6 +138,46 @@ __device__ __forceinline__ float4 ld_peer_f4(const void* p, uint32_t rank) {
     return v;
 }
 
+// Activation rows c = rank, rank + splits, ... of a tile's results part[c][128] (summed over the cluster's CTAs in rank order),
+// scaled and stored, a warp per row.  ga: the rows' scales from the tile's first row on, or one.
+template <typename T, int WARPS, int NT>
+__device__ __forceinline__ void store_rows(const MatmulArgs& args, const float* part, int64_t nt, int64_t m0, int rows, int rank,
+                                           int splits, const float* ga, bool ga_rows) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t n = nt * 128 + 4 * lane;  // this lane's four weight rows
+    const int live = (int)max((int64_t)0, min((int64_t)4, args.N - n));
+    float gb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) gb[i] = i < live ? args.gb[args.gb_rows ? n + i : 0] : 0.f;
+    const bool wide = reinterpret_cast<uintptr_t>(args.y) % 16 == 0 && args.ldy % 4 == 0;
+    const int c0 = rank + splits * warp;
+    float ga_lane = 0.f;  // lane i: the scale of this warp's i-th row (at most 22)
+    if (c0 + splits * WARPS * lane < rows) ga_lane = ga[ga_rows ? c0 + splits * WARPS * lane : 0];
+#pragma unroll 2
+    for (int i = 0; i < (NT + WARPS - 1) / WARPS; ++i) {
+        const int c = c0 + splits * WARPS * i;
+        const float a = __shfl_sync(0xffffffffu, ga_lane, i);
+        if (c >= rows) break;
+        const float* p = part + c * 128 + 4 * lane;
+        float4 v = splits > 1 ? ld_peer_f4(p, 0) : *reinterpret_cast<const float4*>(p);
+        for (int r = 1; r < splits; ++r) {
+            const float4 o = ld_peer_f4(p, r);
+            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        }
+        const float f[4] = {v.x * a * gb[0], v.y * a * gb[1], v.z * a * gb[2], v.w * a * gb[3]};
+        T* y = static_cast<T*>(args.y) + (m0 + c) * args.ldy + n;
+        if (wide && live == 4) {
+            __align__(16) T o[4] = {out_value<T>(f[0]), out_value<T>(f[1]), out_value<T>(f[2]), out_value<T>(f[3])};
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(o);
+            else *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < live) y[j] = out_value<T>(f[j]);
+        }
+    }
+}
+
 // Grid: x = weight tile * splits + rank (a cluster of `splits` CTAs per tile), y = tile of NT activation rows.
 template <int NT, typename T>
 __global__ void __launch_bounds__(kRowsThreads, 1)
@@ -155,27 +195,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const int64_t nt = blockIdx.x / splits, m0 = (int64_t)blockIdx.y * NT;
     const int k0 = (int)((int64_t)args.KT * rank / splits), k1 = (int)((int64_t)args.KT * (rank + 1) / splits);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        mbar_init(acc_full, 1);
-        *abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    constexpr uint32_t kSfBase = NT;  // scale columns after the accumulator
-
     // the weights and the activations of K step kt into stage s
     auto load_w = [&](int s, int kt) {
         unsigned char* p = smem + (size_t)s * kStageBytes;
@@ -189,15 +208,36 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         bulk_load(p + kTile, args.qa + at * kTile + (m0 % 128) * 128, NT * 128, &full[s]);
         bulk_load(p + kTile + NT * 128 + kAtoms * kAtom, args.sa + at * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
     };
+    const int head = min(kStages, k1 - k0);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        // at once: the weights do not depend on the kernel before, and the rest of the set-up runs meanwhile
+        for (int it = 0; it < head; ++it) {
+            mbar_arrive_expect_tx(&full[it], kStageBytes);
+            load_w(it, k0 + it);
+        }
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t kSfBase = NT;  // scale columns after the accumulator
 
     if (warp == 0) {
         if (lane == 0) {
-            int it = 0;
-            const int head = min(kStages, k1 - k0);
-            for (; it < head; ++it) {  // the weights do not depend on the kernel before
-                mbar_arrive_expect_tx(&full[it], kStageBytes);
-                load_w(it, k0 + it);
-            }
+            int it = head;
             pdl_wait();
             for (int i = 0; i < head; ++i) load_x(i, k0 + i);
             for (; it < k1 - k0; ++it) {
@@ -254,39 +294,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     __syncwarp();
     if (splits > 1) cluster_sync();
     else __syncthreads();
-    const int64_t n = nt * 128 + 4 * lane;  // this lane's four weight rows
-    const int live = (int)max((int64_t)0, min((int64_t)4, args.N - n));
-    float gb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) gb[i] = i < live ? args.gb[args.gb_rows ? n + i : 0] : 0.f;
-    const bool wide = reinterpret_cast<uintptr_t>(args.y) % 16 == 0 && args.ldy % 4 == 0;
-    constexpr int kWarps = kRowsThreads / 32;
-    const int c0 = rank + splits * warp;
-    float ga_lane = 0.f;  // lane i: the scale of this warp's i-th row (at most 22)
-    if (c0 + splits * kWarps * lane < rows) ga_lane = args.ga[args.ga_rows ? m0 + c0 + splits * kWarps * lane : 0];
-#pragma unroll 2
-    for (int i = 0; i < (NT + kWarps - 1) / kWarps; ++i) {
-        const int c = c0 + splits * kWarps * i;
-        const float ga = __shfl_sync(0xffffffffu, ga_lane, i);
-        if (c >= rows) break;
-        const float* p = part + c * 128 + 4 * lane;
-        float4 v = splits > 1 ? ld_peer_f4(p, 0) : *reinterpret_cast<const float4*>(p);
-        for (int r = 1; r < splits; ++r) {
-            const float4 o = ld_peer_f4(p, r);
-            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-        }
-        const float f[4] = {v.x * ga * gb[0], v.y * ga * gb[1], v.z * ga * gb[2], v.w * ga * gb[3]};
-        T* y = static_cast<T*>(args.y) + (m0 + c) * args.ldy + n;
-        if (wide && live == 4) {
-            __align__(16) T o[4] = {out_value<T>(f[0]), out_value<T>(f[1]), out_value<T>(f[2]), out_value<T>(f[3])};
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(o);
-            else *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < live) y[j] = out_value<T>(f[j]);
-        }
-    }
+    store_rows<T, kRowsThreads / 32, NT>(args, part, nt, m0, rows, rank, splits, args.ga + (args.ga_rows ? m0 : 0), args.ga_rows != 0);
     if (splits > 1) {
         __syncwarp();
         cluster_sync();  // the partial sums stay until every CTA has read them
@@ -592,27 +600,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-template <int NT>
-cudaError_t launch_rows(const MatmulArgs& a, cudaStream_t st, bool pdl) {
-    const int64_t wt = (a.N + 127) / 128, mt = (a.M + NT - 1) / NT;
-    // split K while the tiles leave SMs idle and every CTA keeps at least two K steps
+// CTAs that share a tile's K range: more while the tiles leave SMs idle and every CTA keeps at least two K steps.
+int k_splits(int64_t tiles, int KT) {
     int splits = 1;
-    while (splits < 8 && wt * mt * splits * 2 <= sm_count() && a.KT / (splits * 2) >= 2) splits *= 2;
-    const void* f = a.dtype == MOE_F32    ? (const void*)nvfp4_rows_matmul_kernel<NT, float>
-                    : a.dtype == MOE_BF16 ? (const void*)nvfp4_rows_matmul_kernel<NT, __nv_bfloat16>
-                                          : (const void*)nvfp4_rows_matmul_kernel<NT, __half>;
-    cudaError_t e = ensure_dyn_smem(f, rows_smem<NT>());
+    while (splits < 8 && tiles * splits * 2 <= sm_count() && KT / (splits * 2) >= 2) splits *= 2;
+    return splits;
+}
+
+cudaError_t launch_cluster(const void* f, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, bool pdl, void** args) {
+    cudaError_t e = ensure_dyn_smem(f, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(wt * splits), (unsigned)mt);
-    cfg.blockDim = dim3(kRowsThreads);
-    cfg.dynamicSmemBytes = rows_smem<NT>();
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (splits > 1) {
+    if (cluster > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = (unsigned)splits;
+        attr[n].val.clusterDim.x = (unsigned)cluster;
         attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
         ++n;
     }
@@ -623,8 +630,18 @@ cudaError_t launch_rows(const MatmulArgs& a, cudaStream_t st, bool pdl) {
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    void* args[] = {const_cast<MatmulArgs*>(&a), &splits};
     return cudaLaunchKernelExC(&cfg, f, args);
+}
+
+template <int NT>
+cudaError_t launch_rows(const MatmulArgs& a, cudaStream_t st, bool pdl) {
+    const int64_t wt = (a.N + 127) / 128, mt = (a.M + NT - 1) / NT;
+    int splits = k_splits(wt * mt, a.KT);
+    const void* f = a.dtype == MOE_F32    ? (const void*)nvfp4_rows_matmul_kernel<NT, float>
+                    : a.dtype == MOE_BF16 ? (const void*)nvfp4_rows_matmul_kernel<NT, __nv_bfloat16>
+                                          : (const void*)nvfp4_rows_matmul_kernel<NT, __half>;
+    void* args[] = {const_cast<MatmulArgs*>(&a), &splits};
+    return launch_cluster(f, dim3((unsigned)(wt * splits), (unsigned)mt), kRowsThreads, rows_smem<NT>(), splits, st, pdl, args);
 }
 
 }  // namespace

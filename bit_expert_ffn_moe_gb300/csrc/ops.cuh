@@ -46,5 +46,4 @@ cudaError_t launch_nvfp4_values(const moe_nvfp4_operand* op, int64_t R, int64_t 
 // y [M][ldy] = A B^T (nvfp4_matmul.cu).  pdl: A comes from the launch before, which lets this one start early.
 cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_operand* B, int64_t M, int64_t N, int64_t K, void* y,
                                 moe_dtype dtype, int64_t ldy, int* status, cudaStream_t st, bool pdl);
-
 }  // namespace moe

@@ -194,8 +194,8 @@ constexpr float kSumErr = 1.8e-7f;  // 1.5 * 2^-23 of the largest value
 
 __device__ __forceinline__ float sigmoid_fast(float l) {
     float e, s;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * l));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.44269504f * l));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
     return s;
 }
 
@@ -431,8 +431,17 @@ __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const Rout
     }
 }
 
-// The lanes' values in descending order: bitonic sort, 15 exchanges.
-__device__ __forceinline__ float sort_lanes_down(float v) {
+// A lower bound of the k-th largest of the lanes' values (the k-th largest itself where they differ): k rounds that drop the
+// largest, at most 12 of them, else the lanes sorted (bitonic, 15 exchanges).
+__device__ __forceinline__ float kth_of_lanes(float v, int k) {
+    if (k <= 12) {
+        float m = 0.f;
+        for (int r = 0; r < k; ++r) {
+            m = warp_max_f32(v);
+            if (v == m) v = -INFINITY;
+        }
+        return m;
+    }
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int n = 2; n <= 32; n *= 2)
@@ -441,7 +450,7 @@ __device__ __forceinline__ float sort_lanes_down(float v) {
             const float o = __shfl_xor_sync(kFull, v, j);
             v = ((lane & n) == 0) == ((lane & j) == 0) ? fmaxf(v, o) : fminf(v, o);
         }
-    return v;
+    return __shfl_sync(kFull, v, k - 1);
 }
 
 // ------------------------------------------------------------------ the few at a border
@@ -578,12 +587,18 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
             const float verr = err_s + (biased ? kSumErr * fmaxf(fabsf(lo), fabsf(hi)) : 0.f);
             if (!(hi - lo > 2.f * verr + kSumErr * fmaxf(fabsf(lo), fabsf(hi)))) careful = true;
         }
-        const GroupOf group_of{plan.group_mul};
+        if (!biased) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (kept) in = e0 + i < E && ((kept >> group_of(e0 + i < E ? e0 + i : 0)) & 1);
-            const float w = biased ? v[i] : l[i];
-            v[i] = in ? w : -INFINITY;
+            for (int i = 0; i < NV; ++i) v[i] = l[i];
+        }
+        if (sh >= 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[i] = in ? v[i] : -INFINITY;
+        } else {
+            const GroupOf group_of{plan.group_mul};
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (e0 + i >= E || !((kept >> group_of(e0 + i < E ? e0 + i : 0)) & 1)) v[i] = -INFINITY;
         }
     }
 
@@ -592,15 +607,16 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 #pragma unroll
     for (int i = 1; i < NV; ++i) head = fmaxf(head, v[i]);
     head = fmaxf(head, -INFINITY);  // (a NaN sorts nowhere)
-    const float bound = __shfl_sync(kFull, sort_lanes_down(head), k - 1);
+    const float bound = kth_of_lanes(head, k);
     float floor_v = biased ? bound - (err_s + kSumErr * fabsf(bound)) : bound;
     int at = 0, m = 0;
     uint32_t take = 0;
     auto count = [&](float least) {
         take = 0;
+        least = fmaxf(least, -kMaxF32);  // (-inf: out of service, or not open)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (v[i] >= least && v[i] > -INFINITY) take |= 1u << i;
+            if (v[i] >= least) take |= 1u << i;
         const int c = __popc(take);
         at = m = 0;
 #pragma unroll

@@ -9,17 +9,17 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kMostThreads = 320;
 constexpr int kSlots = 8;  // slots of a token in registers at a time
 
-// `warps` warps (1, 2, 4, 8) of a CTA share a token: thread c of them the 8-feature pieces c, c + 32 warps, ...
-__global__ void __launch_bounds__(kThreads)
+// `warps` warps of a CTA share a token: thread c of them the 8-feature pieces c, c + 32 warps, ...
+__global__ void __launch_bounds__(kMostThreads, 3)
     combine_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ y_perm,
                             const int32_t* __restrict__ inv_pos, const float* __restrict__ w, int T, int k, int d, int warps,
                             float* __restrict__ dw, uint16_t* __restrict__ dy_perm) {
-    __shared__ float part[kThreads / 32][kSlots];
+    __shared__ float part[kMostThreads / 32][kSlots];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tokens = kThreads / 32 / warps, mine = warp / warps;  // tokens per CTA, this warp's token
+    const int tokens = (int)(blockDim.x >> 5) / warps, mine = warp / warps;  // tokens per CTA, this warp's token
     const int64_t t = (int64_t)blockIdx.x * tokens + mine;
     const bool live = t < T;
     const int first = threadIdx.x - mine * warps * 32, step = warps * 32, pieces = d / 8;
@@ -78,11 +78,15 @@ __global__ void __launch_bounds__(kThreads)
 cudaError_t launch_combine_backward(const uint16_t* dy, const uint16_t* y_perm, const int32_t* inv_pos, const float* w,
                                     int T, int k, int d, float* dw, uint16_t* dy_perm, cudaStream_t st) {
     if (T == 0) return cudaSuccess;
-    int warps = 1;  // enough threads for one or more pieces each
-    while (warps < kThreads / 32 && warps * 32 < d / 8) warps *= 2;
-    const int tokens = kThreads / 32 / warps;
+    // enough threads for one or more pieces each: 1, 2 or 4 warps a token and several tokens a CTA, or one token and as
+    // many warps as hold it (2056 features, 333 tokens: 7.4 us with 8 warps, whose second turn had one thread at work)
+    const int pieces = d / 8;
+    int threads = kThreads, warps = 1;
+    while (warps < kThreads / 32 && warps * 32 < pieces) warps *= 2;
+    if (pieces > kThreads && pieces <= kMostThreads) threads = kMostThreads, warps = kMostThreads / 32;
+    const int tokens = threads / 32 / warps;
     void* args[] = {&dy, &y_perm, &inv_pos, &w, &T, &k, &d, &warps, &dw, &dy_perm};
-    return launch_kernel((const void*)combine_backward_kernel, dim3((T + tokens - 1) / tokens), dim3(kThreads), 0, st, false,
+    return launch_kernel((const void*)combine_backward_kernel, dim3((T + tokens - 1) / tokens), dim3(threads), 0, st, false,
                          args);
 }
 

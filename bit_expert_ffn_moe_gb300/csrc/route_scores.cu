@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 // 1 - s = sigmoid(-l).  Softmax: dl = s (ds - sum ds s); with renormalised weights and no other gradient of
 // the scores that sum is zero by itself, so that, as for sigmoid scores, only the picked experts get a
 // gradient: the row is then written as zeros and the picks' values on top, and only the picked logits are read.
-template <int NV, typename T>
+template <int NV, typename T, bool DENSE>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel(const __grid_constant__ RouteBackwardArgs a, const bool wide) {
     extern __shared__ float rows[];  // per warp, dense gradients only: the gradient of the scores times the scores [E]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -721,7 +721,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel
     if (t >= a.T) return;
     const int E = a.E, k = a.k, e0 = NV * lane;
     const bool softmax = a.rule.score == MOE_SCORE_SOFTMAX, renorm = a.rule.renormalize != 0;
-    const bool dense = a.dscores || (softmax && !renorm);
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
     T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
 
@@ -730,10 +729,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel
     const bool valid = id >= 0 && id < E;
     const float lp = valid ? to_f32(row[id]) : -INFINITY;
     const float dw = valid && in_service(lp) ? a.dw[t * k + lane] * a.rule.scale : 0.f;
-    float l[NV];
+    [[maybe_unused]] float l[NV];
     RowNorm norm = {0.f, 0.f};
-    float* ds = rows + (size_t)warp * E;
-    if (dense) {
+    [[maybe_unused]] float* ds = rows + (size_t)warp * E;
+    if constexpr (DENSE) {
         load_chunk<NV>(row, E, wide, l);
         if (softmax) norm = softmax_norm<NV>(l);
 #pragma unroll
@@ -763,32 +762,32 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel
     } else {
         g = dw * score_f32(lp, softmax, norm);
     }
-    if (!dense) {
+    if constexpr (!DENSE) {
         if (valid) out[id] = from_f32<T>(in_service(lp) ? (softmax ? g : g * sigmoid_f32(-lp)) : 0.f);
-        return;
-    }
-    if (valid) ds[id] = g;
-    __syncwarp();
-    float total = 0.f;  // softmax: sum of ds s over all experts
-    float gs[NV];
+    } else {
+        if (valid) ds[id] = g;
+        __syncwarp();
+        float total = 0.f;  // softmax: sum of ds s over all experts
+        float gs[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        gs[i] = 0.f;
-        if (e0 + i >= E) continue;
-        gs[i] = ds[e0 + i];
-        float extra = 0.f;
-        if (a.dscores && in_service(l[i])) extra = a.dscores[t * E + e0 + i] * score_f32(l[i], softmax, norm);
-        if (!renorm) total += gs[i];
-        total += extra;
-        gs[i] += extra;
-    }
-    if (softmax) total = warp_butterfly_sum(total);
+        for (int i = 0; i < NV; ++i) {
+            gs[i] = 0.f;
+            if (e0 + i >= E) continue;
+            gs[i] = ds[e0 + i];
+            float extra = 0.f;
+            if (a.dscores && in_service(l[i])) extra = a.dscores[t * E + e0 + i] * score_f32(l[i], softmax, norm);
+            if (!renorm) total += gs[i];
+            total += extra;
+            gs[i] += extra;
+        }
+        if (softmax) total = warp_butterfly_sum(total);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (e0 + i >= E) continue;
-        float dl = 0.f;
-        if (in_service(l[i])) dl = softmax ? gs[i] - score_f32(l[i], true, norm) * total : gs[i] * sigmoid_f32(-l[i]);
-        out[e0 + i] = from_f32<T>(dl);
+        for (int i = 0; i < NV; ++i) {
+            if (e0 + i >= E) continue;
+            float dl = 0.f;
+            if (in_service(l[i])) dl = softmax ? gs[i] - score_f32(l[i], true, norm) * total : gs[i] * sigmoid_f32(-l[i]);
+            out[e0 + i] = from_f32<T>(dl);
+        }
     }
 }
 
@@ -803,15 +802,20 @@ const void* scores_kernel(int E) {
                       : (const void*)route_scores_kernel<32, T>;
 }
 
-template <typename T>
+template <typename T, bool DENSE>
 const void* backward_kernel(int E) {
     const int nv = (E + 31) / 32;
-    return nv <= 1    ? (const void*)route_scores_backward_kernel<1, T>
-           : nv <= 2  ? (const void*)route_scores_backward_kernel<2, T>
-           : nv <= 4  ? (const void*)route_scores_backward_kernel<4, T>
-           : nv <= 8  ? (const void*)route_scores_backward_kernel<8, T>
-           : nv <= 16 ? (const void*)route_scores_backward_kernel<16, T>
-                      : (const void*)route_scores_backward_kernel<32, T>;
+    return nv <= 1    ? (const void*)route_scores_backward_kernel<1, T, DENSE>
+           : nv <= 2  ? (const void*)route_scores_backward_kernel<2, T, DENSE>
+           : nv <= 4  ? (const void*)route_scores_backward_kernel<4, T, DENSE>
+           : nv <= 8  ? (const void*)route_scores_backward_kernel<8, T, DENSE>
+           : nv <= 16 ? (const void*)route_scores_backward_kernel<16, T, DENSE>
+                      : (const void*)route_scores_backward_kernel<32, T, DENSE>;
+}
+
+template <typename T>
+const void* backward_kernel(int E, bool dense) {
+    return dense ? backward_kernel<T, true>(E) : backward_kernel<T, false>(E);
 }
 
 }  // namespace
@@ -844,12 +848,12 @@ cudaError_t launch_route_scores(const RouteScoresArgs& a, moe_dtype dtype, cudaS
 
 cudaError_t launch_route_scores_backward(const RouteBackwardArgs& a, moe_dtype dtype, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
-    const void* f = dtype == MOE_F32    ? backward_kernel<float>(a.E)
-                    : dtype == MOE_BF16 ? backward_kernel<__nv_bfloat16>(a.E)
-                                        : backward_kernel<__half>(a.E);
+    const bool dense = a.dscores || (a.rule.score == MOE_SCORE_SOFTMAX && !a.rule.renormalize);
+    const void* f = dtype == MOE_F32    ? backward_kernel<float>(a.E, dense)
+                    : dtype == MOE_BF16 ? backward_kernel<__nv_bfloat16>(a.E, dense)
+                                        : backward_kernel<__half>(a.E, dense);
     bool wide = rows_wide(a.logits, a.ld, dtype) && rows_wide(a.dlogits, a.ldd, dtype);
     void* args[] = {const_cast<RouteBackwardArgs*>(&a), &wide};
-    const bool dense = a.dscores || (a.rule.score == MOE_SCORE_SOFTMAX && !a.rule.renormalize);
     return launch_kernel(f, dim3((a.T + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps),
                          dense ? sizeof(float) * kRouteWarps * (size_t)a.E : 0, st, false, args);
 }

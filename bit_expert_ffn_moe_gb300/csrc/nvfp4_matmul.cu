@@ -312,9 +312,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 // 128 r .. and B rows 128 r .. in shared memory and A rows' results (128 lanes x 256 columns) in its tensor
 // memory; the leader (rank 0) issues the MMAs of both.  Each CTA thus copies 32 KB of codes per K step for
 // 128 x 256 results instead of 48 KB.  The scales of all 256 B rows go to both CTAs' tensor memory.
-//   warp 0     copies this CTA's operands; its copies complete on its own `full` barrier
-//   warp 1     rank 0: waits for its own stage and for the peer's arrival, issues scale copies and MMAs, whose
-//              commit frees the stage in both CTAs; rank 1: forwards its full stages to the leader
+//   warp 0     copies this CTA's operands (tensor copies, whose bytes the leader's barrier counts)
+//   warp 1     rank 0: waits for a stage of both CTAs, issues scale copies and MMAs, whose commit frees the stage
+//              in both
 //   warps 2-9  epilogue: two warps per lane quarter, each half of the columns; registers first, so that the next
 //              tile's MMAs run while these values are scaled and stored
 constexpr int kPairStages = 5;
@@ -377,6 +377,20 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
         "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
+// A box of whole 1 KB rows of an operand's bytes (the map: [bytes / 1024][256 words]) into this CTA's shared memory; the bytes
+// are counted on a barrier of the leader.
+__device__ __forceinline__ void pair_load(void* dst, const CUtensorMap* map, int64_t at, uint32_t leader_bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(0), "r"((int)(at / 1024)), "r"(leader_bar)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t leader_address(const void* p) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
 // Arrive on the barrier at this offset in CTA 0 of the cluster.
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
     asm volatile(
@@ -385,14 +399,20 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
         "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
+struct PairArgs {
+    CUtensorMap qa, sa, qb, sb;  // the operands' bytes in rows of 1 KB
+    MatmulArgs m;
+};
+
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    nvfp4_pair_matmul_kernel(const __grid_constant__ MatmulArgs args, const int MT, const int NT) {
+    nvfp4_pair_matmul_kernel(const __grid_constant__ PairArgs pair, const int MT, const int NT) {
+    const MatmulArgs& args = pair.m;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     float* gb_smem = reinterpret_cast<float*>(smem + kPairStages * kPairStageBytes);  // [epilogue warp][128]
     uint32_t* turn_smem = reinterpret_cast<uint32_t*>(gb_smem + 128 * kPairEpiWarps);  // [epilogue warp][32][17]
-    uint64_t* full = reinterpret_cast<uint64_t*>(turn_smem + kTurnWords * kPairEpiWarps);  // this CTA's copies (rank 0: and the peer)
+    uint64_t* full = reinterpret_cast<uint64_t*>(turn_smem + kTurnWords * kPairEpiWarps);  // rank 0: the copies of both CTAs
     uint64_t* empty = full + kPairStages;
     uint64_t* acc_full = empty + kPairStages;
     uint64_t* acc_empty = acc_full + 1;  // rank 0: the epilogue warps of both CTAs
@@ -403,7 +423,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint32_t rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; ++s) {
-            mbar_init(&full[s], rank == 0 ? 2 : 1);
+            mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
@@ -443,18 +463,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         break;
                     }
                     unsigned char* p = stage(s);
-                    mbar_arrive_expect_tx(&full[s], kPairStageBytes);
-                    bulk_load(p, args.qa + (ka + kt) * kTile, kTile, &full[s]);
-                    bulk_load(p + kTile, args.qb + (kb + kt) * kTile, kTile, &full[s]);
-                    bulk_load(p + 2 * kTile, args.sa + (ka + kt) * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
-                    bulk_load(p + 2 * kTile + 4 * kAtom, args.sb + (kb0 + kt) * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
-                    bulk_load(p + 2 * kTile + 8 * kAtom, args.sb + (kb1 + kt) * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
+                    const uint32_t bar = leader_address(&full[s]);
+                    pair_load(p, &pair.qa, (ka + kt) * kTile, bar);
+                    pair_load(p + kTile, &pair.qb, (kb + kt) * kTile, bar);
+                    pair_load(p + 2 * kTile, &pair.sa, (ka + kt) * kAtoms * kAtom, bar);
+                    pair_load(p + 2 * kTile + 4 * kAtom, &pair.sb, (kb0 + kt) * kAtoms * kAtom, bar);
+                    pair_load(p + 2 * kTile + 8 * kAtom, &pair.sb, (kb1 + kt) * kAtoms * kAtom, bar);
                 }
             }
-            // Copies still in flight land before the CTA's shared memory goes: after the last commit every stage has
-            // been consumed; when aborting, the outstanding ones are given a bounded time (rank 0's barriers also
-            // count the peer, whose stages may never come: the wait then just runs out).
-            if (*abort_flag) {
+            // Copies still in flight land before the CTA's shared memory goes: after the last commit every stage has been
+            // consumed; when aborting, the leader gives the outstanding ones of both CTAs a bounded time.
+            if (*abort_flag && rank == 0) {
                 volatile int never = 0;
                 for (int i = max(0, it - kPairStages); i < it; ++i)
                     mbar_wait(&full[i % kPairStages], (i / kPairStages) & 1, &never, nullptr, 100000000LL);
@@ -483,20 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             pair_commit(acc_full);
         }
         pair_commit(mma_done);
-    } else if (warp == 1) {
-        int it = 0;
-        bool ok = true;
-        for (int t = first; t < n_tiles && ok; t += step)
-            for (int kt = 0; kt < KT; ++kt, ++it) {
-                const int s = it % kPairStages;
-                if (!mbar_wait_warp(&full[s], (it / kPairStages) & 1, abort_flag, args.status)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) arrive_leader(&full[s]);
-                __syncwarp();
-            }
-    } else {
+    } else if (warp >= 2) {
         const int q = warp & 3, half = (warp - 2) / 4;
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;
         const bool wide = reinterpret_cast<uintptr_t>(args.y) % 16 == 0 && (args.ldy * (int64_t)sizeof(T)) % 16 == 0;
@@ -644,6 +651,20 @@ cudaError_t launch_rows(const MatmulArgs& a, cudaStream_t st, bool pdl) {
     return launch_cluster(f, dim3((unsigned)(wt * splits), (unsigned)mt), kRowsThreads, rows_smem<NT>(), splits, st, pdl, args);
 }
 
+// Map of `bytes` bytes as rows of 1 KB, read in boxes of `box` bytes (both multiples of 1 KB).
+cudaError_t byte_map(CUtensorMap* m, const uint8_t* p, int64_t bytes, int box) {
+    encode_tiled_fn enc = tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {256, (cuuint64_t)(bytes / 1024)};
+    const cuuint64_t strides[1] = {1024};
+    const cuuint32_t boxes[2] = {256, (cuuint32_t)(box / 1024)};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(p), dims, strides, boxes, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_operand* B, int64_t M, int64_t N, int64_t K, void* y,
@@ -662,7 +683,15 @@ cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_oper
     if (M <= 128 || ((M + 127) / 128) * ((N + 127) / 128) * 2 <= sm_count()) return launch_rows<128>(a, st, pdl);
     int MT = (int)((M + 255) / 256), NT = (int)((N + 255) / 256);
     const int64_t tiles = (int64_t)MT * NT, pairs = sm_count() / 2;
-    void* args[] = {&a, &MT, &NT};
+    PairArgs p;
+    p.m = a;
+    const int64_t Kp = (int64_t)a.KT * 256, Mp = (M + 127) / 128 * 128, Np = (N + 127) / 128 * 128;
+    cudaError_t e = byte_map(&p.qa, A->q, Mp * Kp / 2, kTile);
+    if (e == cudaSuccess) e = byte_map(&p.sa, A->s, Mp * Kp / 16, kAtoms * kAtom);
+    if (e == cudaSuccess) e = byte_map(&p.qb, B->q, Np * Kp / 2, kTile);
+    if (e == cudaSuccess) e = byte_map(&p.sb, B->s, Np * Kp / 16, kAtoms * kAtom);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&p, &MT, &NT};
     const void* f = dtype == MOE_F32    ? (const void*)nvfp4_pair_matmul_kernel<float>
                     : dtype == MOE_BF16 ? (const void*)nvfp4_pair_matmul_kernel<__nv_bfloat16>
                                         : (const void*)nvfp4_pair_matmul_kernel<__half>;

@@ -252,6 +252,21 @@ PyObject* nvfp4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// nvfp4_room(rows, K, device index) -> q, s, gs, their addresses: room for an operand with a scale per row
+PyObject* nvfp4_room(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        const int64_t rows = integer(a[0]), K = integer(a[1]);
+        const int64_t nq = (int64_t)moe_nvfp4_operand_codes(rows, K), ns = (int64_t)moe_nvfp4_operand_scales(rows, K);
+        if (K < 1 || (nq == 0 && rows != 0)) refuse(PyExc_ValueError, "operand", "unsupported shape");
+        const auto on = at::TensorOptions().device(at::kCUDA, narrow(integer(a[2]), "device"));
+        const at::Tensor q = at::empty({nq}, on.dtype(at::kByte)), s = at::empty({ns}, on.dtype(at::kByte));
+        const at::Tensor gs = at::empty({rows}, on.dtype(at::kFloat));
+        return Py_BuildValue("NNNKKK", wrap(q), wrap(s), wrap(gs), (unsigned long long)reinterpret_cast<uintptr_t>(q.data_ptr()),
+                             (unsigned long long)reinterpret_cast<uintptr_t>(s.data_ptr()),
+                             (unsigned long long)reinterpret_cast<uintptr_t>(gs.data_ptr()));
+    });
+}
+
 // nvfp4_matmul(a (4), b (4), like, workspace, out): like: a tensor whose type the result has, on the operands' device
 PyObject* nvfp4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 12, [&]() -> PyObject* {
@@ -295,8 +310,8 @@ PyObject* set_error(PyObject*, PyObject* kind) {
 }
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(route_scores), FAST(route_scores_backward), FAST(combine_backward), FAST(nvfp4_quantize), FAST(nvfp4_matmul),
-                         FAST(nvfp4_linear), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {FAST(route_scores), FAST(route_scores_backward), FAST(combine_backward), FAST(nvfp4_quantize), FAST(nvfp4_room),
+                         FAST(nvfp4_matmul), FAST(nvfp4_linear), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "moe_torch_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -116,10 +116,14 @@ class Nvfp4Operand:
 
 def nvfp4_operand(rows: int, K: int, device="cuda") -> Nvfp4Operand:
     """Room for an operand [rows, K] with a scale per row."""
-    u8 = dict(dtype=torch.uint8, device=device)
-    return Nvfp4Operand(rows, K, torch.empty(B.moe_nvfp4_operand_codes(rows, K), **u8),
-                        torch.empty(B.moe_nvfp4_operand_scales(rows, K), **u8),
-                        torch.empty(rows, dtype=torch.float32, device=device))
+    on = torch.device(device)
+    _need(on.type == "cuda", "device: a CUDA device expected")
+    index = on.index if on.index is not None else torch.cuda.current_device()
+    op = object.__new__(Nvfp4Operand)  # (its tensors are right as they come)
+    op.q, op.s, op.gs, q, s, gs = (_module or _calls()).nvfp4_room(rows, K, index)
+    op.rows, op.K, op.device = rows, K, index
+    op.struct = B.moe_nvfp4_operand(q, s, gs, 1)
+    return op
 
 
 def nvfp4_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:

@@ -163,7 +163,7 @@ moe_status moe_nvfp4_quantize(const void* x, moe_dtype dtype, int64_t R, int64_t
     if (scratch) MOE_TRY(check_workspace(ws, ws_bytes, sizeof(Ctrl) + 4 * (size_t)((rows ? R : 0) + C)));
     return launch([&] {
         return launch_nvfp4_quantize(x, dtype, R, C, ld, rows, cols, scales_given != 0,
-                                     scratch ? static_cast<char*>(ws) + sizeof(Ctrl) : nullptr, (cudaStream_t)stream, false);
+                                     scratch ? static_cast<char*>(ws) + sizeof(Ctrl) : nullptr, (cudaStream_t)stream);
     });
 }
 
@@ -204,7 +204,7 @@ moe_status moe_nvfp4_linear(const void* x, moe_dtype x_dtype, int64_t M, int64_t
                                      reinterpret_cast<float*>(base + L.gs), 1};
         cudaStream_t st = (cudaStream_t)stream;
         int* status = &static_cast<Ctrl*>(ws)->status;
-        cudaError_t e = launch_nvfp4_quantize(x, x_dtype, M, K, ldx, &A, nullptr, false, nullptr, st, false);
+        cudaError_t e = launch_nvfp4_quantize(x, x_dtype, M, K, ldx, &A, nullptr, false, nullptr, st);
         if (e != cudaSuccess) return e;
         return launch_nvfp4_matmul(&A, W, M, N, K, y, y_dtype, ldy, status, st, true);
     });

@@ -18,6 +18,8 @@ __global__ void __launch_bounds__(kMostThreads, 3)
                             const int32_t* __restrict__ inv_pos, const float* __restrict__ w, int T, int k, int d, int warps,
                             float* __restrict__ dw, uint16_t* __restrict__ dy_perm) {
     __shared__ float part[kMostThreads / 32][kSlots];
+    pdl_wait();
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tokens = (int)(blockDim.x >> 5) / warps, mine = warp / warps;  // tokens per CTA, this warp's token
     const int64_t t = (int64_t)blockIdx.x * tokens + mine;
@@ -86,7 +88,7 @@ cudaError_t launch_combine_backward(const uint16_t* dy, const uint16_t* y_perm, 
     if (pieces > kThreads && pieces <= kMostThreads) threads = kMostThreads, warps = kMostThreads / 32;
     const int tokens = threads / 32 / warps;
     void* args[] = {&dy, &y_perm, &inv_pos, &w, &T, &k, &d, &warps, &dw, &dy_perm};
-    return launch_kernel((const void*)combine_backward_kernel, dim3((T + tokens - 1) / tokens), dim3(threads), 0, st, false,
+    return launch_kernel((const void*)combine_backward_kernel, dim3((T + tokens - 1) / tokens), dim3(threads), 0, st, true,
                          args);
 }
 

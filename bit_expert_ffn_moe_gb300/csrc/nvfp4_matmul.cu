@@ -43,6 +43,7 @@ struct MatmulArgs {
     int dtype;
     int64_t ldy;
     int* status;
+    int weights_ready;  // B is there before the kernel before has ended
 };
 
 template <typename T>
@@ -217,7 +218,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         mbar_init(acc_full, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        // at once: the weights do not depend on the kernel before, and the rest of the set-up runs meanwhile
+        // at once, if they may: the rest of the set-up runs meanwhile
+        if (!args.weights_ready) pdl_wait();
         for (int it = 0; it < head; ++it) {
             mbar_arrive_expect_tx(&full[it], kStageBytes);
             load_w(it, k0 + it);
@@ -269,6 +271,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     }
     __syncwarp();
     pdl_wait();  // ga comes from the kernel before
+    pdl_launch_dependents();
     volatile int never = 0;
     mbar_wait(acc_full, 0, &never, args.status);  // the commit always comes; bounded all the same
     tc_fence_after();
@@ -444,6 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
+    pdl_launch_dependents();
 
     const int n_tiles = MT * NT, KT = args.KT, first = blockIdx.x >> 1, step = gridDim.x >> 1;
     const int64_t last_a = (args.M + 127) / 128 - 1, last_b = (args.N + 127) / 128 - 1;  // last 128-row blocks
@@ -614,7 +618,7 @@ int k_splits(int64_t tiles, int KT) {
     return splits;
 }
 
-cudaError_t launch_cluster(const void* f, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, bool pdl, void** args) {
+cudaError_t launch_cluster(const void* f, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, void** args) {
     cudaError_t e = ensure_dyn_smem(f, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -630,25 +634,23 @@ cudaError_t launch_cluster(const void* f, dim3 grid, int threads, size_t smem, i
         attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
         ++n;
     }
-    if (pdl) {
-        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[n].val.programmaticStreamSerializationAllowed = 1;
-        ++n;
-    }
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
     cfg.attrs = attr;
     cfg.numAttrs = n;
     return cudaLaunchKernelExC(&cfg, f, args);
 }
 
 template <int NT>
-cudaError_t launch_rows(const MatmulArgs& a, cudaStream_t st, bool pdl) {
+cudaError_t launch_rows(const MatmulArgs& a, cudaStream_t st) {
     const int64_t wt = (a.N + 127) / 128, mt = (a.M + NT - 1) / NT;
     int splits = k_splits(wt * mt, a.KT);
     const void* f = a.dtype == MOE_F32    ? (const void*)nvfp4_rows_matmul_kernel<NT, float>
                     : a.dtype == MOE_BF16 ? (const void*)nvfp4_rows_matmul_kernel<NT, __nv_bfloat16>
                                           : (const void*)nvfp4_rows_matmul_kernel<NT, __half>;
     void* args[] = {const_cast<MatmulArgs*>(&a), &splits};
-    return launch_cluster(f, dim3((unsigned)(wt * splits), (unsigned)mt), kRowsThreads, rows_smem<NT>(), splits, st, pdl, args);
+    return launch_cluster(f, dim3((unsigned)(wt * splits), (unsigned)mt), kRowsThreads, rows_smem<NT>(), splits, st, args);
 }
 
 // Map of `bytes` bytes as rows of 1 KB, read in boxes of `box` bytes (both multiples of 1 KB).
@@ -668,19 +670,19 @@ cudaError_t byte_map(CUtensorMap* m, const uint8_t* p, int64_t bytes, int box) {
 }  // namespace
 
 cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_operand* B, int64_t M, int64_t N, int64_t K, void* y,
-                                moe_dtype dtype, int64_t ldy, int* status, cudaStream_t st, bool pdl) {
+                                moe_dtype dtype, int64_t ldy, int* status, cudaStream_t st, bool weights_ready) {
     if (M == 0 || N == 0) return cudaSuccess;
     MatmulArgs a = {A->q, A->s, A->gs, A->gs_rows, B->q, B->s, B->gs, B->gs_rows, M, N, (int)((K + 255) / 256), y, (int)dtype, ldy,
-                    status};
-    if (M <= 8) return launch_rows<8>(a, st, pdl);
-    if (M <= 16) return launch_rows<16>(a, st, pdl);
-    if (M <= 32) return launch_rows<32>(a, st, pdl);
-    if (M <= 64) return launch_rows<64>(a, st, pdl);
+                    status, weights_ready ? 1 : 0};
+    if (M <= 8) return launch_rows<8>(a, st);
+    if (M <= 16) return launch_rows<16>(a, st);
+    if (M <= 32) return launch_rows<32>(a, st);
+    if (M <= 64) return launch_rows<64>(a, st);
     // Beyond 128 rows the pair kernel's tiles are few and large: while 128 x 128 tiles leave half the SMs idle, these, with their
     // K range split over a cluster, finish sooner (us, pair / rows: 256 x 4096 x 8192 17.6 / 12.1, 777 x 1000 x 1544 9.5 / 8.9,
     // 200 x 600 x 300 8.7 / 7.3, 1024^3 7.9 / 8.0; without half the SMs idle, 512 x 4096 x 8192 17.8 / 18.1, 512 x 8192 x 1024
     // 8.4 / 17.5).
-    if (M <= 128 || ((M + 127) / 128) * ((N + 127) / 128) * 2 <= sm_count()) return launch_rows<128>(a, st, pdl);
+    if (M <= 128 || ((M + 127) / 128) * ((N + 127) / 128) * 2 <= sm_count()) return launch_rows<128>(a, st);
     int MT = (int)((M + 255) / 256), NT = (int)((N + 255) / 256);
     const int64_t tiles = (int64_t)MT * NT, pairs = sm_count() / 2;
     PairArgs p;
@@ -695,7 +697,7 @@ cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_oper
     const void* f = dtype == MOE_F32    ? (const void*)nvfp4_pair_matmul_kernel<float>
                     : dtype == MOE_BF16 ? (const void*)nvfp4_pair_matmul_kernel<__nv_bfloat16>
                                         : (const void*)nvfp4_pair_matmul_kernel<__half>;
-    return launch_kernel(f, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPairThreads), kPairSmem, st, pdl, args);
+    return launch_kernel(f, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), dim3(kPairThreads), kPairSmem, st, true, args);
 }
 
 }  // namespace moe

@@ -43,14 +43,17 @@ struct Block {
     static constexpr int kWords = 4 * (int)sizeof(T);
     uint32_t w[kWords];
 
-    // those at or past `live` are zero; wide: p is 16-byte aligned
+    __device__ __forceinline__ void load_wide(const T* p) {  // p is 16-byte aligned
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+    }
+    // those at or past `live` are zero
     __device__ __forceinline__ void load(const T* p, int64_t live, bool wide) {
         if (wide && live >= 16) {
-#pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
-                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-            }
+            load_wide(p);
         } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = i < live ? __float_as_uint(p[i]) : 0u;
@@ -80,6 +83,12 @@ struct Block {
         }
     }
 };
+
+// The first `bytes` (0 .. 16) of 16 bytes; zeros after them.
+__device__ __forceinline__ void cp_async16_part(void* smem, const void* gmem, int bytes) {
+    const uint32_t sa = (uint32_t)__cvta_generic_to_shared(smem);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sa), "l"(gmem), "r"(bytes) : "memory");
+}
 
 // The larger magnitudes of a word of one fp32 or two 16-bit elements (a: magnitudes already).
 template <typename T>
@@ -114,11 +123,6 @@ __device__ __forceinline__ uint32_t block_mag(const Block<T>& b) {
     return mag_f32<T>(m);
 }
 
-__device__ __forceinline__ float row_scale(uint32_t mag) {
-    const float g = __fdiv_rn(__uint_as_float(mag), 2688.f);
-    return g == 0.f ? 1.f : g;
-}
-
 __device__ __forceinline__ float quotient(float a, float b, float y) {  // y = 1 / b rounded
     const float q0 = __fmul_rn(a, y);
     return __fmaf_rn(__fmaf_rn(-q0, b, a), y, q0);
@@ -132,22 +136,32 @@ struct RowScale {
 __device__ __forceinline__ RowScale with_reciprocal(float g) {
     return {g, g >= 8.8817842e-16f && g <= 1.1258999e15f ? __frcp_rn(g) : 0.f};
 }
+// That of a row's largest magnitude: max / 2688, or 1 (the quotient is the rounded one for every mantissa).
+__device__ __forceinline__ RowScale row_scale(uint32_t mag) {
+    const float m = __uint_as_float(mag);
+    float g = quotient(m, 2688.f, 1.f / 2688.f);
+    if (!(m >= 1e-12f && m <= 1e18f)) {
+        g = __fdiv_rn(m, 2688.f);
+        if (g == 0.f) g = 1.f;
+    }
+    return with_reciprocal(g);
+}
 
 // One block of 16 elements of largest magnitude amax under the row scale: 8 bytes of codes; returns the scale byte.
-// given: the row scale is not the row's own and quotients may be far above 6: they saturate.
-template <typename T>
+// PLAIN: rs.y is not 0 and the scale is the row's own; given: it may not be, and quotients may be far above 6: they saturate.
+template <typename T, bool PLAIN>
 __device__ __forceinline__ uint32_t encode_block(float (&v)[16], float amax, RowScale rs, bool given, uint2& codes) {
     float t;
-    if (sizeof(T) == 2 && rs.y != 0.f) t = quotient(quotient(amax, rs.g, rs.y), 6.f, 0.166666672f);
+    if (sizeof(T) == 2 && (PLAIN || rs.y != 0.f)) t = quotient(quotient(amax, rs.g, rs.y), 6.f, 0.166666672f);
     else t = __fdiv_rn(__fdiv_rn(amax, rs.g), 6.f);
     const uint32_t sb = f32_to_e4m3_sat(t);
     const float D = __fmul_rn(e4m3x2_to_f2(sb).x, rs.g);
-    if (given) {
+    if (!PLAIN && given) {
         const float lim = 8.f * D;
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = fminf(fmaxf(v[i], -lim), lim);
     }
-    if (rs.y != 0.f) {
+    if (PLAIN || rs.y != 0.f) {
         float y;  // 1 / D rounded (the hardware's reciprocal and a Newton step); a zero scale gives zero codes
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(D));
         y = sb == 0 ? 0.f : fmaf(y, fmaf(-D, y, 1.f), y);
@@ -184,10 +198,18 @@ __device__ __forceinline__ void encode_unit(const Block<T>& a, const Block<T>& b
                                             uint8_t* q, uint8_t* s, bool live) {
     float v[16];
     uint2 ca, cb;
-    a.values(v);
-    uint32_t word = encode_block<T>(v, __uint_as_float(mag_a), rs, given, ca);
-    b.values(v);
-    word |= encode_block<T>(v, __uint_as_float(mag_b), rs, given, cb) << 8;
+    uint32_t word;
+    if (!given && rs.y != 0.f) {
+        a.values(v);
+        word = encode_block<T, true>(v, __uint_as_float(mag_a), rs, false, ca);
+        b.values(v);
+        word |= encode_block<T, true>(v, __uint_as_float(mag_b), rs, false, cb) << 8;
+    } else {
+        a.values(v);
+        word = encode_block<T, false>(v, __uint_as_float(mag_a), rs, given, ca);
+        b.values(v);
+        word |= encode_block<T, false>(v, __uint_as_float(mag_b), rs, given, cb) << 8;
+    }
     if (live) *reinterpret_cast<uint4*>(q) = make_uint4(ca.x, ca.y, cb.x, cb.y);
     word |= __shfl_down_sync(0xffffffffu, word, 1) << 16;
     if (live && (threadIdx.x & 1) == 0) *reinterpret_cast<uint32_t*>(s) = word;
@@ -200,61 +222,165 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 4)
     nvfp4_rows_kernel(const T* __restrict__ x, int64_t R, int64_t K, int64_t ld, bool wide, int tpr_log, uint8_t* __restrict__ q,
                       uint8_t* __restrict__ s, float* __restrict__ gs, bool given, bool gs_rows) {
-    __shared__ uint32_t part[kThreads / 32];
+    __shared__ __align__(16) uint32_t part[kThreads / 32];
+    pdl_wait();
     pdl_launch_dependents();  // a product launched behind this call fetches its weights meanwhile
     const int tpr = 1 << tpr_log, u0 = threadIdx.x & (tpr - 1);
-    const int64_t r = (int64_t)blockIdx.x * (kThreads >> tpr_log) + (threadIdx.x >> tpr_log);
+    const int64_t first = (int64_t)blockIdx.x * (kThreads >> tpr_log);  // the CTA's rows: inside one 128-row block
+    const uint32_t sub = threadIdx.x >> tpr_log;
+    const bool live = first + sub < R;
     const int units = (int)((K + 255) >> 8) * 8;
-    const bool live = r < R;
-    const T* row = x + (live ? r : 0) * ld;
+    const int whole = wide ? (int)(K >> 5) : 0;  // units that are read in 16-byte pieces
+    const T* row = x + first * ld + (live ? sub * ld : 0);
     Block<T> a, b;
-    auto load = [&](int u, bool take) {
-        const int64_t left = take ? K - 32 * (int64_t)u : 0;
-        a.load(row + 32 * (int64_t)u, left, wide);
-        b.load(row + 32 * (int64_t)u + 16, left - 16, wide);
+    auto load = [&](int u) {
+        const T* p = row + 32 * (int64_t)u;
+        if (u < whole) {
+            a.load_wide(p);
+            b.load_wide(p + 16);
+        } else {
+            const int64_t left = u < units ? K - 32 * (int64_t)u : 0;
+            a.load(p, left, wide);
+            b.load(p + 16, left - 16, wide);
+        }
     };
-    load(u0, live && u0 < units);
+    load(u0);
     uint32_t mag_a = block_mag(a), mag_b = block_mag(b);
     RowScale rs = {1.f, 0.f};
     if (!given) {
         uint32_t m = max(mag_a, mag_b);
         if (units > tpr) {
+#pragma unroll 1
             for (int u = u0 + tpr; u < units; u += tpr) {
-                load(u, live);
+                load(u);
                 m = max(m, max(block_mag(a), block_mag(b)));
             }
-            load(u0, live);
+            load(u0);
         }
         m = __reduce_max_sync(0xffffffffu, m);
         if (tpr > 32) {
             if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
             __syncthreads();
             const int w0 = (threadIdx.x >> tpr_log) << (tpr_log - 5);
-            for (int w = 0; w < tpr >> 5; ++w) m = max(m, part[w0 + w]);
+            if (tpr == kThreads) {
+                const uint4 lo = *reinterpret_cast<const uint4*>(part), hi = *reinterpret_cast<const uint4*>(part + 4);
+                m = max(max(max(lo.x, lo.y), max(lo.z, lo.w)), max(max(hi.x, hi.y), max(hi.z, hi.w)));
+            } else {
+                for (int w = 0; w < tpr >> 5; ++w) m = max(m, part[w0 + w]);
+            }
         }
-        rs = with_reciprocal(row_scale(m));
-        if (live && u0 == 0) gs[r] = rs.g;
+        rs = row_scale(m);
+        if (live && u0 == 0) gs[first + sub] = rs.g;
     } else if (live) {
-        rs = with_reciprocal(gs[gs_rows ? r : 0]);
+        rs = with_reciprocal(gs[gs_rows ? first + sub : 0]);
     }
-    const uint32_t in = (uint32_t)r & 127u;  // row of its 128-row block
-    uint8_t* qr = q + (r >> 7) * (int64_t)units * 2048 + in * 128u;
-    uint8_t* sr = s + (r >> 7) * (int64_t)units * 256 + unit_scales(in, 0);
-    for (int base = 0; base < units; base += tpr) {
-        const int u = base + u0;
-        const bool mine = live && u < units;
-        if (base > 0) {
-            load(u, mine);
-            mag_a = block_mag(a), mag_b = block_mag(b);
+    const uint32_t in = ((uint32_t)first & 127u) + sub;  // row of its 128-row block
+    q += (first >> 7) * units * 2048;
+    s += (first >> 7) * units * 256;
+    int64_t at = unit_codes(in, u0), sat = unit_scales(in, u0);
+    int u = u0;
+    while (true) {
+        encode_unit(a, b, mag_a, mag_b, rs, given, q + at, s + sat, live && u < units);
+        u += tpr;
+        if (u - u0 >= units) break;  // (all threads of a row together)
+        at += tpr * 2048, sat += tpr * 256;
+        load(u);
+        mag_a = block_mag(a), mag_b = block_mag(b);
+    }
+}
+
+// Rows of up to 8192 elements that start on 16 bytes, where there are more than the SMs hold at once: persistent CTAs, each
+// with the next row's copy (cp.async) in flight while this one is reduced and encoded.  A warp reads and encodes what it copied
+// itself; its 16-byte pieces are swizzled, so that lanes reading a unit each meet all banks.
+template <typename T, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS)
+    nvfp4_rows_stream_kernel(const T* __restrict__ x, int64_t R, int64_t K, int64_t ld, int tpr_log, uint8_t* __restrict__ q,
+                             uint8_t* __restrict__ s, float* __restrict__ gs, bool given, bool gs_rows) {
+    extern __shared__ __align__(16) unsigned char rows_smem[];  // two buffers of 32 elements per thread
+    __shared__ __align__(16) uint32_t part[2][kThreads / 32];
+    constexpr int kPieces = 32 * (int)sizeof(T) / 16, kBuffer = kThreads * kPieces * 16, kPer = 16 / (int)sizeof(T);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tpr = 1 << tpr_log, rpc = kThreads >> tpr_log;  // threads a row, rows a turn
+    const int u0 = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31;
+    const uint32_t sub = threadIdx.x >> tpr_log;
+    const int units = (int)((K + 255) >> 8) * 8;
+    const int64_t turns = (R + rpc - 1) / rpc;
+    unsigned char* mine = rows_smem + (threadIdx.x >> 5) * (32 * kPieces * 16);  // this warp's pieces
+    const int warp_e = (u0 & ~31) * 32;  // first element of the warp's part of its row
+    auto fetch = [&](int64_t turn, unsigned char* to) {
+        const int64_t r = turn * rpc + sub;
+        const T* row = x + (r < R ? r : R - 1) * ld;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int p = 32 * i + lane, e = warp_e + p * kPer;
+            const int64_t left = (K - e) * (int64_t)sizeof(T);
+            cp_async16_part(to + (p ^ ((p >> 3) & 7)) * 16, row + (left > 0 ? e : 0), left >= 16 ? 16 : left > 0 ? (int)left : 0);
         }
-        encode_unit(a, b, mag_a, mag_b, rs, given, qr + (int64_t)(u >> 3) * 16384 + (((uint32_t)u ^ in) & 7u) * 16u,
-                    sr + (int64_t)(u >> 1) * 512, mine);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto take = [&](Block<T>& blk, const unsigned char* from, int h) {  // block h of this lane's unit
+#pragma unroll
+        for (int j = 0; j < kPieces / 2; ++j) {
+            const int p = lane * kPieces + h * (kPieces / 2) + j;
+            const uint4 v = *reinterpret_cast<const uint4*>(from + (p ^ ((p >> 3) & 7)) * 16);
+            blk.w[4 * j] = v.x, blk.w[4 * j + 1] = v.y, blk.w[4 * j + 2] = v.z, blk.w[4 * j + 3] = v.w;
+        }
+    };
+    fetch(blockIdx.x, mine);
+    int buf = 0;
+    for (int64_t turn = blockIdx.x; turn < turns; turn += gridDim.x, buf ^= 1) {
+        if (turn + gridDim.x < turns) {
+            fetch(turn + gridDim.x, mine + (buf ^ 1) * kBuffer);
+            cp_async_wait_group<1>();
+        } else {
+            cp_async_wait_group<0>();
+        }
+        __syncwarp();
+        const int64_t r = turn * rpc + sub;
+        const bool live = r < R;
+        Block<T> a, b;
+        take(a, mine + buf * kBuffer, 0);
+        take(b, mine + buf * kBuffer, 1);
+        const uint32_t mag_a = block_mag(a), mag_b = block_mag(b);
+        RowScale rs = {1.f, 0.f};
+        if (!given) {
+            uint32_t m = __reduce_max_sync(0xffffffffu, max(mag_a, mag_b));
+            if (tpr > 32) {
+                if (lane == 0) part[buf][threadIdx.x >> 5] = m;
+                __syncthreads();
+                if (tpr == kThreads) {
+                    const uint4 lo = *reinterpret_cast<const uint4*>(part[buf]), hi = *reinterpret_cast<const uint4*>(part[buf] + 4);
+                    m = max(max(max(lo.x, lo.y), max(lo.z, lo.w)), max(max(hi.x, hi.y), max(hi.z, hi.w)));
+                } else {
+                    const int w0 = (threadIdx.x >> tpr_log) << (tpr_log - 5);
+                    for (int w = 0; w < tpr >> 5; ++w) m = max(m, part[buf][w0 + w]);
+                }
+            }
+            rs = row_scale(m);
+            if (live && u0 == 0) gs[r] = rs.g;
+        } else if (live) {
+            rs = with_reciprocal(gs[gs_rows ? r : 0]);
+        }
+        const uint32_t in = (uint32_t)r & 127u;
+        const int64_t block = (r >> 7) * units;
+        encode_unit(a, b, mag_a, mag_b, rs, given, q + block * 2048 + unit_codes(in, u0), s + block * 256 + unit_scales(in, u0),
+                    live && u0 < units);
+        __syncwarp();  // the buffer is free
     }
 }
 
 // ------------------------------------------------------------------ with columns
-// Maxima of |x| over rows and columns as fp32 bits in row_max[R] and col_max[C] (zeroed before).  A warp takes
-// 32 rows of 16 bytes per lane; the 8 warps of a CTA 256 rows of the same columns.
+__global__ void __launch_bounds__(kThreads) nvfp4_zero_kernel(unsigned* p, int64_t n) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i < n) p[i] = 0u;
+}
+
+// Maxima of |x| over rows and columns as fp32 bits in row_max[R] and col_max[C], which the kernel before zeroes meanwhile.  A
+// warp takes kMaxRows rows of 16 bytes per lane; the 8 warps of a CTA rows of the same columns.
+constexpr int kMaxRows = 16;
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4)
     nvfp4_maxima_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld, bool wide, int col_tiles,
@@ -262,11 +388,12 @@ __global__ void __launch_bounds__(kThreads, 4)
     constexpr int kPer = 16 / (int)sizeof(T), kWarpCols = 32 * kPer;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     __shared__ uint32_t part[kThreads / 32][kWarpCols];
+    pdl_launch_dependents();
     const int64_t col0 = (blockIdx.x % col_tiles) * (int64_t)kWarpCols;
-    const int64_t c0 = col0 + kPer * lane, r0 = (int64_t)(blockIdx.x / col_tiles) * kThreads + 32 * warp;
+    const int64_t c0 = col0 + kPer * lane, r0 = ((int64_t)(blockIdx.x / col_tiles) * (kThreads / 32) + warp) * kMaxRows;
     uint32_t cm[4] = {0u, 0u, 0u, 0u};
     unsigned mine = 0;
-    const int rows = (int)max((int64_t)0, min((int64_t)32, R - r0));
+    const int rows = (int)max((int64_t)0, min((int64_t)kMaxRows, R - r0));
     for (int j0 = 0; j0 < rows; j0 += 8) {
         uint4 u[8];
 #pragma unroll
@@ -294,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 4)
             if (lane == j0 + j) mine = rm;
         }
     }
+    pdl_wait();
     if (row_max && lane < rows) atomicMax(row_max + r0 + lane, mine);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -320,55 +448,69 @@ __global__ void __launch_bounds__(kThreads, 4)
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 3)
     nvfp4_both_kernel(const T* __restrict__ x, int64_t R, int64_t C, int64_t ld, bool wide, int col_tiles, int n_tiles,
-                      const unsigned* __restrict__ row_max, const unsigned* __restrict__ col_max,
+                      const unsigned* row_max, const unsigned* col_max,
                       const __grid_constant__ moe_nvfp4_operand rows, const __grid_constant__ moe_nvfp4_operand cols, bool given) {
     extern __shared__ __align__(16) unsigned char tiles[];  // two buffers
     __shared__ RowScale row_scales[kTileR], col_scales[kTileC];
     constexpr int kPitch = kTileC * (int)sizeof(T), kPer = 16 / (int)sizeof(T), kPieces = kTileC / kPer, kTurn = kPieces / 8;
     const int64_t Cp = pad_to(C, 256), Rp = pad_to(R, 256);
     auto place = [&](int rr, int pc) { return rr * kPitch + ((pc + kTurn * (rr >> 5)) & (kPieces - 1)) * 16; };
-    // fetch tile t into a buffer, and this thread's row and column scale (or maximum) of it into registers
-    float row_v = 0.f, col_v = 0.f;
+    float row_v = 0.f, col_v = 0.f;  // this thread's row and column scale (or maximum) of the tile to come
     auto fetch = [&](int t, unsigned char* to) {
         const int64_t r0 = (int64_t)(t / col_tiles) * kTileR, c0 = (int64_t)(t % col_tiles) * kTileC;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < kTileR * kPieces; i += kThreads) {
-            const int rr = i / kPieces, pc = i % kPieces;
-            const int64_t r = r0 + rr, c = c0 + pc * kPer;
-            const T* p = x + r * ld + c;
-            unsigned char* q = to + place(rr, pc);
-            if (r < R && wide && c + kPer <= C) {
-                cp_async16(q, p);
-            } else {
-                __align__(16) T e[kPer];
+        if (wide && r0 + kTileR <= R && c0 + kTileC <= C) {
+            constexpr int kStep = kThreads / kPieces;  // rows per turn: 32, or 16 of fp32
+            const int rr = threadIdx.x / kPieces, pc = threadIdx.x % kPieces;
+            const T* p = x + (r0 + rr) * ld + c0 + pc * kPer;
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) e[j] = r < R && c + j < C ? p[j] : T(0.f);
-                *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(e);
+            for (int i = 0; i < kTileR / kStep; ++i, p += kStep * ld) cp_async16(to + place(rr + i * kStep, pc), p);
+        } else {
+#pragma unroll 1
+            for (int i = threadIdx.x; i < kTileR * kPieces; i += kThreads) {
+                const int rr = i / kPieces, pc = i % kPieces;
+                const int64_t r = r0 + rr, c = c0 + pc * kPer;
+                const T* p = x + r * ld + c;
+                unsigned char* q = to + place(rr, pc);
+                if (r < R && wide && c + kPer <= C) {
+                    cp_async16(q, p);
+                } else {
+                    __align__(16) T e[kPer];
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) e[j] = r < R && c + j < C ? p[j] : T(0.f);
+                    *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(e);
+                }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        const int64_t r = r0 + threadIdx.x, c = c0 + threadIdx.x;
-        if (rows.q && r < R) row_v = given ? rows.gs[rows.gs_rows ? r : 0] : __uint_as_float(__ldg(row_max + r));
-        if (threadIdx.x < kTileC && c < C) col_v = given ? cols.gs[cols.gs_rows ? c : 0] : __uint_as_float(__ldg(col_max + c));
     };
+    auto fetch_scales = [&](int t) {
+        const int64_t r = (int64_t)(t / col_tiles) * kTileR + threadIdx.x, c = (int64_t)(t % col_tiles) * kTileC + threadIdx.x;
+        if (rows.q && r < R) row_v = given ? rows.gs[rows.gs_rows ? r : 0] : __uint_as_float(__ldcg(row_max + r));
+        if (threadIdx.x < kTileC && c < C) col_v = given ? cols.gs[cols.gs_rows ? c : 0] : __uint_as_float(__ldcg(col_max + c));
+    };
+    if (given) pdl_wait();  // else x is there: the kernel before the maxima's has waited for it
     fetch(blockIdx.x, tiles);
+    pdl_wait();  // the maxima
+    pdl_launch_dependents();
+    fetch_scales(blockIdx.x);
     int buf = 0;
     for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, buf ^= 1) {
         const int64_t r0 = (int64_t)(t / col_tiles) * kTileR, c0 = (int64_t)(t % col_tiles) * kTileC;
         unsigned char* tile = tiles + buf * (kTileR * kPitch);
         auto piece_at = [&](int rr, int pc) { return tile + place(rr, pc); };
         if (rows.q) {
-            const RowScale rs = with_reciprocal(given ? row_v : row_scale(__float_as_uint(row_v)));
+            const RowScale rs = given ? with_reciprocal(row_v) : row_scale(__float_as_uint(row_v));
             row_scales[threadIdx.x] = rs;
             if (!given && c0 == 0 && r0 + threadIdx.x < R) rows.gs[r0 + threadIdx.x] = rs.g;
         }
         if (threadIdx.x < kTileC) {
-            const RowScale rs = with_reciprocal(given ? col_v : row_scale(__float_as_uint(col_v)));
+            const RowScale rs = given ? with_reciprocal(col_v) : row_scale(__float_as_uint(col_v));
             col_scales[threadIdx.x] = rs;
             if (!given && r0 == 0 && c0 + threadIdx.x < C) cols.gs[c0 + threadIdx.x] = rs.g;
         }
         if (t + (int)gridDim.x < n_tiles) {
             fetch(t + gridDim.x, tiles + (buf ^ 1) * (kTileR * kPitch));
+            fetch_scales(t + gridDim.x);
             cp_async_wait_group<1>();
         } else {
             cp_async_wait_group<0>();
@@ -429,8 +571,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 3)
                 m[0] = mag_f32<T>(both & 0xffffu), m[1] = mag_f32<T>(both & 0xffff0000u);
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                sb[e][h] = encode_block<T>(v[e], __uint_as_float(m[e]), col_scales[2 * pair + e], given, codes[e][h]);
+            for (int e = 0; e < 2; ++e) {
+                const RowScale rs = col_scales[2 * pair + e];
+                sb[e][h] = !given && rs.y != 0.f ? encode_block<T, true>(v[e], __uint_as_float(m[e]), rs, false, codes[e][h])
+                                                 : encode_block<T, false>(v[e], __uint_as_float(m[e]), rs, given, codes[e][h]);
+            }
         }
         // the tile's 64 columns lie in one 128-row block of the column operand, its 256 rows in one code tile
         uint8_t* q = cols.q + ((c0 >> 7) * (Rp >> 8) + (r0 >> 8)) * 16384;
@@ -450,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 3)
 
 template <typename T>
 cudaError_t quantize(const T* x, int64_t R, int64_t C, int64_t ld, const moe_nvfp4_operand* rows,
-                     const moe_nvfp4_operand* cols, bool given, unsigned* maxima, cudaStream_t st, bool pdl) {
+                     const moe_nvfp4_operand* cols, bool given, unsigned* maxima, cudaStream_t st) {
     bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
     if (!cols) {
         const int64_t units = pad_to(C, 256) / 32;
@@ -460,19 +605,29 @@ cudaError_t quantize(const T* x, int64_t R, int64_t C, int64_t ld, const moe_nvf
         bool gr = rows->gs_rows != 0;
         uint8_t *q = rows->q, *s = rows->s;
         float* gs = rows->gs;
+        constexpr int kCtas = sizeof(T) == 4 ? 3 : 4;
+        if (wide && units <= kThreads && grid > sm_count() * kCtas) {
+            const void* f = (const void*)nvfp4_rows_stream_kernel<T, kCtas>;
+            const size_t smem = (size_t)2 * kThreads * 32 * sizeof(T);
+            void* args[] = {&x, &R, &C, &ld, &tpr_log, &q, &s, &gs, &given, &gr};
+            return launch_kernel(f, dim3((unsigned)(sm_count() * kCtas)), dim3(kThreads), smem, st, true, args);
+        }
         void* args[] = {&x, &R, &C, &ld, &wide, &tpr_log, &q, &s, &gs, &given, &gr};
-        return launch_kernel((const void*)nvfp4_rows_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, pdl, args);
+        return launch_kernel((const void*)nvfp4_rows_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, true, args);
     }
     unsigned* row_max = rows ? maxima : nullptr;
     unsigned* col_max = maxima + (rows ? R : 0);
     if (!given) {
-        cudaError_t e = cudaMemsetAsync(maxima, 0, sizeof(unsigned) * (size_t)((rows ? R : 0) + C), st);
+        int64_t n = (rows ? R : 0) + C;
+        void* zero_args[] = {&maxima, &n};
+        cudaError_t e = launch_kernel((const void*)nvfp4_zero_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
+                                      true, zero_args);
         if (e != cudaSuccess) return e;
         const int warp_cols = 32 * 16 / (int)sizeof(T);
         int ct = (int)((C + warp_cols - 1) / warp_cols);
-        const int64_t grid = ct * ((R + kThreads - 1) / kThreads);
+        const int64_t grid = ct * ((R + kThreads / 32 * kMaxRows - 1) / (kThreads / 32 * kMaxRows));
         void* args[] = {&x, &R, &C, &ld, &wide, &ct, &row_max, &col_max};
-        e = launch_kernel((const void*)nvfp4_maxima_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, false, args);
+        e = launch_kernel((const void*)nvfp4_maxima_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, true, args);
         if (e != cudaSuccess) return e;
     }
     // the padded contractions: columns to 256 for the row form, rows to 256 for the column form
@@ -483,7 +638,7 @@ cudaError_t quantize(const T* x, int64_t R, int64_t C, int64_t ld, const moe_nvf
     const int resident = sm_count() * (sizeof(T) == 4 ? 1 : 3);
     void* args[] = {&x, &R, &C, &ld, &wide, &ct, &n_tiles, &row_max, &col_max, &a, &b, &given};
     return launch_kernel((const void*)nvfp4_both_kernel<T>, dim3((unsigned)(n_tiles < resident ? n_tiles : resident)), dim3(kThreads),
-                         (size_t)2 * kTileR * kTileC * sizeof(T), st, false, args);
+                         (size_t)2 * kTileR * kTileC * sizeof(T), st, true, args);
 }
 
 // Values of an operand: (E2M1 * E4M3) * row scale, the exact product of the first two rounded once.
@@ -516,12 +671,12 @@ __global__ void __launch_bounds__(kThreads)
 
 cudaError_t launch_nvfp4_quantize(const void* x, moe_dtype dtype, int64_t R, int64_t C, int64_t ld,
                                   const moe_nvfp4_operand* rows, const moe_nvfp4_operand* cols, bool given, void* maxima,
-                                  cudaStream_t st, bool pdl) {
+                                  cudaStream_t st) {
     if (R == 0 || C == 0) return cudaSuccess;
     unsigned* m = static_cast<unsigned*>(maxima);
-    if (dtype == MOE_F32) return quantize(static_cast<const float*>(x), R, C, ld, rows, cols, given, m, st, pdl);
-    if (dtype == MOE_BF16) return quantize(static_cast<const __nv_bfloat16*>(x), R, C, ld, rows, cols, given, m, st, pdl);
-    return quantize(static_cast<const __half*>(x), R, C, ld, rows, cols, given, m, st, pdl);
+    if (dtype == MOE_F32) return quantize(static_cast<const float*>(x), R, C, ld, rows, cols, given, m, st);
+    if (dtype == MOE_BF16) return quantize(static_cast<const __nv_bfloat16*>(x), R, C, ld, rows, cols, given, m, st);
+    return quantize(static_cast<const __half*>(x), R, C, ld, rows, cols, given, m, st);
 }
 
 cudaError_t launch_nvfp4_values(const moe_nvfp4_operand* op, int64_t R, int64_t K, float* v, cudaStream_t st) {

@@ -41,9 +41,10 @@ cudaError_t launch_combine_backward(const uint16_t* dy, const uint16_t* y_perm, 
 // operands' row scales are read, else computed.  maxima: R + C words, for cols with computed scales.
 cudaError_t launch_nvfp4_quantize(const void* x, moe_dtype dtype, int64_t R, int64_t C, int64_t ld,
                                   const moe_nvfp4_operand* rows, const moe_nvfp4_operand* cols, bool given, void* maxima,
-                                  cudaStream_t st, bool pdl);
+                                  cudaStream_t st);
 cudaError_t launch_nvfp4_values(const moe_nvfp4_operand* op, int64_t R, int64_t K, float* v, cudaStream_t st);
-// y [M][ldy] = A B^T (nvfp4_matmul.cu).  pdl: A comes from the launch before, which lets this one start early.
+// y [M][ldy] = A B^T (nvfp4_matmul.cu).  weights_ready: B does not come from the launch before, so its
+// copies may start while that one runs.
 cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_operand* B, int64_t M, int64_t N, int64_t K, void* y,
-                                moe_dtype dtype, int64_t ldy, int* status, cudaStream_t st, bool pdl);
+                                moe_dtype dtype, int64_t ldy, int* status, cudaStream_t st, bool weights_ready);
 }  // namespace moe

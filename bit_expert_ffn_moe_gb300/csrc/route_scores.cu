@@ -487,6 +487,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     constexpr int kBits = NV == 1 ? 1 : NV == 2 ? 2 : NV == 4 ? 3 : NV == 8 ? 4 : NV == 16 ? 5 : 6;  // of a count up to NV
     extern __shared__ double scratch[];
     __shared__ float2 slots[kRouteWarps][32];  // id (bits) and ranking value of the values that pass
+    pdl_wait();
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * warps + warp;
     if (t >= a.T) return;
@@ -716,6 +718,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 template <int NV, typename T, bool DENSE>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel(const __grid_constant__ RouteBackwardArgs a, const bool wide) {
     extern __shared__ float rows[];  // per warp, dense gradients only: the gradient of the scores times the scores [E]
+    pdl_wait();
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * warps + warp;
     if (t >= a.T) return;
@@ -843,7 +847,7 @@ cudaError_t launch_route_scores(const RouteScoresArgs& a, moe_dtype dtype, cudaS
     const int warps = a.E > 512 ? kRouteWarps / 2 : kRouteWarps;  // (less than 60 KB of scratch)
     const size_t smem = (size_t)warps * (kScratchPerExpert * (size_t)a.E + 128);
     void* args[] = {const_cast<RouteScoresArgs*>(&a), &plan};
-    return launch_kernel(f, dim3((a.T + warps - 1) / warps), dim3(32 * warps), smem, st, false, args);
+    return launch_kernel(f, dim3((a.T + warps - 1) / warps), dim3(32 * warps), smem, st, true, args);
 }
 
 cudaError_t launch_route_scores_backward(const RouteBackwardArgs& a, moe_dtype dtype, cudaStream_t st) {
@@ -855,7 +859,7 @@ cudaError_t launch_route_scores_backward(const RouteBackwardArgs& a, moe_dtype d
     bool wide = rows_wide(a.logits, a.ld, dtype) && rows_wide(a.dlogits, a.ldd, dtype);
     void* args[] = {const_cast<RouteBackwardArgs*>(&a), &wide};
     return launch_kernel(f, dim3((a.T + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps),
-                         dense ? sizeof(float) * kRouteWarps * (size_t)a.E : 0, st, false, args);
+                         dense ? sizeof(float) * kRouteWarps * (size_t)a.E : 0, st, true, args);
 }
 
 }  // namespace moe

@@ -71,6 +71,14 @@ __device__ __forceinline__ uint4 out_piece(const uint32_t* v) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// One thread of a converged warp, known as one to the compiler: where it is chosen by its lane number instead, each copy or MMA
+// is issued through a loop over the lanes (about 130 cycles; 8192^3: 165 us, 150 with this for the pair kernel's copies).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
 // ------------------------------------------------------------------ rows kernel
 // One K step (256 values) of M = 128 weight rows x N activation rows: eight scale-atom copies, four MMAs,
 // the commit that frees the stage.  Scale columns of a stage: weights' atom i at sf + 4 i, activations' at
@@ -210,7 +218,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         bulk_load(p + kTile + NT * 128 + kAtoms * kAtom, args.sa + at * kAtoms * kAtom, kAtoms * kAtom, &full[s]);
     };
     const int head = min(kStages, k1 - k0);
-    if (threadIdx.x == 0) {
+    if (warp == 0 && elect_one()) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     constexpr uint32_t kSfBase = NT;  // scale columns after the accumulator
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             int it = head;
             pdl_wait();
             for (int i = 0; i < head; ++i) load_x(i, k0 + i);
@@ -331,53 +339,46 @@ constexpr size_t kPairSmem = (size_t)kPairStages * kPairStageBytes + (512 + 4 * 
 static_assert(kPairStageBytes % 1024 == 0 && kPairSfBase + kPairStages * kPairSfCols <= kTmemCols, "stage alignment, tensor memory");
 static_assert(kPairSmem <= 232448, "shared memory");
 
-// As stage_scales_nv_to_tmem / stage_mmas_nv_commit (tcgen05.cuh) for a CTA pair: the copies run in both CTAs, the
-// commit arrives on the barrier at this offset in both.
-__device__ __forceinline__ void pair_scales_to_tmem(uint32_t sf, uint64_t a, uint64_t b0, uint64_t b1) {
+// The high words of the matrix descriptors of tcgen05.cuh (desc_sw128, desc_sf); the low one is address / 16 | 2^16.
+constexpr uint32_t kSw128High = (1024 >> 4) | (1u << 14) | (2u << 29), kSfHigh = (128 >> 4) | (1u << 14);
+
+// One K step of a pair, by one thread: as stage_scales_nv_to_tmem and stage_mmas_nv_commit (tcgen05.cuh), with copies that run in
+// both CTAs and a commit that arrives on the barrier at this offset in both.  a, b, sa, sb0, sb1: low words.  The step's
+// latency is part of a stage's round trip, so that descriptors are built from 32-bit words, by one thread without a vote.
+__device__ __forceinline__ void pair_scales(uint32_t sf, uint32_t sa, uint32_t sb0, uint32_t sb1) {
     asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%2], %3;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%4], %5;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%6], %7;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%8], %9;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%10], %11;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%12], %13;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%14], %15;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%16], %17;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%18], %19;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%20], %21;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%22], %23;\n\t}" ::"r"(sf),
-        "l"(a), "r"(sf + 4), "l"(a + 32), "r"(sf + 8), "l"(a + 64), "r"(sf + 12), "l"(a + 96), "r"(sf + 16), "l"(b0),
-        "r"(sf + 20), "l"(b1), "r"(sf + 24), "l"(b0 + 32), "r"(sf + 28), "l"(b1 + 32), "r"(sf + 32), "l"(b0 + 64),
-        "r"(sf + 36), "l"(b1 + 64), "r"(sf + 40), "l"(b0 + 96), "r"(sf + 44), "l"(b1 + 96)
+        "{\n\t.reg .b32 c, l;\n\t.reg .b64 t;\n\t"
+#define COPY(column, low, atom)                                                             \
+    "add.u32 c, %0, " #column ";\n\tadd.u32 l, " low ", " #atom ";\n\tmov.b64 t, {l, %4};\n\t" \
+    "tcgen05.cp.cta_group::2.32x128b.warpx4 [c], t;\n\t"
+        COPY(0, "%1", 0) COPY(16, "%2", 0) COPY(20, "%3", 0) COPY(4, "%1", 32) COPY(24, "%2", 32) COPY(28, "%3", 32)
+        COPY(8, "%1", 64) COPY(32, "%2", 64) COPY(36, "%3", 64) COPY(12, "%1", 96) COPY(40, "%2", 96) COPY(44, "%3", 96)
+#undef COPY
+        "}" ::"r"(sf), "r"(sa), "r"(sb0), "r"(sb1), "n"(kSfHigh)
         : "memory");
 }
-__device__ __forceinline__ void pair_mmas_commit(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sf,
-                                                 uint32_t accumulate, uint64_t* bar) {
+__device__ __forceinline__ void pair_products(uint32_t d, uint32_t sf, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                              uint32_t bar) {
     asm volatile(
-        "{\n\t.reg .pred e, p, q;\n\t.reg .b16 both;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b16 both;\n\t.reg .b32 c, e, l, m;\n\t.reg .b64 t, u;\n\t"
         "mov.b16 both, 3;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.eq.b32 q, %4, %4;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %7, %8, %3, [%9], [%10], q;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %11, %12, %3, [%13], [%14], q;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %15, %16, %3, [%17], [%18], q;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%19], both;\n\t}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(sf), "r"(sf + 16), "l"(ad + 2), "l"(bd + 2), "r"(sf + 4), "r"(sf + 24),
-        "l"(ad + 4), "l"(bd + 4), "r"(sf + 8), "r"(sf + 32), "l"(ad + 6), "l"(bd + 6), "r"(sf + 12), "r"(sf + 40),
-        "r"(smem_u32(bar))
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.eq.b32 q, %5, %5;\n\t"
+#define PRODUCT(i, pred)                                                                                   \
+    "add.u32 l, %1, 2*" #i ";\n\tadd.u32 m, %2, 2*" #i ";\n\tmov.b64 t, {l, %7};\n\tmov.b64 u, {m, %7};\n\t" \
+    "add.u32 c, %4, 4*" #i ";\n\tadd.u32 e, %4, 16+8*" #i ";\n\t"                                          \
+    "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], t, u, %3, [c], [e], " pred ";\n\t"
+        PRODUCT(0, "p") PRODUCT(1, "q") PRODUCT(2, "q") PRODUCT(3, "q")
+#undef PRODUCT
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6], both;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(sf), "r"(accumulate), "r"(bar), "n"(kSw128High)
         : "memory");
 }
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {  // by one thread
     asm volatile(
-        "{\n\t.reg .pred e;\n\t.reg .b16 both;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
+        "{\n\t.reg .b16 both;\n\t"
         "mov.b16 both, 3;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n\t}" ::"r"(smem_u32(bar))
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
 // A box of whole 1 KB rows of an operand's bytes (the map: [bytes / 1024][256 words]) into this CTA's shared memory; the bytes
@@ -454,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     auto stage = [&](int s) { return smem + (size_t)s * kPairStageBytes; };
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             int it = 0;
             bool ok = true;
             for (int t = first; t < n_tiles && ok; t += step) {
@@ -485,28 +486,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
         }
     } else if (warp == 1 && rank == 0) {
-        const uint32_t idesc = idesc_mxf4nvf4_ue4m3(256, 256);
-        int it = 0, tile = 0;
-        bool ok = true;
-        for (int t = first; t < n_tiles && ok; t += step, ++tile) {
-            if (!mbar_wait_warp(acc_empty, (tile & 1) ^ 1, abort_flag, args.status)) break;
-            tc_fence_after();
-            for (int kt = 0; kt < KT; ++kt, ++it) {
-                const int s = it % kPairStages;
-                if (!mbar_wait_warp(&full[s], (it / kPairStages) & 1, abort_flag, args.status)) {
-                    ok = false;
-                    break;
-                }
+        if (elect_one()) {
+            const uint32_t idesc = idesc_mxf4nvf4_ue4m3(256, 256), base = smem_u32(smem);
+            int s = 0, tile = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            // waits for a stage and sends its scales to tensor memory
+            auto scales = [&]() {
+                if (!mbar_wait(&full[s], phase, abort_flag, args.status)) return false;
                 tc_fence_after();
-                unsigned char* p = stage(s);
-                const uint32_t sf = tmem + kPairSfBase + s * kPairSfCols;
-                pair_scales_to_tmem(sf, desc_sf(p + 2 * kTile), desc_sf(p + 2 * kTile + 4 * kAtom), desc_sf(p + 2 * kTile + 8 * kAtom));
-                pair_mmas_commit(tmem, desc_sw128(p), desc_sw128(p + kTile), idesc, sf, kt > 0 ? 1u : 0u, &empty[s]);
+                const uint32_t sf = ((base + s * kPairStageBytes + 2 * kTile) >> 4) | (1u << 16);
+                pair_scales(tmem + kPairSfBase + s * kPairSfCols, sf, sf + 4 * kAtom / 16, sf + 8 * kAtom / 16);
+                return true;
+            };
+            auto products = [&](uint32_t accumulate) {
+                const uint32_t p = ((base + s * kPairStageBytes) >> 4) | (1u << 16);
+                pair_products(tmem, tmem + kPairSfBase + s * kPairSfCols, p, p + kTile / 16, idesc, accumulate, smem_u32(&empty[s]));
+                if (++s == kPairStages) s = 0, phase ^= 1;
+            };
+            for (int t = first; t < n_tiles && ok; t += step, ++tile) {
+                // (the first step's scales while the results of the tile before are read)
+                if (!scales() || !mbar_wait(acc_empty, (tile & 1) ^ 1, abort_flag, args.status)) break;
+                tc_fence_after();
+                products(0u);
+                for (int kt = 1; kt < KT; ++kt) {
+                    if (!scales()) {
+                        ok = false;
+                        break;
+                    }
+                    products(1u);
+                }
+                if (ok) pair_commit(acc_full);
             }
-            if (!ok) break;
-            pair_commit(acc_full);
+            pair_commit(mma_done);
         }
-        pair_commit(mma_done);
+        __syncwarp();
     } else if (warp >= 2) {
         const int q = warp & 3, half = (warp - 2) / 4;
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + 128 * half;

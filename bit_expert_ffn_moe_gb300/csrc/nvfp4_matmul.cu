@@ -13,8 +13,12 @@
 //           and each weight byte is read once.  Bound by the weight read; the K range of a tile is split
 //           over the CTAs of a cluster, whose partial sums are exchanged through distributed shared
 //           memory and added in rank order.
-//   pair    more rows: 256 x 256 tiles by pairs of CTAs, persistent; bound by the shared-memory feed and the
-//           FP4 rate.
+//           16 x 4096 x 8192: 6 us with its launch, 3.2 TB/s; 4 us of it are the kernel's fixed chain (set-up, first
+//           copies, last products, exchange, store).
+//   pair    more rows: 256 x 256 tiles by pairs of CTAs, persistent.  8192^3: 152 us, 7.2 PFLOP/s; 4096 x 4096 x 8192: 45.6 us
+//           (256 tiles in 4 waves of 76 pairs).  A K step takes 540 cycles, of which 300 are what it takes to write its
+//           operands to shared memory and 250 .. 380 to read them; a tile adds about 600 cycles without products while
+//           its results are read.
 // Every barrier wait is bounded: on expiry the CTA records MOE_ERR_TIMEOUT, waits (bounded) for its own
 // copies and MMAs, frees tensor memory and exits.
 #include "ops.cuh"
@@ -403,6 +407,26 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
         "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
+// 64 bytes (`left` elements or more) of each of a warp's 32 rows (those below `rows`) from shared memory to y, row by row, a word
+// per lane.  Out of line: the epilogue's code has to stay small, or it waits for its instructions.
+template <typename T>
+__device__ __noinline__ void store_ragged(const uint32_t* turn, T* y, int64_t ldy, int rows, int left) {
+    constexpr int kPerWord = 4 / (int)sizeof(T);
+    const int lane = threadIdx.x & 31, r0 = lane >> 4;
+    left -= kPerWord * (lane & 15);
+    T* to = y + r0 * ldy + kPerWord * (lane & 15);
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i, to += 2 * ldy) {
+        const uint32_t w = turn[17 * (2 * i + r0) + (lane & 15)];
+        if (2 * i + r0 >= rows || left <= 0) continue;
+        if (sizeof(T) == 4 || (left > 1 && reinterpret_cast<uintptr_t>(to) % 4 == 0)) {
+            *reinterpret_cast<uint32_t*>(to) = w;
+        } else {
+            reinterpret_cast<uint16_t*>(to)[0] = (uint16_t)w;
+            if (left > 1) reinterpret_cast<uint16_t*>(to)[1] = (uint16_t)(w >> 16);
+        }
+    }
+}
 struct PairArgs {
     CUtensorMap qa, sa, qb, sb;  // the operands' bytes in rows of 1 KB
     MatmulArgs m;
@@ -577,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 } else {
                     // rows that do not start on 16 bytes, or the ragged last columns: 64 bytes of each of the warp's 32 rows
                     // through shared memory, then stored row by row, a word per lane
-                    constexpr int kHalves = (int)sizeof(T) / 2, kPerWord = 4 / (int)sizeof(T);
+                    constexpr int kHalves = (int)sizeof(T) / 2;
 #pragma unroll
                     for (int h = 0; h < kHalves; ++h) {
 #pragma unroll
@@ -587,21 +611,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                             to[0] = o.x, to[1] = o.y, to[2] = o.z, to[3] = o.w;
                         }
                         __syncwarp();
-                        const int col = 32 * c + (32 / kHalves) * h + kPerWord * (lane & 15), left = live - col;
-                        T* at = y + (m0 + (lane >> 4)) * args.ldy + n0 + col;
-#pragma unroll 4
-                        for (int i = 0; i < 16; ++i) {
-                            const uint32_t w = turn[17 * (2 * i + (lane >> 4)) + (lane & 15)];
-                            if (m0 + 2 * i + (lane >> 4) < args.M && left > 0) {
-                                T* to = at + 2 * i * args.ldy;
-                                if (sizeof(T) == 4 || (left > 1 && reinterpret_cast<uintptr_t>(to) % 4 == 0)) {
-                                    *reinterpret_cast<uint32_t*>(to) = w;
-                                } else {
-                                    reinterpret_cast<uint16_t*>(to)[0] = (uint16_t)w;
-                                    if (left > 1) reinterpret_cast<uint16_t*>(to)[1] = (uint16_t)(w >> 16);
-                                }
-                            }
-                        }
+                        const int col = 32 * c + (32 / kHalves) * h;
+                        store_ragged<T>(turn, y + m0 * args.ldy + n0 + col, args.ldy, (int)min((int64_t)32, args.M - m0), live - col);
                         __syncwarp();
                     }
                 }
@@ -692,11 +703,11 @@ cudaError_t launch_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_oper
     if (M <= 16) return launch_rows<16>(a, st);
     if (M <= 32) return launch_rows<32>(a, st);
     if (M <= 64) return launch_rows<64>(a, st);
-    // Beyond 128 rows the pair kernel's tiles are few and large: while 128 x 128 tiles leave half the SMs idle, these, with their
-    // K range split over a cluster, finish sooner (us, pair / rows: 256 x 4096 x 8192 17.6 / 12.1, 777 x 1000 x 1544 9.5 / 8.9,
-    // 200 x 600 x 300 8.7 / 7.3, 1024^3 7.9 / 8.0; without half the SMs idle, 512 x 4096 x 8192 17.8 / 18.1, 512 x 8192 x 1024
-    // 8.4 / 17.5).
-    if (M <= 128 || ((M + 127) / 128) * ((N + 127) / 128) * 2 <= sm_count()) return launch_rows<128>(a, st);
+    // Beyond 128 rows the pair kernel's tiles are few and large: while one wave of 128 x 128 tiles (their K range split over a
+    // cluster where they leave SMs idle) covers the results, these finish sooner, unless K is so short that the fixed costs
+    // decide (us, rows / pair: 256 x 4096 x 8192 11.1 / 14.5, 512 x 4096 x 8192 13.4 / 15.5, 256 x 8192 x 4096 10.0 / 10.9, 777 x
+    // 1000 x 1544 8.0 / 8.4; beyond a wave, 512 x 8192 x 1024 13.3 / 7.7; short K, 1024^3 7.4 / 7.1, 200 x 600 x 300 6.6 / 6.3).
+    if (M <= 128 || (a.KT > 4 && ((M + 127) / 128) * ((N + 127) / 128) <= sm_count())) return launch_rows<128>(a, st);
     int MT = (int)((M + 255) / 256), NT = (int)((N + 255) / 256);
     const int64_t tiles = (int64_t)MT * NT, pairs = sm_count() / 2;
     PairArgs p;

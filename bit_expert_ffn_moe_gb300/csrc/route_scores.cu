@@ -480,7 +480,8 @@ __device__ __forceinline__ int lanes_before(uint32_t set, double v) {
 // (about k^2 / 64 at random): those go to lanes of their own, in id order, and the smallest are dropped one
 // by one until k are left.  With fp32 ranking values the bound is lowered by their error, so that every value
 // which might belong to the picks is among these; what is too close to the border is settled in 64 bits.
-// Issue-bound, hence the care for instructions: 16384 tokens of 256 fp32 logits are 2.5 us of reading.
+// Issue-bound, hence the care for instructions: 16384 tokens of 256 fp32 logits (2.5 us of reading) take 13.9 us with 8 groups and
+// a bias (about 700 warp instructions a token, 68% of the issue slots), 8.8 us without.
 template <int NV, typename T>
 __global__ void __launch_bounds__(32 * kRouteWarps)
     route_scores_kernel(const __grid_constant__ RouteScoresArgs a, const __grid_constant__ RoutePlan plan) {
@@ -715,9 +716,60 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
 // 1 - s = sigmoid(-l).  Softmax: dl = s (ds - sum ds s); with renormalised weights and no other gradient of
 // the scores that sum is zero by itself, so that, as for sigmoid scores, only the picked experts get a
 // gradient: the row is then written as zeros and the picks' values on top, and only the picked logits are read.
-template <int NV, typename T, bool DENSE>
+// The sparse form: 2^seg_log lanes (k or a few more) share a token, so that a warp's chain of dependent loads (ids, logits)
+// serves several tokens; sums over a segment.  8192 tokens of 256 fp32 logits: 2.9 us (4.2 with a
+// warp per token; 1.3 us is what writing them takes), 65536 of 64 bf16: 5.8 (12.5).
+constexpr int kSparseWarps = 4;
+template <typename T>
+__global__ void __launch_bounds__(32 * kSparseWarps)
+    route_scores_backward_sparse_kernel(const __grid_constant__ RouteBackwardArgs a, const bool wide, const int seg_log) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = 1 << seg_log, per = 32 >> seg_log;
+    const int64_t t0 = ((int64_t)blockIdx.x * kSparseWarps + warp) * per, t = t0 + (lane >> seg_log);
+    if (t0 >= a.T) return;
+    const int E = a.E, k = a.k, j = lane & (seg - 1);
+    const bool softmax = a.rule.score == MOE_SCORE_SOFTMAX, renorm = a.rule.renormalize != 0, on = t < a.T && j < k;
+    T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
+    const int id = on ? a.ids[t * k + j] : -1;
+    const float dw_in = on ? a.dw[t * k + j] : 0.f;
+    const bool valid = id >= 0 && id < E;
+    const float lp = valid ? to_f32(static_cast<const T*>(a.logits)[t * a.ld + id]) : -INFINITY;
+    // zeros, over which the picks' values go
+    const int rows = (int)min((int64_t)per, a.T - t0);
+    T* to = static_cast<T*>(a.dlogits) + t0 * a.ldd;
+    for (int r = 0; r < rows; ++r, to += a.ldd) {
+        if (wide) {
+            for (int p = lane; p < E * (int)sizeof(T) / 16; p += 32) reinterpret_cast<uint4*>(to)[p] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int e = lane; e < E; e += 32) to[e] = from_f32<T>(0.f);
+        }
+    }
+    __syncwarp();
+    const float dw = valid && in_service(lp) ? dw_in * a.rule.scale : 0.f;
+    auto sum = [&](float v) {
+        for (int m = seg >> 1; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        return v;
+    };
+    float g;  // u_j du_j, the product that the logits' gradient needs
+    if (renorm) {
+        float ref = in_service(lp) ? clamp_logit(lp) : -kMaxF32;
+        for (int m = seg >> 1; m > 0; m >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, m));
+        if (!softmax) ref = fminf(ref, 0.f);
+        const float u = score_ratio(lp, softmax, ref);
+        const float S = sum(u);
+        const float r = S > 0.f ? u / S : 0.f;
+        g = r * (dw - sum(dw * r));
+    } else {
+        g = dw * sigmoid_f32(lp);
+    }
+    if (valid) out[id] = from_f32<T>(in_service(lp) ? (softmax ? g : g * sigmoid_f32(-lp)) : 0.f);
+}
+
+// The dense form: one warp per token, as the rules' kernel.
+template <int NV, typename T>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel(const __grid_constant__ RouteBackwardArgs a, const bool wide) {
-    extern __shared__ float rows[];  // per warp, dense gradients only: the gradient of the scores times the scores [E]
+    extern __shared__ float rows[];  // per warp: the gradient of the scores times the scores [E]
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -733,28 +785,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel
     const bool valid = id >= 0 && id < E;
     const float lp = valid ? to_f32(row[id]) : -INFINITY;
     const float dw = valid && in_service(lp) ? a.dw[t * k + lane] * a.rule.scale : 0.f;
-    [[maybe_unused]] float l[NV];
+    float l[NV];
     RowNorm norm = {0.f, 0.f};
-    [[maybe_unused]] float* ds = rows + (size_t)warp * E;
-    if constexpr (DENSE) {
-        load_chunk<NV>(row, E, wide, l);
-        if (softmax) norm = softmax_norm<NV>(l);
+    float* ds = rows + (size_t)warp * E;
+    load_chunk<NV>(row, E, wide, l);
+    if (softmax) norm = softmax_norm<NV>(l);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (e0 + i < E) ds[e0 + i] = 0.f;
-        __syncwarp();
-    } else {  // zeros, over which the picks' values go
-        constexpr int bytes = NV * (int)sizeof(T);
-        if (wide && bytes % 16 == 0 && e0 + NV <= E) {
-#pragma unroll
-            for (int i = 0; i < bytes / 16; ++i) reinterpret_cast<uint4*>(out + e0)[i] = make_uint4(0, 0, 0, 0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                if (e0 + i < E) out[e0 + i] = from_f32<T>(0.f);
-        }
-        __syncwarp();
-    }
+    for (int i = 0; i < NV; ++i)
+        if (e0 + i < E) ds[e0 + i] = 0.f;
+    __syncwarp();
     float g;  // u_j du_j, the product that the logits' gradient needs
     if (renorm) {
         float ref = warp_max_f32(in_service(lp) ? clamp_logit(lp) : -kMaxF32);
@@ -766,32 +805,28 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_scores_backward_kernel
     } else {
         g = dw * score_f32(lp, softmax, norm);
     }
-    if constexpr (!DENSE) {
-        if (valid) out[id] = from_f32<T>(in_service(lp) ? (softmax ? g : g * sigmoid_f32(-lp)) : 0.f);
-    } else {
-        if (valid) ds[id] = g;
-        __syncwarp();
-        float total = 0.f;  // softmax: sum of ds s over all experts
-        float gs[NV];
+    if (valid) ds[id] = g;
+    __syncwarp();
+    float total = 0.f;  // softmax: sum of ds s over all experts
+    float gs[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            gs[i] = 0.f;
-            if (e0 + i >= E) continue;
-            gs[i] = ds[e0 + i];
-            float extra = 0.f;
-            if (a.dscores && in_service(l[i])) extra = a.dscores[t * E + e0 + i] * score_f32(l[i], softmax, norm);
-            if (!renorm) total += gs[i];
-            total += extra;
-            gs[i] += extra;
-        }
-        if (softmax) total = warp_butterfly_sum(total);
+    for (int i = 0; i < NV; ++i) {
+        gs[i] = 0.f;
+        if (e0 + i >= E) continue;
+        gs[i] = ds[e0 + i];
+        float extra = 0.f;
+        if (a.dscores && in_service(l[i])) extra = a.dscores[t * E + e0 + i] * score_f32(l[i], softmax, norm);
+        if (!renorm) total += gs[i];
+        total += extra;
+        gs[i] += extra;
+    }
+    if (softmax) total = warp_butterfly_sum(total);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (e0 + i >= E) continue;
-            float dl = 0.f;
-            if (in_service(l[i])) dl = softmax ? gs[i] - score_f32(l[i], true, norm) * total : gs[i] * sigmoid_f32(-l[i]);
-            out[e0 + i] = from_f32<T>(dl);
-        }
+    for (int i = 0; i < NV; ++i) {
+        if (e0 + i >= E) continue;
+        float dl = 0.f;
+        if (in_service(l[i])) dl = softmax ? gs[i] - score_f32(l[i], true, norm) * total : gs[i] * sigmoid_f32(-l[i]);
+        out[e0 + i] = from_f32<T>(dl);
     }
 }
 
@@ -806,20 +841,15 @@ const void* scores_kernel(int E) {
                       : (const void*)route_scores_kernel<32, T>;
 }
 
-template <typename T, bool DENSE>
+template <typename T>
 const void* backward_kernel(int E) {
     const int nv = (E + 31) / 32;
-    return nv <= 1    ? (const void*)route_scores_backward_kernel<1, T, DENSE>
-           : nv <= 2  ? (const void*)route_scores_backward_kernel<2, T, DENSE>
-           : nv <= 4  ? (const void*)route_scores_backward_kernel<4, T, DENSE>
-           : nv <= 8  ? (const void*)route_scores_backward_kernel<8, T, DENSE>
-           : nv <= 16 ? (const void*)route_scores_backward_kernel<16, T, DENSE>
-                      : (const void*)route_scores_backward_kernel<32, T, DENSE>;
-}
-
-template <typename T>
-const void* backward_kernel(int E, bool dense) {
-    return dense ? backward_kernel<T, true>(E) : backward_kernel<T, false>(E);
+    return nv <= 1    ? (const void*)route_scores_backward_kernel<1, T>
+           : nv <= 2  ? (const void*)route_scores_backward_kernel<2, T>
+           : nv <= 4  ? (const void*)route_scores_backward_kernel<4, T>
+           : nv <= 8  ? (const void*)route_scores_backward_kernel<8, T>
+           : nv <= 16 ? (const void*)route_scores_backward_kernel<16, T>
+                      : (const void*)route_scores_backward_kernel<32, T>;
 }
 
 }  // namespace
@@ -853,13 +883,25 @@ cudaError_t launch_route_scores(const RouteScoresArgs& a, moe_dtype dtype, cudaS
 cudaError_t launch_route_scores_backward(const RouteBackwardArgs& a, moe_dtype dtype, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     const bool dense = a.dscores || (a.rule.score == MOE_SCORE_SOFTMAX && !a.rule.renormalize);
-    const void* f = dtype == MOE_F32    ? backward_kernel<float>(a.E, dense)
-                    : dtype == MOE_BF16 ? backward_kernel<__nv_bfloat16>(a.E, dense)
-                                        : backward_kernel<__half>(a.E, dense);
-    bool wide = rows_wide(a.logits, a.ld, dtype) && rows_wide(a.dlogits, a.ldd, dtype);
+    bool wide = rows_wide(a.dlogits, a.ldd, dtype);
+    if (!dense) {
+        wide = wide && a.E * (dtype == MOE_F32 ? 4 : 2) % 16 == 0;
+        int seg_log = 2;
+        while (1 << seg_log < a.k) ++seg_log;
+        const int tokens = kSparseWarps * (32 >> seg_log);
+        const void* f = dtype == MOE_F32    ? (const void*)route_scores_backward_sparse_kernel<float>
+                        : dtype == MOE_BF16 ? (const void*)route_scores_backward_sparse_kernel<__nv_bfloat16>
+                                            : (const void*)route_scores_backward_sparse_kernel<__half>;
+        void* args[] = {const_cast<RouteBackwardArgs*>(&a), &wide, &seg_log};
+        return launch_kernel(f, dim3((a.T + tokens - 1) / tokens), dim3(32 * kSparseWarps), 0, st, true, args);
+    }
+    const void* f = dtype == MOE_F32    ? backward_kernel<float>(a.E)
+                    : dtype == MOE_BF16 ? backward_kernel<__nv_bfloat16>(a.E)
+                                        : backward_kernel<__half>(a.E);
+    wide = wide && rows_wide(a.logits, a.ld, dtype);
     void* args[] = {const_cast<RouteBackwardArgs*>(&a), &wide};
     return launch_kernel(f, dim3((a.T + kRouteWarps - 1) / kRouteWarps), dim3(32 * kRouteWarps),
-                         dense ? sizeof(float) * kRouteWarps * (size_t)a.E : 0, st, true, args);
+                         sizeof(float) * kRouteWarps * (size_t)a.E, st, true, args);
 }
 
 }  // namespace moe

@@ -289,3 +289,55 @@ def test_no_rows_other_streams_and_capture():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ops.nvfp4_linear(x, W, ws))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("R_,C", [(5000, 40), (2500, 1544), (650, 7112), (700, 8192)])
+def test_operands_of_many_rows(dtype, R_, C):
+    """More rows than the SMs hold at once; rows of zeros, and of scales that take the division (fp32), among them."""
+    x = matrix(R_, C, dtype, R_ + C)
+    x[R_ // 3] = 0
+    x[R_ - 1] *= 2.0 ** -10
+    if dtype == "fp32":
+        x[5] *= 1e-30
+    op, strided = ops.nvfp4_operand(R_, C), ops.nvfp4_operand(R_, C)
+    ops.nvfp4_quantize(x.cuda(), op)
+    check_operand(op, x.float().numpy())
+    wide = torch.zeros(R_, C + 24, dtype=x.dtype, device="cuda")
+    wide[:, 8:C + 8] = x.cuda()
+    ops.nvfp4_quantize(wide[:, 8:C + 8], strided)
+    check_operand(strided, x.float().numpy())
+    given = ops.nvfp4_operand(R_, C)
+    given.gs.copy_(op.gs)
+    ops.nvfp4_quantize(x.cuda(), given, scales_given=True)
+    assert torch.equal(given.values(), op.values())
+
+
+def test_calls_in_a_row_see_what_the_calls_before_them_wrote():
+    """No synchronisation between the steps: operands of a weight and of x are made right before the products that read them."""
+    def steps(pause):
+        out = []
+        x = matrix(300, 520, "bf16", 1).cuda()
+        w = matrix(264, 520, "bf16", 2).cuda()
+        W, Wt, X = ops.nvfp4_operand(264, 520), ops.nvfp4_operand(520, 264), ops.nvfp4_operand(300, 520)
+        ws = ops.nvfp4_workspace(300, 520, 520)
+        for i in range(24):
+            x.mul_(1.03125)
+            w.add_(0.0625 * (i % 3))
+            pause()
+            ops.nvfp4_quantize(w, W, Wt, ws)
+            pause()
+            y = ops.nvfp4_linear(x[:1 + 13 * i], W, ws)
+            pause()
+            ops.nvfp4_quantize(x, X)
+            pause()
+            z = ops.nvfp4_matmul(X, W, torch.bfloat16, ws)
+            pause()
+            back = ops.nvfp4_linear(z, Wt, ws)
+            pause()
+            out += [y, z, back]
+        torch.cuda.synchronize()
+        return out
+    together, apart = steps(lambda: None), steps(torch.cuda.synchronize)
+    for a, b in zip(together, apart):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))

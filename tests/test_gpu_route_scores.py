@@ -210,3 +210,20 @@ def test_logits_call_feeds_the_rules():
     B.moe_route(x, W_r, b, cfg.T, cfg.d, cfg.E, cfg.k, ids0, w0, ws)
     assert torch.equal(ids, ids0)
     np.testing.assert_allclose(w.cpu().numpy(), w0.cpu().numpy(), rtol=2.0 ** -19)
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 7, 1), (3, 33, 3), (67, 1000, 32), (130, 64, 5), (1001, 300, 17)])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_sparse_gradient_equals_the_dense_one(score, T, E, k):
+    """A gradient of the scores of zero asks for the dense kernel: it rounds the same products, of a softmax with one subtraction of a
+    sum that is zero but for its roundings (k products, each off by 2^-24 of itself or less, and k sums)."""
+    g = torch.Generator().manual_seed(T + E)
+    logits = (3 * torch.randn(T, E + 5, generator=g)).cuda()[:, 2:2 + E]
+    dw = torch.randn(T, k, generator=g).cuda()
+    rule = ops.route_rule(score, scale=1.5)
+    ids, _ = ops.route_scores(logits, k, rule)
+    sparse = ops.route_scores_backward(logits, ids, dw, rule)
+    dense = ops.route_scores_backward(logits, ids, dw, rule, torch.zeros(T, E, device="cuda"))
+    bound = 1.5 * dw.abs().sum(1, keepdim=True) * (4 * k + 16) * 2.0 ** -24
+    assert ((sparse - dense).abs() <= bound).all()
+    assert (sparse.gather(1, ids.long()) != 0).any() or k == 1

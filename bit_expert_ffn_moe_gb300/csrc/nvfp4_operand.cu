@@ -15,15 +15,16 @@
 // reciprocal with one Newton step; a GPU test runs all mantissas of D against the division.  fp32 maxima, and
 // row scales outside 2^-50 .. 2^50, take the division.
 //
-// A thread encodes a block of 16: its maximum is taken on the packed bits (two 16-bit elements per
-// instruction), few enough registers keep most of an SM's warps resident, which hides the loads.
-//   rows only   the threads of a row hold it in registers (up to 8192 elements), reduce its maximum, encode.
+// A thread encodes blocks of 16: their maximum is taken on the packed bits (two 16-bit elements per instruction).
+//   rows only   the threads of a row hold it in registers (up to 8192 elements), reduce its maximum, encode; many rows
+//               are streamed through shared memory by persistent CTAs.
 //   with columns  two passes over x: the row and column maxima (integer maxima of the bits: the order of the
 //               atomics does not matter), then tiles of 256 rows x 64 columns through shared memory, encoded
 //               along their rows and along their columns, two columns per thread; 256 rows are a whole
-//               128-byte row of a column operand's code tile.
-// HBM bounds both: (2 or 4) R C bytes in, 9/16 R C out per form; the second pass of the two-form kernel
-// finds x in L2 while it fits there.
+//               128-byte row of a column operand's code tile.  The second pass finds x in L2 while it fits there.
+// (2 or 4) R C bytes in, 9/16 R C out per form.  Rows of a bf16 matrix 4096 x 8192: 19 us (4.5 TB/s), both forms 45.7 us (11 of
+// them the maxima).  The encoding, about 110 warp instructions per block and lane, keeps 58% of the issue slots busy; leaving out
+// the stores (43.7 us) or smaller tiles with a third more warps (49) hardly matter or hurt.
 #include <type_traits>
 
 #include "ops.cuh"

@@ -14,7 +14,7 @@ constexpr int kThreads = 256, kMostThreads = 320;
 
 // `warps` warps of a CTA share a token: thread c of them the 8-feature pieces c, c + 32 warps, ...  SLOTS slots of a token are
 // in registers at a time, and PIECES pieces of each, so that tokens of few slots have as many loads in flight (6546 tokens of
-// one slot, d = 6632: 46.8 us, 81 with one piece; 800 tokens of 12 slots, d = 6448: @@B@@ us as 6 + 6, 57 as 8 + 4).
+// one slot, d = 6632: 46.8 us, 81 with one piece; 800 tokens of 12 slots, d = 6448: 46.8 us as 6 + 6, 54 as 8 + 4).
 template <int SLOTS, int PIECES>
 __global__ void __launch_bounds__(kMostThreads, 3)
     combine_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ y_perm,

@@ -91,6 +91,15 @@ __device__ __forceinline__ void cp_async16_part(void* smem, const void* gmem, in
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sa), "l"(gmem), "r"(bytes) : "memory");
 }
 
+// The same of 4 bytes.
+__device__ __forceinline__ void cp_async4_part(void* smem, const void* gmem, int bytes) {
+    const uint32_t sa = (uint32_t)__cvta_generic_to_shared(smem);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sa), "l"(gmem), "r"(bytes) : "memory");
+}
+// Shared memory of a warp's 32 units in the streaming kernel.
+template <typename T, bool WIDE>
+__host__ __device__ constexpr int stream_warp_bytes() { return WIDE ? 32 * 32 * (int)sizeof(T) : (32 * (8 * (int)sizeof(T) + 1) + 4) * 4; }
+
 // The larger magnitudes of a word of one fp32 or two 16-bit elements (a: magnitudes already).
 template <typename T>
 __device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b) {
@@ -290,16 +299,22 @@ __global__ void __launch_bounds__(kThreads, 4)
     }
 }
 
-// Rows of up to 8192 elements that start on 16 bytes, where there are more than the SMs hold at once: persistent CTAs, each
-// with the next row's copy (cp.async) in flight while this one is reduced and encoded.  A warp reads and encodes what it copied
-// itself; its 16-byte pieces are swizzled, so that lanes reading a unit each meet all banks.
-template <typename T, int CTAS>
+// Rows of up to 8192 elements: persistent CTAs, each with the next row's copy (cp.async) in flight while this one is reduced and
+// encoded.  A warp reads and encodes what it copied itself.
+//   WIDE   rows that start on 16 bytes, where there are more than twice what the SMs hold at once: pieces of 16 bytes, swizzled, so that
+//          lanes reading a unit each meet all banks.
+//   else   words of 4 bytes from the aligned one that holds the row's first element (its other half, when the element is the
+//          second of two, lies in front of it in the same allocation, which starts on 4 bytes at least), a word of padding per
+//          unit; a row that starts on 2 bytes is shifted while it is read.  4096 x 8191 bf16: 24.6 us, 64 where every thread
+//          loads its own elements.
+template <typename T, int CTAS, bool WIDE>
 __global__ void __launch_bounds__(kThreads, CTAS)
     nvfp4_rows_stream_kernel(const T* __restrict__ x, int64_t R, int64_t K, int64_t ld, int tpr_log, uint8_t* __restrict__ q,
                              uint8_t* __restrict__ s, float* __restrict__ gs, bool given, bool gs_rows) {
     extern __shared__ __align__(16) unsigned char rows_smem[];  // two buffers of 32 elements per thread
     __shared__ __align__(16) uint32_t part[2][kThreads / 32];
-    constexpr int kPieces = 32 * (int)sizeof(T) / 16, kBuffer = kThreads * kPieces * 16, kPer = 16 / (int)sizeof(T);
+    constexpr int kPieces = 32 * (int)sizeof(T) / 16, kPer = 16 / (int)sizeof(T), kUnitWords = 4 * kPieces;
+    constexpr int kWarpBytes = stream_warp_bytes<T, WIDE>(), kBuffer = kThreads / 32 * kWarpBytes;
     pdl_wait();
     pdl_launch_dependents();
     const int tpr = 1 << tpr_log, rpc = kThreads >> tpr_log;  // threads a row, rows a turn
@@ -307,25 +322,61 @@ __global__ void __launch_bounds__(kThreads, CTAS)
     const uint32_t sub = threadIdx.x >> tpr_log;
     const int units = (int)((K + 255) >> 8) * 8;
     const int64_t turns = (R + rpc - 1) / rpc;
-    unsigned char* mine = rows_smem + (threadIdx.x >> 5) * (32 * kPieces * 16);  // this warp's pieces
+    unsigned char* mine = rows_smem + (threadIdx.x >> 5) * kWarpBytes;  // this warp's pieces
     const int warp_e = (u0 & ~31) * 32;  // first element of the warp's part of its row
     auto fetch = [&](int64_t turn, unsigned char* to) {
         const int64_t r = turn * rpc + sub;
         const T* row = x + (r < R ? r : R - 1) * ld;
+        if constexpr (WIDE) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int p = 32 * i + lane, e = warp_e + p * kPer;
-            const int64_t left = (K - e) * (int64_t)sizeof(T);
-            cp_async16_part(to + (p ^ ((p >> 3) & 7)) * 16, row + (left > 0 ? e : 0), left >= 16 ? 16 : left > 0 ? (int)left : 0);
+            for (int i = 0; i < kPieces; ++i) {
+                const int p = 32 * i + lane, e = warp_e + p * kPer;
+                const int64_t left = (K - e) * (int64_t)sizeof(T);
+                cp_async16_part(to + (p ^ ((p >> 3) & 7)) * 16, row + (left > 0 ? e : 0), left >= 16 ? 16 : left > 0 ? (int)left : 0);
+            }
+        } else {
+            const int ahead = sizeof(T) == 2 ? (int)(reinterpret_cast<uintptr_t>(row) & 2) : 0;
+            const char* first = reinterpret_cast<const char*>(row) - ahead;
+            const char* from = first + warp_e * (int)sizeof(T) + 4 * lane;
+            unsigned char* at = to + 4 * (lane + lane / kUnitWords);
+            // bytes of the row from this lane's first word on
+            const int64_t left = (K - warp_e) * (int64_t)sizeof(T) + ahead - 4 * lane;
+            constexpr int kTurn = 4 * (32 + 32 / kUnitWords);
+            if ((K - warp_e) * (int64_t)sizeof(T) >= 128 * kUnitWords) {
+#pragma unroll
+                for (int i = 0; i < kUnitWords; ++i) cp_async4_part(at + kTurn * i, from + 128 * i, 4);
+            } else {
+#pragma unroll 4
+                for (int i = 0; i < kUnitWords; ++i) {
+                    const int n = (int)max((int64_t)0, min((int64_t)4, left - 128 * i));
+                    cp_async4_part(at + kTurn * i, n > 0 ? from + 128 * i : first, n);
+                }
+            }
+            if (sizeof(T) == 2 && lane == 0) {  // the word that the last lane's unit ends in
+                const int n = (int)max((int64_t)0, min((int64_t)4, left - 128 * kUnitWords));
+                cp_async4_part(at + kTurn * kUnitWords, n > 0 ? from + 128 * kUnitWords : first, n);
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto take = [&](Block<T>& blk, const unsigned char* from, int h) {  // block h of this lane's unit
+    auto take = [&](Block<T>& blk, const unsigned char* from, int h, int ahead) {  // block h of this lane's unit
+        if constexpr (WIDE) {
 #pragma unroll
-        for (int j = 0; j < kPieces / 2; ++j) {
-            const int p = lane * kPieces + h * (kPieces / 2) + j;
-            const uint4 v = *reinterpret_cast<const uint4*>(from + (p ^ ((p >> 3) & 7)) * 16);
-            blk.w[4 * j] = v.x, blk.w[4 * j + 1] = v.y, blk.w[4 * j + 2] = v.z, blk.w[4 * j + 3] = v.w;
+            for (int j = 0; j < kPieces / 2; ++j) {
+                const int p = lane * kPieces + h * (kPieces / 2) + j;
+                const uint4 v = *reinterpret_cast<const uint4*>(from + (p ^ ((p >> 3) & 7)) * 16);
+                blk.w[4 * j] = v.x, blk.w[4 * j + 1] = v.y, blk.w[4 * j + 2] = v.z, blk.w[4 * j + 3] = v.w;
+            }
+        } else {
+            constexpr int kHalf = kUnitWords / 2;
+            const uint32_t* word = reinterpret_cast<const uint32_t*>(from) + (kUnitWords + 1) * lane + kHalf * h;
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) blk.w[j] = word[j];
+            if (ahead) {  // (after a unit's last word comes its padding)
+                const uint32_t next = word[h == 0 ? kHalf : kHalf + 1];
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j) blk.w[j] = __funnelshift_r(blk.w[j], j + 1 < kHalf ? blk.w[j + 1] : next, 16);
+            }
         }
     };
     fetch(blockIdx.x, mine);
@@ -341,8 +392,9 @@ __global__ void __launch_bounds__(kThreads, CTAS)
         const int64_t r = turn * rpc + sub;
         const bool live = r < R;
         Block<T> a, b;
-        take(a, mine + buf * kBuffer, 0);
-        take(b, mine + buf * kBuffer, 1);
+        const int ahead = !WIDE && sizeof(T) == 2 ? (int)(reinterpret_cast<uintptr_t>(x + (live ? r : R - 1) * ld) & 2) : 0;
+        take(a, mine + buf * kBuffer, 0, ahead);
+        take(b, mine + buf * kBuffer, 1, ahead);
         const uint32_t mag_a = block_mag(a), mag_b = block_mag(b);
         RowScale rs = {1.f, 0.f};
         if (!given) {
@@ -607,11 +659,14 @@ cudaError_t quantize(const T* x, int64_t R, int64_t C, int64_t ld, const moe_nvf
         uint8_t *q = rows->q, *s = rows->s;
         float* gs = rows->gs;
         constexpr int kCtas = sizeof(T) == 4 ? 3 : 4;
-        if (wide && units <= kThreads && grid > sm_count() * kCtas) {
-            const void* f = (const void*)nvfp4_rows_stream_kernel<T, kCtas>;
-            const size_t smem = (size_t)2 * kThreads * 32 * sizeof(T);
+        const int64_t resident = sm_count() * kCtas;
+        // (us, streamed / not: aligned rows 4096 x 8192 18.4 / 19.3, 16384 x 512 9.2 / 9.6, but two waves or less, 8192 x 1024, 6.0 / 4.6;
+        // others 4096 x 8191 24.6 / 64, 8192 x 700 10.1 / 12.8, but half a warp's units, 8192 x 257, 10.2 / 6.8)
+        if (units <= kThreads && (wide ? grid > 2 * resident : units > 16)) {
+            const void* f = wide ? (const void*)nvfp4_rows_stream_kernel<T, kCtas, true> : (const void*)nvfp4_rows_stream_kernel<T, kCtas, false>;
+            const size_t smem = 2 * (kThreads / 32) * (size_t)(wide ? stream_warp_bytes<T, true>() : stream_warp_bytes<T, false>());
             void* args[] = {&x, &R, &C, &ld, &tpr_log, &q, &s, &gs, &given, &gr};
-            return launch_kernel(f, dim3((unsigned)(sm_count() * kCtas)), dim3(kThreads), smem, st, true, args);
+            return launch_kernel(f, dim3((unsigned)(grid < resident ? grid : resident)), dim3(kThreads), smem, st, true, args);
         }
         void* args[] = {&x, &R, &C, &ld, &wide, &tpr_log, &q, &s, &gs, &given, &gr};
         return launch_kernel((const void*)nvfp4_rows_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, true, args);

@@ -341,3 +341,25 @@ def test_calls_in_a_row_see_what_the_calls_before_them_wrote():
     together, apart = steps(lambda: None), steps(torch.cuda.synchronize)
     for a, b in zip(together, apart):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("R_,C,first", [(1, 1, 1), (2, 31, 1), (9, 1023, 3), (9, 1024, 1), (9, 1025, 2), (37, 2047, 0), (1300, 300, 1),
+                                        (700, 7111, 5), (3, 8192, 1)])
+def test_operands_of_rows_that_start_anywhere(dtype, R_, C, first):
+    whole = matrix(R_ + 1, C + 7, dtype, R_ + C)
+    x = whole.flatten()[first:first + R_ * (C + 5)].view(R_, C + 5)[:, :C]
+    dev = whole.cuda().flatten()[first:first + R_ * (C + 5)].view(R_, C + 5)[:, :C]
+    op = ops.nvfp4_operand(R_, C)
+    ops.nvfp4_quantize(dev, op)
+    check_operand(op, x.float().numpy())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("R_,C", [(10000, 40), (5003, 1544), (1301, 7112), (1300, 8192)])
+def test_operands_of_rows_by_the_thousand(dtype, R_, C):
+    x = matrix(R_, C, dtype, R_ + C)
+    x[7] = 0
+    op = ops.nvfp4_operand(R_, C)
+    ops.nvfp4_quantize(x.cuda(), op)
+    check_operand(op, x.float().numpy())

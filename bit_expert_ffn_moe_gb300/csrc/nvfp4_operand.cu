@@ -22,7 +22,7 @@
 //               atomics does not matter), then tiles of 256 rows x 64 columns through shared memory, encoded
 //               along their rows and along their columns, two columns per thread; 256 rows are a whole
 //               128-byte row of a column operand's code tile.  The second pass finds x in L2 while it fits there.
-// (2 or 4) R C bytes in, 9/16 R C out per form.  Rows of a bf16 matrix 4096 x 8192: 19 us (4.5 TB/s), both forms 45.7 us (11 of
+// (2 or 4) R C bytes in, 9/16 R C out per form.  Rows of a bf16 matrix 4096 x 8192: 19 us (4.5 TB/s), both forms 45 us (11 of
 // them the maxima).  The encoding, about 110 warp instructions per block and lane, keeps 58% of the issue slots busy; leaving out
 // the stores (43.7 us) or smaller tiles with a third more warps (49) hardly matter or hurt.
 #include <type_traits>
@@ -424,6 +424,24 @@ __global__ void __launch_bounds__(kThreads, CTAS)
 }
 
 // ------------------------------------------------------------------ with columns
+// 16 bytes of elements from p on, of which `left` are in the row: zeros after them.  p may start anywhere: aligned words, shifted
+// (an element in front of p or behind the 16 bytes may be read with them, in words that hold elements of the piece or the row).
+template <typename T>
+__device__ __forceinline__ uint4 load_piece(const T* p, int64_t left) {
+    constexpr int kPer = 16 / (int)sizeof(T);
+    const uint32_t ahead = sizeof(T) == 2 ? (uint32_t)(reinterpret_cast<uintptr_t>(p) & 2) : 0u;
+    if (left > kPer || (left == kPer && ahead == 0)) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(reinterpret_cast<const char*>(p) - ahead);
+        const uint32_t a = __ldg(q), b = __ldg(q + 1), c = __ldg(q + 2), d = __ldg(q + 3), e = ahead ? __ldg(q + 4) : 0u;
+        return make_uint4(__funnelshift_r(a, b, 8 * ahead), __funnelshift_r(b, c, 8 * ahead), __funnelshift_r(c, d, 8 * ahead),
+                          __funnelshift_r(d, e, 8 * ahead));
+    }
+    __align__(16) T t[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) t[i] = i < left ? p[i] : T(0.f);
+    return *reinterpret_cast<const uint4*>(t);
+}
+
 __global__ void __launch_bounds__(kThreads) nvfp4_zero_kernel(unsigned* p, int64_t n) {
     pdl_wait();
     pdl_launch_dependents();
@@ -457,10 +475,7 @@ __global__ void __launch_bounds__(kThreads, 4)
             if (wide && c0 + kPer <= C) {
                 u[j] = __ldg(reinterpret_cast<const uint4*>(p));
             } else {
-                __align__(16) T e[kPer];
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) e[i] = c0 + i < C ? p[i] : T(0.f);
-                u[j] = *reinterpret_cast<const uint4*>(e);
+                u[j] = load_piece(p, C - c0);
             }
         }
 #pragma unroll
@@ -517,21 +532,28 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 ? 1 : 3)
             const T* p = x + (r0 + rr) * ld + c0 + pc * kPer;
 #pragma unroll
             for (int i = 0; i < kTileR / kStep; ++i, p += kStep * ld) cp_async16(to + place(rr + i * kStep, pc), p);
-        } else {
+        } else if (wide) {  // at the edges
 #pragma unroll 1
             for (int i = threadIdx.x; i < kTileR * kPieces; i += kThreads) {
                 const int rr = i / kPieces, pc = i % kPieces;
-                const int64_t r = r0 + rr, c = c0 + pc * kPer;
-                const T* p = x + r * ld + c;
-                unsigned char* q = to + place(rr, pc);
-                if (r < R && wide && c + kPer <= C) {
-                    cp_async16(q, p);
-                } else {
-                    __align__(16) T e[kPer];
+                const int64_t r = r0 + rr, c = c0 + pc * kPer, left = r < R && c < C ? (C - c) * (int64_t)sizeof(T) : 0;
+                cp_async16_part(to + place(rr, pc), left > 0 ? x + r * ld + c : x, left >= 16 ? 16 : (int)left);
+            }
+        } else {
+            constexpr int kFly = 4;  // pieces in flight
+            static_assert(kTileR * kPieces % (kFly * kThreads) == 0, "whole turns");
+#pragma unroll 1
+            for (int i = threadIdx.x; i < kTileR * kPieces; i += kFly * kThreads) {
+                uint4 v[kFly];
 #pragma unroll
-                    for (int j = 0; j < kPer; ++j) e[j] = r < R && c + j < C ? p[j] : T(0.f);
-                    *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(e);
+                for (int h = 0; h < kFly; ++h) {
+                    const int rr = (i + h * kThreads) / kPieces, pc = (i + h * kThreads) % kPieces;
+                    const int64_t r = r0 + rr, c = c0 + pc * kPer;
+                    v[h] = r < R ? load_piece(x + r * ld + c, C - c) : make_uint4(0, 0, 0, 0);
                 }
+#pragma unroll
+                for (int h = 0; h < kFly; ++h)
+                    *reinterpret_cast<uint4*>(to + place((i + h * kThreads) / kPieces, (i + h * kThreads) % kPieces)) = v[h];
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");

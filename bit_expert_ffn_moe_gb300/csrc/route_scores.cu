@@ -51,6 +51,14 @@ __device__ __forceinline__ double warp_sum_f64(double v) {
     for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(kFull, v, m);
     return v;
 }
+__device__ __forceinline__ double warp_max_f64(double v) {  // (no NaN)
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) {
+        const double o = __shfl_xor_sync(kFull, v, m);
+        v = o > v ? o : v;
+    }
+    return v;
+}
 // Largest value of the warp (NaN ignored unless every lane has one).
 __device__ __forceinline__ float warp_max_f32(float v) {
     float m;
@@ -127,11 +135,11 @@ __device__ __forceinline__ int group_lane_shift(int G) { return G <= 1 ? 5 : G <
 // Score of group lane >> sh from values val[e] (-inf: out of service); every lane of the group gets it, and
 // in *least the smaller of the values it is made of.
 template <typename F>
-__device__ __forceinline__ F group_score(const F* val, int G, int S, int sh, bool top2, F* least = nullptr) {
+__device__ __forceinline__ F group_score(const float* val, int G, int S, int sh, bool top2, F* least = nullptr) {
     const int lane = threadIdx.x & 31, g = lane >> sh, lp = 1 << sh;
     Top2<F> t{(F)-INFINITY, (F)-INFINITY};
     if (g < G)
-        for (int j = lane & (lp - 1); j < S; j += lp) t.add(val[g * S + j]);
+        for (int j = lane & (lp - 1); j < S; j += lp) t.add((F)val[g * S + j]);
     for (int m = 1; m < lp; m <<= 1) t.merge(m);
     if (least) *least = top2 && t.b > -INFINITY ? t.b : t.a;
     return t.score(top2);
@@ -238,6 +246,9 @@ __device__ __forceinline__ Scratch warp_scratch(void* smem, int E, int warps, in
 // The whole choice for one token by one warp from shared memory: experts out of service inside the
 // choice, and values closer than their error, of which those that could stand on either side of the border
 // (a few) are computed in 64 bits, one per lane.  Writes the k ids in ascending order to picks[].
+//   An infinite bias ranks its expert before or behind all finite values: such a value is exact, so the error's bound is
+// that of the finite ones, and no border between values of which one is infinite is in doubt (each comparison below is
+// false for a difference of inf or NaN).  Groups are scored in 64 bits, where sums of finite values stay finite.
 template <typename T>
 __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const RoutePlan& plan, const T* row, const Scratch sc) {
     const int lane = threadIdx.x & 31;
@@ -285,7 +296,7 @@ __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const Rout
         float v = lv;
         if (biased && in_service(lv)) {
             v = score32(lv) + __ldg(a.bias + e);
-            vmax = fmaxf(vmax, fabsf(v));
+            if (fabsf(v) < INFINITY) vmax = fmaxf(vmax, fabsf(v));
         }
         // (a NaN value comes from a NaN bias: ranked like an expert out of service)
         sc.key[e] = in_service(lv) && v == v ? logit_key(v) : kOutKey;
@@ -304,17 +315,17 @@ __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const Rout
             val[e] = q == kOutKey ? -INFINITY : (biased || raw) ? key_logit(q) : score32(to_f32(row[e]));
         }
         __syncwarp();
-        float second;
-        const float gs = group_score<float>(val, G, S, sh, top2, &second);
-        kept = best_groups<float>(gs, G == 32 ? kFull : (1u << G) - 1, G, sh, keep);
+        constexpr double kInf = INFINITY;
+        double second;
+        const double gs = group_score<double>(val, G, S, sh, top2, &second);
+        kept = best_groups<double>(gs, G == 32 ? kFull : (1u << G) - 1, G, sh, keep);
         if (!raw) {
-            const bool mine = g < G && gs > -INFINITY;
+            const bool mine = g < G && gs > -kInf;
             const bool in = g < G && ((kept >> g) & 1);
-            const float lo = warp_max_f32(mine && !in ? gs : -INFINITY);   // best left out
-            const float hi = -warp_max_f32(mine && in ? -gs : -INFINITY);  // worst kept
-            const float verr = biased ? err : err_s;
-            const float gerr = 2.f * verr + kSumErr * fmaxf(fabsf(lo), fabsf(hi));
-            if (lo > -INFINITY && hi < INFINITY && hi - lo <= gerr) {
+            const double lo = warp_max_f64(mine && !in ? gs : -kInf);   // best left out
+            const double hi = -warp_max_f64(mine && in ? -gs : -kInf);  // worst kept
+            const double verr = biased ? err : err_s, gerr = 2.0 * verr;
+            if (lo > -kInf && hi < kInf && hi - lo <= gerr) {
                 const bool is_open = mine && gs >= hi - gerr && gs <= lo + gerr;
                 const uint32_t lanes = __ballot_sync(kFull, is_open);
                 const uint32_t sure = __ballot_sync(kFull, mine && gs > lo + gerr);
@@ -324,7 +335,7 @@ __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const Rout
                     in_mask |= ((sure >> (j << sh)) & 1u) << j;
                 }
                 // of the open groups, the values that may be among a group's best one or two
-                if ((lane & ((1 << sh) - 1)) == 0) sc.picks[g] = __float_as_int(second - verr);
+                if ((lane & ((1 << sh) - 1)) == 0) sc.picks[g] = __float_as_int(__double2float_rd(second - verr));
                 __syncwarp();
                 int n = 0;
                 for (int i = 0; i < nv; ++i) {
@@ -512,7 +523,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     }
 
     // ranking values: the logits, or scores (+ bias).  An expert out of service has -inf (NaN logits: NaN, which no
-    // comparison below lets pass; sigmoid_fast(-inf) is 0 and needs the test)
+    // comparison below lets pass; sigmoid_fast(-inf) is 0 and needs the test).  A NaN bias ranks like -inf (the fmaxf), an infinite
+    // one makes its value infinite: where that reaches a border, the choice is the careful one.
     float v[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = l[i];
@@ -521,8 +533,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
         if (biased) load_chunk<NV>(a.bias, E, plan.wide_bias, b);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const float s = softmax ? score_f32(l[i], true, norm) : sigmoid_fast(clamp_logit(l[i]));
-            v[i] = in_service(l[i]) ? (biased ? s + b[i] : s) : -INFINITY;
+            const float s = softmax ? score_f32(l[i], true, norm) : sigmoid_fast(l[i]);
+            v[i] = in_service(l[i]) ? (biased ? fmaxf(s + b[i], -INFINITY) : s) : -INFINITY;
         }
     }
     const float err_s = softmax ? softmax_err(NV, norm.inv_sum) : kSigmoidErr;

@@ -70,7 +70,7 @@ def route_scores(logits: torch.Tensor, k: int, rule: B.moe_route_rule, bias: Opt
                  scores: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None
                  ) -> Tuple[torch.Tensor, torch.Tensor]:
     """ids int32 [T, k] (ascending) and weights fp32 [T, k] of logits [T, E] under `rule`; `bias` fp32 [E] takes part in the
-    choice only.  Logits of -inf take an expert out of service.  scores fp32 [T, E] and counts int32 [E], when given, receive
+    choice only (+inf: picked first, -inf: last).  Logits of -inf take an expert out of service.  scores fp32 [T, E] and counts int32 [E], when given, receive
     all the scores and the picks per expert."""
     return (_module or _calls()).route_scores(logits, k, rule, bias, scores, counts)
 

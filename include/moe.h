@@ -456,7 +456,7 @@ moe_status moe_route_logits(const uint16_t* x, const float* W_r, const float* b,
                             moe_stream_t stream);
 
 /* Scores s = sigmoid(l) or softmax(l) of logits [T][ld] (dtype; ld >= E); ranking values v = s + bias (bias fp32
- * [E], finite, or NULL: then the logits are ranked, which is the order of the scores; sums of a group's
+ * [E], or NULL: then the logits are ranked, which is the order of the scores; sums of a group's
  * two largest are then sums of scores).  The top_groups best groups stay, then the k largest v among their
  * experts; ties go to the lower id.  The choice is the one that 64-bit arithmetic makes on the given logits
  * and bias.  ids int32 [T][k]: the set in ascending order; w fp32 [T][k]: s of the picks (without bias), divided by
@@ -464,6 +464,9 @@ moe_status moe_route_logits(const uint16_t* x, const float* W_r, const float* b,
  *   An expert whose logit is -inf or NaN is out of service: score 0, ranked below every other expert of the
  * open groups, and picked (lowest id first, weight 0) only when fewer than k others are there; a group without
  * an expert in service ranks last.  A logit of +inf scores like the largest finite number.
+ *   A bias of +inf ranks its expert (in service) before all that have a finite value, and its group likewise; one of -inf
+ * ranks it behind them, one of NaN with the experts out of service, and neither counts in its group's score.  Weights do
+ * not see the bias.
  *   scores (optional) fp32 [T][E]: s.  counts (optional) int32 [E]: picks per expert, overwritten.
  * T >= 0, 1 <= k <= 32, E <= 1024, k <= top_groups * E / groups. */
 moe_status moe_route_scores(const void* logits, moe_dtype dtype, int64_t ld, const float* bias, int T, int E, int k,

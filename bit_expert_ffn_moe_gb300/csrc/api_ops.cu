@@ -10,6 +10,9 @@ using namespace moe;
 namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// Whether all of these (null ones among them) start on 4 bytes: arrays of floats and of ints.
+template <typename... P>
+bool words(const P*... p) { return (aligned(p, 4) && ...); }
 
 #define MOE_TRY(expr)                \
     do {                             \
@@ -93,7 +96,7 @@ moe_status moe_route_logits(const uint16_t* x, const float* W_r, const float* b,
                             moe_stream_t stream) {
     MOE_TRY(check_shape(T, d, E, 1, 32, MOE_ACT_BF16));
     if (T == 0) return MOE_OK;
-    if (!x || !W_r || !logits || !aligned(x, 16) || !aligned(W_r, 16)) return MOE_ERR_INVALID_ARG;
+    if (!x || !W_r || !logits || !aligned(x, 16) || !aligned(W_r, 16) || !words(b, logits)) return MOE_ERR_INVALID_ARG;
     return launch([&] { return launch_route_logits(x, W_r, b, T, d, E, logits, (cudaStream_t)stream, false); });
 }
 
@@ -104,6 +107,7 @@ moe_status moe_route_scores(const void* logits, moe_dtype dtype, int64_t ld, con
     if (dtype_size(dtype) == 0) return MOE_ERR_INVALID_ARG;
     if (ld < E) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T > 0 && (!logits || !ids || !w || !aligned(logits, dtype_size(dtype)))) return MOE_ERR_INVALID_ARG;
+    if (!words(bias, ids, w, scores, counts)) return MOE_ERR_INVALID_ARG;
     if (T == 0 && !counts) return MOE_OK;
     return launch([&] {
         cudaStream_t st = (cudaStream_t)stream;
@@ -123,7 +127,8 @@ moe_status moe_route_scores_backward(const void* logits, moe_dtype dtype, int64_
     if (dtype_size(dtype) == 0) return MOE_ERR_INVALID_ARG;
     if (ld < E || ldd < E) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return MOE_OK;
-    if (!logits || !ids || !dw || !dlogits || !aligned(logits, dtype_size(dtype)) || !aligned(dlogits, dtype_size(dtype)))
+    if (!logits || !ids || !dw || !dlogits || !aligned(logits, dtype_size(dtype)) || !aligned(dlogits, dtype_size(dtype)) ||
+        !words(ids, dw, dscores))
         return MOE_ERR_INVALID_ARG;
     return launch([&] {
         RouteBackwardArgs a = {logits, ld, T, E, k, *rule, ids, dw, dscores, dlogits, ldd};
@@ -139,6 +144,7 @@ moe_status moe_combine_backward(const uint16_t* dy, const uint16_t* y_perm, cons
     if (!dy || !inv_pos || !aligned(dy, 16) || (!dw && !dy_perm)) return MOE_ERR_INVALID_ARG;
     if (dw && (!y_perm || !aligned(y_perm, 16))) return MOE_ERR_INVALID_ARG;
     if (dy_perm && (!w || !aligned(dy_perm, 16))) return MOE_ERR_INVALID_ARG;
+    if (!words(inv_pos, w, dw)) return MOE_ERR_INVALID_ARG;
     return launch([&] { return launch_combine_backward(dy, y_perm, inv_pos, w, T, k, d, dw, dy_perm, (cudaStream_t)stream); });
 }
 

@@ -434,7 +434,7 @@ moe_status moe_dense_linear(const uint16_t* x, int T, int K, int N, const moe_mx
  * apply the other rules that sparse layers use: scores by sigmoid or softmax, a balance bias that takes
  * part in the choice and not in the weights, experts in groups of which only the best are open to a
  * token, renormalised weights.  Their ids and w go into moe_permute, the expert calls and moe_combine as
- * moe_route's do. */
+ * moe_route's do.  Arrays of floats and ints have to start on 4 bytes, matrices of a moe_dtype on an element. */
 
 typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
 typedef enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 } moe_score;

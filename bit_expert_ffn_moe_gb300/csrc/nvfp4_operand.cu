@@ -100,7 +100,8 @@ __device__ __forceinline__ void cp_async4_part(void* smem, const void* gmem, int
 template <typename T, bool WIDE>
 __host__ __device__ constexpr int stream_warp_bytes() { return WIDE ? 32 * 32 * (int)sizeof(T) : (32 * (8 * (int)sizeof(T) + 1) + 4) * 4; }
 
-// The larger magnitudes of a word of one fp32 or two 16-bit elements (a: magnitudes already).
+// The larger magnitudes of a word of one fp32 or two 16-bit elements (a: magnitudes already).  A NaN is the largest of all, so that it
+// reaches the scale: as an integer of fp32 bits it is by itself.
 template <typename T>
 __device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b) {
     if constexpr (sizeof(T) == 4) {
@@ -108,9 +109,9 @@ __device__ __forceinline__ uint32_t mag_max(uint32_t a, uint32_t b) {
     } else {
         uint32_t r;
         if constexpr (std::is_same<T, __half>::value) {
-            asm("{\n\t.reg .b32 m;\n\tabs.f16x2 m, %2;\n\tmax.f16x2 %0, %1, m;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+            asm("{\n\t.reg .b32 m;\n\tabs.f16x2 m, %2;\n\tmax.NaN.f16x2 %0, %1, m;\n\t}" : "=r"(r) : "r"(a), "r"(b));
         } else {
-            asm("{\n\t.reg .b32 m;\n\tabs.bf16x2 m, %2;\n\tmax.bf16x2 %0, %1, m;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+            asm("{\n\t.reg .b32 m;\n\tabs.bf16x2 m, %2;\n\tmax.NaN.bf16x2 %0, %1, m;\n\t}" : "=r"(r) : "r"(a), "r"(b));
         }
         return r;
     }

@@ -65,3 +65,79 @@ def test_given_scales_saturate_whatever_the_type(dtype, R, C, extra):
     assert torch.isfinite(want["rows"]).all() and torch.isfinite(want["cols"]).all()
     for form, op in all_forms(x, gs_rows, gs_cols, extra):
         assert torch.equal(op.values().cpu(), want[form]), form
+
+
+def both_ways(x, extra=0):
+    """Values of x's operand rows from the row form alone and from the call for both, and of its columns from both calls that make them."""
+    R, C = x.shape
+    dev = torch.zeros(R, C + extra, dtype=x.dtype, device="cuda")[:, :C]
+    dev.copy_(x)
+    ws = ops.nvfp4_workspace(R, C, C)
+    r, r2, c, c2 = (ops.nvfp4_operand(*s) for s in ((R, C), (R, C), (C, R), (C, R)))
+    ops.nvfp4_quantize(dev, r)
+    ops.nvfp4_quantize(dev, r2, c, ws)
+    ops.nvfp4_quantize(dev, None, c2, ws)
+    return (r, r2), (c, c2)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("R,C,extra", SHAPES)
+def test_a_nan_reaches_its_row_and_no_other(dtype, R, C, extra):
+    g = torch.Generator().manual_seed(R * C)
+    x = torch.randn(R, C, generator=g).to(TYPES[dtype])
+    clean = both_ways(x, extra)
+    at = [(0, 0), (2, C - 1), (2, 17), (R - 1, 33)]
+    for r, c in at:
+        x[r, c] = float("nan")
+    x[1] = float("nan")           # a whole row
+    x[3, 5] = -float("inf")       # an infinite scale
+    bad_rows = torch.zeros(R, dtype=torch.bool)
+    bad_rows[[0, 1, 2, 3, R - 1]] = True
+    got = both_ways(x, extra)
+    for now, was in zip(got[0], clean[0]):
+        v = now.values().cpu()
+        assert torch.isnan(v[bad_rows]).all() and torch.isnan(now.gs.cpu()[[0, 1, 2, R - 1]]).all()
+        assert torch.equal(v[~bad_rows], was.values().cpu()[~bad_rows])
+    for op in got[1]:
+        assert torch.isnan(op.values()).all()  # (row 1 reaches every column)
+    x[1] = 0.5
+    bad_cols = torch.zeros(C, dtype=torch.bool)
+    bad_cols[[0, C - 1, 17, 33, 5]] = True
+    y = x.clone()
+    y[:, bad_cols] = 0.0
+    for now, was in zip(both_ways(x, extra)[1], both_ways(y, extra)[1]):
+        v = now.values().cpu()
+        assert torch.isnan(v[bad_cols]).all()
+        assert torch.equal(v[~bad_cols], was.values().cpu()[~bad_cols])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_a_nan_under_given_scales_reaches_its_block(dtype):
+    R, C = 40, 300
+    x = torch.randn(R, C, generator=torch.Generator().manual_seed(1)).to(TYPES[dtype])
+    gs_rows, gs_cols = torch.full((R,), 2.0 ** -10), torch.full((C,), 2.0 ** -9)
+    want = {"rows": rule_values(x, gs_rows), "cols": rule_values(x.T.contiguous(), gs_cols)}
+    x[7, 40] = float("nan")
+    for form, op in all_forms(x, gs_rows, gs_cols):
+        v, r, b = op.values().cpu(), *((7, 32) if form == "rows" else (40, 0))
+        assert torch.isnan(v[r, b:b + 16]).all()
+        v[r, b:b + 16] = want[form][r, b:b + 16]
+        assert torch.equal(v, want[form]), form
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("M", [1, 5, 40, 200, 1500])
+def test_a_nan_activation_shows_in_its_row_of_the_product(dtype, M):
+    N, K = 1600, 300
+    g = torch.Generator(device="cuda").manual_seed(M)
+    W = ops.nvfp4_operand(N, K)
+    ops.nvfp4_quantize(torch.randn(N, K, generator=g, device="cuda"), W)
+    x = torch.randn(M, K, generator=g, device="cuda").to(TYPES[dtype])
+    ws = ops.nvfp4_workspace(M, N, K)
+    clean = ops.nvfp4_linear(x, W, ws)
+    x[M // 2, 250] = float("nan")
+    y = ops.nvfp4_linear(x, W, ws)
+    assert torch.isnan(y[M // 2]).all()
+    others = torch.arange(M, device="cuda") != M // 2
+    assert torch.equal(y[others], clean[others])
+    assert B.moe_get_device_status(ws) == B.MOE_OK

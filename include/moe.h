@@ -514,8 +514,8 @@ size_t moe_nvfp4_workspace_size(int64_t M, int64_t N, int64_t K);
 /* Operands of x [R][C] (dtype, row stride ld >= C): `rows` is that of x ([R] rows contracting along C), `cols` that of
  * its transpose ([C] rows contracting along R); either may be NULL.  The rule is moe_nvfp4_pack's with
  * a global scale per operand row, computed from the row (scales_given = 0; gs_rows must be 1), so a row's operand
- * does not depend on the others; or with the scales found in gs (scales_given != 0): values beyond their range
- * saturate.  Other than moe_nvfp4_pack, which passes over it, a NaN makes its operand row NaN (as an infinity does there), or
+ * does not depend on the others; or with the scales found in gs (scales_given != 0; finite, not negative): values beyond
+ * their range saturate, under a scale of 0 to 0.  Other than moe_nvfp4_pack, which passes over it, a NaN makes its operand row NaN (as an infinity does there), or
  * under a given scale its block of 16.  ws: used by cols with computed scales only (may be NULL otherwise). */
 moe_status moe_nvfp4_quantize(const void* x, moe_dtype dtype, int64_t R, int64_t C, int64_t ld,
                               const moe_nvfp4_operand* rows, const moe_nvfp4_operand* cols, int scales_given, void* ws,

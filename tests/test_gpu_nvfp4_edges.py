@@ -141,3 +141,24 @@ def test_a_nan_activation_shows_in_its_row_of_the_product(dtype, M):
     others = torch.arange(M, device="cuda") != M // 2
     assert torch.equal(y[others], clean[others])
     assert B.moe_get_device_status(ws) == B.MOE_OK
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("R,C,extra", SHAPES)
+def test_a_given_scale_of_zero_makes_zeros(dtype, R, C, extra):
+    g = torch.Generator().manual_seed(R)
+    x = torch.randn(R, C, generator=g).to(TYPES[dtype])
+    x[0] = 0.0                      # what a scale of zero is usually worked out from
+    x[1, :16] = 0.0
+    x[:, 1] = 0.0
+    x[2, 20] = float("inf")
+    gs_rows, gs_cols = torch.full((R,), 2.0 ** -9), torch.full((C,), 2.0 ** -9)
+    gs_rows[:3], gs_cols[:3] = 0.0, 0.0
+    want = {"rows": rule_values(x, torch.where(gs_rows > 0, gs_rows, 1.0)), "cols": rule_values(x.T.contiguous(), torch.where(gs_cols > 0, gs_cols, 1.0))}
+    want["rows"][:3], want["cols"][:3] = 0.0, 0.0
+    for form, op in all_forms(x, gs_rows, gs_cols, extra):
+        assert torch.equal(op.values().cpu(), want[form]), form
+        other = ops.nvfp4_operand(9, op.K)
+        ops.nvfp4_quantize(torch.ones(9, op.K, device="cuda"), other)
+        y = ops.nvfp4_matmul(op, other, torch.float32, ops.nvfp4_workspace(op.rows, 9, op.K))
+        assert (y[:3] == 0).all() and torch.isfinite(y).all()

@@ -112,6 +112,9 @@ __device__ __forceinline__ float smaller(float x, float y) { return fminf(x, y);
 __device__ __forceinline__ double larger(double x, double y) { return x > y ? x : y; }
 __device__ __forceinline__ double smaller(double x, double y) { return x > y ? y : x; }
 
+__device__ __forceinline__ float lowest(float) { return -kMaxF32; }
+__device__ __forceinline__ double lowest(double) { return -1.7976931348623157e308; }
+
 // The two largest of a stream of values.
 template <typename F>
 struct Top2 {
@@ -125,24 +128,25 @@ struct Top2 {
         b = larger(larger(b, ob), smaller(a, oa));
         a = larger(a, oa);
     }
-    // sum of the (up to) two best, or the best alone
-    __device__ __forceinline__ F score(bool top2) const { return (top2 && b > -INFINITY) ? a + b : a; }
+    // sum of the (up to) two best (finite where they are low: -inf is a group without any), or the best alone; the smaller of the
+    // values it is made of
+    __device__ __forceinline__ bool two(bool top2) const { return top2 && b > -INFINITY; }
+    __device__ __forceinline__ F score(bool top2) const { return two(top2) ? larger(a + b, lowest(a)) : a; }
+    __device__ __forceinline__ F least(bool top2) const { return two(top2) ? b : a; }
 };
 
 // 2^shift lanes share an expert group: as many as G groups leave to each.
 __device__ __forceinline__ int group_lane_shift(int G) { return G <= 1 ? 5 : G <= 2 ? 4 : G <= 4 ? 3 : G <= 8 ? 2 : G <= 16 ? 1 : 0; }
 
-// Score of group lane >> sh from values val[e] (-inf: out of service); every lane of the group gets it, and
-// in *least the smaller of the values it is made of.
+// The best two of group lane >> sh from values val[e] (-inf: out of service), in every lane of the group.
 template <typename F>
-__device__ __forceinline__ F group_score(const float* val, int G, int S, int sh, bool top2, F* least = nullptr) {
+__device__ __forceinline__ Top2<F> group_best(const float* val, int G, int S, int sh) {
     const int lane = threadIdx.x & 31, g = lane >> sh, lp = 1 << sh;
     Top2<F> t{(F)-INFINITY, (F)-INFINITY};
     if (g < G)
         for (int j = lane & (lp - 1); j < S; j += lp) t.add((F)val[g * S + j]);
     for (int m = 1; m < lp; m <<= 1) t.merge(m);
-    if (least) *least = top2 && t.b > -INFINITY ? t.b : t.a;
-    return t.score(top2);
+    return t;
 }
 
 // Bit g of the result: group g is among the `keep` best of the candidate groups (ties to the lower group).
@@ -199,6 +203,18 @@ __device__ __forceinline__ void load_chunk(const T* row, int E, bool wide, float
 constexpr float kSigmoidErr = 5.6e-7f;  // 2 * 2.3 * 2^-23
 __device__ __forceinline__ float softmax_err(int nv, float largest) { return (float)(nv + 16) * 1.1920929e-7f * largest; }
 constexpr float kSumErr = 1.8e-7f;  // 1.5 * 2^-23 of the largest value
+
+// Bounds of a group's score in 64 bits: half of the above for each value in it (values that cancel keep their errors) and for
+// their sum.  No bound below a score of +inf, which may be a sum that overflowed; none above one of -inf.
+struct Range {
+    float low, high;
+};
+__device__ __forceinline__ Range group_range(const Top2<float>& best, bool top2, float err_s) {
+    const float gs = best.score(top2), two = best.two(top2) ? 1.f : 0.f;
+    const float sizes = fabsf(best.a) + fabsf(gs) + (two != 0.f ? fabsf(best.b) : 0.f);
+    const float err = 0.5f * ((1.f + two) * err_s + kSumErr * sizes);
+    return {fmaxf(gs - err, -INFINITY), fmaxf(gs + err, -INFINITY)};  // (fmaxf: of NaN)
+}
 
 __device__ __forceinline__ float sigmoid_fast(float l) {
     float e, s;
@@ -316,8 +332,8 @@ __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const Rout
         }
         __syncwarp();
         constexpr double kInf = INFINITY;
-        double second;
-        const double gs = group_score<double>(val, G, S, sh, top2, &second);
+        const Top2<double> best = group_best<double>(val, G, S, sh);
+        const double gs = best.score(top2);
         kept = best_groups<double>(gs, G == 32 ? kFull : (1u << G) - 1, G, sh, keep);
         if (!raw) {
             const bool mine = g < G && gs > -kInf;
@@ -335,7 +351,7 @@ __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const Rout
                     in_mask |= ((sure >> (j << sh)) & 1u) << j;
                 }
                 // of the open groups, the values that may be among a group's best one or two
-                if ((lane & ((1 << sh) - 1)) == 0) sc.picks[g] = __float_as_int(__double2float_rd(second - verr));
+                if ((lane & ((1 << sh) - 1)) == 0) sc.picks[g] = __float_as_int(__double2float_rd(best.least(top2) - verr));
                 __syncwarp();
                 int n = 0;
                 for (int i = 0; i < nv; ++i) {
@@ -543,7 +559,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
     if (grouped) {
         const int S = plan.S, sh = plan.lane_shift, lanes = 1 << (sh & 31);
         const bool raw = !want_scores;
-        float hi, lo;  // worst group kept, best left out
+        float hi = 0.f, lo = -INFINITY;  // lower bound of the worst group kept, upper bound of the best left out
         bool in = false, decided = false;
         uint32_t kept = 0;
         if (sh >= 0) {  // 2^sh whole lanes share a group
@@ -553,23 +569,26 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
             for (int m = 1; m < lanes; m <<= 1) best.merge(m);
             const float gs = best.score(top2);
             float left = e0 < E ? gs : NAN;
-            hi = 0.f;
             for (int r = 0; r < a.rule.top_groups; ++r) {  // the best group left, ties to the lower group
-                hi = warp_max_f32(left);
-                const int first = __ffs(__ballot_sync(kFull, left == hi)) - 1;
+                const float most = warp_max_f32(left);
+                const int first = __ffs(__ballot_sync(kFull, left == most)) - 1;
                 if (lane >> sh == first >> sh) in = true, left = NAN;
             }
-            lo = warp_max_f32(left == left ? left : -INFINITY);
-            const float verr = err_s + (biased ? kSumErr * fmaxf(fabsf(lo), fabsf(hi)) : 0.f);
-            const float gerr = 2.f * verr + kSumErr * fmaxf(fabsf(lo), fabsf(hi));
-            if (!raw && !softmax && lo > -INFINITY && hi - lo <= gerr) {
-                // the open groups' scores in 64 bits, from the values that may be among a group's best
-                const bool live = e0 < E && gs > -INFINITY, open = live && gs >= hi - gerr && gs <= lo + gerr;
-                const float least = (top2 && best.b > -INFINITY ? best.b : best.a) - verr;
+            Range range = {0.f, 0.f};
+            if (!raw) {
+                range = group_range(best, top2, err_s);
+                lo = warp_max_f32(in ? -INFINITY : range.high);
+                hi = -warp_max_f32(in ? -range.low : -INFINITY);
+            }
+            if (!softmax && lo > -INFINITY && !(hi > lo)) {
+                // Kept groups that lie above all left out are in, those left out below all kept are out; the scores of the others (all in
+                // service) in 64 bits, from the values that may be among a group's best
+                const bool live = gs > -INFINITY, open = live && (in ? range.low <= lo : range.high >= hi);
+                const float small = best.least(top2), least = small - (err_s + kSumErr * fabsf(small));
                 uint32_t take = 0;
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
-                    if (open && v[i] > -INFINITY && v[i] >= least) take |= 1u << i;
+                    if (open && v[i] > -INFINITY && !(v[i] < least)) take |= 1u << i;  // (a bound of inf - inf takes all)
                 Top2<double> x{-(double)INFINITY, -(double)INFINITY};
                 for (; take; take &= take - 1) {
                     const int e = e0 + __ffs(take) - 1;
@@ -578,10 +597,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
                 __syncwarp();
                 for (int m = 1; m < lanes; m <<= 1) x.merge(m);
                 const bool head = (lane & (lanes - 1)) == 0;
-                const uint32_t set = __ballot_sync(kFull, open && head), sure = __ballot_sync(kFull, live && head && gs > lo + gerr);
+                const bool above = in && range.low > lo;
+                const uint32_t set = __ballot_sync(kFull, open && head), sure = __ballot_sync(kFull, above && head);
                 int before = lanes_before(set, x.score(top2));
                 before = __shfl_sync(kFull, before, lane & ~(lanes - 1));
-                in = live && (gs > lo + gerr || (open && before + __popc(sure) < a.rule.top_groups));
+                in = above || (open && before + __popc(sure) < a.rule.top_groups);
                 decided = true;
             }
         } else {  // through shared memory
@@ -591,17 +611,17 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
                 if (e0 + i < E) val[e0 + i] = v[i];
             __syncwarp();
             const int gsh = group_lane_shift(G), g = lane >> gsh;
-            const float gs = group_score<float>(val, G, S, gsh, top2);
-            kept = best_groups<float>(gs, G == 32 ? kFull : (1u << G) - 1, G, gsh, a.rule.top_groups);
-            const bool mine = g < G && ((kept >> g) & 1);
-            lo = warp_max_f32(g < G && !mine ? gs : -INFINITY);
-            hi = -warp_max_f32(mine ? -gs : -INFINITY);
+            const Top2<float> best = group_best<float>(val, G, S, gsh);
+            kept = best_groups<float>(best.score(top2), G == 32 ? kFull : (1u << G) - 1, G, gsh, a.rule.top_groups);
+            if (!raw) {
+                const bool mine = g < G && ((kept >> g) & 1);
+                const Range range = group_range(best, top2, err_s);
+                lo = warp_max_f32(g < G && !mine ? range.high : -INFINITY);
+                hi = -warp_max_f32(mine ? -range.low : -INFINITY);
+            }
             __syncwarp();
         }
-        if (!raw && !decided && lo > -INFINITY) {
-            const float verr = err_s + (biased ? kSumErr * fmaxf(fabsf(lo), fabsf(hi)) : 0.f);
-            if (!(hi - lo > 2.f * verr + kSumErr * fmaxf(fabsf(lo), fabsf(hi)))) careful = true;
-        }
+        careful = !decided && lo > -INFINITY && !(hi > lo);
         if (!biased) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) v[i] = l[i];

@@ -94,3 +94,36 @@ def test_bias_values_of_every_kind(score, groups, top_groups, group_score, seed)
                 odd = rng.random(E) < share
                 bias[odd] = kinds[rng.integers(0, len(kinds), int(odd.sum()))]
                 check(l, bias, min(k, top_groups * (E // groups)), score, groups, top_groups, group_score)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,top_groups", [(64, 32, 5), (96, 32, 5), (100, 20, 7), (256, 32, 3), (64, 8, 3)])
+@pytest.mark.parametrize("size", [10.0, 1000.0, 1e5])
+def test_groups_whose_best_two_cancel(score, E, groups, top_groups, size):
+    """Bias values of opposite sign in each group: the sum of its two best is a thousandth of either, and fp32 knows it to the rounding of
+    those."""
+    rng = np.random.default_rng(int(size) + E)
+    l = (1e-3 * rng.standard_normal((300, E))).astype(np.float32)
+    bias = np.full(E, -size, np.float32)
+    bias[::E // groups] = size
+    for k in (1, top_groups):
+        check(l, bias, k, score, groups, top_groups, "top2")
+    bias += (1e-4 * rng.standard_normal(E)).astype(np.float32)
+    check(l, bias, 2, score, groups, top_groups, "top2")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,top_groups", [(64, 32, 20), (96, 32, 20), (100, 20, 15), (64, 8, 6)])
+@pytest.mark.parametrize("group_score", ["max", "top2"])
+def test_groups_of_the_lowest_bias_rank_before_groups_out_of_service(score, E, groups, top_groups, group_score):
+    """The type's lowest number as the bias that switches experts off: two of them add up below fp32's range."""
+    rng = np.random.default_rng(E)
+    l = rng.standard_normal((64, E)).astype(np.float32)
+    per = E // groups
+    bias = np.zeros(E, np.float32)
+    bias[3 * per:] = np.finfo(np.float32).min
+    for t in range(64):
+        for g in rng.permutation(groups)[:groups - top_groups + rng.integers(-2, 3)]:
+            l[t, g * per:(g + 1) * per] = -np.inf
+    for k in (1, 5, min(30, top_groups * per)):
+        check(l, bias, k, score, groups, top_groups, group_score)

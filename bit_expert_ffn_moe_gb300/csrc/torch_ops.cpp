@@ -5,6 +5,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -38,9 +39,17 @@ moe_dtype dtype_of(const at::Tensor& t, const char* what) {
     }
 }
 
+// Kernels run on the current device and its current stream: a tensor of another device is refused.
+void here(const at::Tensor& t, const char* what) {
+    c10::DeviceIndex current = -1;
+    if (c10::cuda::GetDevice(&current) != cudaSuccess) current = -1;
+    if (!t.is_cuda() || t.get_device() != current) refuse(PyExc_ValueError, what, "on another device than the current one");
+}
+
 // Row stride of a 2-D CUDA tensor whose rows are contiguous and do not overlap.
 int64_t matrix(const at::Tensor& t, const char* what) {
     if (t.dim() != 2 || !t.is_cuda()) refuse(PyExc_ValueError, what, "a CUDA matrix expected");
+    here(t, what);
     if (t.size(1) > 1 && t.stride(1) != 1) refuse(PyExc_ValueError, what, "contiguous rows expected");
     if (t.size(0) <= 1) return t.size(1);
     if (t.stride(0) < t.size(1)) refuse(PyExc_ValueError, what, "rows may not overlap");
@@ -174,6 +183,7 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& dy = tensor(a[0], "dy");
         if (dy.dim() != 2 || !dy.is_cuda() || dy.scalar_type() != at::kBFloat16 || !dy.is_contiguous())
             refuse(PyExc_ValueError, "dy", "contiguous bf16 [T, d] on CUDA expected");
+        here(dy, "dy");
         const at::Tensor& w0 = tensor(a[3], "w");
         if (w0.dim() != 2) refuse(PyExc_ValueError, "w", "[T, k] expected");
         const int64_t T = dy.size(0), d = dy.size(1), k = w0.size(1);
@@ -273,6 +283,7 @@ PyObject* nvfp4_room(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* nvfp4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 12, [&]() -> PyObject* {
         const at::Tensor& like = tensor(a[8], "operand");
+        here(like, "a, b");
         const Operand A = operand(a, like, "a"), B = operand(a + 4, like, "b");
         if (!A.op || !B.op) refuse(PyExc_ValueError, "a, b", "operands expected");
         expect(B, B.rows, A.K, "b");

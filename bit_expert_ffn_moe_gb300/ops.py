@@ -1,7 +1,8 @@
 """Routing rules, their gradients and dense NVFP4 products on torch tensors.
 
 Each function checks its tensors, allocates its results and makes one call of the library, in an extension module; the work is
-the library's kernels, on torch's current stream.  None of them synchronises.
+the library's kernels, on torch's current stream.  None of them synchronises.  Tensors of another device than the current one are
+refused (`with torch.cuda.device(...)` makes theirs the current one).
 """
 from __future__ import annotations
 
@@ -39,6 +40,10 @@ def _need(cond: bool, what: str) -> None:
         raise ValueError(what)
 
 
+def _need_current(device: torch.device, what: str) -> None:
+    _need(device.index is None or device.index == torch.cuda.current_device(), "%s: on another device than the current one" % what)
+
+
 # ------------------------------------------------------------------ routing rules
 
 def route_rule(score: str = "sigmoid", groups: int = 1, top_groups: int = 1, group_score: str = "top2",
@@ -55,6 +60,7 @@ def route_rule(score: str = "sigmoid", groups: int = 1, top_groups: int = 1, gro
 def route_logits(x: torch.Tensor, W_r: torch.Tensor, b: Optional[torch.Tensor] = None) -> torch.Tensor:
     """fp32 router logits [T, E] of bf16 x [T, d] and fp32 W_r [E, d] in the layer's fixed order, b added."""
     _need(x.dim() == 2 and x.is_cuda and x.dtype == torch.bfloat16 and x.is_contiguous(), "x: contiguous bf16 [T, d] expected")
+    _need_current(x.device, "x")
     T, d = x.shape
     _need(W_r.dim() == 2 and W_r.shape[1] == d and W_r.dtype == torch.float32 and W_r.device == x.device and W_r.is_contiguous(),
           "W_r: contiguous fp32 [E, d] expected")
@@ -109,6 +115,7 @@ class Nvfp4Operand:
 
     def values(self) -> torch.Tensor:
         """The numbers it stands for, fp32 [rows, K]."""
+        _need_current(self.q.device, "operand")
         v = torch.empty((self.rows, self.K), dtype=torch.float32, device=self.q.device)
         B.moe_nvfp4_operand_values(self.struct, self.rows, self.K, v)
         return v
@@ -130,6 +137,7 @@ def nvfp4_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
     """Workspace of nvfp4_linear, nvfp4_matmul and nvfp4_quantize at these sizes, initialised."""
     n = B.moe_nvfp4_workspace_size(M, N, K)
     _need(n > 0, "unsupported shape M=%d N=%d K=%d" % (M, N, K))
+    _need_current(torch.device(device), "workspace")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     B.moe_workspace_init(ws)
     return ws

@@ -1,5 +1,7 @@
 """Refusals of the routing rules, the weighted sum's gradients and the NVFP4 products beyond those of null pointers and shapes."""
 import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 
 from bit_expert_ffn_moe_gb300 import binding as B
 from bit_expert_ffn_moe_gb300 import ops
@@ -29,3 +31,43 @@ def test_arrays_of_words_start_on_four_bytes(off):
         assert combine(**{name: bad}) == INVALID, name
     assert lib.moe_route_logits(256, 256, bad, 4, 128, 8, 256, None) == INVALID
     assert lib.moe_route_logits(256, 256, None, 4, 128, 8, bad, None) == INVALID
+
+
+def on_another_device():
+    """Tensors that say they are on the GPU after the current one, without any memory there."""
+    index = torch.cuda.current_device() + 1 if torch.cuda.is_available() else 1
+    return FakeTensorMode(allow_non_fake_inputs=True), torch.device("cuda", index)
+
+
+def refused_elsewhere():
+    mode, device = on_another_device()
+
+    def new(*shape, dtype=torch.float32):
+        with mode:
+            return torch.empty(shape, dtype=dtype, device=device)
+    rule, i32, bf16, u8 = ops.route_rule(), torch.int32, torch.bfloat16, torch.uint8
+    op = object.__new__(ops.Nvfp4Operand)
+    op.rows, op.K, op.device, op.struct = 128, 256, device.index, B.moe_nvfp4_operand(256, 256, 256, 1)
+    op.q, op.s, op.gs = new(128 * 128, dtype=u8), new(2048, dtype=u8), new(128)
+    ws = new(1 << 20, dtype=u8)
+    calls = [lambda: ops.route_scores(new(4, 64), 8, rule),
+             lambda: ops.route_scores_backward(new(4, 64), new(4, 8, dtype=i32), new(4, 8), rule),
+             lambda: ops.combine_backward(new(4, 64, dtype=bf16), new(8, 64, dtype=bf16), new(8, dtype=i32), new(4, 2)),
+             lambda: ops.nvfp4_quantize(new(128, 256), op),
+             lambda: ops.nvfp4_matmul(op, op, torch.float32, ws),
+             lambda: ops.nvfp4_linear(new(4, 256), op, ws)]
+    if torch.cuda.is_available():  # (the Python-level checks ask torch for the current device)
+        calls += [lambda: ops.route_logits(new(4, 128, dtype=bf16), new(8, 128)), op.values,
+                  lambda: ops.nvfp4_workspace(4, 128, 256, device)]
+    for call in calls:
+        with pytest.raises(ValueError, match="another device than the current one"):
+            call()
+
+
+def test_tensors_of_another_device_are_refused():
+    refused_elsewhere()
+
+
+@pytest.mark.gpu
+def test_tensors_of_another_device_are_refused_beside_a_gpu():
+    refused_elsewhere()

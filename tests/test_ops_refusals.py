@@ -1,7 +1,6 @@
 """Refusals of the routing rules, the weighted sum's gradients and the NVFP4 products beyond those of null pointers and shapes."""
 import pytest
 import torch
-from torch._subclasses.fake_tensor import FakeTensorMode
 
 from bit_expert_ffn_moe_gb300 import binding as B
 from bit_expert_ffn_moe_gb300 import ops
@@ -33,18 +32,16 @@ def test_arrays_of_words_start_on_four_bytes(off):
     assert lib.moe_route_logits(256, 256, None, 4, 128, 8, bad, None) == INVALID
 
 
-def on_another_device():
-    """Tensors that say they are on the GPU after the current one, without any memory there."""
-    index = torch.cuda.current_device() + 1 if torch.cuda.is_available() else 1
-    return FakeTensorMode(allow_non_fake_inputs=True), torch.device("cuda", index)
+class Elsewhere(torch.Tensor):
+    """A tensor without memory that says which device it is on."""
+    __torch_dispatch__ = None
 
 
 def refused_elsewhere():
-    mode, device = on_another_device()
+    device = torch.device("cuda", torch.cuda.current_device() + 1 if torch.cuda.is_available() else 1)
 
     def new(*shape, dtype=torch.float32):
-        with mode:
-            return torch.empty(shape, dtype=dtype, device=device)
+        return torch.Tensor._make_wrapper_subclass(Elsewhere, shape, dtype=dtype, device=device)
     rule, i32, bf16, u8 = ops.route_rule(), torch.int32, torch.bfloat16, torch.uint8
     op = object.__new__(ops.Nvfp4Operand)
     op.rows, op.K, op.device, op.struct = 128, 256, device.index, B.moe_nvfp4_operand(256, 256, 256, 1)

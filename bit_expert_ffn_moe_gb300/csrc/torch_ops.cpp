@@ -86,6 +86,11 @@ int64_t integer(PyObject* o) {
     if (v == -1 && PyErr_Occurred()) throw Refused();
     return v;
 }
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused();
+    return v == 1;
+}
 int32_t narrow(int64_t v, const char* what) {
     if (v < INT32_MIN || v > INT32_MAX) refuse(PyExc_ValueError, what, "too large");
     return (int32_t)v;
@@ -187,7 +192,7 @@ PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor& w0 = tensor(a[3], "w");
         if (w0.dim() != 2) refuse(PyExc_ValueError, "w", "[T, k] expected");
         const int64_t T = dy.size(0), d = dy.size(1), k = w0.size(1);
-        const bool need_dw = PyObject_IsTrue(a[4]) == 1, need_dyp = PyObject_IsTrue(a[5]) == 1;
+        const bool need_dw = truth(a[4]), need_dyp = truth(a[5]);
         const float* w = static_cast<const float*>(plain(a[3], at::kFloat, T, k, dy, "w").data_ptr());
         const int32_t* inv = static_cast<const int32_t*>(plain(a[2], at::kInt, T * k, -1, dy, "inv_pos").data_ptr());
         const uint16_t* yp = nullptr;
@@ -258,7 +263,7 @@ PyObject* nvfp4_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (rows.op) expect(rows, R, C, "rows");
         if (cols.op) expect(cols, C, R, "cols");
         const Space ws = space(a[9], x);
-        check(moe_nvfp4_quantize(x.data_ptr(), dt, R, C, ld, rows.op, cols.op, PyObject_IsTrue(a[10]) == 1, ws.p, ws.bytes, stream()),
+        check(moe_nvfp4_quantize(x.data_ptr(), dt, R, C, ld, rows.op, cols.op, truth(a[10]), ws.p, ws.bytes, stream()),
               "moe_nvfp4_quantize");
         Py_RETURN_NONE;
     });

@@ -68,3 +68,16 @@ def test_tensors_of_another_device_are_refused():
 @pytest.mark.gpu
 def test_tensors_of_another_device_are_refused_beside_a_gpu():
     refused_elsewhere()
+
+
+@pytest.mark.gpu
+def test_a_flag_without_a_truth_value_raises_its_own_error():
+    two = torch.tensor([True, False])
+    dy, w = torch.zeros(4, 64, device="cuda").bfloat16(), torch.zeros(4, 2, device="cuda")
+    inv = torch.arange(8, dtype=torch.int32, device="cuda")
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        ops.combine_backward(dy, dy.repeat(2, 1), inv, w, need_dw=two)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        ops.combine_backward(dy, dy.repeat(2, 1), inv, w, need_dy_perm=two)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        ops.nvfp4_quantize(dy, ops.nvfp4_operand(4, 64), scales_given=two)

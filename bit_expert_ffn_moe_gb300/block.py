@@ -71,6 +71,11 @@ class LatentBlock:
 
     def __call__(self, x: torch.Tensor) -> Tuple[torch.Tensor, dict]:
         """y bf16 [T, D] of bf16 x [T, D], and what router_gradient needs of this pass."""
+        y, past = self._pass(x)
+        return ops.tied("LatentBlock computes its router's gradient alone (router_gradient)", y, x), past
+
+    @torch.no_grad()
+    def _pass(self, x: torch.Tensor) -> Tuple[torch.Tensor, dict]:
         cfg, T = self.layer.cfg, x.shape[0]
         if T > self.max_tokens:
             raise ValueError("at most %d tokens, got %d" % (self.max_tokens, T))
@@ -82,6 +87,7 @@ class LatentBlock:
         B.moe_combine(y_perm, self.inv, w, T, cfg.k, cfg.d, s)
         return self.widen(s), dict(z=z, logits=logits, ids=ids, w=w, y_perm=y_perm, inv=self.inv[:T * cfg.k].clone())
 
+    @torch.no_grad()
     def router_gradient(self, dy: torch.Tensor, past: dict) -> torch.Tensor:
         """Gradient fp32 [E, d] of the router's matrix from that of y, experts and projections held fixed."""
         ds = self.widen.input_gradient(dy)

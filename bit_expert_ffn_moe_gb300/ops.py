@@ -2,7 +2,8 @@
 
 Each function checks its tensors, allocates its results and makes one call of the library, in an extension module; the work is
 the library's kernels, on torch's current stream.  None of them synchronises.  Tensors of another device than the current one are
-refused (`with torch.cuda.device(...)` makes theirs the current one).
+refused (`with torch.cuda.device(...)` makes theirs the current one).  None of them takes part in autograd: gradients come from the
+calls that compute them, and backward() through a result raises an error rather than leave its gradient out.
 """
 from __future__ import annotations
 
@@ -44,6 +45,26 @@ def _need_current(device: torch.device, what: str) -> None:
     _need(device.index is None or device.index == torch.cuda.current_device(), "%s: on another device than the current one" % what)
 
 
+class _Tied(torch.autograd.Function):
+    """A result that hangs on inputs which require a gradient, without a formula for it."""
+
+    @staticmethod
+    def forward(ctx, hint, result, *inputs):
+        ctx.hint = hint
+        return result.detach()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("no autograd formula: %s" % ctx.hint)
+
+
+def tied(hint: str, result: torch.Tensor, *inputs: Optional[torch.Tensor]) -> torch.Tensor:
+    """`result`, which backward() does not get past where one of the inputs requires a gradient: an error with the hint."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        return _Tied.apply(hint, result, *inputs)
+    return result
+
+
 # ------------------------------------------------------------------ routing rules
 
 def route_rule(score: str = "sigmoid", groups: int = 1, top_groups: int = 1, group_score: str = "top2",
@@ -69,7 +90,7 @@ def route_logits(x: torch.Tensor, W_r: torch.Tensor, b: Optional[torch.Tensor] =
           "b: contiguous fp32 [E] expected")
     logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
     B.moe_route_logits(x, W_r, b, T, d, E, logits)
-    return logits
+    return tied("route_logits' gradients are products of dlogits with x and W_r", logits, x, W_r, b)
 
 
 def route_scores(logits: torch.Tensor, k: int, rule: B.moe_route_rule, bias: Optional[torch.Tensor] = None,
@@ -78,7 +99,10 @@ def route_scores(logits: torch.Tensor, k: int, rule: B.moe_route_rule, bias: Opt
     """ids int32 [T, k] (ascending) and weights fp32 [T, k] of logits [T, E] under `rule`; `bias` fp32 [E] takes part in the
     choice only (+inf: picked first, -inf: last).  Logits of -inf take an expert out of service.  scores fp32 [T, E] and counts int32 [E], when given, receive
     all the scores and the picks per expert."""
-    return (_module or _calls()).route_scores(logits, k, rule, bias, scores, counts)
+    ids, w = (_module or _calls()).route_scores(logits, k, rule, bias, scores, counts)
+    if logits.requires_grad:
+        w = tied("route_scores' gradient is route_scores_backward", w, logits)
+    return ids, w
 
 
 def route_scores_backward(logits: torch.Tensor, ids: torch.Tensor, dw: torch.Tensor, rule: B.moe_route_rule,
@@ -163,4 +187,7 @@ def nvfp4_matmul(a: Nvfp4Operand, b: Nvfp4Operand, dtype: torch.dtype, workspace
 
 def nvfp4_linear(x: torch.Tensor, W: Nvfp4Operand, workspace: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [M, K] times W [N, K] transposed, x quantised row by row: [M, N] of x's type (or of `out`'s)."""
-    return (_module or _calls()).nvfp4_linear(x, W.struct, W.rows, W.K, W.device, workspace, out)
+    y = (_module or _calls()).nvfp4_linear(x, W.struct, W.rows, W.K, W.device, workspace, out)
+    if x.requires_grad and out is None:
+        y = tied("nvfp4_linear's gradients are nvfp4_matmul of transposed operands", y, x)
+    return y

@@ -149,7 +149,7 @@ def load(build_if_missing: bool = True):
         return _lib
     path = _build.LIB
     if build_if_missing:
-        path = _build.build()
+        path = _build.build(torch_ops=False)
     if not os.path.exists(path):
         raise RuntimeError("libmoe_gb300.so is not built (run __graft_entry__.build())")
     lib = ctypes.CDLL(path)

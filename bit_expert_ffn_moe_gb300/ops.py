@@ -27,7 +27,8 @@ def _calls():
     global _module
     if _module is None:
         import importlib.util
-        B.load()  # builds both when needed
+        _build.build()  # (where the library or the module is not there, or older than what it is made of)
+        B.load()
         spec = importlib.util.spec_from_file_location("moe_torch_ops", _build.TORCH_OPS)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

@@ -30,12 +30,15 @@ class Nvfp4Linear:
         return ops.nvfp4_linear(x, self.forward_operand, self.workspace)
 
     def input_gradient(self, dy: torch.Tensor) -> torch.Tensor:
+        if self.transposed is None:
+            raise ValueError("input_gradient: built without gradients")
         return ops.nvfp4_linear(dy, self.transposed, self.back_workspace)
 
 
 class LatentBlock:
-    """W_out experts(W_in x): `layer` holds the experts and the router (d, E, k, I), `rule` the routing rule, `balance` an fp32 [E]
-    bias of the choice.  Calls take up to max_tokens tokens; the expert path is that of MXFP4 activations."""
+    """W_out experts(W_in x): `layer` holds the experts and the router's matrix (d, E, k, I; the bias of its logits is not used), `rule`
+    the routing rule, `balance` an fp32 [E] bias of the choice, which balance_step moves in place.  Calls take up to max_tokens tokens; the
+    expert path is that of MXFP4 activations."""
 
     def __init__(self, layer: DeviceLayer, rule: B.moe_route_rule, W_in: torch.Tensor, W_out: torch.Tensor, max_tokens: int,
                  balance: Optional[torch.Tensor] = None, gradients: bool = False):
@@ -97,5 +100,7 @@ class LatentBlock:
 
     def balance_step(self, rate: float) -> None:
         """Moves the balance bias against the load of the last pass: up for experts below the mean, down above."""
+        if self.balance is None:
+            raise ValueError("balance_step: built without a balance bias")
         load = self.counts.float()
         self.balance += rate * torch.sign(load.mean() - load)

@@ -65,6 +65,8 @@ class LatentBlock:
         cfg, W, T = self.layer.cfg, self.layer.weights, z.shape[0]
         shape = (T, cfg.d, cfg.E, cfg.k, cfg.I)
         y_perm = torch.empty((T * cfg.k, cfg.d), dtype=torch.bfloat16, device=z.device)
+        if T == 0:
+            return y_perm
         B.moe_permute(z, ids, T, cfg.d, cfg.E, cfg.k, B.MOE_ACT_MXFP4, self.picked, self.offsets, self.perm, self.inv, self.xa,
                       self.xa_s, self.ws)
         B.moe_expert_up_swiglu(None, self.xa, self.xa_s, B.MOE_ACT_MXFP4, self.perm, self.offsets, *shape, W, self.h, self.h_s,

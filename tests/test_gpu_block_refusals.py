@@ -23,3 +23,11 @@ def test_gradients_and_balance_have_to_be_asked_for():
         block.balance_step(0.1)
     with pytest.raises(ValueError, match="at most 4 tokens"):
         block(torch.randn(5, 1024, device="cuda").bfloat16())
+
+
+def test_no_tokens():
+    import latent_block as example
+    block = example.build(4)
+    y, past = block(torch.empty(0, 1024, device="cuda").bfloat16())
+    assert y.shape == (0, 1024) and int(block.counts.sum()) == 0
+    assert (block.router_gradient(y, past) == 0).all()

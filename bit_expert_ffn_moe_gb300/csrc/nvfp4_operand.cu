@@ -159,16 +159,14 @@ __device__ __forceinline__ RowScale row_scale(uint32_t mag) {
 }
 
 // One block of 16 elements of largest magnitude amax under the row scale: 8 bytes of codes; returns the scale byte.
-// PLAIN: rs.y is not 0 and the scale is the row's own; given: it may not be, and quotients may be far above 6: they saturate.  amax is
-// then cut at 4096 g, where the block's scale is at its largest (2688 g gives it) and no step of the quotient overflows.  A given scale of
-// zero leaves room for zeros alone: block scale 0, for blocks of zeros too (0 / 0 would make it NaN).
+// PLAIN: rs.y is not 0 and the scale is the row's own; given: it may not be, and quotients may be far above 6: they saturate.  The block's
+// scale is then found by divisions, which give inf and not NaN where they overflow, and by a scale of zero as by the smallest
+// number: its blocks of zeros stay zeros (0 / 0 would make them NaN), and D = 0 makes zeros of all others.
 template <typename T, bool PLAIN>
 __device__ __forceinline__ uint32_t encode_block(float (&v)[16], float amax, RowScale rs, bool given, uint2& codes) {
     float t;
-    if (sizeof(T) == 2 && !PLAIN && rs.y != 0.f && amax > 4096.f * rs.g) amax = 4096.f * rs.g;
-    if (sizeof(T) == 2 && (PLAIN || rs.y != 0.f)) t = quotient(quotient(amax, rs.g, rs.y), 6.f, 0.166666672f);
-    else if (!PLAIN && given && rs.g == 0.f) t = amax == amax ? 0.f : amax;
-    else t = __fdiv_rn(__fdiv_rn(amax, rs.g), 6.f);
+    if (sizeof(T) == 2 && PLAIN) t = quotient(quotient(amax, rs.g, rs.y), 6.f, 0.166666672f);
+    else t = __fdiv_rn(__fdiv_rn(amax, PLAIN ? rs.g : fmaxf(rs.g, 1e-45f)), 6.f);
     const uint32_t sb = f32_to_e4m3_sat(t);
     const float D = __fmul_rn(e4m3x2_to_f2(sb).x, rs.g);
     if (!PLAIN && given) {

@@ -75,6 +75,23 @@ __device__ __forceinline__ uint4 out_piece(const uint32_t* v) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// A result is (sum * ga) * gb.  Its first product leaves fp32's range only where a row's scale is far from 1 (a sum is 0 or 2^-20 ..
+// 2^45; a row of the type's largest numbers has a scale of 2^117): then all rows' scales of the warp times a power of two and
+// the columns' scales divided by it, which is exact, keep what fp32 can hold.
+__device__ __forceinline__ bool far_scale(float ga) { return ga > 0x1p80f || ga < 0x1p-100f; }
+// That power of two for the rows' scales ga (one per lane) and the columns' between gb_min and gb_max (per lane): no further than
+// leaves every scale in range.
+__device__ __noinline__ float scale_shift(float ga, float gb_min, float gb_max) {
+    auto exponent = [](float v) { return (int)(__float_as_uint(v) >> 23) - 127; };
+    const bool counts = ga > 0.f && ga < INFINITY;
+    const int a1 = __reduce_max_sync(0xffffffffu, counts ? exponent(ga) : -200), a0 = __reduce_min_sync(0xffffffffu, counts ? exponent(ga) : 200);
+    const int c1 = __reduce_max_sync(0xffffffffu, exponent(gb_max)), c0 = __reduce_min_sync(0xffffffffu, exponent(gb_min));
+    int p = 0;
+    if (a1 > 80) p = min(max(max(80 - a1, c1 - 127), -100 - a0), 0);
+    else if (a0 < -100) p = max(min(min(-100 - a0, 80 - a1), c0 + 126), 0);
+    return __uint_as_float((uint32_t)(127 + p) << 23);
+}
+
 // One thread of a converged warp, known as one to the compiler: where it is chosen by its lane number instead, each copy or MMA
 // is issued through a loop over the lanes (about 130 cycles; 8192^3: 165 us, 150 with this for the pair kernel's copies).
 __device__ __forceinline__ bool elect_one() {
@@ -164,8 +181,18 @@ __device__ __forceinline__ void store_rows(const MatmulArgs& args, const float* 
     for (int i = 0; i < 4; ++i) gb[i] = i < live ? args.gb[args.gb_rows ? n + i : 0] : 0.f;
     const bool wide = reinterpret_cast<uintptr_t>(args.y) % 16 == 0 && args.ldy % 4 == 0;
     const int c0 = rank + splits * warp;
-    float ga_lane = 0.f;  // lane i: the scale of this warp's i-th row (at most 22)
+    float ga_lane = 1.f;  // lane i: the scale of this warp's i-th row (at most 22)
     if (c0 + splits * WARPS * lane < rows) ga_lane = ga[ga_rows ? c0 + splits * WARPS * lane : 0];
+    if (__any_sync(0xffffffffu, far_scale(ga_lane))) {
+        float least = INFINITY, most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < live) least = fminf(least, gb[i]), most = fmaxf(most, gb[i]);
+        const float f = scale_shift(ga_lane, least, most);
+        ga_lane *= f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) gb[i] /= f;
+    }
 #pragma unroll 2
     for (int i = 0; i < (NT + WARPS - 1) / WARPS; ++i) {
         const int c = c0 + splits * WARPS * i;
@@ -556,12 +583,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (int t = first; t < n_tiles; t += step, ++tile) {
             const int64_t m0 = (int64_t)(t / NT) * 256 + 128 * rank + 32 * q, n0 = (int64_t)(t % NT) * 256 + 128 * half;
             const int64_t m = m0 + lane;
-            const float ga = m < args.M ? args.ga[args.ga_rows ? m : 0] : 0.f;
+            float ga = m < args.M ? args.ga[args.ga_rows ? m : 0] : 1.f;
             const int live = (int)max((int64_t)0, min((int64_t)128, args.N - n0));  // columns of this warp's half
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 if (32 * c + lane < live) gb[32 * c + lane] = args.gb[args.gb_rows ? n0 + 32 * c + lane : 0];
             __syncwarp();
+            if (__any_sync(0xffffffffu, far_scale(ga))) {
+                float least = INFINITY, most = 0.f;
+                for (int i = lane; i < live; i += 32) least = fminf(least, gb[i]), most = fmaxf(most, gb[i]);
+                const float f = scale_shift(ga, least, most);
+                ga *= f;
+                for (int i = lane; i < live; i += 32) gb[i] /= f;
+                __syncwarp();
+            }
             if (!mbar_wait(acc_full, tile & 1, abort_flag, args.status)) break;
             tc_fence_after();
             uint32_t v[4][32];

@@ -162,3 +162,38 @@ def test_a_given_scale_of_zero_makes_zeros(dtype, R, C, extra):
         ops.nvfp4_quantize(torch.ones(9, op.K, device="cuda"), other)
         y = ops.nvfp4_matmul(op, other, torch.float32, ops.nvfp4_workspace(op.rows, 9, op.K))
         assert (y[:3] == 0).all() and torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 130, 300), (9, 264, 1024), (40, 130, 300), (100, 1000, 520), (200, 600, 300), (1500, 1501, 300)])
+@pytest.mark.parametrize("x_size,w_size", [(3e38, 1e-9), (3e38, 1e-37), (1e36, 1e-30), (1e-37, 1e30), (2e-44, 1e36), (1e-18, 1e-18), (1e18, 1e18)])
+def test_rows_of_any_size_give_what_fp32_can_hold(out, M, N, K, x_size, w_size):
+    """Rows of x of magnitude 1 and of x_size (the type's largest, say, as a mask value) times weights around w_size.  Against 64-bit products of
+    the operands' values: (4 K/256 + 4) 2^-22 of the sum of the magnitudes, as in the other tests of the products, half a step of the result's type
+    and of the smallest number that it has; results beyond the type are infinite."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, K, generator=g, device="cuda").clamp(-1, 1)
+    w = torch.randn(N, K, generator=g, device="cuda").clamp(-1, 1).double() * w_size
+    big = torch.rand(M, 1, generator=g, device="cuda") < 0.5
+    big[0] = True
+    x = torch.where(big, x.double() * x_size, x.double()).float()
+    a, b = ops.nvfp4_operand(M, K), ops.nvfp4_operand(N, K)
+    ops.nvfp4_quantize(x, a)
+    ops.nvfp4_quantize(w.float(), b)
+    ws = ops.nvfp4_workspace(M, N, K)
+    y = ops.nvfp4_matmul(a, b, TYPES[out], ws).double()
+    va, vb = (exact_values(o) for o in (a, b))
+    ref, mag = va @ vb.T, va.abs() @ vb.abs().T
+    info = torch.finfo(TYPES[out])
+    tol = (4 * -(-K // 256) + 4) * 2.0 ** -22 * mag + info.eps / 2 * ref.abs() + info.smallest_normal * info.eps
+    sure = ref.abs() + tol <= info.max
+    assert ((y - ref).abs() <= tol)[sure].all()
+    assert torch.isinf(y[ref.abs() - tol > 1.01 * info.max]).all()
+    assert torch.equal(y.to(TYPES[out]), ops.nvfp4_linear(x, b, ws, torch.empty(M, N, dtype=TYPES[out], device="cuda")))
+    assert B.moe_get_device_status(ws) == B.MOE_OK
+
+
+def exact_values(op):
+    """An operand's numbers without the rounding of its values(): that of the same codes under scales of one, times the row scales."""
+    one = ops.Nvfp4Operand(op.rows, op.K, op.q, op.s, torch.ones_like(op.gs))
+    return one.values().double() * op.gs.double()[:, None]

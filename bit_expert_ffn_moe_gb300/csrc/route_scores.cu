@@ -51,14 +51,6 @@ __device__ __forceinline__ double warp_sum_f64(double v) {
     for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(kFull, v, m);
     return v;
 }
-__device__ __forceinline__ double warp_max_f64(double v) {  // (no NaN)
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-        const double o = __shfl_xor_sync(kFull, v, m);
-        v = o > v ? o : v;
-    }
-    return v;
-}
 // Largest value of the warp (NaN ignored unless every lane has one).
 __device__ __forceinline__ float warp_max_f32(float v) {
     float m;
@@ -139,12 +131,11 @@ struct Top2 {
 __device__ __forceinline__ int group_lane_shift(int G) { return G <= 1 ? 5 : G <= 2 ? 4 : G <= 4 ? 3 : G <= 8 ? 2 : G <= 16 ? 1 : 0; }
 
 // The best two of group lane >> sh from values val[e] (-inf: out of service), in every lane of the group.
-template <typename F>
-__device__ __forceinline__ Top2<F> group_best(const float* val, int G, int S, int sh) {
+__device__ __forceinline__ Top2<float> group_best(const float* val, int G, int S, int sh) {
     const int lane = threadIdx.x & 31, g = lane >> sh, lp = 1 << sh;
-    Top2<F> t{(F)-INFINITY, (F)-INFINITY};
+    Top2<float> t{-INFINITY, -INFINITY};
     if (g < G)
-        for (int j = lane & (lp - 1); j < S; j += lp) t.add((F)val[g * S + j]);
+        for (int j = lane & (lp - 1); j < S; j += lp) t.add(val[g * S + j]);
     for (int m = 1; m < lp; m <<= 1) t.merge(m);
     return t;
 }
@@ -224,10 +215,18 @@ __device__ __forceinline__ float sigmoid_fast(float l) {
 }
 
 // ------------------------------------------------------------------ the careful choice
-// A 64-bit key in the order of doubles (no NaN).
+// A 64-bit key in the order of doubles (no NaN), and back: comparisons of keys are integer instructions.
 __device__ __forceinline__ unsigned long long key64(double v) {
     const long long u = __double_as_longlong(v == 0.0 ? 0.0 : v);
     return u < 0 ? ~(unsigned long long)u : (unsigned long long)u | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double key_double(unsigned long long k) {
+    return __longlong_as_double((long long)(k >> 63 ? k & 0x7fffffffffffffffull : ~k));
+}
+__device__ __forceinline__ unsigned long long warp_max_key(unsigned long long k) {
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) k = max(k, __shfl_xor_sync(kFull, k, m));
+    return k;
 }
 
 // What the launcher works out once: experts per group, ceil(2^20 / that), whether rows and bias may be read in wide
@@ -264,7 +263,7 @@ __device__ __forceinline__ Scratch warp_scratch(void* smem, int E, int warps, in
 // (a few) are computed in 64 bits, one per lane.  Writes the k ids in ascending order to picks[].
 //   An infinite bias ranks its expert before or behind all finite values: such a value is exact, so the error's bound is
 // that of the finite ones, and no border between values of which one is infinite is in doubt (each comparison below is
-// false for a difference of inf or NaN).  Groups are scored in 64 bits, where sums of finite values stay finite.
+// false for a difference of inf or NaN).  Groups' sums are 64-bit, where those of finite values stay finite.
 template <typename T>
 __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const RoutePlan& plan, const T* row, const Scratch sc) {
     const int lane = threadIdx.x & 31;
@@ -332,14 +331,16 @@ __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const Rout
         }
         __syncwarp();
         constexpr double kInf = INFINITY;
-        const Top2<double> best = group_best<double>(val, G, S, sh);
-        const double gs = best.score(top2);
-        kept = best_groups<double>(gs, G == 32 ? kFull : (1u << G) - 1, G, sh, keep);
+        const Top2<float> best = group_best(val, G, S, sh);
+        const double gs = best.two(top2) ? (double)best.a + (double)best.b : (double)best.a;
+        const unsigned long long gkey = key64(gs);
+        kept = best_groups<unsigned long long>(gkey, G == 32 ? kFull : (1u << G) - 1, G, sh, keep);
         if (!raw) {
             const bool mine = g < G && gs > -kInf;
             const bool in = g < G && ((kept >> g) & 1);
-            const double lo = warp_max_f64(mine && !in ? gs : -kInf);   // best left out
-            const double hi = -warp_max_f64(mine && in ? -gs : -kInf);  // worst kept
+            const unsigned long long none = key64(-kInf);
+            const double lo = key_double(warp_max_key(mine && !in ? gkey : none));     // best left out
+            const double hi = key_double(~warp_max_key(mine && in ? ~gkey : ~key64(kInf)));  // worst kept
             const double verr = biased ? err : err_s, gerr = 2.0 * verr;
             if (lo > -kInf && hi < kInf && hi - lo <= gerr) {
                 const bool is_open = mine && gs >= hi - gerr && gs <= lo + gerr;
@@ -351,7 +352,7 @@ __device__ __noinline__ void choose_careful(const RouteScoresArgs& a, const Rout
                     in_mask |= ((sure >> (j << sh)) & 1u) << j;
                 }
                 // of the open groups, the values that may be among a group's best one or two
-                if ((lane & ((1 << sh) - 1)) == 0) sc.picks[g] = __float_as_int(__double2float_rd(best.least(top2) - verr));
+                if ((lane & ((1 << sh) - 1)) == 0) sc.picks[g] = __float_as_int(__fsub_rd(best.least(top2), biased ? err : err_s));
                 __syncwarp();
                 int n = 0;
                 for (int i = 0; i < nv; ++i) {
@@ -611,7 +612,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps)
                 if (e0 + i < E) val[e0 + i] = v[i];
             __syncwarp();
             const int gsh = group_lane_shift(G), g = lane >> gsh;
-            const Top2<float> best = group_best<float>(val, G, S, gsh);
+            const Top2<float> best = group_best(val, G, S, gsh);
             kept = best_groups<float>(best.score(top2), G == 32 ? kFull : (1u << G) - 1, G, gsh, a.rule.top_groups);
             if (!raw) {
                 const bool mine = g < G && ((kept >> g) & 1);

@@ -4,8 +4,8 @@
 // the tensor-core layout of nvfp4_operand.cu: code tiles of 128 rows x 256 values with the 128-byte swizzle and
 // 512-byte scale atoms, so that every piece is one contiguous bulk copy and ragged sizes need no
 // masks before the store (padding along K holds zeros; padding rows only reach results that are not stored).
-// Products and sums are the tensor core's (fp32 accumulators); each result is scaled by ga and gb in fp32
-// and rounded once.
+// Products and sums are the tensor core's (fp32 accumulators); each result is multiplied by ga, then by gb, in fp32
+// and rounded to y's type.
 //
 // Two kernels:
 //   rows    up to 128 activation rows per tile: the weights are the MMA's M side (128 weight rows), the

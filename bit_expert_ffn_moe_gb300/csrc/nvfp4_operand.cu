@@ -22,7 +22,7 @@
 //               atomics does not matter), then tiles of 256 rows x 64 columns through shared memory, encoded
 //               along their rows and along their columns, two columns per thread; 256 rows are a whole
 //               128-byte row of a column operand's code tile.  The second pass finds x in L2 while it fits there.
-// (2 or 4) R C bytes in, 9/16 R C out per form.  Rows of a bf16 matrix 4096 x 8192: 19 us (4.5 TB/s), both forms 45 us (11 of
+// (2 or 4) R C bytes in, 9/16 R C out per form.  Rows of a bf16 matrix 4096 x 8192: 18 us (4.8 TB/s), both forms 44.6 us (11 of
 // them the maxima).  The encoding, about 110 warp instructions per block and lane, keeps 58% of the issue slots busy; leaving out
 // the stores (43.7 us) or smaller tiles with a third more warps (49) hardly matter or hurt.
 #include <type_traits>
@@ -452,8 +452,8 @@ __global__ void __launch_bounds__(kThreads) nvfp4_zero_kernel(unsigned* p, int64
     if (i < n) p[i] = 0u;
 }
 
-// Maxima of |x| over rows and columns as fp32 bits in row_max[R] and col_max[C], which the kernel before zeroes meanwhile.  A
-// warp takes kMaxRows rows of 16 bytes per lane; the 8 warps of a CTA rows of the same columns.
+// Maxima of |x| over rows and columns as fp32 bits in row_max[R] and col_max[C], which the kernel before zeroes meanwhile: x is
+// read ahead of the wait, since that kernel has waited for what was written before it.  A warp takes kMaxRows rows of 16 bytes per lane; the 8 warps of a CTA rows of the same columns.
 constexpr int kMaxRows = 16;
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4)

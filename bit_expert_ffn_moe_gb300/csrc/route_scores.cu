@@ -508,8 +508,8 @@ __device__ __forceinline__ int lanes_before(uint32_t set, double v) {
 // (about k^2 / 64 at random): those go to lanes of their own, in id order, and the smallest are dropped one
 // by one until k are left.  With fp32 ranking values the bound is lowered by their error, so that every value
 // which might belong to the picks is among these; what is too close to the border is settled in 64 bits.
-// Issue-bound, hence the care for instructions: 16384 tokens of 256 fp32 logits (2.5 us of reading) take 13.9 us with 8 groups and
-// a bias (about 700 warp instructions a token, 68% of the issue slots), 8.8 us without.
+// Issue-bound, hence the care for instructions: 16384 tokens of 256 fp32 logits (2.5 us of reading) take 14.0 us with 8 groups and
+// a bias (about 700 warp instructions a token, 68% of the issue slots), 9.8 us without.
 template <int NV, typename T>
 __global__ void __launch_bounds__(32 * kRouteWarps)
     route_scores_kernel(const __grid_constant__ RouteScoresArgs a, const __grid_constant__ RoutePlan plan) {

@@ -117,7 +117,7 @@ def combine_backward(dy: torch.Tensor, y_perm: Optional[torch.Tensor], inv_pos: 
                      need_dw: bool = True, need_dy_perm: bool = True
                      ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
     """Gradients of the weighted sum y[t] = sum_j w[t, j] y_perm[inv_pos[t k + j]]: dw fp32 [T, k] and dy_perm bf16 [T k, d]
-    (None where not needed) from dy bf16 [T, d]."""
+    (None where not needed) from dy bf16 [T, d].  Rows of dy_perm that no entry of inv_pos names are not written."""
     return (_module or _calls()).combine_backward(dy, y_perm, inv_pos, w, need_dw, need_dy_perm)
 
 

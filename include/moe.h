@@ -484,7 +484,8 @@ moe_status moe_route_scores_backward(const void* logits, moe_dtype dtype, int64_
 /* Gradients of moe_combine's weighted sum: dw[t][j] = sum_i dy[t][i] * y_perm[inv_pos[t*k+j]][i] (fp32) and
  * dy_perm[inv_pos[t*k+j]] = w[t][j] * dy[t] (bf16).  dy bf16 [T][d]; y_perm, dy_perm bf16 [T*k][d]; w, dw fp32 [T][k].
  * Either result may be NULL (not computed; y_perm is needed for dw only, w for dy_perm only).  inv_pos
- * names each row at most once; an entry outside [0, T*k) gives dw 0.  d % 8 == 0, 1 <= k <= 32; 16-byte aligned. */
+ * names each row at most once; an entry outside [0, T*k) gives dw 0, and rows of dy_perm that no entry names are left as
+ * they are.  d % 8 == 0, 1 <= k <= 32; 16-byte aligned. */
 moe_status moe_combine_backward(const uint16_t* dy, const uint16_t* y_perm, const int32_t* inv_pos, const float* w, int T,
                                 int k, int d, float* dw, uint16_t* dy_perm, moe_stream_t stream);
 
@@ -524,8 +525,8 @@ moe_status moe_nvfp4_quantize(const void* x, moe_dtype dtype, int64_t R, int64_t
 /* The numbers an operand stands for, fp32 v [rows][K]: (E2M1 * E4M3) * gs, rounded once. */
 moe_status moe_nvfp4_operand_values(const moe_nvfp4_operand* op, int64_t rows, int64_t K, float* v, moe_stream_t stream);
 
-/* y [M][ldy] (dtype) = A [M][K] * B [N][K]^T: fp32 sums on the tensor cores, times the rows' scales, rounded
- * once.  K >= 1, ldy >= N; y aligned to its element. */
+/* y [M][ldy] (dtype) = A [M][K] * B [N][K]^T: fp32 sums on the tensor cores, times the scale of A's row, times that of
+ * B's (two fp32 products), rounded to dtype.  K >= 1, ldy >= N; y aligned to its element. */
 moe_status moe_nvfp4_matmul(const moe_nvfp4_operand* A, const moe_nvfp4_operand* B, int64_t M, int64_t N, int64_t K, void* y,
                             moe_dtype dtype, int64_t ldy, void* ws, size_t ws_bytes, moe_stream_t stream);
 

@@ -49,6 +49,10 @@ EXPORTED = (
     "moe_route_logits", "moe_route_scores", "moe_route_scores_backward", "moe_combine_backward", "moe_nvfp4_operand_codes",
     "moe_nvfp4_operand_scales", "moe_nvfp4_workspace_size", "moe_nvfp4_quantize", "moe_nvfp4_operand_values",
     "moe_nvfp4_matmul", "moe_nvfp4_linear",
+    "moe_expert_order", "moe_tokens_to_experts", "moe_tokens_to_experts_backward", "moe_experts_to_tokens",
+    "moe_experts_to_tokens_backward", "moe_int8_weights_bytes", "moe_int8_weights_layout", "moe_int8_weights_quantize",
+    "moe_int8_rows_room", "moe_int8_rows_bytes", "moe_int8_quantize", "moe_int8_workspace_size", "moe_int8_matmul", "moe_int8_linear",
+    "moe_int8_experts_workspace_size", "moe_int8_experts",
 )
 
 
@@ -81,6 +85,14 @@ class moe_nvfp4_operand(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "s", "gs")] + [("gs_rows", ctypes.c_int32)]
 
 
+class moe_int8_weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "s")]
+
+
+class moe_int8_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "s")] + [("room", ctypes.c_int64)]
+
+
 _lib = None
 P = ctypes.c_void_p
 I32, I64, U32, U64 = ctypes.c_int, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64
@@ -89,6 +101,8 @@ WP = ctypes.POINTER(moe_expert_weights)
 MP = ctypes.POINTER(moe_mxfp4_matrix)
 RP = ctypes.POINTER(moe_route_rule)
 OP = ctypes.POINTER(moe_nvfp4_operand)
+W8 = ctypes.POINTER(moe_int8_weights)
+R8 = ctypes.POINTER(moe_int8_rows)
 
 _SIGS = {
     "moe_status_string": (ctypes.c_char_p, [I32]),
@@ -135,6 +149,22 @@ _SIGS = {
     "moe_nvfp4_operand_values": (I32, [OP, I64, I64, P, P]),
     "moe_nvfp4_matmul": (I32, [OP, OP, I64, I64, I64, P, I32, I64, P, SZ, P]),
     "moe_nvfp4_linear": (I32, [P, I32, I64, I64, I64, OP, I64, P, I32, I64, P, SZ, P]),
+    "moe_expert_order": (I32, [P, I32, I32, I32, P, P, P]),
+    "moe_tokens_to_experts": (I32, [P, I32, I64, P, P, I32, I32, I32, P, I64, P]),
+    "moe_tokens_to_experts_backward": (I32, [P, I32, I64, P, I64, P, P, I32, I32, I32, P, I64, P, P]),
+    "moe_experts_to_tokens": (I32, [P, I32, I64, P, P, I32, I32, I32, P, I64, P]),
+    "moe_experts_to_tokens_backward": (I32, [P, I32, I64, P, I64, P, P, I32, I32, I32, P, I64, P, P]),
+    "moe_int8_weights_bytes": (SZ, [I64, I64]),
+    "moe_int8_weights_layout": (I32, [P, P, I32, I64, I64, I64, I64, I64, I64, W8, P]),
+    "moe_int8_weights_quantize": (I32, [P, I32, I32, I64, I64, I64, I64, I64, I64, W8, P]),
+    "moe_int8_rows_room": (I64, [I64, I32]),
+    "moe_int8_rows_bytes": (SZ, [I64, I64]),
+    "moe_int8_quantize": (I32, [P, I32, I64, I64, I64, P, I32, P, I32, R8, P]),
+    "moe_int8_workspace_size": (SZ, [I64, I64, I64]),
+    "moe_int8_matmul": (I32, [R8, P, I32, I64, W8, I64, I64, I32, P, I32, I64, P, SZ, P]),
+    "moe_int8_linear": (I32, [P, I32, I64, I64, I64, W8, I64, I32, P, I32, I64, P, SZ, P]),
+    "moe_int8_experts_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32]),
+    "moe_int8_experts": (I32, [P, I32, I64, P, P, I32, I32, I32, I32, I32, W8, W8, P, I64, P, SZ, P]),
 }
 
 
@@ -447,4 +477,82 @@ def moe_nvfp4_matmul(A: moe_nvfp4_operand, B: moe_nvfp4_operand, M, N, K, y, dty
 
 def moe_nvfp4_linear(x, x_dtype, M, K, ldx, W: moe_nvfp4_operand, N, y, y_dtype, ldy, ws, ws_bytes=None, stream=None):
     _check("moe_nvfp4_linear", load().moe_nvfp4_linear(_p(x), x_dtype, M, K, ldx, W, N, _p(y), y_dtype, ldy, _p(ws),
+                                                       _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+# ------------------------------------------------------------------ rows between tokens and experts, products in 8-bit integers
+
+def moe_expert_order(ids, T, k, E, offsets, inv, stream=None):
+    _check("moe_expert_order", load().moe_expert_order(_p(ids), T, k, E, _p(offsets), _p(inv), _stream(stream)))
+
+
+def moe_tokens_to_experts(x, dtype, ldx, inv, w, T, k, d, rows, ldr, stream=None):
+    _check("moe_tokens_to_experts", load().moe_tokens_to_experts(_p(x), dtype, ldx, _p(inv), _p(w), T, k, d, _p(rows), ldr,
+                                                                 _stream(stream)))
+
+
+def moe_tokens_to_experts_backward(drows, dtype, ldr, x, ldx, inv, w, T, k, d, dx, ldd, dw, stream=None):
+    _check("moe_tokens_to_experts_backward",
+           load().moe_tokens_to_experts_backward(_p(drows), dtype, ldr, _p(x), ldx, _p(inv), _p(w), T, k, d, _p(dx), ldd, _p(dw),
+                                                 _stream(stream)))
+
+
+def moe_experts_to_tokens(rows, dtype, ldr, inv, w, T, k, d, y, ldy, stream=None):
+    _check("moe_experts_to_tokens", load().moe_experts_to_tokens(_p(rows), dtype, ldr, _p(inv), _p(w), T, k, d, _p(y), ldy,
+                                                                 _stream(stream)))
+
+
+def moe_experts_to_tokens_backward(dy, dtype, ldy, rows, ldr, inv, w, T, k, d, drows, ldg, dw, stream=None):
+    _check("moe_experts_to_tokens_backward",
+           load().moe_experts_to_tokens_backward(_p(dy), dtype, ldy, _p(rows), ldr, _p(inv), _p(w), T, k, d, _p(drows), ldg, _p(dw),
+                                                 _stream(stream)))
+
+
+def moe_int8_weights_bytes(N, K) -> int:
+    return int(load().moe_int8_weights_bytes(N, K))
+
+
+def moe_int8_weights_layout(w, s_in, E, rows, K, ld, first, step, N, W: moe_int8_weights, stream=None):
+    _check("moe_int8_weights_layout", load().moe_int8_weights_layout(_p(w), _p(s_in), E, rows, K, ld, first, step, N, W,
+                                                                     _stream(stream)))
+
+
+def moe_int8_weights_quantize(w, dtype, E, rows, K, ld, first, step, N, W: moe_int8_weights, stream=None):
+    _check("moe_int8_weights_quantize", load().moe_int8_weights_quantize(_p(w), dtype, E, rows, K, ld, first, step, N, W,
+                                                                         _stream(stream)))
+
+
+def moe_int8_rows_room(M, E=0) -> int:
+    return int(load().moe_int8_rows_room(M, E))
+
+
+def moe_int8_rows_bytes(room, K) -> int:
+    return int(load().moe_int8_rows_bytes(room, K))
+
+
+def moe_int8_quantize(x, dtype, T, K, ldx, inv, k, offsets, E, rows: moe_int8_rows, stream=None):
+    _check("moe_int8_quantize", load().moe_int8_quantize(_p(x), dtype, T, K, ldx, _p(inv), k, _p(offsets), E, rows, _stream(stream)))
+
+
+def moe_int8_workspace_size(M, N, K) -> int:
+    return int(load().moe_int8_workspace_size(M, N, K))
+
+
+def moe_int8_matmul(rows: moe_int8_rows, offsets, E, M, W: moe_int8_weights, N, K, gated, y, dtype, ldy, ws, ws_bytes=None, stream=None):
+    _check("moe_int8_matmul", load().moe_int8_matmul(rows, _p(offsets), E, M, W, N, K, int(gated), _p(y), dtype, ldy, _p(ws),
+                                                     _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_int8_linear(x, x_dtype, M, K, ldx, W: moe_int8_weights, N, gated, y, y_dtype, ldy, ws, ws_bytes=None, stream=None):
+    _check("moe_int8_linear", load().moe_int8_linear(_p(x), x_dtype, M, K, ldx, W, N, int(gated), _p(y), y_dtype, ldy, _p(ws),
+                                                     _ws_bytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_int8_experts_workspace_size(T, d, E, k, I, dtype) -> int:  # noqa: E741
+    return int(load().moe_int8_experts_workspace_size(T, d, E, k, I, dtype))
+
+
+def moe_int8_experts(x, dtype, ldx, ids, w, T, d, E, k, I, up: moe_int8_weights, down: moe_int8_weights, y, ldy, ws,  # noqa: E741
+                     ws_bytes=None, stream=None):
+    _check("moe_int8_experts", load().moe_int8_experts(_p(x), dtype, ldx, _p(ids), _p(w), T, d, E, k, I, up, down, _p(y), ldy, _p(ws),
                                                        _ws_bytes(ws, ws_bytes), _stream(stream)))

@@ -106,3 +106,43 @@ class LatentBlock:
             raise ValueError("balance_step: built without a balance bias")
         load = self.counts.float()
         self.balance += rate * torch.sign(load.mean() - load)
+
+
+class Int8Linear:
+    """y = x W^T with W [N, K] (int8 with a scale per row, or numbers to quantise), x quantised row by row."""
+
+    def __init__(self, W: torch.Tensor, max_rows: int, scales: Optional[torch.Tensor] = None):
+        self.weights = ops.int8_weights(W, scales)
+        self.workspace = ops.int8_workspace(max_rows, self.weights.N, self.weights.K, W.device)
+
+    def __call__(self, x: torch.Tensor) -> torch.Tensor:
+        return ops.int8_linear(x, self.weights, self.workspace)
+
+
+class Int8Experts:
+    """A sparse layer in 8-bit integers behind any routing rule: `up` the gated weights [E, 2 I, d], `down` [E, d, I]
+    (ops.int8_weights).  Calls take up to max_tokens tokens of k slots, of dtype (or another type of no more bytes)."""
+
+    def __init__(self, up: ops.Int8Weights, down: ops.Int8Weights, max_tokens: int, k: int, dtype: torch.dtype = torch.bfloat16):
+        if up.E != down.E or up.K != down.N or up.N != 2 * down.K:
+            raise ValueError("up [E, 2 I, d] and down [E, d, I] expected")
+        self.up, self.down, self.max_tokens, self.k = up, down, max_tokens, k
+        self.workspace = ops.int8_experts_workspace(max_tokens, k, up.K, down.K, up.E, dtype, up.q.device)
+
+    def _check(self, x: torch.Tensor, ids: torch.Tensor) -> None:
+        if x.shape[0] > self.max_tokens or ids.dim() != 2 or ids.shape[1] != self.k:
+            raise ValueError("at most %d tokens of %d slots expected" % (self.max_tokens, self.k))
+
+    def __call__(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor) -> torch.Tensor:
+        """y [T, d] of x [T, d] and the routing ids int32 [T, k], w fp32 [T, k]."""
+        self._check(x, ids)
+        return ops.int8_experts(x, ids, w, self.up, self.down, self.workspace)
+
+    @torch.no_grad()
+    def outputs(self, x: torch.Tensor, ids: torch.Tensor) -> Tuple[torch.Tensor, ops.ExpertOrder]:
+        """The experts' outputs [T k, d] in expert order, and that order: the layer without its weighted sum, for the gradient of the
+        routing weights (ops.experts_to_tokens_backward)."""
+        self._check(x, ids)
+        order = ops.expert_order(ids, self.up.E)
+        h = ops.int8_matmul(ops.int8_quantize(x, order), self.up, x.dtype, self.workspace, gated=True)
+        return ops.int8_matmul(ops.int8_quantize(h, order, ordered=True), self.down, x.dtype, self.workspace), order

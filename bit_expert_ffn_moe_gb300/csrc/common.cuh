@@ -25,6 +25,7 @@ constexpr int kTokTile = 128;   // token tile (MMA N) of the tcgen05 grouped GEM
 constexpr int kDecTickets = 64;
 constexpr int kDecSlots = 512;
 constexpr int kDecSplitCounters = 1024;  // (slot, block) arrival counters of split gate/up tiles
+constexpr int kInt8Splits = 256;  // arrivals at the tiles that CTAs of an 8-bit product share (at most one starts in a CTA's share)
 struct Ctrl {
     int status;
     unsigned route_ticket;
@@ -33,7 +34,8 @@ struct Ctrl {
     unsigned dec_ticket[kDecTickets];
     unsigned dec_ready[kDecSlots];
     unsigned dec_split[kDecSplitCounters];
-    int pad[444];
+    unsigned int8_split[kInt8Splits];
+    int pad[444 - kInt8Splits];
 };
 static_assert(sizeof(Ctrl) == 8192, "control block size");
 
@@ -504,6 +506,8 @@ cudaError_t ensure_dyn_smem(const void* func, size_t bytes);
 // Launch with the programmatic-dependent-launch attribute when pdl is true.
 cudaError_t launch_kernel(const void* func, dim3 grid, dim3 block, size_t smem, cudaStream_t st, bool pdl,
                           void** args);
+// The same with the attribute, as clusters of `cluster` CTAs (1: none).
+cudaError_t launch_cluster(const void* func, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, void** args);
 int sm_count();  // SMs of the current device
 
 cudaError_t launch_synth(uint64_t seed, uint32_t tensor_id, uint32_t expert_first, uint32_t n_experts, int64_t rows,

@@ -1,0 +1,242 @@
+// int8_operand.cu -- operands of the 8-bit products.  A row v of K numbers is held as whole numbers q and one fp32 scale s:
+//   s = max |v| / 127 (1 for a row of zeros),  q = v / s rounded to the nearest whole number, ties to even, within -127 .. 127
+// (each step rounded to fp32).  A row with a NaN or an infinity gets s = NaN and q = 0, which makes its results NaN.
+// Layouts: ops.cuh.  Weights are kept in one byte each; activations as fp16 numbers, which is what the tensor cores take
+// (sm_103a's have no 8-bit whole numbers), in the layout that they read, so that a product's copies are contiguous.
+#include "ops.cuh"
+#include "route_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKept = 4;  // pieces of 8 values that a thread keeps between the two passes over its row (256 threads: 8192 values)
+
+// The largest magnitude as the bits of |v|: NaN above infinity above all numbers.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+struct Scale {
+    float s, inverse;
+    bool bad;
+};
+__device__ __forceinline__ Scale scale_of(uint32_t most) {
+    Scale r;
+    r.bad = most >= 0x7f800000u;
+    r.s = __fdiv_rn(__uint_as_float(most), 127.f);
+    if (!(r.s > 0.f)) r.s = 1.f;
+    r.inverse = 1.f / r.s;
+    if (r.bad) r.s = __uint_as_float(0x7fffffffu);
+    return r;
+}
+// v / s, rounded to fp32, rounded to a whole number.  The product with the reciprocal is within 127 x 2^-22 of the quotient, so it
+// decides wherever it is further than that from a half; elsewhere (and where the reciprocal is infinite) the division does.
+__device__ __forceinline__ float whole(float v, const Scale& r) {
+    if (r.bad) return 0.f;
+    const float t = v * r.inverse;
+    float q = rintf(t);
+    if (!(fabsf(t - q) < 0.4999f)) q = rintf(__fdiv_rn(v, r.s));
+    return fminf(fmaxf(q, -127.f), 127.f);
+}
+
+template <typename T>
+__device__ __forceinline__ float value(T v);
+template <>
+__device__ __forceinline__ float value<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float value<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float value<__half>(__half v) { return __half2float(v); }
+
+// Values c .. c + 7 of a row of K, zeros behind its end.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t K, float (&v)[8]) {
+    if (WIDE && c + 8 <= K) {
+        constexpr int kLoads = sizeof(T) * 8 / 16 ? (int)(sizeof(T) * 8 / 16) : 1;
+        uint4 u[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
+        const T* t = reinterpret_cast<const T*>(u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = value<T>(t[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < K ? value<T>(row[c + i]) : 0.f;
+    }
+}
+
+// The largest of a row's magnitudes over the `warps` warps that share it (all of them call this).
+__device__ __forceinline__ uint32_t most_of(uint32_t m, int warps, uint32_t* part) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (warps == 1) return m;
+    const int warp = threadIdx.x >> 5, first = warp / warps * warps;
+    if ((threadIdx.x & 31) == 0) part[warp] = m;
+    __syncthreads();
+    for (int i = 0; i < warps; ++i) m = max(m, part[first + i]);
+    return m;
+}
+
+// The expert whose rows hold row r < offsets[E]: the last e with offsets[e] <= r.
+__device__ __forceinline__ int expert_of(const int32_t* __restrict__ offsets, int E, int r) {
+    int lo = 0, hi = E;  // offsets[lo] <= r < offsets[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (__ldg(offsets + mid) <= r) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// `warps` warps of a CTA share a row; it is read once into registers (its first kKept pieces per thread; what is longer is read
+// again), quantised, and written to the rows that it goes to.  Bound by the writing of k rows in 16 bits.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(kThreads) int8_rows_kernel(const Int8RowsArgs a, const int warps) {
+    __shared__ uint32_t part[kThreads / 32];
+    __shared__ int64_t to_smem[kThreads / 32][kMaxK];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = kThreads / 32 / warps, mine = warp / warps;
+    const int64_t t = (int64_t)blockIdx.x * rows + mine;
+    const int first = threadIdx.x - mine * warps * 32, step = warps * 32;
+    const int k = a.inv ? a.k : 1;
+    bool live = t < a.T;
+    if (warp % warps == 0 && lane < k) {  // where the row goes
+        int64_t to = -1;
+        if (live) {
+            const int64_t r = a.inv ? (int64_t)__ldg(a.inv + t * k + lane) : t;
+            if (!a.offsets) {
+                to = r;
+            } else if (r >= 0 && r < __ldg(a.offsets + a.E)) {
+                const int e = expert_of(a.offsets, a.E, (int)r);
+                const int o = __ldg(a.offsets + e);
+                to = int8_first_row(o, e) + r - o;
+            }
+            if (to >= a.room) to = -1;
+        }
+        to_smem[mine][lane] = to;
+    }
+    if (warps == 1) __syncwarp();
+    else __syncthreads();
+    bool wanted = false;
+    for (int j = 0; j < k; ++j) wanted |= to_smem[mine][j] >= 0;
+    live = live && wanted;
+    const T* x = static_cast<const T*>(a.x) + t * a.ld;
+    const int64_t Kp = (a.K + 63) / 64 * 64;
+    const int pieces = (int)(Kp / 8);
+    float kept[kKept][8];
+    uint32_t most = 0;
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < kKept; ++i) {
+            const int c = first + i * step;
+            if (c < pieces) load8<T, WIDE>(x, 8 * (int64_t)c, a.K, kept[i]);
+            else
+#pragma unroll
+                for (int u = 0; u < 8; ++u) kept[i][u] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kKept; ++i)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) most = max(most, magnitude(kept[i][u]));
+        for (int c = first + kKept * step; c < pieces; c += step) {
+            float v[8];
+            load8<T, WIDE>(x, 8 * (int64_t)c, a.K, v);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) most = max(most, magnitude(v[u]));
+        }
+    }
+    const Scale s = scale_of(most_of(most, warps, part));
+    if (!live) return;
+    if (first < k && to_smem[mine][first] >= 0) a.s[to_smem[mine][first]] = s.s;
+    auto put = [&](int c, const float (&v)[8]) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(whole(v[2 * i], s), whole(v[2 * i + 1], s));
+            o[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        for (int j = 0; j < k; ++j) {
+            const int64_t to = to_smem[mine][j];
+            if (to >= 0)
+                *reinterpret_cast<uint4*>(a.q + ((int64_t)(c / 8) * a.room + to) * 64 + ((c % 8) ^ (int)(to % 8)) * 8) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+        if (first + i * step < pieces) put(first + i * step, kept[i]);
+    for (int c = first + kKept * step; c < pieces; c += step) {
+        float v[8];
+        load8<T, WIDE>(x, 8 * (int64_t)c, a.K, v);
+        put(c, v);
+    }
+}
+
+// One CTA per row of weights.  INT8: the numbers as they are given.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) int8_pack_kernel(const Int8PackArgs a) {
+    constexpr bool kWhole = sizeof(T) == 1;
+    __shared__ uint32_t part[kThreads / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t row = blockIdx.x;  // of E * rows
+    const int64_t e = row / a.rows, n = a.first + a.step * (row - e * a.rows);
+    const T* w = static_cast<const T*>(a.w) + row * a.ld;
+    const int64_t KT = (a.K + 63) / 64;
+    Scale s = {};
+    if constexpr (!kWhole) {
+        uint32_t most = 0;
+        for (int64_t c = threadIdx.x; c < a.K; c += kThreads) most = max(most, magnitude(value<T>(w[c])));
+        s = scale_of(most_of(most, kThreads / 32, part));
+    }
+    if (threadIdx.x == 0) a.s[e * a.N + n] = kWhole ? a.s_in[row] : s.s;
+    uint8_t* q = a.q + e * int8_tiles(a.N, a.K) * kInt8Tile + (n / 128) * KT * kInt8Tile + (n % 128) * 16;
+    for (int64_t c = threadIdx.x; c < 4 * KT; c += kThreads) {
+        uint32_t o[4] = {};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int64_t at = 16 * c + i;
+            int b = 0;
+            if (at < a.K) {
+                if constexpr (kWhole) b = w[at];
+                else b = (int)whole(value<T>(w[at]), s);
+            }
+            o[i / 4] |= (uint32_t)(b & 255) << (8 * (i % 4));
+        }
+        *reinterpret_cast<uint4*>(q + (c / 4) * kInt8Tile + (c % 4) * 2048) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+template <typename T>
+cudaError_t launch_rows(Int8RowsArgs a, cudaStream_t st) {
+    const int pieces = (int)((a.K + 63) / 64 * 8);
+    int warps = 1;
+    while (warps < kThreads / 32 && warps * 32 * kKept < pieces) warps *= 2;
+    const int64_t rows = kThreads / 32 / warps;
+    const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ld * (int64_t)sizeof(T)) % 16 == 0;
+    const void* f = wide ? (const void*)int8_rows_kernel<T, true> : (const void*)int8_rows_kernel<T, false>;
+    void* args[] = {&a, &warps};
+    return launch_kernel(f, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(kThreads), 0, st, true, args);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_rows(const Int8RowsArgs& a, moe_dtype dtype, cudaStream_t st) {
+    if (a.T == 0) return cudaSuccess;
+    switch (dtype) {
+        case MOE_F32: return launch_rows<float>(a, st);
+        case MOE_BF16: return launch_rows<__nv_bfloat16>(a, st);
+        default: return launch_rows<__half>(a, st);
+    }
+}
+
+cudaError_t launch_int8_pack(const Int8PackArgs& a, int dtype, cudaStream_t st) {
+    if (a.E == 0 || a.rows == 0) return cudaSuccess;
+    const void* f = dtype < 0             ? (const void*)int8_pack_kernel<int8_t>
+                    : dtype == MOE_F32    ? (const void*)int8_pack_kernel<float>
+                    : dtype == MOE_BF16   ? (const void*)int8_pack_kernel<__nv_bfloat16>
+                                          : (const void*)int8_pack_kernel<__half>;
+    void* args[] = {const_cast<Int8PackArgs*>(&a)};
+    return launch_kernel(f, dim3((unsigned)(a.E * a.rows)), dim3(kThreads), 0, st, true, args);
+}
+
+}  // namespace moe

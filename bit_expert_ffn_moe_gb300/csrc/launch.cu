@@ -52,4 +52,28 @@ cudaError_t launch_kernel(const void* func, dim3 grid, dim3 block, size_t smem, 
     return cudaLaunchKernelExC(&cfg, func, args);
 }
 
+cudaError_t launch_cluster(const void* f, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st, void** args) {
+    cudaError_t e = ensure_dyn_smem(f, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelExC(&cfg, f, args);
+}
+
 }  // namespace moe

@@ -320,6 +320,213 @@ PyObject* nvfp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// ------------------------------------------------------------------ rows between tokens and experts
+PyObject* none() { return Py_INCREF(Py_None), Py_None; }
+
+// expert_order(ids, E) -> offsets, inv
+PyObject* expert_order(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 2, [&]() -> PyObject* {
+        const at::Tensor& ids = tensor(a[0], "ids");
+        const int64_t E = integer(a[1]);
+        if (ids.dim() != 2 || !ids.is_cuda() || ids.scalar_type() != at::kInt || !ids.is_contiguous())
+            refuse(PyExc_ValueError, "ids", "contiguous int32 [T, k] on CUDA expected");
+        here(ids, "ids");
+        if (E < 1 || E > 1024) refuse(PyExc_ValueError, "E", "1 .. 1024 expected");
+        const int64_t T = ids.size(0), k = ids.size(1);
+        at::Tensor offsets = at::detail::empty_cuda({E + 1}, at::kInt, ids.device(), std::nullopt), inv = fresh(T, k, at::kInt, ids);
+        check(moe_expert_order(static_cast<const int32_t*>(ids.data_ptr()), narrow(T, "T"), narrow(k, "k"), (int)E,
+                               static_cast<int32_t*>(offsets.data_ptr()), static_cast<int32_t*>(inv.data_ptr()), stream()),
+              "moe_expert_order");
+        return pair(wrap(offsets), wrap(inv));
+    });
+}
+
+// A matrix [rows, d] of like's type on its device, with its row stride.
+const at::Tensor& expert_matrix(PyObject* o, int64_t rows, int64_t d, const at::Tensor& like, const char* what, int64_t* ld) {
+    const at::Tensor& t = tensor(o, what);
+    if (t.dim() != 2 || t.size(0) != rows || t.size(1) != d || t.scalar_type() != like.scalar_type() || t.device() != like.device())
+        refuse(PyExc_ValueError, what, "a matrix of the expected shape, type and device expected");
+    *ld = matrix(t, what);
+    return t;
+}
+struct Slots {
+    const int32_t* inv;
+    const float* w;
+    int64_t T, k;
+};
+Slots slots(PyObject* inv, PyObject* w, const at::Tensor& like) {
+    const at::Tensor& t = tensor(inv, "order");
+    if (t.dim() != 2) refuse(PyExc_ValueError, "order", "[T, k] expected");
+    const int64_t T = t.size(0), k = t.size(1);
+    return {static_cast<const int32_t*>(plain(inv, at::kInt, T, k, like, "order").data_ptr()), data<float>(w, at::kFloat, T, k, like, "w"), T,
+            k};
+}
+
+// move_rows(spread, x, inv, w, out): tokens to experts, or experts to tokens
+PyObject* move_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&]() -> PyObject* {
+        const bool spread = truth(a[0]);
+        const char* what = spread ? "x" : "rows";
+        const at::Tensor& x = tensor(a[1], what);
+        int64_t ld = matrix(x, what), ldo = 0;
+        const moe_dtype dt = dtype_of(x, what);
+        const Slots s = slots(a[2], a[3], x);
+        const int64_t d = x.size(1), from = spread ? s.T : s.T * s.k, to = spread ? s.T * s.k : s.T;
+        if (x.size(0) != from) refuse(PyExc_ValueError, what, "another number of rows than the order's expected");
+        at::Tensor out = given(a[4]) ? expert_matrix(a[4], to, d, x, "out", &ldo) : fresh(to, d, x.scalar_type(), x);
+        if (!given(a[4])) ldo = d;
+        const int T = narrow(s.T, "T"), k = narrow(s.k, "k"), w = narrow(d, "d");
+        if (spread)
+            check(moe_tokens_to_experts(x.data_ptr(), dt, ld, s.inv, s.w, T, k, w, out.data_ptr(), ldo, stream()), "moe_tokens_to_experts");
+        else
+            check(moe_experts_to_tokens(x.data_ptr(), dt, ld, s.inv, s.w, T, k, w, out.data_ptr(), ldo, stream()), "moe_experts_to_tokens");
+        return wrap(out);
+    });
+}
+
+// move_backward(spread, g, inv, other, w, need): the gradients of experts to tokens (spread: g = dy, other = rows) or of tokens to experts
+// (g = drows, other = x) -> the gradient of other or None, dw or None (without weights or without `other`)
+PyObject* move_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 6, [&]() -> PyObject* {
+        const bool spread = truth(a[0]), need = truth(a[5]);
+        const char* what = spread ? "dy" : "drows";
+        const at::Tensor& g = tensor(a[1], what);
+        const int64_t ld = matrix(g, what), d = g.size(1);
+        int64_t ldo = 0;
+        const moe_dtype dt = dtype_of(g, what);
+        const Slots s = slots(a[2], a[4], g);
+        const int64_t from = spread ? s.T : s.T * s.k, to = spread ? s.T * s.k : s.T;
+        if (g.size(0) != from) refuse(PyExc_ValueError, what, "another number of rows than the order's expected");
+        const bool weights = s.w && given(a[3]);
+        const void* other = given(a[3]) ? expert_matrix(a[3], to, d, g, spread ? "rows" : "x", &ldo).data_ptr() : nullptr;
+        at::Tensor out, dw;
+        if (need) out = fresh(to, d, g.scalar_type(), g);
+        if (weights) dw = fresh(s.T, s.k, at::kFloat, g);
+        const int T = narrow(s.T, "T"), k = narrow(s.k, "k"), w = narrow(d, "d");
+        void* po = need ? out.data_ptr() : nullptr;
+        float* pw = weights ? static_cast<float*>(dw.data_ptr()) : nullptr;
+        if (spread && (need || weights))
+            check(moe_experts_to_tokens_backward(g.data_ptr(), dt, ld, other, ldo, s.inv, s.w, T, k, w, po, d, pw, stream()),
+                  "moe_experts_to_tokens_backward");
+        else if (need || weights)
+            check(moe_tokens_to_experts_backward(g.data_ptr(), dt, ld, other, ldo, s.inv, s.w, T, k, w, po, d, pw, stream()),
+                  "moe_tokens_to_experts_backward");
+        PyObject* first = need ? wrap(out) : none();
+        return pair(first, weights ? wrap(dw) : none());
+    });
+}
+
+// ------------------------------------------------------------------ products in 8-bit integers
+// Weights as ops.py passes them: their structure, E, N, K and device index.
+struct Weights8 {
+    const moe_int8_weights* p;
+    int64_t E, N, K;
+};
+Weights8 weights8(PyObject* const* a, const at::Tensor& like, const char* what) {
+    const Weights8 w = {structure<moe_int8_weights>(a[0], what), integer(a[1]), integer(a[2]), integer(a[3])};
+    if (integer(a[4]) != like.get_device()) refuse(PyExc_ValueError, what, "on another device than the tensors");
+    return w;
+}
+int64_t columns8(const Weights8& W, bool gated) {
+    if (gated && W.N % 2 != 0) refuse(PyExc_ValueError, "W", "gated: an even number of rows expected");
+    return gated ? W.N / 2 : W.N;
+}
+
+// int8_room(M, E, K, device index) -> q, s, their addresses, room
+PyObject* int8_room(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 4, [&]() -> PyObject* {
+        const int64_t M = integer(a[0]), K = integer(a[2]);
+        const int64_t room = moe_int8_rows_room(M, narrow(integer(a[1]), "E"));
+        const int64_t bytes = (int64_t)moe_int8_rows_bytes(room, K);
+        if (K < 1 || (bytes == 0 && M != 0)) refuse(PyExc_ValueError, "x", "unsupported shape");
+        const at::Device on(at::kCUDA, (c10::DeviceIndex)narrow(integer(a[3]), "device"));
+        const at::Tensor q = at::detail::empty_cuda({bytes / 2}, at::kHalf, on, std::nullopt);
+        const at::Tensor s = at::detail::empty_cuda({room}, at::kFloat, on, std::nullopt);
+        return Py_BuildValue("NNKKL", wrap(q), wrap(s), (unsigned long long)reinterpret_cast<uintptr_t>(q.data_ptr()),
+                             (unsigned long long)reinterpret_cast<uintptr_t>(s.data_ptr()), (long long)room);
+    });
+}
+
+// int8_quantize(x, inv, offsets, E, rows)
+PyObject* int8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 5, [&]() -> PyObject* {
+        const at::Tensor& x = tensor(a[0], "x");
+        const int64_t ld = matrix(x, "x"), T = x.size(0);
+        const moe_dtype dt = dtype_of(x, "x");
+        const int64_t E = integer(a[3]);
+        const Slots s = given(a[1]) ? slots(a[1], nullptr, x) : Slots{nullptr, nullptr, T, 1};
+        if (s.T != T) refuse(PyExc_ValueError, "x", "another number of rows than the order's expected");
+        const int32_t* offsets = data<int32_t>(a[2], at::kInt, E + 1, -1, x, "order");
+        check(moe_int8_quantize(x.data_ptr(), dt, T, x.size(1), ld, s.inv, narrow(s.k, "k"), offsets, narrow(E, "E"),
+                                structure<moe_int8_rows>(a[4], "rows"), stream()),
+              "moe_int8_quantize");
+        Py_RETURN_NONE;
+    });
+}
+
+// int8_matmul(rows, s (its tensor), M, K, offsets, E, W (5), type, workspace, gated, out) -> y
+PyObject* int8_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&]() -> PyObject* {
+        const at::Tensor& like = tensor(a[1], "rows");
+        here(like, "rows");
+        const int64_t M = integer(a[2]), K = integer(a[3]), E = integer(a[5]);
+        const int32_t* offsets = data<int32_t>(a[4], at::kInt, E + 1, -1, like, "order");
+        const Weights8 W = weights8(a + 6, like, "W");
+        if (W.K != K || W.E != (E > 0 ? E : 1)) refuse(PyExc_ValueError, "W", "weights of the rows' width and number of experts expected");
+        const at::ScalarType type = static_cast<at::ScalarType>(integer(a[11]));
+        const Space ws = space(a[12], like);
+        const bool gated = truth(a[13]);
+        at::Tensor y = output(a[14], M, columns8(W, gated), type, like);
+        if (y.scalar_type() != type) refuse(PyExc_ValueError, "out", "another type expected");
+        check(moe_int8_matmul(structure<moe_int8_rows>(a[0], "rows"), offsets, narrow(E, "E"), M, W.p, W.N, K, gated, y.data_ptr(),
+                              dtype_of(y, "out"), matrix(y, "out"), ws.p, ws.bytes, stream()),
+              "moe_int8_matmul");
+        return wrap(y);
+    });
+}
+
+// int8_linear(x, W (5), workspace, gated, out) -> y
+PyObject* int8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject* {
+        const at::Tensor& x = tensor(a[0], "x");
+        const int64_t ld = matrix(x, "x"), M = x.size(0), K = x.size(1);
+        const moe_dtype dt = dtype_of(x, "x");
+        const Weights8 W = weights8(a + 1, x, "W");
+        if (W.K != K || W.E != 1) refuse(PyExc_ValueError, "W", "one matrix of x's width expected");
+        const Space ws = space(a[6], x);
+        const bool gated = truth(a[7]);
+        at::Tensor y = output(a[8], M, columns8(W, gated), x.scalar_type(), x);
+        check(moe_int8_linear(x.data_ptr(), dt, M, K, ld, W.p, W.N, gated, y.data_ptr(), dtype_of(y, "out"), matrix(y, "out"), ws.p, ws.bytes,
+                              stream()),
+              "moe_int8_linear");
+        return wrap(y);
+    });
+}
+
+// int8_experts(x, ids, w, up (5), down (5), workspace, out) -> y
+PyObject* int8_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&]() -> PyObject* {
+        const at::Tensor& x = tensor(a[0], "x");
+        const int64_t ld = matrix(x, "x"), T = x.size(0), d = x.size(1);
+        const moe_dtype dt = dtype_of(x, "x");
+        const at::Tensor& ids = tensor(a[1], "ids");
+        if (ids.dim() != 2) refuse(PyExc_ValueError, "ids", "[T, k] expected");
+        const int64_t k = ids.size(1);
+        const int32_t* pi = static_cast<const int32_t*>(plain(a[1], at::kInt, T, k, x, "ids").data_ptr());
+        const float* pw = static_cast<const float*>(plain(a[2], at::kFloat, T, k, x, "w").data_ptr());
+        const Weights8 up = weights8(a + 3, x, "up"), down = weights8(a + 8, x, "down");
+        if (up.K != d || down.N != d || up.N % 2 != 0 || down.K != up.N / 2 || up.E != down.E)
+            refuse(PyExc_ValueError, "up, down", "matrices [2 I, d] and [d, I] of as many experts expected");
+        const Space ws = space(a[13], x);
+        int64_t ldy = d;
+        at::Tensor y = given(a[14]) ? expert_matrix(a[14], T, d, x, "out", &ldy) : fresh(T, d, x.scalar_type(), x);
+        check(moe_int8_experts(x.data_ptr(), dt, ld, pi, pw, narrow(T, "T"), narrow(d, "d"), narrow(up.E, "E"), narrow(k, "k"),
+                               narrow(down.K, "I"), up.p, down.p, y.data_ptr(), ldy, ws.p, ws.bytes, stream()),
+              "moe_int8_experts");
+        return wrap(y);
+    });
+}
+
 PyObject* set_error(PyObject*, PyObject* kind) {
     Py_XDECREF(g_error);
     Py_INCREF(kind);
@@ -329,7 +536,8 @@ PyObject* set_error(PyObject*, PyObject* kind) {
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(route_scores), FAST(route_scores_backward), FAST(combine_backward), FAST(nvfp4_quantize), FAST(nvfp4_room),
-                         FAST(nvfp4_matmul), FAST(nvfp4_linear), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+                         FAST(nvfp4_matmul), FAST(nvfp4_linear), FAST(expert_order), FAST(move_rows), FAST(move_backward),
+                         FAST(int8_room), FAST(int8_quantize), FAST(int8_matmul), FAST(int8_linear), FAST(int8_experts), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "moe_torch_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,4 +1,4 @@
-"""Routing rules, their gradients and dense NVFP4 products on torch tensors.
+"""Routing rules, their gradients, dense NVFP4 products, rows between tokens and experts and products in 8-bit integers on torch tensors.
 
 Each function checks its tensors, allocates its results and makes one call of the library, in an extension module; the work is
 the library's kernels, on torch's current stream.  None of them synchronises.  Tensors of another device than the current one are
@@ -191,4 +191,191 @@ def nvfp4_linear(x: torch.Tensor, W: Nvfp4Operand, workspace: torch.Tensor, out:
     y = (_module or _calls()).nvfp4_linear(x, W.struct, W.rows, W.K, W.device, workspace, out)
     if x.requires_grad and out is None:
         y = tied("nvfp4_linear's gradients are nvfp4_matmul of transposed operands", y, x)
+    return y
+
+
+# ------------------------------------------------------------------ rows between tokens and experts
+
+class ExpertOrder:
+    """Pairs (token, slot) in the order of (expert, token, slot): offsets int32 [E + 1], inv int32 [T, k] the row of a pair in that
+    order, -1 without an expert."""
+    __slots__ = ("T", "k", "E", "offsets", "inv")
+
+    def __init__(self, E: int, offsets: torch.Tensor, inv: torch.Tensor):
+        self.E, self.offsets, self.inv = E, offsets, inv
+        self.T, self.k = inv.shape
+
+
+def expert_order(ids: torch.Tensor, E: int) -> ExpertOrder:
+    """The order by expert of ids int32 [T, k]; an id outside [0, E) has no expert and its pair no row."""
+    return ExpertOrder(E, *(_module or _calls()).expert_order(ids, E))
+
+
+def _asks(*tensors: Optional[torch.Tensor]) -> bool:
+    return any(t is not None and t.requires_grad for t in tensors)
+
+
+def tokens_to_experts(x: torch.Tensor, order: ExpertOrder, w: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rows [T k, d] of x [T, d] (bf16, fp16, fp32) in expert order, times w fp32 [T, k] when given.  Rows behind the last pair with an
+    expert are not written."""
+    rows = (_module or _calls()).move_rows(True, x, order.inv, w, out)
+    if out is None and _asks(x, w):
+        rows = tied("tokens_to_experts' gradients are tokens_to_experts_backward", rows, x, w)
+    return rows
+
+
+def tokens_to_experts_backward(drows: torch.Tensor, order: ExpertOrder, x: Optional[torch.Tensor] = None,
+                               w: Optional[torch.Tensor] = None, need_dx: bool = True
+                               ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of tokens_to_experts: dx [T, d] and, where x and w are given, dw fp32 [T, k] (else None)."""
+    return (_module or _calls()).move_backward(False, drows, order.inv, x, w, need_dx)
+
+
+def experts_to_tokens(rows: torch.Tensor, order: ExpertOrder, w: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [T, d]: the sum over a token's slots of its rows [T k, d] (bf16, fp16, fp32), times w fp32 [T, k] when given."""
+    y = (_module or _calls()).move_rows(False, rows, order.inv, w, out)
+    if out is None and _asks(rows, w):
+        y = tied("experts_to_tokens' gradients are experts_to_tokens_backward", y, rows, w)
+    return y
+
+
+def experts_to_tokens_backward(dy: torch.Tensor, order: ExpertOrder, rows: Optional[torch.Tensor] = None,
+                               w: Optional[torch.Tensor] = None, need_drows: bool = True
+                               ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of experts_to_tokens: drows [T k, d] (rows behind the last pair with an expert are not written) and, where rows and w are
+    given, dw fp32 [T, k] (else None)."""
+    return (_module or _calls()).move_backward(True, dy, order.inv, rows, w, need_drows)
+
+
+# ------------------------------------------------------------------ products in 8-bit integers
+
+_DTYPES = {torch.float32: B.MOE_F32, torch.bfloat16: B.MOE_BF16, torch.float16: B.MOE_F16}
+
+
+class Int8Weights:
+    """One matrix [N, K] of 8-bit whole numbers, or those of E experts, as the products read them: tiles q (int8 or uint8,
+    binding.moe_int8_weights_bytes a matrix) and fp32 scales s, one for each row.  int8_weights makes them of matrices."""
+
+    def __init__(self, N: int, K: int, q: torch.Tensor, s: torch.Tensor):
+        n = B.moe_int8_weights_bytes(N, K)
+        _need(n > 0, "unsupported shape [%d, %d]" % (N, K))
+        _need(q.is_cuda and q.dtype in (torch.int8, torch.uint8) and q.is_contiguous() and q.numel() > 0 and q.numel() % n == 0,
+              "q: contiguous CUDA bytes, a multiple of %d, expected" % n)
+        self.E = q.numel() // n
+        _need(s.dtype == torch.float32 and s.device == q.device and s.is_contiguous() and s.numel() == self.E * N,
+              "s: contiguous fp32 [%d, %d] expected" % (self.E, N))
+        self.N, self.K, self.q, self.s = N, K, q, s
+        self.struct = B.moe_int8_weights(q.data_ptr(), s.data_ptr())
+        self.args = (self.struct, self.E, N, K, q.get_device())  # as the extension module takes them
+
+    def values(self) -> torch.Tensor:
+        """The numbers they stand for, fp32 [E, N, K]."""
+        KT, NT = -(-self.K // 64), -(-self.N // 128)
+        t = self.q.view(torch.int8).view(self.E, NT, KT, 4, 128, 16).permute(0, 1, 4, 2, 3, 5)
+        return t.reshape(self.E, NT * 128, KT * 64)[:, :self.N, :self.K].float() * self.s.view(self.E, self.N, 1)
+
+
+def int8_weights(w: torch.Tensor, scales: Optional[torch.Tensor] = None, up: Optional[torch.Tensor] = None,
+                 up_scales: Optional[torch.Tensor] = None) -> Int8Weights:
+    """Weights of w [N, K] or [E, N, K]: int8 with fp32 scales [.., N], or fp32, bf16 or fp16, which are quantised row by row.  With
+    `up` (of w's shape, type) they are those of a gated product: w the gate, 2 N rows in all."""
+    parts = [(w, scales)] if up is None else [(w, scales), (up, up_scales)]
+    _need(w.dim() in (2, 3) and w.is_cuda, "w: a CUDA tensor [N, K] or [E, N, K] expected")
+    _need_current(w.device, "w")
+    E, (N, K) = (1 if w.dim() == 2 else w.shape[0]), w.shape[-2:]
+    bytes_ = B.moe_int8_weights_bytes(N * len(parts), K)
+    _need(bytes_ > 0 and N > 0 and E > 0, "unsupported shape %s" % (tuple(w.shape),))
+    W = Int8Weights(N * len(parts), K, torch.empty(E * bytes_, dtype=torch.uint8, device=w.device),
+                    torch.empty(E * N * len(parts), dtype=torch.float32, device=w.device))
+    for i, (m, s) in enumerate(parts):
+        _need(m.shape == w.shape and m.dtype == w.dtype and m.device == w.device and m.is_contiguous(), "up: contiguous, as w, expected")
+        if m.dtype == torch.int8:
+            _need(s is not None and s.shape == w.shape[:-1] and s.dtype == torch.float32 and s.device == w.device and s.is_contiguous(),
+                  "scales: contiguous fp32 %s expected" % (tuple(w.shape[:-1]),))
+            B.moe_int8_weights_layout(m, s, E, N, K, K, i, len(parts), W.N, W.struct)
+        else:
+            _need(m.dtype in _DTYPES and s is None, "w: int8 with scales, or fp32, bf16 or fp16 without, expected")
+            B.moe_int8_weights_quantize(m, _DTYPES[m.dtype], E, N, K, K, i, len(parts), W.N, W.struct)
+    return W
+
+
+class Int8Rows:
+    """Rows [M, K] of activations in 8 bits, of no expert or in an order's: what int8_quantize makes and int8_matmul takes."""
+
+    def __init__(self, M: int, K: int, order: Optional[ExpertOrder], device: int):
+        self.M, self.K, self.order = M, K, order
+        self.q, self.s, q, s, self.room = (_module or _calls()).int8_room(M, order.E if order else 0, K, device)
+        self.struct = B.moe_int8_rows(q, s, self.room)
+
+    def values(self) -> torch.Tensor:
+        """The numbers they stand for, fp32 [room, K] (rows that no row was put into: anything)."""
+        r = torch.arange(self.room, device=self.q.device)
+        at = torch.arange(8, device=self.q.device)[None, :] ^ (r[:, None] % 8)
+        t = self.q.view(-1, self.room, 8, 8)
+        t = t.gather(2, at[None, :, :, None].expand_as(t))
+        return t.permute(1, 0, 2, 3).reshape(self.room, -1)[:, :self.K].float() * self.s[:, None]
+
+
+def int8_quantize(x: torch.Tensor, order: Optional[ExpertOrder] = None, ordered: bool = False) -> Int8Rows:
+    """Rows of x [M, K] in 8 bits; with an order those of its tokens x [T, K], spread into expert order, or, `ordered`, of x [T k, K] in
+    expert order already."""
+    _need(x.dim() == 2 and x.is_cuda, "x: a CUDA matrix expected")
+    M = x.shape[0] if order is None else order.T * order.k
+    _need(order is None or x.shape[0] == (M if ordered else order.T), "x: another number of rows than the order's expected")
+    rows = Int8Rows(M, x.shape[1], order, x.get_device())
+    inv, offsets, E = (None, None, 0) if order is None else (None if ordered else order.inv, order.offsets, order.E)
+    (_module or _calls()).int8_quantize(x, inv, offsets, E, rows.struct)
+    return rows
+
+
+def int8_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
+    """Workspace of int8_linear and int8_matmul for up to M rows, initialised."""
+    n = B.moe_int8_workspace_size(M, N, K)
+    _need(n > 0, "unsupported shape M=%d N=%d K=%d" % (M, N, K))
+    _need_current(torch.device(device), "workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    B.moe_workspace_init(ws)
+    return ws
+
+
+def int8_matmul(rows: Int8Rows, W: Int8Weights, dtype: torch.dtype, workspace: torch.Tensor, gated: bool = False,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """rows [M, K] times W [N, K] transposed, or each expert's rows times its matrix: [M, N] of dtype, gated [M, N / 2] (rows behind the last
+    pair with an expert are not written)."""
+    code = _SCALAR_TYPES.get(dtype)
+    if code is None:
+        raise TypeError("fp32, bf16 or fp16 expected, got %s" % (dtype,))
+    offsets, E = (None, 0) if rows.order is None else (rows.order.offsets, rows.order.E)
+    return (_module or _calls()).int8_matmul(rows.struct, rows.s, rows.M, rows.K, offsets, E, *W.args, code, workspace, gated, out)
+
+
+def int8_linear(x: torch.Tensor, W: Int8Weights, workspace: torch.Tensor, gated: bool = False,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [M, K] times W [N, K] transposed, x quantised row by row: [M, N] of x's type (or of `out`'s), gated [M, N / 2]."""
+    y = (_module or _calls()).int8_linear(x, *W.args, workspace, gated, out)
+    if out is None and x.requires_grad:
+        y = tied("int8_linear's input gradient is int8_linear of the transposed weights", y, x)
+    return y
+
+
+def int8_experts_workspace(T: int, k: int, d: int, I: int, E: int, dtype: torch.dtype = torch.bfloat16,  # noqa: E741
+                           device="cuda") -> torch.Tensor:
+    """Workspace of int8_experts for up to T tokens of k slots, initialised."""
+    n = B.moe_int8_experts_workspace_size(T, d, E, k, I, _DTYPES[dtype])
+    _need(n > 0, "unsupported shape T=%d k=%d d=%d I=%d E=%d" % (T, k, d, I, E))
+    _need_current(torch.device(device), "workspace")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    B.moe_workspace_init(ws)
+    return ws
+
+
+def int8_experts(x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, up: Int8Weights, down: Int8Weights, workspace: torch.Tensor,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A sparse layer behind its router: y [T, d] of x [T, d], ids int32 [T, k] and w fp32 [T, k]; `up` the gated weights [E, 2 I, d],
+    `down` [E, d, I].  The same as int8_quantize, int8_matmul (gated, in x's type), int8_quantize, int8_matmul and experts_to_tokens."""
+    y = (_module or _calls()).int8_experts(x, ids, w, *up.args, *down.args, workspace, out)
+    if out is None and _asks(x, w):
+        y = tied("int8_experts computes no gradients; the weights' is experts_to_tokens_backward", y, x, w)
     return y

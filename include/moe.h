@@ -536,6 +536,106 @@ moe_status moe_nvfp4_linear(const void* x, moe_dtype x_dtype, int64_t M, int64_t
                             int64_t N, void* y, moe_dtype y_dtype, int64_t ldy, void* ws, size_t ws_bytes,
                             moe_stream_t stream);
 
+/* ---------------------------------------------------------------- rows between tokens and experts
+ * What surrounds experts that work on rows of numbers (bf16, fp16, fp32): their rows in expert order, and back, with the routing
+ * weights on either way, and the gradients of both.  (moe_permute orders the pairs for the layer's own 4-bit experts and quantises
+ * their rows.)  Row strides (ld.) count elements and are at least d; T*k <= 2^30, T*k*d <= 2^38, 1 <= k <= 32.  Results may not overlap
+ * what is read. */
+
+/* The pairs (t, j) of ids int32 [T][k] in the order of (ids[t][j], t, j):
+ *   offsets int32 [E+1]   pairs of the experts before e; offsets[E]: all pairs with an expert
+ *   inv int32 [T*k]       the row of pair (t, j) in that order, at t*k + j; -1 where ids[t][j] is outside [0, E)
+ * An expert may be named several times by a token.  E <= 1024. */
+moe_status moe_expert_order(const int32_t* ids, int T, int k, int E, int32_t* offsets, int32_t* inv, moe_stream_t stream);
+
+/* rows[inv[t*k+j]] = w[t][j] * x[t]; w fp32 [T][k], or NULL: ones (a copy).  x [T][ldx], rows [T*k][ldr], both of dtype; a
+ * product in fp32, rounded once.  An entry of inv outside [0, T*k) is passed over, and rows that no entry names are left as they are;
+ * no row is named twice. */
+moe_status moe_tokens_to_experts(const void* x, moe_dtype dtype, int64_t ldx, const int32_t* inv, const float* w, int T, int k, int d,
+                                 void* rows, int64_t ldr, moe_stream_t stream);
+
+/* Its gradients: dx[t] = sum_j w[t][j] * drows[inv[t*k+j]] (fp32 sum in slot order, rounded once) and dw[t][j] = <x[t],
+ * drows[inv[t*k+j]]> (fp32; 0 where the entry is outside [0, T*k)).  dx or dw may be NULL (x is needed for dw only). */
+moe_status moe_tokens_to_experts_backward(const void* drows, moe_dtype dtype, int64_t ldr, const void* x, int64_t ldx,
+                                          const int32_t* inv, const float* w, int T, int k, int d, void* dx, int64_t ldd, float* dw,
+                                          moe_stream_t stream);
+
+/* y[t] = sum_j w[t][j] * rows[inv[t*k+j]]: fp32 sum in slot order, rounded once (moe_combine in every type, width and stride).  A token
+ * without rows gets zeros. */
+moe_status moe_experts_to_tokens(const void* rows, moe_dtype dtype, int64_t ldr, const int32_t* inv, const float* w, int T, int k,
+                                 int d, void* y, int64_t ldy, moe_stream_t stream);
+
+/* Its gradients: drows[inv[t*k+j]] = w[t][j] * dy[t] and dw[t][j] = <dy[t], rows[inv[t*k+j]]>.  drows or dw may be NULL (rows is
+ * needed for dw only). */
+moe_status moe_experts_to_tokens_backward(const void* dy, moe_dtype dtype, int64_t ldy, const void* rows, int64_t ldr,
+                                          const int32_t* inv, const float* w, int T, int k, int d, void* drows, int64_t ldg, float* dw,
+                                          moe_stream_t stream);
+
+/* ---------------------------------------------------------------- products in 8-bit integers
+ * y = x W^T with 8-bit whole numbers on both sides, a scale for each row of x (token) and of W (channel): dense projections and
+ * shared experts, and sparse layers whose experts come in this format.
+ *   A row v is held as s = max |v| / 127 (1 for a row of zeros) and whole numbers q = v / s rounded to the nearest, ties to even,
+ * within -127 .. 127, each step rounded to fp32; a row of x with a NaN or an infinity gives a row of NaN.
+ *   y[m][n] = (sum_k qx[m][k] qw[n][k]) * sx[m] * sw[n]: the sum is exact up to 2^24 (always for K <= 1040) and rounded to fp32
+ * beyond, the two products are in fp32, the result is rounded once to y's type.
+ *   gated: rows 2 i and 2 i + 1 of W are the gate and the up row of channel i, and y [M][N/2] is silu(gate) * up (N even).
+ * 1 <= K <= 131072. */
+
+/* One matrix [N][K], or those of E experts, one behind the other: tiles of 128 rows x 64 values (rows and K padded), tile (R, C) of a
+ * matrix at index R*ceil(K/64) + C, value (r, c) of a tile at byte (c/16)*2048 + r*16 + c%16. */
+typedef struct moe_int8_weights {
+    const uint8_t* q; /* E * moe_int8_weights_bytes(N, K) bytes, 16-byte aligned */
+    const float* s;   /* [E][N] */
+} moe_int8_weights;
+
+size_t moe_int8_weights_bytes(int64_t N, int64_t K); /* of one matrix; 0 for an unsupported shape */
+
+/* Lays rows of w int8 [E][rows][ld] with their scales s_in [E][rows] out into W: row i of a matrix becomes its row first + step * i
+ * (0 and 1 for a whole matrix; 0 and 2, 1 and 2 for the gate and the up rows of a gated one), first + step * (rows - 1) < N. */
+moe_status moe_int8_weights_layout(const int8_t* w, const float* s_in, int E, int64_t rows, int64_t K, int64_t ld, int64_t first,
+                                   int64_t step, int64_t N, const moe_int8_weights* W, moe_stream_t stream);
+/* The same from rows of dtype, which it quantises. */
+moe_status moe_int8_weights_quantize(const void* w, moe_dtype dtype, int E, int64_t rows, int64_t K, int64_t ld, int64_t first,
+                                     int64_t step, int64_t N, const moe_int8_weights* W, moe_stream_t stream);
+
+/* Rows of activations: the whole numbers as fp16, q [ceil(K/64)][room][64] with the 16-byte piece j of row r at place j XOR (r%8) of its
+ * 128 bytes, and s [room].  Without experts row r is row r; else row offsets[e] + i is row 8 * ceil(offsets[e] / 8) + 8 e + i. */
+typedef struct moe_int8_rows {
+    uint16_t* q;  /* moe_int8_rows_bytes(room, K) bytes, 16-byte aligned */
+    float* s;
+    int64_t room; /* moe_int8_rows_room(M, E) */
+} moe_int8_rows;
+
+int64_t moe_int8_rows_room(int64_t M, int E); /* for M rows, of E experts or (0) of none; 0 for an unsupported shape */
+size_t moe_int8_rows_bytes(int64_t room, int64_t K);
+
+/* Rows of x [T][ldx].  offsets and inv NULL (E = 0): as they are.  offsets [E+1] (moe_expert_order's) alone: x is in expert order, rows
+ * from offsets[E] on are passed over.  Both: token t goes to the rows inv[t*k .. t*k+k-1], quantised once. */
+moe_status moe_int8_quantize(const void* x, moe_dtype dtype, int64_t T, int64_t K, int64_t ldx, const int32_t* inv, int k,
+                             const int32_t* offsets, int E, const moe_int8_rows* rows, moe_stream_t stream);
+
+/* Workspace of moe_int8_linear and moe_int8_matmul for up to M rows; initialise it once with moe_workspace_init. */
+size_t moe_int8_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/* y [M][ldy] of rows and W: of all M rows with one matrix (offsets NULL, E = 0), or of rows offsets[e] .. offsets[e+1] - 1 with
+ * matrix e (M: the rows at most; rows of y from offsets[E] on are left as they are). */
+moe_status moe_int8_matmul(const moe_int8_rows* rows, const int32_t* offsets, int E, int64_t M, const moe_int8_weights* W, int64_t N,
+                           int64_t K, int gated, void* y, moe_dtype dtype, int64_t ldy, void* ws, size_t ws_bytes,
+                           moe_stream_t stream);
+
+/* y [M][ldy] of x [M][ldx] and one matrix: its rows quantised into the workspace, then the product. */
+moe_status moe_int8_linear(const void* x, moe_dtype x_dtype, int64_t M, int64_t K, int64_t ldx, const moe_int8_weights* W, int64_t N,
+                           int gated, void* y, moe_dtype y_dtype, int64_t ldy, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* A sparse layer behind its router, on x [T][ldx] of dtype: rows quantised into expert order, h = silu(x Wg^T) * (x Wu^T) rounded to
+ * dtype (up: gated, [2 I][d] a matrix), rows of h quantised, their products with down ([d][I] a matrix) rounded to dtype, and the sum
+ * y[t] = sum_j w[t][j] * output of expert ids[t][j] (fp32 in slot order, rounded once).  A pair whose id is outside [0, E) takes no
+ * part.  ids int32 [T][k], w fp32 [T][k]; E <= 1024.  ws: moe_int8_experts_workspace_size bytes, initialised once. */
+size_t moe_int8_experts_workspace_size(int T, int d, int E, int k, int I, moe_dtype dtype); /* 0 for an unsupported shape */
+moe_status moe_int8_experts(const void* x, moe_dtype dtype, int64_t ldx, const int32_t* ids, const float* w, int T, int d, int E, int k,
+                            int I, const moe_int8_weights* up, const moe_int8_weights* down, void* y, int64_t ldy, void* ws,
+                            size_t ws_bytes, moe_stream_t stream);
+
 /* ---------------------------------------------------------------- failure-detection self-test
  * Not part of the layer.  Every barrier wait in the library's kernels is bounded: when it runs out
  * the kernel records MOE_ERR_TIMEOUT in the workspace status word and finishes, so a lost copy or

@@ -351,7 +351,7 @@ moe_status moe_experts_to_tokens_backward(const void* dy, moe_dtype dtype, int64
 
 size_t moe_int8_weights_bytes(int64_t N, int64_t K) { return int8_ok(N, K) ? (size_t)int8_tiles(N, K) * kInt8Tile : 0; }
 int64_t moe_int8_rows_room(int64_t M, int E) {
-    return M < 0 || M > kMaxDim || E < 0 || E > kMaxE ? 0 : (M + 7) / 8 * 8 + 8 * (int64_t)E;
+    return M < 0 || M > kMaxDim || E < 0 || E > kMaxE ? 0 : (M + 7) / 8 * 8 + 8 * (int64_t)E + 16;
 }
 size_t moe_int8_rows_bytes(int64_t room, int64_t K) { return int8_ok(room, K) ? (size_t)room * pad(K, 64) * 2 : 0; }
 
@@ -408,7 +408,7 @@ moe_status moe_int8_matmul(const moe_int8_rows* rows, const int32_t* offsets, in
     MOE_TRY(check_workspace(ws, ws_bytes, L.q));
     return launch([&] {
         return launch_int8_product({W->q, W->s, rows->q, rows->s, rows->room, offsets, offsets ? E : 1, M, N, K, y, ldy, static_cast<Ctrl*>(ws),
-                                    reinterpret_cast<float*>(static_cast<char*>(ws) + L.partials)},
+                                    reinterpret_cast<float*>(static_cast<char*>(ws) + L.partials), 0},
                                    dtype, gated != 0, (cudaStream_t)stream);
     });
 }
@@ -433,7 +433,7 @@ moe_status moe_int8_linear(const void* x, moe_dtype x_dtype, int64_t M, int64_t 
         const cudaError_t e = launch_int8_rows({x, ldx, M, K, nullptr, 1, nullptr, 0, room, q, s}, x_dtype, st);
         if (e != cudaSuccess) return e;
         return launch_int8_product({W->q, W->s, q, s, room, nullptr, 1, M, N, K, y, ldy, static_cast<Ctrl*>(ws),
-                                    reinterpret_cast<float*>(base + L.partials)},
+                                    reinterpret_cast<float*>(base + L.partials), 1},
                                    y_dtype, gated != 0, st);
     });
 }
@@ -467,11 +467,11 @@ moe_status moe_int8_experts(const void* x, moe_dtype dtype, int64_t ldx, const i
         cudaError_t e = launch_expert_order(ids, (int)P, E, offsets, inv, st);
         if (e == cudaSuccess) e = launch_int8_rows({x, ldx, T, d, inv, k, offsets, E, L.room, xq, xs}, dtype, st);
         if (e == cudaSuccess)
-            e = launch_int8_product({up->q, up->s, xq, xs, L.room, offsets, E, P, 2 * (int64_t)I, d, base + L.h, I, ctrl, partials}, dtype,
+            e = launch_int8_product({up->q, up->s, xq, xs, L.room, offsets, E, P, 2 * (int64_t)I, d, base + L.h, I, ctrl, partials, 1}, dtype,
                                     true, st);
         if (e == cudaSuccess) e = launch_int8_rows({base + L.h, I, P, I, nullptr, 1, offsets, E, L.room, hq, hs}, dtype, st);
         if (e == cudaSuccess)
-            e = launch_int8_product({down->q, down->s, hq, hs, L.room, offsets, E, P, d, I, base + L.rows, d, ctrl, partials}, dtype, false,
+            e = launch_int8_product({down->q, down->s, hq, hs, L.room, offsets, E, P, d, I, base + L.rows, d, ctrl, partials, 1}, dtype, false,
                                     st);
         if (e == cudaSuccess)
             e = launch_expert_rows(false, dtype, nullptr, 0, base + L.rows, d, y, ldy, inv, w, nullptr, T, k, d, st);

@@ -4,10 +4,11 @@
 // The sum of whole numbers is exact up to 2^24 and rounded to fp32 beyond; the two products with the scales are in fp32, in this
 // order, and the result is rounded once to y's type.
 //
+//   mma     (int8_mma.cu) the tensor cores, on fp16 that holds the whole numbers
 //   dot     few rows: dot products of four bytes (dp4a), the weights read once.  The rows of all active experts' matrices are
 //           dealt out evenly to the CTAs, so that no partial sums have to be exchanged; a warp takes every 16th step of 64 values
 //           of 32 weight rows.
-#include "ops.cuh"
+#include "int8_common.cuh"
 
 namespace moe {
 namespace {
@@ -16,22 +17,6 @@ constexpr int kDotThreads = 512, kDotWarps = kDotThreads / 32;
 constexpr int kDotRows = 32;     // weight rows at a time
 constexpr int kDotTokens = 4;    // activation rows at a time
 constexpr int kDotK = 16384;     // values of them in shared memory at a time
-
-template <typename T>
-__device__ __forceinline__ T out_value(float v);
-template <>
-__device__ __forceinline__ float out_value<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 out_value<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half out_value<__half>(float v) { return __float2half_rn(v); }
-
-// silu(gate) up.  For a negative gate exp(gate) as a square, one factor on either side, so that neither it nor exp(-gate) leaves fp32's
-// range before the result does.
-__device__ __forceinline__ float gated_value(float gate, float up) {
-    const float e = expf(gate < 0.f ? 0.5f * gate : -gate);
-    return gate < 0.f ? (gate * e) * (up * e) / (1.f + e * e) : gate / (1.f + e) * up;
-}
 
 // Four fp16 whole numbers as four bytes.
 __device__ __forceinline__ uint32_t bytes_of(uint2 h) {
@@ -154,8 +139,8 @@ __global__ void __launch_bounds__(kDotThreads, 1) int8_dot_kernel(const Int8Prod
                     const float* sw = a.sw + (int64_t)e * a.N + n + r;
                     const float v = (float)s0 * sx * sw[0];
                     T* y = static_cast<T*>(a.y) + (first + t0 + t) * a.ldy;
-                    if (GATED) y[(n + r) / 2] = out_value<T>(gated_value(v, (float)s1 * sx * sw[1]));
-                    else y[n + r] = out_value<T>(v);
+                    if (GATED) y[(n + r) / 2] = int8_result<T>(int8_gated(v, (float)s1 * sx * sw[1]));
+                    else y[n + r] = int8_result<T>(v);
                 }
                 __syncthreads();
             }
@@ -172,11 +157,18 @@ const void* dot_kernel(moe_dtype dtype) {
 
 }  // namespace
 
-cudaError_t launch_int8_product(const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st) {
-    if (a.M == 0 || a.N == 0) return cudaSuccess;
+cudaError_t launch_int8_dot(const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st) {
     void* args[] = {const_cast<Int8ProductArgs*>(&a)};
     return launch_kernel(gated ? dot_kernel<true>(dtype) : dot_kernel<false>(dtype), dim3(sm_count()), dim3(kDotThreads),
                          kDotTokens * kDotK, st, true, args);
+}
+
+cudaError_t launch_int8_product(const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st) {
+    if (a.M == 0 || a.N == 0) return cudaSuccess;
+    // Us, dot / one CTA a tile / pairs: 1 x 4096 x 8192 9.6 / 17 / 18, 4 x 4096 x 8192 12.5 / 17 / 18, 16: 36 / 17 / 18; 128: 29 / 29, 256: 34 / 31,
+    // 4096: 220 / 161; by expert, 128 of 4096 x 8192, a mean of 0.25 rows: 157 / 153 / 153, 4: 593 / 592, 16: 704 / 647, 64: 1041 / 805.
+    if (a.M <= 4) return launch_int8_dot(a, dtype, gated, st);
+    return launch_int8_mma(a, dtype, gated, a.offsets ? a.M / a.E >= 16 : a.M > 128, st);
 }
 
 }  // namespace moe

@@ -1,0 +1,667 @@
+// int8_mma.cu -- the 8-bit products on the tensor cores.  sm_103a's have no 8-bit whole numbers, but numbers up to 2048 are exact in fp16,
+// their products and sums up to 2^24 exact in the fp32 accumulators: so kind::f16, at the rate of bf16.
+//   The weights are the MMA's M side (128 weight rows a CTA) and come from tensor memory: read as bytes, turned into fp16 in
+// registers by sixteen warps, stored to tensor memory, so that they cost one byte of memory traffic and shared memory sees them
+// once.  The activations are the N side (16 .. 192 rows), fp16 already, copied as they lie.
+//   warps 0-15   conversion: four sets of four warps, each a quarter of the tiles of 64 values
+//   warps 16-19  epilogue: accumulators (two, so that the next tile's products run meanwhile), scales, store
+//   warp 20      copies: three bulk copies a step of 128 values
+//   warp 21      products
+// PAIR: two CTAs share a tile of 256 weight rows (cta_group::2), each with half of the activation rows in its shared memory; the
+// leader (rank 0) issues the products of both.
+// Work: the steps of all tiles of all experts in a row, dealt out evenly by what they cost.  A tile that several CTAs share is
+// summed by the last of them to arrive, from partial sums in memory, in the order of the CTAs.
+// Every barrier wait is bounded: on expiry the CTA records MOE_ERR_TIMEOUT, waits (bounded) for its own copies and products,
+// frees tensor memory and exits.
+#include "int8_common.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kSets = 4, kConvWarps = 4 * kSets, kEpiWarps = 4, kCopyWarp = kConvWarps + kEpiWarps, kMmaWarp = kCopyWarp + 1;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kMostRows = 192;       // activation rows of a tile
+constexpr int kMostStages = 16;
+// A step is two tiles of weights, 128 values (the last one of an odd number of tiles: one).  The converted weights of a tile are a slot in
+// tensor memory; set i of the converting warps fills slot i, with tile i % 2 of every other step.
+constexpr uint32_t kTmemCols = 512, kSlotCols = 32, kSlotBase = 2 * kMostRows;
+static_assert(kSlotBase + kSets * kSlotCols == kTmemCols, "tensor memory");
+constexpr int kLeastSteps = 8;       // steps that a CTA's share of split tiles has at least, and that splitting has to save
+constexpr size_t kSmemMost = 232448;
+
+struct Shared {
+    uint64_t full[kMostStages], ready[kMostStages], empty[kMostStages], acc_full[2], acc_empty[2], epilogue, parts, done;
+    uint32_t tmem;
+    volatile int abort;
+    int last[2];  // whether this CTA is the last to arrive at a shared tile (it has two at most)
+    int split, ctas, whole;  // tiles that CTAs (PAIR: pairs) share, how many of these do, and tiles that one CTA computes
+    alignas(16) float sx[kEpiWarps][kMostRows];
+    int32_t tiles[kMaxE + 1], offset[kMaxE + 1];  // tiles and rows of the experts before
+};
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Arrive on the barrier at this place in CTA 0 of the cluster.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    if constexpr (PAIR) arrive_leader(bar);
+    else mbar_arrive(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .b16 both;\n\t"
+            "mov.b16 both, 3;\n\t"
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n\t}" ::"r"(smem_u32(bar))
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A step's four products of 16 values: A from tensor memory (8 columns each), B 32 bytes further along its rows each.
+template <bool PAIR>
+__device__ __forceinline__ void step_products(uint32_t d, uint32_t a, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
+    constexpr uint32_t kHigh = (1024 >> 4) | (1u << 14) | (2u << 29);  // of desc_sw128
+#define MOE_PRODUCT(group, i, pred)                                                     \
+    "add.u32 c, %1, 8*" #i ";\n\tadd.u32 l, %2, 2*" #i ";\n\tmov.b64 t, {l, %5};\n\t" \
+    "tcgen05.mma.cta_group::" group ".kind::f16 [%0], [c], t, %3, " pred ";\n\t"
+#define MOE_STEP(group)                                                                                                       \
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 c, l;\n\t.reg .b64 t;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %4, %4;\n\t" \
+                 MOE_PRODUCT(group, 0, "p") MOE_PRODUCT(group, 1, "q") MOE_PRODUCT(group, 2, "q") MOE_PRODUCT(group, 3, "q") "}" ::"r"(d), \
+                 "r"(a), "r"(b_low), "r"(idesc), "r"(accumulate), "n"(kHigh)                                                  \
+                 : "memory")
+    if constexpr (PAIR) MOE_STEP("2");
+    else MOE_STEP("1");
+#undef MOE_STEP
+#undef MOE_PRODUCT
+}
+
+// Four whole numbers of eight bits as fp16: with 128 added they are the last eight bits of numbers from 1024 on.
+__device__ __forceinline__ void to_fp16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = w ^ 0x80808080u, bias = 0x64806480u;  // 1024 + 128, twice
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&bias));
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&bias));
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+        "r"(taddr)
+        : "memory");
+}
+
+// An expert's rows as mt tiles of up to n rows (a multiple of 16).
+struct Rows {
+    int64_t count;
+    int mt, n;
+};
+__device__ __forceinline__ Rows rows_of(int64_t count, int most) {
+    Rows r;
+    r.count = count;
+    r.mt = (int)((count + most - 1) / most);
+    r.n = count > 0 ? ((int)((count + r.mt - 1) / r.mt) + 15) / 16 * 16 : 16;
+    return r;
+}
+
+// Steps k .. k1 - 1 of a tile: of expert e, its weight tile nt and activation tile mt.
+struct Part {
+    int id, e, nt, mt, k, k1;  // id: among all tiles (M N is at most 2^40: they fit)
+    bool last;                 // of the CTA
+    Rows r;
+};
+
+// The tiles of all experts in a row, expert by expert, weight tile by weight tile.  CTAs take them in turns, so that at any time
+// neighbours work on the same weights and rows, which then come out of L2 (contiguous shares: each tile's operands from memory, 2.7
+// ms instead of 1.5 for the gate and up products of 4096 tokens).  The last `split` of them, fewer than there are CTAs, are dealt
+// out by their steps, evenly, so that all CTAs end at the same time.  (Shared tiles first, their sums made while the next
+// tile's products run: the sums' loads waited behind the copies for longer than that tile took, 94 us instead of 50 for 1024 x 4096 x 8192.)
+template <bool PAIR>
+struct Work {
+    const Shared& s;
+    const int64_t M;  // rows of a dense product (by expert: -1)
+    const int NT, E, KS, most, G;  // weight tiles (PAIR: of 256 rows), experts, steps of a tile, CTAs
+
+    __device__ __forceinline__ Rows rows(int e) const { return rows_of(M >= 0 ? M : s.offset[e + 1] - s.offset[e], most); }
+    // The first step of CTA c's share of the split tiles.  (32 bits: fewer tiles than CTAs, 1024 steps a tile at most.)
+    __device__ __forceinline__ int share(int c) const { return (int)((unsigned)(s.split * KS) * (unsigned)c / (unsigned)s.ctas); }
+    // The CTAs that share tile `id`: those whose shares have its first step and its last one.  (share(c) <= u where split KS c < (u + 1) ctas.)
+    __device__ __forceinline__ void sharers(int id, int& first, int& last) const {
+        const unsigned all = s.split * KS, b = (id - s.whole) * KS;
+        first = (int)(((b + 1) * (unsigned)s.ctas - 1) / all);
+        last = (int)(((b + KS) * (unsigned)s.ctas - 1) / all);
+    }
+    // f(part) for CTA c's work, until it returns false.
+    template <typename F>
+    __device__ __forceinline__ void each(int c, F f) const {
+        Part p;
+        p.e = -1;
+        int left = 0, k = 0, id = c, shared = 0;  // steps of the share; its first, and its first tile
+        if (c < s.ctas) {
+            const int u = share(c);
+            left = share(c + 1) - u;
+            shared = u / KS;
+            k = u - shared * KS;
+            shared += s.whole;
+        }
+        while (true) {
+            p.k = 0, p.k1 = KS;
+            if (id < s.whole) {
+                p.id = id;
+                id += G;
+            } else {
+                if (left <= 0) return;
+                p.id = shared++;
+                p.k = k;
+                p.k1 = min(KS, k + left);
+                left -= p.k1 - k;
+                k = 0;
+            }
+            p.last = left <= 0 && id >= s.whole;
+            if (p.e < 0 || s.tiles[p.e + 1] <= p.id) {
+                do ++p.e;
+                while (s.tiles[p.e + 1] <= p.id);
+                p.r = rows(p.e);
+            }
+            const int tile = p.id - s.tiles[p.e];
+            p.nt = tile / p.r.mt;
+            p.mt = tile - p.nt * p.r.mt;
+            if (!f(p)) return;
+        }
+    }
+};
+
+// Activation rows of a tile, rounded up to 16.
+__device__ __forceinline__ int tile_rows(const Part& p) {
+    return min(p.r.n, ((int)min((int64_t)kMostRows, p.r.count - (int64_t)p.mt * p.r.n) + 15) / 16 * 16);
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+// A place in a ring of `size`, and how often it has gone round, modulo 2.
+struct Turn {
+    const int size;
+    int at = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ explicit Turn(int n) : size(n) {}
+    __device__ __forceinline__ void next() {
+        if (++at == size) at = 0, parity ^= 1;
+    }
+};
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+                 "r"(bar)
+                 : "memory");
+}
+
+struct MmaArgs {
+    Int8ProductArgs p;
+    int most, stages, stage_bytes, x_bytes;  // activation rows of a tile at most; the ring; its activations of a tile of weights
+    int slot_rows;  // of partial sums, a multiple of 16
+    int early;  // weights and offsets were there before the kernel in front started its dependents
+};
+
+template <typename T, bool GATED, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_constant__ MmaArgs args) {
+    const Int8ProductArgs& a = args.p;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Shared& s = *reinterpret_cast<Shared*>(ring + (size_t)args.stages * args.stage_bytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = args.stages;
+    const int rank = PAIR ? (int)cluster_rank() : 0, cta = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+    const int KT = (int)((a.K + 63) / 64), KS = (KT + 1) / 2;
+    const int NT128 = (int)((a.N + 127) / 128), NT = PAIR ? (NT128 + 1) / 2 : NT128;
+    const Work<PAIR> work = {s, a.offsets ? -1 : a.M, NT, a.E, KS, args.most, PAIR ? (int)gridDim.x / 2 : (int)gridDim.x};
+
+    if (warp == kCopyWarp) {
+        if (lane < S) {
+            mbar_init(&s.full[lane], 1);
+            mbar_init(&s.ready[lane], PAIR ? 16 : 8);
+            mbar_init(&s.empty[lane], 1);
+        }
+        if (lane < 2) {
+            mbar_init(&s.acc_full[lane], 1);
+            mbar_init(&s.acc_empty[lane], PAIR ? 2 * kEpiWarps : kEpiWarps);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(&s.epilogue, kEpiWarps);
+        mbar_init(&s.parts, 1);
+        mbar_init(&s.done, 1);
+        s.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)), "r"(kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)), "r"(kTmemCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
+    }
+    if (!args.early) pdl_wait();
+    if (warp == 0) {  // the table of the experts' tiles
+        int sum = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            int64_t first = 0, count = 0;
+            if (e < a.E) {
+                first = a.offsets ? __ldcg(a.offsets + e) : 0;
+                count = a.offsets ? __ldcg(a.offsets + e + 1) - first : a.M;
+            }
+            const int own = rows_of(count, args.most).mt * NT;
+            int incl = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (e < a.E) {
+                s.tiles[e] = sum + incl - own;
+                s.offset[e] = (int32_t)first;
+                if (e == a.E - 1) s.offset[a.E] = (int32_t)(first + (a.offsets ? count : 0));
+            }
+            sum += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) {
+            const int G = work.G, rest = sum % G, ctas = min(G, max(rest, (int)min((int64_t)G, (int64_t)rest * KS / kLeastSteps)));
+            const bool split = rest > 0 && KS - (int)(((int64_t)rest * KS + ctas - 1) / ctas) >= kLeastSteps;
+            s.tiles[a.E] = sum;
+            s.split = split ? rest : 0;
+            s.ctas = split ? ctas : 0;
+            s.whole = sum - s.split;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // both CTAs' barriers and tensor memory are ready
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    int* const status = &a.ctrl->status;
+
+    if (warp == kCopyWarp) {
+        if (elect_one()) {
+            const uint32_t full0 = smem_u32(s.full), ring0 = smem_u32(ring);
+            const int64_t x_step = a.room * 128;
+            Turn t(S);
+            // where a tile's weights and activations of step k begin, and the activations' bytes a tile of weights
+            auto sources = [&](const Part& p, const uint8_t*& w, const uint8_t*& x) {
+                const int nt = min(PAIR ? 2 * p.nt + rank : p.nt, NT128 - 1), n = tile_rows(p) / (PAIR ? 2 : 1);
+                const int64_t row = (a.offsets ? int8_first_row(s.offset[p.e], p.e) : 0) + (int64_t)p.mt * p.r.n + (PAIR ? rank * n : 0);
+                w = a.w + (((int64_t)p.e * NT128 + nt) * KT + 2 * p.k) * kInt8Tile;
+                x = reinterpret_cast<const uint8_t*>(a.x) + 2 * p.k * x_step + row * 128;
+                return n * 128;
+            };
+            int head = 0;  // steps whose weights are on their way and whose activations are not
+            bool ok = true;
+            if (args.early) {  // the first steps' weights, before the activations are there
+                work.each(cta, [&](const Part& p) {
+                    const uint8_t *w, *x;
+                    const int bytes = sources(p, w, x);
+                    for (int k = p.k; k < p.k1; ++k, w += 2 * kInt8Tile, ++head) {
+                        if (head == S) return false;
+                        const int tiles = min(2, KT - 2 * k);
+                        expect_bytes(full0 + 8 * head, tiles * (kInt8Tile + bytes));
+                        bulk_copy(ring0 + head * args.stage_bytes + 2 * args.x_bytes, w, tiles * kInt8Tile, full0 + 8 * head);
+                    }
+                    return true;
+                });
+                pdl_wait();
+            }
+            int it = 0;
+            work.each(cta, [&](const Part& p) {
+                const uint8_t *w, *x;
+                const int bytes = sources(p, w, x);
+                for (int k = p.k; k < p.k1; ++k, w += 2 * kInt8Tile, x += 2 * x_step, ++it, t.next()) {
+                    const uint32_t bar = full0 + 8 * t.at, to = ring0 + t.at * args.stage_bytes;
+                    const int tiles = min(2, KT - 2 * k);
+                    if (it >= head) {
+                        if (!mbar_wait(&s.empty[t.at], t.parity ^ 1, &s.abort, status)) return ok = false;
+                        expect_bytes(bar, tiles * (kInt8Tile + bytes));
+                        bulk_copy(to + 2 * args.x_bytes, w, tiles * kInt8Tile, bar);
+                    }
+                    bulk_copy(to, x, bytes, bar);
+                    if (tiles == 2) bulk_copy(to + args.x_bytes, x + x_step, bytes, bar);
+                }
+                return true;
+            });
+            if (!ok) {  // copies in flight land before the CTA's shared memory goes
+                volatile int never = 0;
+                for (int i = max(0, it - S); i < it; ++i) mbar_wait(&s.full[i % S], (i / S) & 1, &never, nullptr, 100000000LL);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        if (rank == 0 && elect_one()) {
+            const uint32_t base = smem_u32(ring);
+            Turn t(S);
+            int tile = 0;
+            uint32_t slot = tmem + kSlotBase;
+            work.each(cta, [&](const Part& p) {
+                const int n = tile_rows(p), b = tile & 1;
+                const uint32_t idesc = (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)((PAIR ? 256 : 128) >> 4) << 24);
+                const uint32_t acc = tmem + b * kMostRows;
+                if (!mbar_wait(&s.acc_empty[b], ((tile >> 1) & 1) ^ 1, &s.abort, status)) return false;
+                tc_fence_after();
+                for (int k = p.k; k < p.k1; ++k, t.next(), slot ^= 2 * kSlotCols) {
+                    if (!mbar_wait(&s.ready[t.at], t.parity, &s.abort, status)) return false;
+                    tc_fence_after();
+                    const uint32_t x = ((base + t.at * args.stage_bytes) >> 4) | (1u << 16);
+                    step_products<PAIR>(acc, slot, x, idesc, k > p.k ? 1u : 0u);
+                    if (2 * k + 1 < KT) step_products<PAIR>(acc, slot + kSlotCols, x + (args.x_bytes >> 4), idesc, 1u);
+                    commit<PAIR>(&s.empty[t.at]);
+                }
+                commit<PAIR>(&s.acc_full[b]);
+                ++tile;
+                return true;
+            });
+            commit<PAIR>(&s.done);
+        }
+    } else if (warp < kConvWarps) {
+        const int set = warp >> 2, q = warp & 3;
+        const unsigned char* w0 = ring + 2 * args.x_bytes + (set & 1) * kInt8Tile + (32 * q + lane) * 16;
+        const uint32_t slot = tmem + ((uint32_t)(32 * q) << 16) + kSlotBase + set * kSlotCols;
+        Turn t(S), old(S);  // the step; the one before the last
+        int it = 0;
+        work.each(cta, [&](const Part& p) {
+            for (int k = p.k; k < p.k1; ++k, ++it, t.next()) {
+                if (it >= 3) old.next();
+                // (of every step: a barrier's phase that nobody waits for could be taken for the one after the next)
+                if (!mbar_wait_warp(&s.full[t.at], t.parity, &s.abort, status)) return false;
+                if ((it & 1) != set >> 1) continue;
+                if (2 * k + (set & 1) < KT) {
+                    const unsigned char* w = w0 + (size_t)t.at * args.stage_bytes;
+                    uint4 v[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint4*>(w + j * 2048);
+                    uint32_t h[32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        to_fp16(v[j].x, h[8 * j], h[8 * j + 1]);
+                        to_fp16(v[j].y, h[8 * j + 2], h[8 * j + 3]);
+                        to_fp16(v[j].z, h[8 * j + 4], h[8 * j + 5]);
+                        to_fp16(v[j].w, h[8 * j + 6], h[8 * j + 7]);
+                    }
+                    // the products of the step before the last have read this slot (its phase is not mistaken: this step was copied
+                    // after the products of the step S before had completed)
+                    if (it >= 2 && !mbar_wait_warp(&s.empty[old.at], old.parity, &s.abort, status)) return false;
+                    tc_fence_after();
+                    tmem_st32(slot, h);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) arrive<PAIR>(&s.ready[t.at]);
+            }
+            return true;
+        });
+    } else {
+        const int q = warp & 3;
+        if (args.early) pdl_wait();
+        pdl_launch_dependents();
+        uint32_t turn = 0, parts = 0, shares = 0;
+        auto epilogue_sync = [&] {  // of the epilogue's warps; bounded, like every wait
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.epilogue);
+            return mbar_wait_warp(&s.epilogue, turn++ & 1, &s.abort, status);
+        };
+        const bool pairs = sizeof(T) == 2 && reinterpret_cast<uintptr_t>(a.y) % 4 == 0 && a.ldy % 2 == 0;
+        const bool speaker = threadIdx.x == 32 * kConvWarps;
+        int tile = 0;
+        work.each(cta, [&](const Part& p) {
+            const int b = tile & 1;
+            const int64_t m0 = (int64_t)p.mt * p.r.n;
+            const int live = (int)min((int64_t)p.r.n, p.r.count - m0);
+            const float* const sx = a.sx + (a.offsets ? int8_first_row(s.offset[p.e], p.e) : 0) + m0;
+            const int n0 = (PAIR ? 2 * p.nt + rank : p.nt) * 128 + 32 * q, n = n0 + lane, N = (int)a.N;  // (N is at most 2^28)
+            const float sw = n < N ? __ldg(a.sw + (int64_t)p.e * a.N + n) : 0.f;
+            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + b * kMostRows;
+            __syncwarp();
+#pragma unroll
+            for (int c0 = 0; c0 < kMostRows; c0 += 32)
+                if (c0 + lane < live) s.sx[q][c0 + lane] = __ldcg(sx + c0 + lane);
+            if (!mbar_wait_warp(&s.acc_full[b], (tile >> 1) & 1, &s.abort, status)) return false;
+            tc_fence_after();
+            int first = cta, last = cta;  // the CTAs that share the tile
+            bool mine = true;
+            // The partial sums of a CTA, [16 activation rows][4][128][4]: of the tile that it begins, or (1) goes on with.
+            auto slot = [&](int c) {
+                return a.partials + (((int64_t)c * (PAIR ? 2 : 1) + rank) * 2 + (c > first)) * 128 * args.slot_rows;
+            };
+            if (p.k > 0 || p.k1 < KS) {
+                work.sharers(p.id, first, last);
+                unsigned* const count = &a.ctrl->int8_split[first * (PAIR ? 2 : 1) + rank];
+                volatile int* const verdict = &s.last[shares++ & 1];
+                // the last CTA to arrive adds the others' sums to its own; where the others are there already, it need not store them
+                if (speaker) *verdict = ld_acquire(count) == (unsigned)(last - first);
+                if (!epilogue_sync()) return false;
+                mine = *verdict != 0;
+                if (!mine) {
+                    float4* to = reinterpret_cast<float4*>(slot(cta)) + 32 * q + lane;
+                    for (int c0 = 0; c0 < live; c0 += 16, to += 4 * 128) {  // (slots have room for whole sixteens)
+                        uint32_t v[16];
+                        tmem_ld16(acc + c0, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            __stcg(to + i * 128, make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                             __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+                    }
+                    __threadfence();
+                    if (!epilogue_sync()) return false;
+                    if (speaker) {
+                        *verdict = atomicAdd(count, 1u) == (unsigned)(last - first);
+                        __threadfence();
+                    }
+                    if (!epilogue_sync()) return false;
+                    mine = *verdict != 0;
+                }
+                if (mine && speaker) *count = 0;  // (every one of them has arrived)
+            }
+            if (mine) {
+                const bool odd = lane & 1, whole = n0 + 32 <= N;
+                T* y = static_cast<T*>(a.y) + ((a.offsets ? s.offset[p.e] : 0) + m0) * a.ldy;
+                if constexpr (GATED) y += odd * a.ldy + n / 2;
+                else y += pairs ? odd * a.ldy + (n & ~1) : n;
+                // Others' sums: in the CTA's last part (most often it is that) through the ring, which nothing uses any more, as many rows at a
+                // time as fit; else straight from memory.
+                const int others = last - first, ring_rows = p.last && others > 0 ? S * args.stage_bytes / (others * 512) / 16 * 16 : 0;
+                int have = 0, begin = 0;  // rows begin .. have - 1 are in the ring
+#pragma unroll 1
+                for (int c0 = 0; c0 < live; c0 += 16, y += 16 * a.ldy) {
+                    if (ring_rows > 0 && c0 == have) {
+                        begin = c0, have = min(c0 + ring_rows, (live + 15) / 16 * 16);
+                        if (!epilogue_sync()) return false;  // what was there has been read
+                        if (speaker) {
+                            const int bytes = (have - begin) * 512;
+                            asm volatile("fence.proxy.async;" ::: "memory");
+                            expect_bytes(smem_u32(&s.parts), others * bytes);
+                            uint32_t to = smem_u32(ring);
+                            for (int c = first; c <= last; ++c)
+                                if (c != cta) bulk_copy(to, slot(c) + c0 * 128, bytes, smem_u32(&s.parts)), to += bytes;
+                        }
+                        __syncwarp();
+                        if (!mbar_wait_warp(&s.parts, parts++ & 1, &s.abort, status)) return false;
+                    }
+                    uint32_t v[16];
+                    tmem_ld16(acc + c0, v);
+                    tmem_ld_wait();
+                    if (others > 0) {
+                        float4 sum[4] = {};
+                        const float4* h = reinterpret_cast<const float4*>(ring) + (c0 - begin) * 32 + 32 * q + lane;
+                        for (int c = first; c <= last; ++c) {
+                            float4 o[4];
+                            if (c == cta) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    o[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                                                       __uint_as_float(v[4 * i + 3]));
+                            } else if (ring_rows > 0) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[i] = h[i * 128];
+                                h += (have - begin) * 32;
+                            } else {
+                                const float4* const g = reinterpret_cast<const float4*>(slot(c)) + c0 * 32 + 32 * q + lane;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[i] = __ldcg(g + i * 128);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) sum[i].x += o[i].x, sum[i].y += o[i].y, sum[i].z += o[i].z, sum[i].w += o[i].w;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            v[4 * i] = __float_as_uint(sum[i].x), v[4 * i + 1] = __float_as_uint(sum[i].y);
+                            v[4 * i + 2] = __float_as_uint(sum[i].z), v[4 * i + 3] = __float_as_uint(sum[i].w);
+                        }
+                    }
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 g = *reinterpret_cast<const float4*>(&s.sx[q][c0 + i]);
+                        f[i] = __uint_as_float(v[i]) * g.x * sw;
+                        f[i + 1] = __uint_as_float(v[i + 1]) * g.y * sw;
+                        f[i + 2] = __uint_as_float(v[i + 2]) * g.z * sw;
+                        f[i + 3] = __uint_as_float(v[i + 3]) * g.w * sw;
+                    }
+                    const bool all = whole && c0 + 16 <= live;  // (of the warp)
+                    if (GATED || pairs) {
+                        // lanes 2 i and 2 i + 1 exchange: the even one gets both weight rows of row i, the odd one of row i + 1
+                        float lo[8], hi[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float got = __shfl_xor_sync(0xffffffffu, odd ? f[2 * i] : f[2 * i + 1], 1);
+                            lo[i] = odd ? got : f[2 * i], hi[i] = odd ? f[2 * i + 1] : got;
+                        }
+                        if constexpr (GATED) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) lo[i] = int8_gated(lo[i], hi[i]);
+                            if (all) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) y[2 * i * a.ldy] = int8_result<T>(lo[i]);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    if (c0 + 2 * i + odd < live && n < N) y[2 * i * a.ldy] = int8_result<T>(lo[i]);
+                            }
+                        } else if (all) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const T u[2] = {int8_result<T>(lo[i]), int8_result<T>(hi[i])};
+                                if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(y + 2 * i * a.ldy) = *reinterpret_cast<const uint32_t*>(u);
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                if (c0 + 2 * i + odd < live && (n & ~1) < N) y[2 * i * a.ldy] = int8_result<T>(lo[i]);
+                                if (c0 + 2 * i + odd < live && (n | 1) < N) y[2 * i * a.ldy + 1] = int8_result<T>(hi[i]);
+                            }
+                        }
+                    } else if (all) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i * a.ldy] = int8_result<T>(f[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c0 + i < live && n < N) y[i * a.ldy] = int8_result<T>(f[i]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive<PAIR>(&s.acc_empty[b]);
+            ++tile;
+            return true;
+        });
+    }
+    __syncwarp();
+    {
+        // every product has completed: the leader commits `done` last, aborting or not
+        volatile int never = 0;
+        mbar_wait(&s.done, 0, &never, nullptr);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();  // neither CTA's shared or tensor memory goes while the other may use it
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+template <typename T, bool GATED>
+const void* mma_kernel(bool pair) {
+    return pair ? (const void*)int8_mma_kernel<T, GATED, true> : (const void*)int8_mma_kernel<T, GATED, false>;
+}
+template <typename T>
+const void* mma_kernel(bool gated, bool pair) {
+    return gated ? mma_kernel<T, true>(pair) : mma_kernel<T, false>(pair);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_mma(const Int8ProductArgs& a, moe_dtype dtype, bool gated, bool pair, cudaStream_t st) {
+    MmaArgs m = {};
+    m.p = a;
+    m.early = a.early;
+    m.slot_rows = (int)(a.M > kMostRows ? kMostRows : (a.M + 15) / 16 * 16);
+    // By expert the ring has room for tiles of four times the mean (more of an expert's rows are several tiles): small ones leave
+    // room for more steps of weights on their way.
+    const int64_t rows = a.offsets && 4 * a.M / a.E + 16 < a.M ? 4 * a.M / a.E + 16 : a.M;
+    m.most = (int)(rows > kMostRows ? kMostRows : (rows + 15) / 16 * 16);
+    m.x_bytes = m.most * 128 / (pair ? 2 : 1);
+    m.x_bytes = (m.x_bytes + 1023) / 1024 * 1024;
+    m.stage_bytes = 2 * (m.x_bytes + kInt8Tile);
+    const int fit = (int)((kSmemMost - 1024 - sizeof(Shared)) / m.stage_bytes);
+    m.stages = fit < kMostStages ? fit : kMostStages;
+    // (more than half of the SM's shared memory, so that one CTA per SM owns its tensor memory)
+    size_t smem = (size_t)m.stages * m.stage_bytes + sizeof(Shared) + 1024;
+    if (smem < 120 * 1024) smem = 120 * 1024;
+    int ctas = sm_count() < kInt8Ctas ? sm_count() : kInt8Ctas;
+    if (pair) ctas = ctas / 2 * 2;
+    const void* f = dtype == MOE_F32    ? mma_kernel<float>(gated, pair)
+                    : dtype == MOE_BF16 ? mma_kernel<__nv_bfloat16>(gated, pair)
+                                        : mma_kernel<__half>(gated, pair);
+    void* args[] = {&m};
+    return launch_cluster(f, dim3(ctas), kThreads, smem, pair ? 2 : 1, st, args);
+}
+
+}  // namespace moe

@@ -102,9 +102,10 @@ struct Int8ProductArgs {
     int64_t ldy;
     Ctrl* ctrl;
     float* partials;  // int8_partial_bytes(M)
+    int early;        // w, sw and offsets were there before the kernel in front started its dependents
 };
 // Partial sums of the tiles that CTAs share: two tiles of 128 weight rows a CTA, by as many activation rows as a tile has at most.
 constexpr int kInt8Ctas = 160;  // CTAs at most
-inline size_t int8_partial_bytes(int64_t M) { return (size_t)kInt8Ctas * 2 * 128 * 4 * (size_t)(M > 256 ? 256 : (M + 15) / 16 * 16); }
+inline size_t int8_partial_bytes(int64_t M) { return (size_t)kInt8Ctas * 2 * 128 * 4 * (size_t)(M > 192 ? 192 : (M + 15) / 16 * 16); }
 cudaError_t launch_int8_product(const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st);
 }  // namespace moe

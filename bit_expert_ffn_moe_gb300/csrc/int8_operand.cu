@@ -12,7 +12,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kKept = 4;  // pieces of 8 values that a thread keeps between the two passes over its row (256 threads: 8192 values)
 
-// The largest magnitude as the bits of |v|: NaN above infinity above all numbers.
+// The bits of |v|: NaN above infinity above all numbers.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 struct Scale {
@@ -28,14 +28,27 @@ __device__ __forceinline__ Scale scale_of(uint32_t most) {
     if (r.bad) r.s = __uint_as_float(0x7fffffffu);
     return r;
 }
-// v / s, rounded to fp32, rounded to a whole number.  The product with the reciprocal is within 127 x 2^-22 of the quotient, so it
-// decides wherever it is further than that from a half; elsewhere (and where the reciprocal is infinite) the division does.
-__device__ __forceinline__ float whole(float v, const Scale& r) {
-    if (r.bad) return 0.f;
-    const float t = v * r.inverse;
-    float q = rintf(t);
-    if (!(fabsf(t - q) < 0.4999f)) q = rintf(__fdiv_rn(v, r.s));
-    return fminf(fmaxf(q, -127.f), 127.f);
+// v / s, rounded to fp32, rounded to a whole number, by the division.
+__device__ __noinline__ float whole(float v, float s, bool bad) {
+    return bad ? 0.f : fminf(fmaxf(rintf(__fdiv_rn(v, s)), -127.f), 127.f);
+}
+// The same of eight values.  The product with the reciprocal is within 127 x 2^-22 of the quotient, so it decides wherever it is further
+// than that from a half; elsewhere (and where the reciprocal is infinite or the row bad: their differences are not numbers) the
+// division does.  Adding 1.5 x 2^23 rounds to a whole number, ties to even.
+__device__ __forceinline__ void whole8(const float (&v)[8], const Scale& s, float (&q)[8]) {
+    float off = 0.f;
+    bool sure = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = v[i] * s.inverse;
+        q[i] = (t + 12582912.f) - 12582912.f;
+        off = fmaxf(off, fabsf(t - q[i]));
+        sure = sure && fabsf(t) < 127.25f;  // (false for NaN)
+    }
+    if (!(sure && off < 0.4999f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = whole(v[i], s.s, s.bad);
+    }
 }
 
 template <typename T>
@@ -47,27 +60,74 @@ __device__ __forceinline__ float value<__nv_bfloat16>(__nv_bfloat16 v) { return 
 template <>
 __device__ __forceinline__ float value<__half>(__half v) { return __half2float(v); }
 
-// Values c .. c + 7 of a row of K, zeros behind its end.
-template <typename T, bool WIDE>
-__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t K, float (&v)[8]) {
-    if (WIDE && c + 8 <= K) {
-        constexpr int kLoads = sizeof(T) * 8 / 16 ? (int)(sizeof(T) * 8 / 16) : 1;
-        uint4 u[kLoads];
+// Values c .. c + 7 of a row of K as they come, zeros behind its end.  WIDE: rows that start on 16 bytes.
+template <typename T>
+struct Eight {
+    static constexpr int kWords = 2 * (int)sizeof(T);
+    uint32_t w[kWords];
+
+    template <bool WIDE>
+    __device__ __forceinline__ void load(const T* row, int64_t c, int64_t K) {
+        if (WIDE && c + 8 <= K) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
-        const T* t = reinterpret_cast<const T*>(u);
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
+                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            }
+        } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = value<T>(t[i]);
-    } else {
+            for (int i = 0; i < 8; ++i) w[i] = c + i < K ? __ldg(reinterpret_cast<const uint32_t*>(row + c + i)) : 0;
+        } else {
+            // whole words, shifted where the row begins in the middle of one; of those that begin behind the row's end the last one again
+            const uintptr_t at = reinterpret_cast<uintptr_t>(row + min(c, K - 1)), end = reinterpret_cast<uintptr_t>(row + K - 1) & ~(uintptr_t)3;
+            const uint32_t shift = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 2) * 8;
+            uint32_t u[5];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < K ? value<T>(row[c + i]) : 0.f;
+            for (int i = 0; i < 5; ++i) u[i] = __ldg(reinterpret_cast<const uint32_t*>(min((at & ~(uintptr_t)3) + 4 * i, end)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = __funnelshift_r(u[i], u[i + 1], shift);
+                const int64_t left = K - c - 2 * i;
+                w[i] = left >= 2 ? w[i] : left == 1 ? w[i] & 0xffffu : 0;
+            }
+        }
     }
-}
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    // The larger of `most` and its magnitudes; 16-bit ones in halves.
+    __device__ __forceinline__ uint32_t most(uint32_t m) const {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) m = sizeof(T) == 4 ? max(m, w[i] & 0x7fffffffu) : __vmaxu2(m, w[i] & 0x7fff7fffu);
+        return m;
+    }
+    // That of a row, as the bits of an fp32 number (NaN above infinity above all numbers).
+    __device__ __forceinline__ static uint32_t as_fp32(uint32_t m) {
+        if constexpr (sizeof(T) == 4) return m;
+        const uint16_t b = (uint16_t)max(m & 0xffffu, m >> 16);
+        return __float_as_uint(value<T>(*reinterpret_cast<const T*>(&b))) & 0x7fffffffu;
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else {
+                const uint16_t b = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+                f[i] = value<T>(*reinterpret_cast<const T*>(&b));
+            }
+        }
+    }
+};
 
 // The largest of a row's magnitudes over the `warps` warps that share it (all of them call this).
 __device__ __forceinline__ uint32_t most_of(uint32_t m, int warps, uint32_t* part) {
     m = __reduce_max_sync(0xffffffffu, m);
-    if (warps == 1) return m;
+    if (warps == 1) {
+        __syncwarp();
+        return m;
+    }
     const int warp = threadIdx.x >> 5, first = warp / warps * warps;
     if ((threadIdx.x & 31) == 0) part[warp] = m;
     __syncthreads();
@@ -76,82 +136,76 @@ __device__ __forceinline__ uint32_t most_of(uint32_t m, int warps, uint32_t* par
 }
 
 // The expert whose rows hold row r < offsets[E]: the last e with offsets[e] <= r.
-__device__ __forceinline__ int expert_of(const int32_t* __restrict__ offsets, int E, int r) {
+__device__ __forceinline__ int expert_of(const int32_t* offsets, int E, int r) {
     int lo = 0, hi = E;  // offsets[lo] <= r < offsets[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
-        if (__ldg(offsets + mid) <= r) lo = mid;
+        if (offsets[mid] <= r) lo = mid;
         else hi = mid;
     }
     return lo;
 }
 
 // `warps` warps of a CTA share a row; it is read once into registers (its first kKept pieces per thread; what is longer is read
-// again), quantised, and written to the rows that it goes to.  Bound by the writing of k rows in 16 bits.
+// again), quantised, and written to the rows that it goes to.  Bound by the writing of k rows in 16 bits; for few rows by its chain of
+// loads, so the row's, the offsets' and its places' are all in flight together.
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads) int8_rows_kernel(const Int8RowsArgs a, const int warps) {
+__global__ void __launch_bounds__(kThreads, 4) int8_rows_kernel(const Int8RowsArgs a, const int warps) {
     __shared__ uint32_t part[kThreads / 32];
     __shared__ int64_t to_smem[kThreads / 32][kMaxK];
+    extern __shared__ int32_t offsets[];  // [E + 1]
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = kThreads / 32 / warps, mine = warp / warps;
     const int64_t t = (int64_t)blockIdx.x * rows + mine;
     const int first = threadIdx.x - mine * warps * 32, step = warps * 32;
     const int k = a.inv ? a.k : 1;
-    bool live = t < a.T;
-    if (warp % warps == 0 && lane < k) {  // where the row goes
-        int64_t to = -1;
-        if (live) {
-            const int64_t r = a.inv ? (int64_t)__ldg(a.inv + t * k + lane) : t;
-            if (!a.offsets) {
-                to = r;
-            } else if (r >= 0 && r < __ldg(a.offsets + a.E)) {
-                const int e = expert_of(a.offsets, a.E, (int)r);
-                const int o = __ldg(a.offsets + e);
-                to = int8_first_row(o, e) + r - o;
-            }
-            if (to >= a.room) to = -1;
-        }
-        to_smem[mine][lane] = to;
-    }
-    if (warps == 1) __syncwarp();
-    else __syncthreads();
-    bool wanted = false;
-    for (int j = 0; j < k; ++j) wanted |= to_smem[mine][j] >= 0;
-    live = live && wanted;
+    const bool live = t < a.T, places = warp % warps == 0 && lane < k && live;
     const T* x = static_cast<const T*>(a.x) + t * a.ld;
-    const int64_t Kp = (a.K + 63) / 64 * 64;
-    const int pieces = (int)(Kp / 8);
-    float kept[kKept][8];
-    uint32_t most = 0;
-    if (live) {
+    const int pieces = (int)((a.K + 63) / 64 * 8);
+    int64_t r = t;
+    if (places && a.inv) r = __ldg(a.inv + t * k + lane);
+    Eight<T> kept[kKept];
 #pragma unroll
-        for (int i = 0; i < kKept; ++i) {
-            const int c = first + i * step;
-            if (c < pieces) load8<T, WIDE>(x, 8 * (int64_t)c, a.K, kept[i]);
-            else
-#pragma unroll
-                for (int u = 0; u < 8; ++u) kept[i][u] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < kKept; ++i)
-#pragma unroll
-            for (int u = 0; u < 8; ++u) most = max(most, magnitude(kept[i][u]));
-        for (int c = first + kKept * step; c < pieces; c += step) {
-            float v[8];
-            load8<T, WIDE>(x, 8 * (int64_t)c, a.K, v);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) most = max(most, magnitude(v[u]));
-        }
+    for (int i = 0; i < kKept; ++i) {
+        if (live && first + i * step < pieces) kept[i].template load<WIDE>(x, 8 * (int64_t)(first + i * step), a.K);
+        else kept[i].clear();
     }
-    const Scale s = scale_of(most_of(most, warps, part));
+    if (a.offsets) {
+        for (int e = threadIdx.x; e <= a.E; e += kThreads) offsets[e] = __ldg(a.offsets + e);
+        __syncthreads();
+    }
+    if (places) {  // where the row goes
+        int64_t to = r;
+        if (a.offsets) {
+            to = -1;
+            if (r >= 0 && r < offsets[a.E]) {
+                const int e = expert_of(offsets, a.E, (int)r);
+                to = int8_first_row(offsets[e], e) + r - offsets[e];
+            }
+        }
+        to_smem[mine][lane] = to < a.room ? to : -1;
+    }
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) most = kept[i].most(most);
+    if (live)
+        for (int c = first + kKept * step; c < pieces; c += step) {
+            Eight<T> v;
+            v.template load<WIDE>(x, 8 * (int64_t)c, a.K);
+            most = v.most(most);
+        }
+    const Scale s = scale_of(most_of(Eight<T>::as_fp32(most), warps, part));  // (and the places are there)
     if (!live) return;
     if (first < k && to_smem[mine][first] >= 0) a.s[to_smem[mine][first]] = s.s;
-    auto put = [&](int c, const float (&v)[8]) {
+    auto put = [&](int c, const Eight<T>& x8) {
+        float v[8], q[8];
+        x8.get(v);
+        whole8(v, s, q);
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __half2 h = __floats2half2_rn(whole(v[2 * i], s), whole(v[2 * i + 1], s));
+            const __half2 h = __floats2half2_rn(q[2 * i], q[2 * i + 1]);
             o[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
         for (int j = 0; j < k; ++j) {
@@ -165,8 +219,8 @@ __global__ void __launch_bounds__(kThreads) int8_rows_kernel(const Int8RowsArgs 
     for (int i = 0; i < kKept; ++i)
         if (first + i * step < pieces) put(first + i * step, kept[i]);
     for (int c = first + kKept * step; c < pieces; c += step) {
-        float v[8];
-        load8<T, WIDE>(x, 8 * (int64_t)c, a.K, v);
+        Eight<T> v;
+        v.template load<WIDE>(x, 8 * (int64_t)c, a.K);
         put(c, v);
     }
 }
@@ -198,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) int8_pack_kernel(const Int8PackArgs 
             int b = 0;
             if (at < a.K) {
                 if constexpr (kWhole) b = w[at];
-                else b = (int)whole(value<T>(w[at]), s);
+                else b = (int)whole(value<T>(w[at]), s.s, s.bad);
             }
             o[i / 4] |= (uint32_t)(b & 255) << (8 * (i % 4));
         }
@@ -215,7 +269,8 @@ cudaError_t launch_rows(Int8RowsArgs a, cudaStream_t st) {
     const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ld * (int64_t)sizeof(T)) % 16 == 0;
     const void* f = wide ? (const void*)int8_rows_kernel<T, true> : (const void*)int8_rows_kernel<T, false>;
     void* args[] = {&a, &warps};
-    return launch_kernel(f, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(kThreads), 0, st, true, args);
+    const size_t smem = a.offsets ? sizeof(int32_t) * (size_t)(a.E + 1) : 0;
+    return launch_kernel(f, dim3((unsigned)((a.T + rows - 1) / rows)), dim3(kThreads), smem, st, true, args);
 }
 
 }  // namespace

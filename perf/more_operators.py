@@ -280,7 +280,7 @@ def _run_own(case, op, st):
     order = ops.expert_order(st["ids"], case["E"])
     rows = ops.tokens_to_experts(st["x"], order, weights_in)
     if op == "sort":
-        return {"rows": rows, "ends": order.offsets[1:], "place": order.inv}
+        return {"rows": rows, "ends": order.offsets[1:], "place": order.inv.view(-1)}
     y = ops.experts_to_tokens(st["outputs"], order, weights_out)
     doutputs, dw_out = ops.experts_to_tokens_backward(st["dy"], order, st["outputs"], weights_out)
     dx, dw_in = ops.tokens_to_experts_backward(st["drows"], order, st["x"], weights_in)

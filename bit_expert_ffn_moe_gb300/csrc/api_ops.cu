@@ -430,11 +430,10 @@ moe_status moe_int8_linear(const void* x, moe_dtype x_dtype, int64_t M, int64_t 
         const int64_t room = moe_int8_rows_room(M, 0);
         uint16_t* q = reinterpret_cast<uint16_t*>(base + L.q);
         float* s = reinterpret_cast<float*>(base + L.s);
-        const cudaError_t e = launch_int8_rows({x, ldx, M, K, nullptr, 1, nullptr, 0, room, q, s}, x_dtype, st);
-        if (e != cudaSuccess) return e;
-        return launch_int8_product({W->q, W->s, q, s, room, nullptr, 1, M, N, K, y, ldy, static_cast<Ctrl*>(ws),
-                                    reinterpret_cast<float*>(base + L.partials), 1},
-                                   y_dtype, gated != 0, st);
+        return launch_int8_linear(x, x_dtype, ldx, q, s,
+                                  {W->q, W->s, nullptr, nullptr, room, nullptr, 1, M, N, K, y, ldy, static_cast<Ctrl*>(ws),
+                                   reinterpret_cast<float*>(base + L.partials), 0},
+                                  y_dtype, gated != 0, st);
     });
 }
 

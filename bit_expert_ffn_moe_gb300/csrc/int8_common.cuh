@@ -21,7 +21,123 @@ __device__ __forceinline__ float int8_gated(float gate, float up) {
     return gate < 0.f ? (gate * e) * (up * e) / (1.f + e * e) : gate / (1.f + e) * up;
 }
 
-cudaError_t launch_int8_dot(const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st);
+// ------------------------------------------------------------------ rows in 8 bits
+// The bits of |v|: NaN above infinity above all numbers.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+struct Scale {
+    float s, inverse;
+    bool bad;
+};
+__device__ __forceinline__ Scale scale_of(uint32_t most) {
+    Scale r;
+    r.bad = most >= 0x7f800000u;
+    r.s = __fdiv_rn(__uint_as_float(most), 127.f);
+    if (!(r.s > 0.f)) r.s = 1.f;
+    r.inverse = 1.f / r.s;
+    if (r.bad) r.s = __uint_as_float(0x7fffffffu);
+    return r;
+}
+// v / s, rounded to fp32, rounded to a whole number, by the division.
+static __device__ __noinline__ float whole(float v, float s, bool bad) {
+    return bad ? 0.f : fminf(fmaxf(rintf(__fdiv_rn(v, s)), -127.f), 127.f);
+}
+// The same of eight values.  The product with the reciprocal is within 127 x 2^-22 of the quotient, so it decides wherever it is further
+// than that from a half; elsewhere (and where the reciprocal is infinite or the row bad: their differences are not numbers) the
+// division does.  Adding 1.5 x 2^23 rounds to a whole number, ties to even.
+__device__ __forceinline__ void whole8(const float (&v)[8], const Scale& s, float (&q)[8]) {
+    float off = 0.f;
+    bool sure = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = v[i] * s.inverse;
+        q[i] = (t + 12582912.f) - 12582912.f;
+        off = fmaxf(off, fabsf(t - q[i]));
+        sure = sure && fabsf(t) < 127.25f;  // (false for NaN)
+    }
+    if (!(sure && off < 0.4999f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = whole(v[i], s.s, s.bad);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ float value(T v);
+template <>
+__device__ __forceinline__ float value<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float value<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float value<__half>(__half v) { return __half2float(v); }
+
+// Values c .. c + 7 of a row of K as they come, zeros behind its end.  WIDE: rows that start on 16 bytes.
+template <typename T>
+struct Eight {
+    static constexpr int kWords = 2 * (int)sizeof(T);
+    uint32_t w[kWords];
+
+    template <bool WIDE>
+    __device__ __forceinline__ void load(const T* row, int64_t c, int64_t K) {
+        if (WIDE && c + 8 <= K) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + c) + i);
+                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = c + i < K ? __ldg(reinterpret_cast<const uint32_t*>(row + c + i)) : 0;
+        } else {
+            // whole words, shifted where the row begins in the middle of one; of those that begin behind the row's end the last one again
+            const uintptr_t at = reinterpret_cast<uintptr_t>(row + min(c, K - 1)), end = reinterpret_cast<uintptr_t>(row + K - 1) & ~(uintptr_t)3;
+            const uint32_t shift = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 2) * 8;
+            uint32_t u[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) u[i] = __ldg(reinterpret_cast<const uint32_t*>(min((at & ~(uintptr_t)3) + 4 * i, end)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                w[i] = __funnelshift_r(u[i], u[i + 1], shift);
+                const int64_t left = K - c - 2 * i;
+                w[i] = left >= 2 ? w[i] : left == 1 ? w[i] & 0xffffu : 0;
+            }
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    // The larger of `most` and its magnitudes; 16-bit ones in halves.
+    __device__ __forceinline__ uint32_t most(uint32_t m) const {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) m = sizeof(T) == 4 ? max(m, w[i] & 0x7fffffffu) : __vmaxu2(m, w[i] & 0x7fff7fffu);
+        return m;
+    }
+    // That of a row, as the bits of an fp32 number (NaN above infinity above all numbers).
+    __device__ __forceinline__ static uint32_t as_fp32(uint32_t m) {
+        if constexpr (sizeof(T) == 4) return m;
+        const uint16_t b = (uint16_t)max(m & 0xffffu, m >> 16);
+        return __float_as_uint(value<T>(*reinterpret_cast<const T*>(&b))) & 0x7fffffffu;
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = __uint_as_float(w[i]);
+            } else {
+                const uint16_t b = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
+                f[i] = value<T>(*reinterpret_cast<const T*>(&b));
+            }
+        }
+    }
+};
+
+// Few rows: of the operand, or, where x is not null, [M][ldx] of x_dtype, quantised by every CTA for itself (K at most kInt8DotK).
+constexpr int kInt8DotK = 16384;
+cudaError_t launch_int8_dot(const Int8ProductArgs& a, moe_dtype dtype, bool gated, const void* x, moe_dtype x_dtype, int64_t ldx,
+                            cudaStream_t st);
+// A few dozen rows with one matrix, where its tiles do not outnumber the SMs.
+bool int8_few_fits(const Int8ProductArgs& a);
+cudaError_t launch_int8_few(const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st);
 cudaError_t launch_int8_mma(const Int8ProductArgs& a, moe_dtype dtype, bool gated, bool pair, cudaStream_t st);
 
 }  // namespace moe

@@ -108,4 +108,8 @@ struct Int8ProductArgs {
 constexpr int kInt8Ctas = 160;  // CTAs at most
 inline size_t int8_partial_bytes(int64_t M) { return (size_t)kInt8Ctas * 2 * 128 * 4 * (size_t)(M > 192 ? 192 : (M + 15) / 16 * 16); }
 cudaError_t launch_int8_product(const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st);
+// The same of rows x [a.M][ldx], quantised into q and s (a.room rows) where the product does not do it itself; a.early: whether w and
+// sw were there before the kernel in front started its dependents.
+cudaError_t launch_int8_linear(const void* x, moe_dtype x_dtype, int64_t ldx, uint16_t* q, float* s, const Int8ProductArgs& a, moe_dtype dtype,
+                               bool gated, cudaStream_t st);
 }  // namespace moe

@@ -4,7 +4,8 @@
 // registers by sixteen warps, stored to tensor memory, so that they cost one byte of memory traffic and shared memory sees them
 // once.  The activations are the N side (16 .. 192 rows), fp16 already, copied as they lie.
 //   warps 0-15   conversion: four sets of four warps, each a quarter of the tiles of 64 values
-//   warps 16-19  epilogue: accumulators (two, so that the next tile's products run meanwhile), scales, store
+//   warps 16-19  epilogue: accumulators (two, so that the next tile's products run meanwhile), scales, store; of the CTA's last
+//                part all twenty warps (1024 x 4096 x 8192: 76 us with four, 59 with twenty)
 //   warp 20      copies: three bulk copies a step of 128 values
 //   warp 21      products
 // PAIR: two CTAs share a tile of 256 weight rows (cta_group::2), each with half of the activation rows in its shared memory; the
@@ -30,13 +31,20 @@ constexpr int kLeastSteps = 8;       // steps that a CTA's share of split tiles 
 constexpr size_t kSmemMost = 232448;
 
 struct Shared {
-    uint64_t full[kMostStages], ready[kMostStages], empty[kMostStages], acc_full[2], acc_empty[2], epilogue, parts, done;
+    uint64_t full[kMostStages], ready[kMostStages], empty[kMostStages], acc_full[2], acc_empty[2], epilogue, all, parts, done;
     uint32_t tmem;
     volatile int abort;
-    int last[2];  // whether this CTA is the last to arrive at a shared tile (it has two at most)
+    int last[3];  // whether this CTA is the last to arrive at a shared tile: at the one before the last, or the last
     int split, ctas, whole;  // tiles that CTAs (PAIR: pairs) share, how many of these do, and tiles that one CTA computes
-    alignas(16) float sx[kEpiWarps][kMostRows];
+    alignas(16) float sx[kEpiWarps + 1][kMostRows];  // scales of the rows of the epilogue's warps' tiles; of the last part
     int32_t tiles[kMaxE + 1], offset[kMaxE + 1];  // tiles and rows of the experts before
+};
+
+struct MmaArgs {
+    Int8ProductArgs p;
+    int most, stages, stage_bytes, x_bytes;  // activation rows of a tile at most; the ring; its activations of a tile of weights
+    int slot_rows;  // of partial sums, a multiple of 16
+    int early;  // weights and offsets were there before the kernel in front started its dependents
 };
 
 // An expert's rows as mt tiles of up to n rows (a multiple of 16).
@@ -70,6 +78,10 @@ struct Work {
     const int64_t M;  // rows of a dense product (by expert: -1)
     const int NT, E, KS, most, G;  // weight tiles (PAIR: of 256 rows), experts, steps of a tile, CTAs
 
+    __device__ __forceinline__ Work(const Shared& shared, const MmaArgs& args)
+        : s(shared), M(args.p.offsets ? -1 : args.p.M), NT((int)((args.p.N + (PAIR ? 255 : 127)) / (PAIR ? 256 : 128))), E(args.p.E),
+          KS((int)((args.p.K + 127) / 128)), most(args.most), G(PAIR ? (int)gridDim.x / 2 : (int)gridDim.x) {}
+
     __device__ __forceinline__ Rows rows(int e) const { return rows_of(M >= 0 ? M : s.offset[e + 1] - s.offset[e], most); }
     // The first step of CTA c's share of the split tiles.  (32 bits: fewer tiles than CTAs, 1024 steps a tile at most.)
     __device__ __forceinline__ int share(int c) const { return (int)((unsigned)(s.split * KS) * (unsigned)c / (unsigned)s.ctas); }
@@ -78,6 +90,35 @@ struct Work {
         const unsigned all = s.split * KS, b = (id - s.whole) * KS;
         first = (int)(((b + 1) * (unsigned)s.ctas - 1) / all);
         last = (int)(((b + KS) * (unsigned)s.ctas - 1) / all);
+    }
+    // CTA c's last part, and its number among the CTA's parts (-1: no work).
+    __device__ __forceinline__ int last(int c, Part& p) const {
+        int number = c < s.whole ? (s.whole - 1 - c) / G : -1;  // of its whole tiles' last one
+        p.id = c + number * G;
+        p.k = 0, p.k1 = KS;
+        if (c < s.ctas) {
+            const int u = share(c), end = share(c + 1), tile = (end - 1) / KS;
+            number += tile - u / KS + 1;
+            p.id = s.whole + tile;
+            p.k = max(0, u - tile * KS);
+            p.k1 = end - tile * KS;
+        }
+        if (number < 0) return -1;
+        p.last = true;
+        place(p, -1);
+        return number;
+    }
+    // Expert and tiles of p.id; e: an expert before its.
+    __device__ __forceinline__ void place(Part& p, int e) const {
+        if (e < 0 || s.tiles[e + 1] <= p.id) {
+            do ++e;
+            while (s.tiles[e + 1] <= p.id);
+            p.r = rows(e);
+        }
+        p.e = e;
+        const int tile = p.id - s.tiles[e];
+        p.nt = tile / p.r.mt;
+        p.mt = tile - p.nt * p.r.mt;
     }
     // f(part) for CTA c's work, until it returns false.
     template <typename F>
@@ -106,14 +147,7 @@ struct Work {
                 k = 0;
             }
             p.last = left <= 0 && id >= s.whole;
-            if (p.e < 0 || s.tiles[p.e + 1] <= p.id) {
-                do ++p.e;
-                while (s.tiles[p.e + 1] <= p.id);
-                p.r = rows(p.e);
-            }
-            const int tile = p.id - s.tiles[p.e];
-            p.nt = tile / p.r.mt;
-            p.mt = tile - p.nt * p.r.mt;
+            place(p, p.e);
             if (!f(p)) return;
         }
     }
@@ -128,12 +162,177 @@ __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-struct MmaArgs {
-    Int8ProductArgs p;
-    int most, stages, stage_bytes, x_bytes;  // activation rows of a tile at most; the ring; its activations of a tile of weights
-    int slot_rows;  // of partial sums, a multiple of 16
-    int early;  // weights and offsets were there before the kernel in front started its dependents
-};
+
+// Results of the CTA's part p, its tile number `tile`: this warp's lane quarter, units of 16 activation rows unit0, unit0 + stride, ...
+// sx: room for the rows' scales, of this warp or with the same from others; verdict: a word of the warps that sync() brings together.
+template <typename T, bool GATED, bool PAIR, typename Sync>
+__device__ __forceinline__ bool finish(const MmaArgs& args, Shared& s, unsigned char* ring, const Work<PAIR>& work, uint32_t tmem, const Part& p, int tile,
+                                       int unit0, int stride, float* sx, volatile int* verdict, Sync sync) {
+    const Int8ProductArgs& a = args.p;
+    const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, b = tile & 1;
+    const int rank = PAIR ? (int)cluster_rank() : 0, cta = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+    const bool speaker = threadIdx.x == 32 * kConvWarps;
+    int* const status = &a.ctrl->status;
+    const int64_t m0 = (int64_t)p.mt * p.r.n;
+    const int live = (int)min((int64_t)p.r.n, p.r.count - m0);
+    const int n0 = (PAIR ? 2 * p.nt + rank : p.nt) * 128 + 32 * q, n = n0 + lane, N = (int)a.N;  // (N is at most 2^28)
+    const float sw = n < N ? __ldg(a.sw + (int64_t)p.e * a.N + n) : 0.f;
+    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + b * kMostRows;
+    {
+        const float* const from = a.sx + (a.offsets ? int8_first_row(s.offset[p.e], p.e) : 0) + m0;
+        __syncwarp();
+#pragma unroll
+        for (int c0 = 0; c0 < kMostRows; c0 += 32)
+            if (c0 + lane < live) sx[c0 + lane] = __ldcg(from + c0 + lane);
+    }
+    if (!mbar_wait_warp(&s.acc_full[b], (tile >> 1) & 1, &s.abort, status)) return false;
+    tc_fence_after();
+    int first = cta, last = cta;  // the CTAs that share the tile
+    // The partial sums of a CTA, [16 activation rows][4][128][4]: of the tile that it begins, or (1) goes on with.
+    auto slot = [&](int c) {
+        return reinterpret_cast<float4*>(a.partials + (((int64_t)c * (PAIR ? 2 : 1) + rank) * 2 + (c > first)) * 128 * args.slot_rows);
+    };
+    if (p.k > 0 || p.k1 < work.KS) {
+        work.sharers(p.id, first, last);
+        unsigned* const count = &a.ctrl->int8_split[first * (PAIR ? 2 : 1) + rank];
+        // the last CTA to arrive adds the others' sums to its own; where the others are there already, it need not store them
+        if (speaker) *verdict = ld_acquire(count) == (unsigned)(last - first);
+        if (!sync()) return false;
+        bool mine = *verdict != 0;
+        if (!mine) {
+            for (int c0 = 16 * unit0; c0 < live; c0 += 16 * stride) {  // (slots have room for whole sixteens)
+                float4* const to = slot(cta) + c0 * 32 + 32 * q + lane;
+                uint32_t v[16];
+                tmem_ld16(acc + c0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    __stcg(to + i * 128, make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                                                     __uint_as_float(v[4 * i + 3])));
+            }
+            __threadfence();
+            if (!sync()) return false;
+            if (speaker) {
+                *verdict = atomicAdd(count, 1u) == (unsigned)(last - first);
+                __threadfence();
+            }
+            if (!sync()) return false;
+            mine = *verdict != 0;
+        }
+        if (!mine) return true;
+        if (speaker) *count = 0;  // (every one of them has arrived)
+    }
+    const bool odd = lane & 1, whole = n0 + 32 <= N;
+    const bool pairs = sizeof(T) == 2 && reinterpret_cast<uintptr_t>(a.y) % 4 == 0 && a.ldy % 2 == 0;
+    T* const out = static_cast<T*>(a.y) + ((a.offsets ? s.offset[p.e] : 0) + m0) * a.ldy +
+                   (GATED ? odd * a.ldy + n / 2 : pairs ? odd * a.ldy + (n & ~1) : (int64_t)n);
+    // Others' sums: in the CTA's last part (most often it is that) through the ring, which nothing uses any more, as many rows at a
+    // time as fit; else straight from memory.
+    const int others = last - first, ring_rows = p.last && others > 0 ? args.stages * args.stage_bytes / (others * 512) / 16 * 16 : 0;
+    uint32_t parts = 0;
+    for (int begin = 0, end; begin < live; begin = end) {
+        end = ring_rows > 0 ? min(begin + ring_rows, (live + 15) / 16 * 16) : (live + 15) / 16 * 16;
+        if (ring_rows > 0) {
+            if (!sync()) return false;  // what was there has been read
+            if (speaker) {
+                const int bytes = (end - begin) * 512;
+                asm volatile("fence.proxy.async;" ::: "memory");
+                expect_bytes(smem_u32(&s.parts), others * bytes);
+                uint32_t to = smem_u32(ring);
+                for (int c = first; c <= last; ++c)
+                    if (c != cta) bulk_copy(to, slot(c) + begin * 32, bytes, smem_u32(&s.parts)), to += bytes;
+            }
+            __syncwarp();
+            if (!mbar_wait_warp(&s.parts, parts++ & 1, &s.abort, status)) return false;
+        }
+#pragma unroll 1
+        for (int c0 = begin + 16 * unit0; c0 < end; c0 += 16 * stride) {
+            uint32_t v[16];
+            tmem_ld16(acc + c0, v);
+            tmem_ld_wait();
+            if (others > 0) {
+                float4 sum[4] = {};
+                const float4* h = reinterpret_cast<const float4*>(ring) + (c0 - begin) * 32 + 32 * q + lane;
+                for (int c = first; c <= last; ++c) {
+                    float4 o[4];
+                    if (c == cta) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                                               __uint_as_float(v[4 * i + 3]));
+                    } else if (ring_rows > 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = h[i * 128];
+                        h += (end - begin) * 32;
+                    } else {
+                        const float4* const g = slot(c) + c0 * 32 + 32 * q + lane;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = __ldcg(g + i * 128);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sum[i].x += o[i].x, sum[i].y += o[i].y, sum[i].z += o[i].z, sum[i].w += o[i].w;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[4 * i] = __float_as_uint(sum[i].x), v[4 * i + 1] = __float_as_uint(sum[i].y);
+                    v[4 * i + 2] = __float_as_uint(sum[i].z), v[4 * i + 3] = __float_as_uint(sum[i].w);
+                }
+            }
+            float f[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 g = *reinterpret_cast<const float4*>(sx + c0 + i);
+                f[i] = __uint_as_float(v[i]) * g.x * sw;
+                f[i + 1] = __uint_as_float(v[i + 1]) * g.y * sw;
+                f[i + 2] = __uint_as_float(v[i + 2]) * g.z * sw;
+                f[i + 3] = __uint_as_float(v[i + 3]) * g.w * sw;
+            }
+            T* const y = out + (int64_t)c0 * a.ldy;
+            const bool all = whole && c0 + 16 <= live;  // (of the warp)
+            if (GATED || pairs) {
+                // lanes 2 i and 2 i + 1 exchange: the even one gets both weight rows of row i, the odd one of row i + 1
+                float lo[8], hi[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float got = __shfl_xor_sync(0xffffffffu, odd ? f[2 * i] : f[2 * i + 1], 1);
+                    lo[i] = odd ? got : f[2 * i], hi[i] = odd ? f[2 * i + 1] : got;
+                }
+                if constexpr (GATED) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) lo[i] = int8_gated(lo[i], hi[i]);
+                    if (all) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[2 * i * a.ldy] = int8_result<T>(lo[i]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (c0 + 2 * i + odd < live && n < N) y[2 * i * a.ldy] = int8_result<T>(lo[i]);
+                    }
+                } else if (all) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const T u[2] = {int8_result<T>(lo[i]), int8_result<T>(hi[i])};
+                        if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(y + 2 * i * a.ldy) = *reinterpret_cast<const uint32_t*>(u);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (c0 + 2 * i + odd < live && (n & ~1) < N) y[2 * i * a.ldy] = int8_result<T>(lo[i]);
+                        if (c0 + 2 * i + odd < live && (n | 1) < N) y[2 * i * a.ldy + 1] = int8_result<T>(hi[i]);
+                    }
+                }
+            } else if (all) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i * a.ldy] = int8_result<T>(f[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c0 + i < live && n < N) y[i * a.ldy] = int8_result<T>(f[i]);
+            }
+        }
+    }
+    return true;
+}
 
 template <typename T, bool GATED, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_constant__ MmaArgs args) {
@@ -145,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
     const int rank = PAIR ? (int)cluster_rank() : 0, cta = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
     const int KT = (int)((a.K + 63) / 64), KS = (KT + 1) / 2;
     const int NT128 = (int)((a.N + 127) / 128), NT = PAIR ? (NT128 + 1) / 2 : NT128;
-    const Work<PAIR> work = {s, a.offsets ? -1 : a.M, NT, a.E, KS, args.most, PAIR ? (int)gridDim.x / 2 : (int)gridDim.x};
+    const Work<PAIR> work(s, args);
 
     if (warp == kCopyWarp) {
         if (lane < S) {
@@ -161,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
     }
     if (threadIdx.x == 0) {
         mbar_init(&s.epilogue, kEpiWarps);
+        mbar_init(&s.all, kCopyWarp);
         mbar_init(&s.parts, 1);
         mbar_init(&s.done, 1);
         s.abort = 0;
@@ -228,12 +428,15 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
                 x = reinterpret_cast<const uint8_t*>(a.x) + 2 * p.k * x_step + row * 128;
                 return n * 128;
             };
-            int head = 0;  // steps whose weights are on their way and whose activations are not
+            int head = 0, tail = 0;  // steps whose weights are on their way, and whose activations are too
             bool ok = true;
             if (args.early) {  // the first steps' weights, before the activations are there
+                const uint8_t* x0 = nullptr;  // of the first part
+                int bytes0 = 0, k0 = 0, steps0 = 0;
                 work.each(cta, [&](const Part& p) {
                     const uint8_t *w, *x;
                     const int bytes = sources(p, w, x);
+                    if (head == 0) x0 = x, bytes0 = bytes, k0 = p.k, steps0 = p.k1 - p.k;
                     for (int k = p.k; k < p.k1; ++k, w += 2 * kInt8Tile, ++head) {
                         if (head == S) return false;
                         const int tiles = min(2, KT - 2 * k);
@@ -243,6 +446,11 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
                     return true;
                 });
                 pdl_wait();
+                for (; tail < min(head, steps0); ++tail, x0 += 2 * x_step) {
+                    const uint32_t to = ring0 + tail * args.stage_bytes;
+                    bulk_copy(to, x0, bytes0, full0 + 8 * tail);
+                    if (2 * (k0 + tail) + 1 < KT) bulk_copy(to + args.x_bytes, x0 + x_step, bytes0, full0 + 8 * tail);
+                }
             }
             int it = 0;
             work.each(cta, [&](const Part& p) {
@@ -256,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
                         expect_bytes(bar, tiles * (kInt8Tile + bytes));
                         bulk_copy(to + 2 * args.x_bytes, w, tiles * kInt8Tile, bar);
                     }
+                    if (it < tail) continue;
                     bulk_copy(to, x, bytes, bar);
                     if (tiles == 2) bulk_copy(to + args.x_bytes, x + x_step, bytes, bar);
                 }
@@ -297,8 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
         const unsigned char* w0 = ring + 2 * args.x_bytes + (set & 1) * kInt8Tile + (32 * q + lane) * 16;
         const uint32_t slot = tmem + ((uint32_t)(32 * q) << 16) + kSlotBase + set * kSlotCols;
         Turn t(S), old(S);  // the step; the one before the last
-        int it = 0;
+        int it = 0, tile = 0;
         work.each(cta, [&](const Part& p) {
+            // (of every tile but the last two: below, a phase that nobody waited for could be taken for the last part's)
+            if (tile >= 2 && !mbar_wait_warp(&s.acc_full[tile & 1], ((tile >> 1) - 1) & 1, &s.abort, status)) return false;
+            ++tile;
             for (int k = p.k; k < p.k1; ++k, ++it, t.next()) {
                 if (it >= 3) old.next();
                 // (of every step: a barrier's phase that nobody waits for could be taken for the one after the next)
@@ -321,182 +533,48 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
             return true;
         });
     } else {
-        const int q = warp & 3;
         if (args.early) pdl_wait();
         pdl_launch_dependents();
-        uint32_t turn = 0, parts = 0, shares = 0;
-        auto epilogue_sync = [&] {  // of the epilogue's warps; bounded, like every wait
+        uint32_t turn = 0;
+        auto sync = [&] {  // of the epilogue's warps; bounded, like every wait
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.epilogue);
             return mbar_wait_warp(&s.epilogue, turn++ & 1, &s.abort, status);
         };
-        const bool pairs = sizeof(T) == 2 && reinterpret_cast<uintptr_t>(a.y) % 4 == 0 && a.ldy % 2 == 0;
-        const bool speaker = threadIdx.x == 32 * kConvWarps;
         int tile = 0;
         work.each(cta, [&](const Part& p) {
-            const int b = tile & 1;
-            const int64_t m0 = (int64_t)p.mt * p.r.n;
-            const int live = (int)min((int64_t)p.r.n, p.r.count - m0);
-            const float* const sx = a.sx + (a.offsets ? int8_first_row(s.offset[p.e], p.e) : 0) + m0;
-            const int n0 = (PAIR ? 2 * p.nt + rank : p.nt) * 128 + 32 * q, n = n0 + lane, N = (int)a.N;  // (N is at most 2^28)
-            const float sw = n < N ? __ldg(a.sw + (int64_t)p.e * a.N + n) : 0.f;
-            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + b * kMostRows;
-            __syncwarp();
-#pragma unroll
-            for (int c0 = 0; c0 < kMostRows; c0 += 32)
-                if (c0 + lane < live) s.sx[q][c0 + lane] = __ldcg(sx + c0 + lane);
-            if (!mbar_wait_warp(&s.acc_full[b], (tile >> 1) & 1, &s.abort, status)) return false;
-            tc_fence_after();
-            int first = cta, last = cta;  // the CTAs that share the tile
-            bool mine = true;
-            // The partial sums of a CTA, [16 activation rows][4][128][4]: of the tile that it begins, or (1) goes on with.
-            auto slot = [&](int c) {
-                return a.partials + (((int64_t)c * (PAIR ? 2 : 1) + rank) * 2 + (c > first)) * 128 * args.slot_rows;
-            };
-            if (p.k > 0 || p.k1 < KS) {
-                work.sharers(p.id, first, last);
-                unsigned* const count = &a.ctrl->int8_split[first * (PAIR ? 2 : 1) + rank];
-                volatile int* const verdict = &s.last[shares++ & 1];
-                // the last CTA to arrive adds the others' sums to its own; where the others are there already, it need not store them
-                if (speaker) *verdict = ld_acquire(count) == (unsigned)(last - first);
-                if (!epilogue_sync()) return false;
-                mine = *verdict != 0;
-                if (!mine) {
-                    float4* to = reinterpret_cast<float4*>(slot(cta)) + 32 * q + lane;
-                    for (int c0 = 0; c0 < live; c0 += 16, to += 4 * 128) {  // (slots have room for whole sixteens)
-                        uint32_t v[16];
-                        tmem_ld16(acc + c0, v);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            __stcg(to + i * 128, make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                                             __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
-                    }
-                    __threadfence();
-                    if (!epilogue_sync()) return false;
-                    if (speaker) {
-                        *verdict = atomicAdd(count, 1u) == (unsigned)(last - first);
-                        __threadfence();
-                    }
-                    if (!epilogue_sync()) return false;
-                    mine = *verdict != 0;
-                }
-                if (mine && speaker) *count = 0;  // (every one of them has arrived)
-            }
-            if (mine) {
-                const bool odd = lane & 1, whole = n0 + 32 <= N;
-                T* y = static_cast<T*>(a.y) + ((a.offsets ? s.offset[p.e] : 0) + m0) * a.ldy;
-                if constexpr (GATED) y += odd * a.ldy + n / 2;
-                else y += pairs ? odd * a.ldy + (n & ~1) : n;
-                // Others' sums: in the CTA's last part (most often it is that) through the ring, which nothing uses any more, as many rows at a
-                // time as fit; else straight from memory.
-                const int others = last - first, ring_rows = p.last && others > 0 ? S * args.stage_bytes / (others * 512) / 16 * 16 : 0;
-                int have = 0, begin = 0;  // rows begin .. have - 1 are in the ring
-#pragma unroll 1
-                for (int c0 = 0; c0 < live; c0 += 16, y += 16 * a.ldy) {
-                    if (ring_rows > 0 && c0 == have) {
-                        begin = c0, have = min(c0 + ring_rows, (live + 15) / 16 * 16);
-                        if (!epilogue_sync()) return false;  // what was there has been read
-                        if (speaker) {
-                            const int bytes = (have - begin) * 512;
-                            asm volatile("fence.proxy.async;" ::: "memory");
-                            expect_bytes(smem_u32(&s.parts), others * bytes);
-                            uint32_t to = smem_u32(ring);
-                            for (int c = first; c <= last; ++c)
-                                if (c != cta) bulk_copy(to, slot(c) + c0 * 128, bytes, smem_u32(&s.parts)), to += bytes;
-                        }
-                        __syncwarp();
-                        if (!mbar_wait_warp(&s.parts, parts++ & 1, &s.abort, status)) return false;
-                    }
-                    uint32_t v[16];
-                    tmem_ld16(acc + c0, v);
-                    tmem_ld_wait();
-                    if (others > 0) {
-                        float4 sum[4] = {};
-                        const float4* h = reinterpret_cast<const float4*>(ring) + (c0 - begin) * 32 + 32 * q + lane;
-                        for (int c = first; c <= last; ++c) {
-                            float4 o[4];
-                            if (c == cta) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    o[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
-                                                       __uint_as_float(v[4 * i + 3]));
-                            } else if (ring_rows > 0) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) o[i] = h[i * 128];
-                                h += (have - begin) * 32;
-                            } else {
-                                const float4* const g = reinterpret_cast<const float4*>(slot(c)) + c0 * 32 + 32 * q + lane;
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) o[i] = __ldcg(g + i * 128);
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) sum[i].x += o[i].x, sum[i].y += o[i].y, sum[i].z += o[i].z, sum[i].w += o[i].w;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            v[4 * i] = __float_as_uint(sum[i].x), v[4 * i + 1] = __float_as_uint(sum[i].y);
-                            v[4 * i + 2] = __float_as_uint(sum[i].z), v[4 * i + 3] = __float_as_uint(sum[i].w);
-                        }
-                    }
-                    float f[16];
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 g = *reinterpret_cast<const float4*>(&s.sx[q][c0 + i]);
-                        f[i] = __uint_as_float(v[i]) * g.x * sw;
-                        f[i + 1] = __uint_as_float(v[i + 1]) * g.y * sw;
-                        f[i + 2] = __uint_as_float(v[i + 2]) * g.z * sw;
-                        f[i + 3] = __uint_as_float(v[i + 3]) * g.w * sw;
-                    }
-                    const bool all = whole && c0 + 16 <= live;  // (of the warp)
-                    if (GATED || pairs) {
-                        // lanes 2 i and 2 i + 1 exchange: the even one gets both weight rows of row i, the odd one of row i + 1
-                        float lo[8], hi[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float got = __shfl_xor_sync(0xffffffffu, odd ? f[2 * i] : f[2 * i + 1], 1);
-                            lo[i] = odd ? got : f[2 * i], hi[i] = odd ? f[2 * i + 1] : got;
-                        }
-                        if constexpr (GATED) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) lo[i] = int8_gated(lo[i], hi[i]);
-                            if (all) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) y[2 * i * a.ldy] = int8_result<T>(lo[i]);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    if (c0 + 2 * i + odd < live && n < N) y[2 * i * a.ldy] = int8_result<T>(lo[i]);
-                            }
-                        } else if (all) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const T u[2] = {int8_result<T>(lo[i]), int8_result<T>(hi[i])};
-                                if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(y + 2 * i * a.ldy) = *reinterpret_cast<const uint32_t*>(u);
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                if (c0 + 2 * i + odd < live && (n & ~1) < N) y[2 * i * a.ldy] = int8_result<T>(lo[i]);
-                                if (c0 + 2 * i + odd < live && (n | 1) < N) y[2 * i * a.ldy + 1] = int8_result<T>(hi[i]);
-                            }
-                        }
-                    } else if (all) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i * a.ldy] = int8_result<T>(f[i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c0 + i < live && n < N) y[i * a.ldy] = int8_result<T>(f[i]);
-                    }
-                }
-            }
+            if (p.last) return false;
+            if (!finish<T, GATED, PAIR>(args, s, ring, work, tmem, p, tile, 0, 1, s.sx[warp & 3], &s.last[tile & 1], sync)) return false;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive<PAIR>(&s.acc_empty[b]);
+            if (lane == 0) arrive<PAIR>(&s.acc_empty[tile & 1]);
             ++tile;
             return true;
         });
+    }
+    // The CTA's last part is finished by the converting warps too, which have nothing else to do then: five warps a lane quarter.
+    if (warp < kCopyWarp) {
+        __syncwarp();
+        // (Everything it needs is found again from here: what lives on until here costs the loops above registers.)
+        const MmaArgs* args2 = &args;
+        unsigned char* raw2 = smem_raw;
+        asm volatile("" : "+l"(args2), "+l"(raw2));
+        unsigned char* const ring2 = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw2) + 1023) & ~uintptr_t(1023));
+        Shared& s2 = *reinterpret_cast<Shared*>(ring2 + (size_t)args2->stages * args2->stage_bytes);
+        const Work<PAIR> work2(s2, *args2);
+        Part p;
+        const int tile = work2.last(PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, p), part = (int)threadIdx.x >> 7;
+        if (tile >= 0 && !s2.abort) {
+            if (args2->early && part < kSets) pdl_wait();
+            uint32_t turn = 0;
+            auto sync = [&] {
+                __syncwarp();
+                if (threadIdx.x % 32 == 0) mbar_arrive(&s2.all);
+                return mbar_wait_warp(&s2.all, turn++ & 1, &s2.abort, &args2->p.ctrl->status);
+            };
+            finish<T, GATED, PAIR>(*args2, s2, ring2, work2, s2.tmem, p, tile, part, kCopyWarp / 4, s2.sx[4], &s2.last[2], sync);
+            tc_fence_before();
+        }
     }
     __syncwarp();
     {

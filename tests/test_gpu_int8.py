@@ -29,6 +29,8 @@ def scales(g, *shape):
 SHAPES = [(1, 1, 1), (1, 130, 64), (1, 4096, 2048), (2, 7, 63), (3, 128, 65), (4, 256, 128), (5, 100, 1000), (8, 1000, 320), (16, 129, 777),
           (17, 64, 64), (33, 300, 130), (64, 512, 1024), (100, 333, 500), (129, 257, 192), (256, 128, 4096), (257, 384, 320), (300, 1001, 1543),
           (520, 640, 512), (1000, 2000, 96), (2100, 1300, 700)]
+# whole tiles and shared ones behind them, in one CTA and in several, and products whose last tiles alone are shared
+MANY = [(1100, 4100, 2100), (2500, 5000, 1500), (450, 9000, 4096), (3500, 2000, 3300)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -38,6 +40,18 @@ def test_linear(M, N, K, dtype):
     x, wq, ws = acts(g, M, K, dtype), whole(g, N, K), scales(g, N)
     y = ops.int8_linear(x, ops.int8_weights(wq, ws), ops.int8_workspace(M, N, K))
     assert y.dtype == dtype and torch.equal(y, R.product(*R.numbers(x), wq, ws, dtype))
+
+
+@pytest.mark.parametrize("M,N,K", MANY)
+def test_more_tiles_than_ctas(M, N, K):
+    g = gen(M + N + K)
+    x, wq, ws = acts(g, M, K, torch.bfloat16), whole(g, N, K), scales(g, N)
+    W, space = ops.int8_weights(wq, ws), ops.int8_workspace(M, N, K)
+    want = R.product(*R.numbers(x), wq, ws, torch.bfloat16)
+    for _ in range(3):
+        assert torch.equal(ops.int8_linear(x, W, space), want)
+    y, bound = R.gated_bound(R.product(*R.numbers(x), wq, ws, torch.float32), torch.bfloat16)
+    assert ((ops.int8_linear(x, W, space, gated=True).double() - y).abs() <= bound).all()
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -144,6 +158,25 @@ def test_results_in_another_type():
         want = R.product(*R.numbers(x), wq, s, dtype)
         assert torch.equal(ops.int8_matmul(ops.int8_quantize(x), W, dtype, ws), want)
         assert torch.equal(ops.int8_linear(x, W, ws, out=torch.empty(20, 30, dtype=dtype, device="cuda")), want)
+
+
+def test_experts_of_many_tiles():
+    """Whole and shared tiles of experts of every size, with single CTAs and with pairs."""
+    g = gen(12)
+    for counts in ([700, 0, 30, 1, 900, 200], [5] * 60 + [0, 300, 77]):
+        E, N, K = len(counts), 1300, 2100
+        ids, order = sorted_order(counts)
+        M = len(ids)
+        x, wq, ws = acts(g, M, K, torch.bfloat16), whole(g, E, N, K), scales(g, E, N)
+        W, space = ops.int8_weights(wq, ws), ops.int8_workspace(M, N, K)
+        q, s = R.numbers(x)
+        want = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        for e in range(E):
+            t = (ids.view(-1) == e).nonzero().view(-1)
+            want[order.inv.view(-1)[t].long()] = R.product(q[t], s[t], wq[e], ws[e], torch.bfloat16)
+        rows = ops.int8_quantize(x, order)
+        for _ in range(2):
+            assert torch.equal(ops.int8_matmul(rows, W, torch.bfloat16, space), want)
 
 
 COUNTS = [[1], [0, 0, 1], [1] * 8, [3, 0, 5, 1, 0, 2], [0, 40, 0, 7], [300, 0, 1, 17, 256, 257, 0], [16, 15, 17, 128, 129], [0, 0]]

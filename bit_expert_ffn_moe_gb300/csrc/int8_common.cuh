@@ -27,7 +27,7 @@ __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(
 
 struct Scale {
     float s, inverse;
-    bool bad;
+    bool bad, sure;  // with a NaN or an infinity; neither the scale nor remainders lose bits to the range
 };
 __device__ __forceinline__ Scale scale_of(uint32_t most) {
     Scale r;
@@ -35,6 +35,7 @@ __device__ __forceinline__ Scale scale_of(uint32_t most) {
     r.s = __fdiv_rn(__uint_as_float(most), 127.f);
     if (!(r.s > 0.f)) r.s = 1.f;
     r.inverse = 1.f / r.s;
+    r.sure = !r.bad && r.s > 0x1p-80f && r.s < 0x1p100f;
     if (r.bad) r.s = __uint_as_float(0x7fffffffu);
     return r;
 }
@@ -42,20 +43,20 @@ __device__ __forceinline__ Scale scale_of(uint32_t most) {
 static __device__ __noinline__ float whole(float v, float s, bool bad) {
     return bad ? 0.f : fminf(fmaxf(rintf(__fdiv_rn(v, s)), -127.f), 127.f);
 }
-// The same of eight values.  The product with the reciprocal is within 127 x 2^-22 of the quotient, so it decides wherever it is further
-// than that from a half; elsewhere (and where the reciprocal is infinite or the row bad: their differences are not numbers) the
-// division does.  Adding 1.5 x 2^23 rounds to a whole number, ties to even.
+// The same of eight values.  The product with the reciprocal (correctly rounded) is within two steps of the quotient; correcting it by its
+// remainder, which an fma gives, makes it one of the quotient's two neighbours, and correcting that once more the quotient rounded to
+// fp32 (Markstein 1990).  Quotients of 16-bit numbers are halves of whole numbers often enough that a test for these, with the division
+// behind it, took twice as long.  Adding 1.5 x 2^23 rounds to a whole number, ties to even.
 __device__ __forceinline__ void whole8(const float (&v)[8], const Scale& s, float (&q)[8]) {
-    float off = 0.f;
-    bool sure = true;
+    if (s.sure) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float t = v[i] * s.inverse;
-        q[i] = (t + 12582912.f) - 12582912.f;
-        off = fmaxf(off, fabsf(t - q[i]));
-        sure = sure && fabsf(t) < 127.25f;  // (false for NaN)
-    }
-    if (!(sure && off < 0.4999f)) {
+        for (int i = 0; i < 8; ++i) {
+            float t = v[i] * s.inverse;
+            t = fmaf(fmaf(-t, s.s, v[i]), s.inverse, t);
+            t = fmaf(fmaf(-t, s.s, v[i]), s.inverse, t);
+            q[i] = (t + 12582912.f) - 12582912.f;
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) q[i] = whole(v[i], s.s, s.bad);
     }
@@ -69,6 +70,28 @@ template <>
 __device__ __forceinline__ float value<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <>
 __device__ __forceinline__ float value<__half>(__half v) { return __half2float(v); }
+
+// The larger of the magnitudes in m and the magnitude of w, of 16-bit numbers in both halves; NaN above all.
+template <typename T>
+__device__ __forceinline__ uint32_t larger(uint32_t m, uint32_t w);
+template <>
+__device__ __forceinline__ uint32_t larger<float>(uint32_t m, uint32_t w) { return max(m, w & 0x7fffffffu); }
+template <>
+__device__ __forceinline__ uint32_t larger<__nv_bfloat16>(uint32_t m, uint32_t w) {
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t larger<__half>(uint32_t m, uint32_t w) {
+    const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&m), __habs2(*reinterpret_cast<const __half2*>(&w)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <typename T>
+__device__ __forceinline__ float2 two(uint32_t w);
+template <>
+__device__ __forceinline__ float2 two<__nv_bfloat16>(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+template <>
+__device__ __forceinline__ float2 two<__half>(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
 // Values c .. c + 7 of a row of K as they come, zeros behind its end.  WIDE: rows that start on 16 bytes.
 template <typename T>
@@ -109,23 +132,25 @@ struct Eight {
     // The larger of `most` and its magnitudes; 16-bit ones in halves.
     __device__ __forceinline__ uint32_t most(uint32_t m) const {
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) m = sizeof(T) == 4 ? max(m, w[i] & 0x7fffffffu) : __vmaxu2(m, w[i] & 0x7fff7fffu);
+        for (int i = 0; i < kWords; ++i) m = larger<T>(m, w[i]);
         return m;
     }
     // That of a row, as the bits of an fp32 number (NaN above infinity above all numbers).
     __device__ __forceinline__ static uint32_t as_fp32(uint32_t m) {
         if constexpr (sizeof(T) == 4) return m;
-        const uint16_t b = (uint16_t)max(m & 0xffffu, m >> 16);
-        return __float_as_uint(value<T>(*reinterpret_cast<const T*>(&b))) & 0x7fffffffu;
+        else {
+            const float2 v = two<T>(m);
+            return max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu);
+        }
     }
     __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kWords; ++i) {
             if constexpr (sizeof(T) == 4) {
                 f[i] = __uint_as_float(w[i]);
             } else {
-                const uint16_t b = (uint16_t)(w[i / 2] >> (16 * (i % 2)));
-                f[i] = value<T>(*reinterpret_cast<const T*>(&b));
+                const float2 v = two<T>(w[i]);
+                f[2 * i] = v.x, f[2 * i + 1] = v.y;
             }
         }
     }

@@ -38,9 +38,12 @@ __device__ __forceinline__ int expert_of(const int32_t* offsets, int E, int r) {
 
 // `warps` warps of a CTA share a row; it is read once into registers (its first kKept pieces per thread; what is longer is read
 // again), quantised, and written to the rows that it goes to.  Bound by the writing of k rows in 16 bits; for few rows by its chain of
-// loads, so the row's, the offsets' and its places' are all in flight together.
+// loads, so the row's, the offsets' and its places' are all in flight together.  4096 x 8192 in bf16: 29.3 us (4.6 TB/s), in fp32 34.4 us
+// (5.9 TB/s), to 8 rows each 98 us (6.2 TB/s); 16 x 4096: 2.2 us.  Wide loads of 16-bit numbers run with 5 CTAs on an SM (48 registers; with
+// 4, 31.2 us); fp32 with 4, since 48 registers do not hold its pieces (with 5, 45.0 us), and so do loads of single numbers (2000 x 1543 in
+// bf16: 6.8 us with 4, 7.6 with 5).
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 4) int8_rows_kernel(const Int8RowsArgs a, const int warps) {
+__global__ void __launch_bounds__(kThreads, WIDE && sizeof(T) == 2 ? 5 : 4) int8_rows_kernel(const Int8RowsArgs a, const int warps) {
     __shared__ uint32_t part[kThreads / 32];
     __shared__ int64_t to_smem[kThreads / 32][kMaxK];
     extern __shared__ int32_t offsets[];  // [E + 1]
@@ -153,8 +156,9 @@ __global__ void __launch_bounds__(kThreads) int8_pack_kernel(const Int8PackArgs 
 template <typename T>
 cudaError_t launch_rows(Int8RowsArgs a, cudaStream_t st) {
     const int pieces = (int)((a.K + 63) / 64 * 8);
+    // warps for a row: so many that they keep it; of few rows more, down to a piece a thread
     int warps = 1;
-    while (warps < kThreads / 32 && warps * 32 * kKept < pieces) warps *= 2;
+    while (warps < kThreads / 32 && (warps * 32 * kKept < pieces || (warps * 32 < pieces && a.T * warps < (int64_t)sm_count() * 8))) warps *= 2;
     const int64_t rows = kThreads / 32 / warps;
     const bool wide = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.ld * (int64_t)sizeof(T)) % 16 == 0;
     const void* f = wide ? (const void*)int8_rows_kernel<T, true> : (const void*)int8_rows_kernel<T, false>;

@@ -382,8 +382,9 @@ moe_status moe_int8_quantize(const void* x, moe_dtype dtype, int64_t T, int64_t 
                              const int32_t* offsets, int E, const moe_int8_rows* rows, moe_stream_t stream) {
     if (dtype_size(dtype) == 0 || (inv && !offsets) || (offsets ? !experts_ok(E) : E != 0)) return MOE_ERR_INVALID_ARG;
     if (inv && (k < 1 || k > kMaxK)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T < 0 || T > kMaxDim) return MOE_ERR_UNSUPPORTED_SHAPE;
     const int64_t M = inv ? T * k : T;
-    if (T < 0 || T > kMaxDim || M > kMaxDim || !int8_ok(M, K)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (M > kMaxDim || !int8_ok(M, K)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return MOE_OK;
     if (ldx < K) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (!matrix_ok(x, dtype, K, ldx) || !words(inv, offsets)) return MOE_ERR_INVALID_ARG;

@@ -156,6 +156,11 @@ struct Eight {
     }
 };
 
+// Where expert e's rows start; offsets of other rows than these lead nowhere outside them.
+__device__ __forceinline__ int64_t int8_offset(const Int8ProductArgs& a, int e) {
+    return min(max((int64_t)__ldcg(a.offsets + e), (int64_t)0), a.M);
+}
+
 // Few rows: of the operand, or, where x is not null, [M][ldx] of x_dtype, quantised by every CTA for itself (K at most kInt8DotK).
 constexpr int kInt8DotK = 16384;
 cudaError_t launch_int8_dot(const Int8ProductArgs& a, moe_dtype dtype, bool gated, const void* x, moe_dtype x_dtype, int64_t ldx,

@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_dot_kernel(const Int8Product
         int n = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + lane;
-            const bool has = e < a.E && (a.offsets ? __ldcg(a.offsets + e + 1) > __ldcg(a.offsets + e) : a.M > 0);
+            const bool has = e < a.E && (a.offsets ? int8_offset(a, e + 1) > int8_offset(a, e) : a.M > 0);
             const unsigned b = __ballot_sync(0xffffffffu, has);
             if (has) s.active[n + __popc(b & ((1u << lane) - 1u))] = e;
             n += __popc(b);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_dot_kernel(const Int8Product
         const int e = s.active[at / NP];
         const int64_t n0 = 2 * (at % NP), n1 = min(min(a.N, n0 + 2 * (end - at)), n0 + kRows);
         at += (n1 - n0 + 1) / 2;
-        const int64_t first = a.offsets ? __ldcg(a.offsets + e) : 0, count = a.offsets ? __ldcg(a.offsets + e + 1) - first : a.M;
+        const int64_t first = a.offsets ? int8_offset(a, e) : 0, count = a.offsets ? int8_offset(a, e + 1) - first : a.M;
         const int64_t row0 = a.offsets ? int8_first_row(first, e) : 0;
         for (int64_t t0 = 0; t0 < count; t0 += kTokens) {
             const int tokens = (int)min((int64_t)kTokens, count - t0);

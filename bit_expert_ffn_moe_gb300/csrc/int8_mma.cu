@@ -382,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
             const int e = e0 + lane;
             int64_t first = 0, count = 0;
             if (e < a.E) {
-                first = a.offsets ? __ldcg(a.offsets + e) : 0;
-                count = a.offsets ? __ldcg(a.offsets + e + 1) - first : a.M;
+                first = a.offsets ? int8_offset(a, e) : 0;
+                count = a.offsets ? max(int8_offset(a, e + 1) - first, (int64_t)0) : a.M;
             }
             const int own = rows_of(count, args.most).mt * NT;
             int incl = own;

@@ -40,10 +40,12 @@ moe_dtype dtype_of(const at::Tensor& t, const char* what) {
 }
 
 // Kernels run on the current device and its current stream: a tensor of another device is refused.
-void here(const at::Tensor& t, const char* what) {
+int current_device() {
     c10::DeviceIndex current = -1;
-    if (c10::cuda::GetDevice(&current) != cudaSuccess) current = -1;
-    if (!t.is_cuda() || t.get_device() != current) refuse(PyExc_ValueError, what, "on another device than the current one");
+    return c10::cuda::GetDevice(&current) == cudaSuccess ? current : -1;
+}
+void here(const at::Tensor& t, const char* what) {
+    if (!t.is_cuda() || t.get_device() != current_device()) refuse(PyExc_ValueError, what, "on another device than the current one");
 }
 
 // Row stride of a 2-D CUDA tensor whose rows are contiguous and do not overlap.
@@ -436,6 +438,7 @@ int64_t columns8(const Weights8& W, bool gated) {
 PyObject* int8_room(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 4, [&]() -> PyObject* {
         const int64_t M = integer(a[0]), K = integer(a[2]);
+        if (integer(a[3]) != current_device()) refuse(PyExc_ValueError, "x", "on another device than the current one");
         const int64_t room = moe_int8_rows_room(M, narrow(integer(a[1]), "E"));
         const int64_t bytes = (int64_t)moe_int8_rows_bytes(room, K);
         if (K < 1 || (bytes == 0 && M != 0)) refuse(PyExc_ValueError, "x", "unsupported shape");

@@ -287,6 +287,7 @@ def int8_weights(w: torch.Tensor, scales: Optional[torch.Tensor] = None, up: Opt
     E, (N, K) = (1 if w.dim() == 2 else w.shape[0]), w.shape[-2:]
     bytes_ = B.moe_int8_weights_bytes(N * len(parts), K)
     _need(bytes_ > 0 and N > 0 and E > 0, "unsupported shape %s" % (tuple(w.shape),))
+    _need(up is not None or up_scales is None, "up_scales without up")
     W = Int8Weights(N * len(parts), K, torch.empty(E * bytes_, dtype=torch.uint8, device=w.device),
                     torch.empty(E * N * len(parts), dtype=torch.float32, device=w.device))
     for i, (m, s) in enumerate(parts):

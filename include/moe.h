@@ -576,10 +576,10 @@ moe_status moe_experts_to_tokens_backward(const void* dy, moe_dtype dtype, int64
  * shared experts, and sparse layers whose experts come in this format.
  *   A row v is held as s = max |v| / 127 (1 for a row of zeros) and whole numbers q = v / s rounded to the nearest, ties to even,
  * within -127 .. 127, each step rounded to fp32; a row of x with a NaN or an infinity gives a row of NaN.
- *   y[m][n] = (sum_k qx[m][k] qw[n][k]) * sx[m] * sw[n]: the sum is exact up to 2^24 (always for K <= 1040) and rounded to fp32
+ *   y[m][n] = (sum_k qx[m][k] qw[n][k]) * sx[m] * sw[n]: the sum is exact up to 2^24 (always for K <= 1032) and rounded to fp32
  * beyond, the two products are in fp32, the result is rounded once to y's type.
  *   gated: rows 2 i and 2 i + 1 of W are the gate and the up row of channel i, and y [M][N/2] is silu(gate) * up (N even).
- * 1 <= K <= 131072. */
+ * 1 <= K <= 131072.  Weights given as whole numbers may hold -128 too.  y may not overlap what is read. */
 
 /* One matrix [N][K], or those of E experts, one behind the other: tiles of 128 rows x 64 values (rows and K padded), tile (R, C) of a
  * matrix at index R*ceil(K/64) + C, value (r, c) of a tile at byte (c/16)*2048 + r*16 + c%16. */
@@ -618,7 +618,7 @@ moe_status moe_int8_quantize(const void* x, moe_dtype dtype, int64_t T, int64_t 
 size_t moe_int8_workspace_size(int64_t M, int64_t N, int64_t K);
 
 /* y [M][ldy] of rows and W: of all M rows with one matrix (offsets NULL, E = 0), or of rows offsets[e] .. offsets[e+1] - 1 with
- * matrix e (M: the rows at most; rows of y from offsets[E] on are left as they are). */
+ * matrix e (M: the rows at most, offsets beyond it count as M; rows of y from offsets[E] on are left as they are). */
 moe_status moe_int8_matmul(const moe_int8_rows* rows, const int32_t* offsets, int E, int64_t M, const moe_int8_weights* W, int64_t N,
                            int64_t K, int gated, void* y, moe_dtype dtype, int64_t ldy, void* ws, size_t ws_bytes,
                            moe_stream_t stream);

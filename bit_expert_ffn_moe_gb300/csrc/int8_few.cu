@@ -177,6 +177,13 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const __grid_cons
     __syncwarp();
     pdl_wait();
     pdl_launch_dependents();
+    // This lane's four weight rows, and this warp's activation rows: their scales are on their way while the last products run
+    const int n = nt * 128 + 4 * lane, N = (int)a.N;
+    float sw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sw[i] = n + i < N ? __ldg(a.sw + n + i) : 0.f;
+    int c = rank + splits * warp;
+    float sx = c < live ? __ldcg(a.sx + m0 + c) : 0.f;
     {
         // every product has completed: the commit comes, aborting or not
         volatile int never = 0;
@@ -204,14 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const __grid_cons
     } else {
         __syncthreads();
     }
-    const int n = nt * 128 + 4 * lane, N = (int)a.N;  // this lane's four weight rows
-    float sw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sw[i] = n + i < N ? __ldg(a.sw + n + i) : 0.f;
     const int64_t size = args.y_dtype == MOE_F32 ? 4 : 2;
     const bool wide = reinterpret_cast<uintptr_t>(a.y) % (4 * size) == 0 && a.ldy % 4 == 0;
-    for (int c = rank + splits * warp; c < live; c += splits * kWarps) {
-        const float sx = __ldcg(a.sx + m0 + c);
+    while (c < live) {
         const float* from = part + c * 128 + 4 * lane;
         float4 o[8];
 #pragma unroll
@@ -228,6 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const __grid_cons
             else if (args.y_dtype == MOE_BF16) store4<__nv_bfloat16, GATED>(a.y, row, n, N, v, wide);
             else store4<__half, GATED>(a.y, row, n, N, v, wide);
         }
+        c += splits * kWarps;
+        if (c < live) sx = __ldcg(a.sx + m0 + c);
     }
     if (splits > 1) {
         __syncwarp();

@@ -572,7 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
                 if (threadIdx.x % 32 == 0) mbar_arrive(&s2.all);
                 return mbar_wait_warp(&s2.all, turn++ & 1, &s2.abort, &args2->p.ctrl->status);
             };
-            finish<T, GATED, PAIR>(*args2, s2, ring2, work2, s2.tmem, p, tile, part, kCopyWarp / 4, s2.sx[4], &s2.last[2], sync);
+            // (the epilogue's warps, which have been waiting for the accumulators, take the first rows)
+            finish<T, GATED, PAIR>(*args2, s2, ring2, work2, s2.tmem, p, tile, (part + 1) % (kCopyWarp / 4), kCopyWarp / 4, s2.sx[4], &s2.last[2],
+                                   sync);
             tc_fence_before();
         }
     }
@@ -608,9 +610,9 @@ cudaError_t launch_int8_mma(const Int8ProductArgs& a, moe_dtype dtype, bool gate
     m.p = a;
     m.early = a.early;
     m.slot_rows = (int)(a.M > kMostRows ? kMostRows : (a.M + 15) / 16 * 16);
-    // By expert the ring has room for tiles of four times the mean (more of an expert's rows are several tiles): small ones leave
-    // room for more steps of weights on their way.
-    const int64_t rows = a.offsets && 4 * a.M / a.E + 16 < a.M ? 4 * a.M / a.E + 16 : a.M;
+    // By expert the ring has room for tiles of four times the mean, or 64 rows above it (more of an expert's rows are several tiles): small
+    // ones leave room for more steps of weights on their way.
+    const int64_t mean = a.M / a.E, cap = mean + (mean < 16 ? 3 * mean + 16 : 64), rows = a.offsets && cap < a.M ? cap : a.M;
     m.most = (int)(rows > kMostRows ? kMostRows : (rows + 15) / 16 * 16);
     m.x_bytes = m.most * 128 / (pair ? 2 : 1);
     m.x_bytes = (m.x_bytes + 1023) / 1024 * 1024;

@@ -465,14 +465,14 @@ moe_status moe_int8_experts(const void* x, moe_dtype dtype, int64_t ldx, const i
         Ctrl* ctrl = static_cast<Ctrl*>(ws);
         float* partials = reinterpret_cast<float*>(base + L.partials);
         cudaError_t e = launch_expert_order(ids, (int)P, E, offsets, inv, st);
-        if (e == cudaSuccess) e = launch_int8_rows({x, ldx, T, d, inv, k, offsets, E, L.room, xq, xs}, dtype, st);
         if (e == cudaSuccess)
-            e = launch_int8_product({up->q, up->s, xq, xs, L.room, offsets, E, P, 2 * (int64_t)I, d, base + L.h, I, ctrl, partials, 1}, dtype,
-                                    true, st);
-        if (e == cudaSuccess) e = launch_int8_rows({base + L.h, I, P, I, nullptr, 1, offsets, E, L.room, hq, hs}, dtype, st);
-        if (e == cudaSuccess)
-            e = launch_int8_product({down->q, down->s, hq, hs, L.room, offsets, E, P, d, I, base + L.rows, d, ctrl, partials, 1}, dtype, false,
-                                    st);
+            e = launch_int8_by_expert(x, ldx, T, inv, k, xq, xs, {up->q, up->s, nullptr, nullptr, L.room, offsets, E, P, 2 * (int64_t)I, d,
+                                                                  base + L.h, I, ctrl, partials, 0},
+                                      dtype, true, st);
+        if (e == cudaSuccess)  // (the kernel in front has waited for the order)
+            e = launch_int8_by_expert(base + L.h, I, P, nullptr, 1, hq, hs, {down->q, down->s, nullptr, nullptr, L.room, offsets, E, P, d, I,
+                                                                             base + L.rows, d, ctrl, partials, 1},
+                                      dtype, false, st);
         if (e == cudaSuccess)
             e = launch_expert_rows(false, dtype, nullptr, 0, base + L.rows, d, y, ldy, inv, w, nullptr, T, k, d, st);
         return e;

@@ -161,10 +161,11 @@ __device__ __forceinline__ int64_t int8_offset(const Int8ProductArgs& a, int e) 
     return min(max((int64_t)__ldcg(a.offsets + e), (int64_t)0), a.M);
 }
 
-// Few rows: of the operand, or, where x is not null, [M][ldx] of x_dtype, quantised by every CTA for itself (K at most kInt8DotK).
+// Few rows: of the operand, or, where x is not null, [..][ldx] of x_dtype, quantised by every CTA for itself (K at most kInt8DotK); with
+// inv [T][k], M = T k at most 32, row inv[t k + j] is row t of x.
 constexpr int kInt8DotK = 16384;
 cudaError_t launch_int8_dot(const Int8ProductArgs& a, moe_dtype dtype, bool gated, const void* x, moe_dtype x_dtype, int64_t ldx,
-                            cudaStream_t st);
+                            const int32_t* inv, int k, cudaStream_t st);
 // A few dozen rows with one matrix, where its tiles do not outnumber the SMs.
 bool int8_few_fits(const Int8ProductArgs& a);
 cudaError_t launch_int8_few(const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st);

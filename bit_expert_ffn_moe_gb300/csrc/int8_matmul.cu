@@ -11,14 +11,20 @@
 
 namespace moe {
 
-constexpr int kDotRows = 4;
+constexpr int kDotRows = 4, kDotExpertRows = 32;
+
+namespace {
+// Few rows, and not so many to an expert that their dot products take longer than the weights' way.
+bool few_by_expert(const Int8ProductArgs& a) { return a.M <= kDotExpertRows && a.M <= 8 * (int64_t)a.E; }
+}  // namespace
 
 cudaError_t launch_int8_product(const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st) {
     if (a.M == 0 || a.N == 0) return cudaSuccess;
-    // us for 4096 x 8192 weights, dot / few / mma with one CTA a tile / with pairs: 1 row 10.0 / 12.5 / 17.4 / 18.6, 4: 12.3 / 12.5, 16: 36 / 12.7 /
-    // 17.2 / 18.6, 128: 15.6 / 28.8 / 29.6, 512: 34.7 / 44.5 / 40.9, 4096: - / 220 / 161.  By expert, 128 of 4096 x 8192: 32 rows 147 / - / 155,
-    // 64: 264 / - / 246; one CTA a tile / pairs, a mean of 4 rows 593 / 592, 16: 704 / 647, 64: 1041 / 805.
-    if (a.M <= (a.offsets ? 32 : kDotRows)) return launch_int8_dot(a, dtype, gated, nullptr, MOE_F32, 0, st);
+    // us for 4096 x 8192 weights, dot / few / mma with one CTA a tile / with pairs: 1 row 10.2 / 12.0 / 17.4 / 18.6, 2: 10.9 / 12.0, 4: 12.5 / 12.0,
+    // 16: 36 / 12.0 / 17.2 / 18.6, 128: - / 15.0 / 28.8 / 29.6, 512: - / 34.4 / 44.5 / 40.9, 4096: - / - / 220 / 160.  By expert, 128 of 4096 x 8192: 32 rows 147 / - / 155,
+    // 64: 264 / - / 246; 2 of 2048 x 4096: 4 rows each 11.0 / - / 16.3, 15: 27.0 / - / 16.1; one CTA
+    // a tile / pairs, 128 experts and a mean of 4 rows 593 / 592, 16: 704 / 647, 64: 1041 / 805.
+    if (a.offsets ? few_by_expert(a) : a.M <= (int8_few_fits(a) ? 2 : kDotRows)) return launch_int8_dot(a, dtype, gated, nullptr, MOE_F32, 0, nullptr, 1, st);
     if (int8_few_fits(a)) return launch_int8_few(a, dtype, gated, st);
     return launch_int8_mma(a, dtype, gated, a.offsets ? a.M / a.E >= 16 : a.M > 128, st);
 }
@@ -26,8 +32,20 @@ cudaError_t launch_int8_product(const Int8ProductArgs& a, moe_dtype dtype, bool 
 cudaError_t launch_int8_linear(const void* x, moe_dtype x_dtype, int64_t ldx, uint16_t* q, float* s, const Int8ProductArgs& a, moe_dtype dtype,
                                bool gated, cudaStream_t st) {
     if (a.M == 0 || a.N == 0) return cudaSuccess;
-    if (a.M <= kDotRows && a.M * a.K <= kInt8DotK) return launch_int8_dot(a, dtype, gated, x, x_dtype, ldx, st);
+    if (a.M <= kDotRows && a.M * a.K <= kInt8DotK) return launch_int8_dot(a, dtype, gated, x, x_dtype, ldx, nullptr, 1, st);
     const cudaError_t e = launch_int8_rows({x, ldx, a.M, a.K, nullptr, 1, nullptr, 0, a.room, q, s}, x_dtype, st);
+    if (e != cudaSuccess) return e;
+    Int8ProductArgs p = a;
+    p.x = q, p.sx = s;
+    p.early = 1;  // (the rows' kernel has waited for what was in front of it)
+    return launch_int8_product(p, dtype, gated, st);
+}
+
+cudaError_t launch_int8_by_expert(const void* x, int64_t ldx, int64_t T, const int32_t* inv, int k, uint16_t* q, float* s,
+                                  const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st) {
+    // Without kernels of the rows' own the layer of a token with 8 of 128 experts of 8192 x 2048 takes 79.1 us instead of 83.4.
+    if (few_by_expert(a) && a.K <= kInt8DotK) return launch_int8_dot(a, dtype, gated, x, dtype, ldx, inv, k, st);
+    const cudaError_t e = launch_int8_rows({x, ldx, T, a.K, inv, k, a.offsets, a.E, a.room, q, s}, dtype, st);
     if (e != cudaSuccess) return e;
     Int8ProductArgs p = a;
     p.x = q, p.sx = s;

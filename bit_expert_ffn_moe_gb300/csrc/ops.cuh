@@ -112,4 +112,8 @@ cudaError_t launch_int8_product(const Int8ProductArgs& a, moe_dtype dtype, bool 
 // sw were there before the kernel in front started its dependents.
 cudaError_t launch_int8_linear(const void* x, moe_dtype x_dtype, int64_t ldx, uint16_t* q, float* s, const Int8ProductArgs& a, moe_dtype dtype,
                                bool gated, cudaStream_t st);
+// The same by expert, of T rows x of the results' type: tokens that go to the rows inv [T][k] in expert order, or (inv null) rows in that
+// order.  a.early as above, and for a.offsets.
+cudaError_t launch_int8_by_expert(const void* x, int64_t ldx, int64_t T, const int32_t* inv, int k, uint16_t* q, float* s,
+                                  const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st);
 }  // namespace moe

@@ -318,3 +318,18 @@ def test_example_runs():
     losses = example.tune(layer, x, torch.zeros_like(x), 3, 0.1)
     assert len(losses) == 3 and all(v == v and v < float("inf") for v in losses)
     assert B.moe_get_device_status(layer.experts.workspace) == B.MOE_OK
+
+
+@pytest.mark.parametrize("T,k,d,E,I,kind", [(1, 8, 640, 128, 96, "distinct"), (4, 8, 300, 16, 130, "any"), (31, 1, 129, 4, 64, "dropped"),
+                                            (30, 1, 256, 2, 64, "any"), (16, 2, 16500, 8, 40, "any"), (2, 4, 200, 5, 16500, "distinct"),
+                                            (32, 1, 64, 1024, 7, "any"), (5, 3, 1000, 1, 33, "any")])
+def test_a_few_pairs_are_the_products_of_their_parts(T, k, d, E, I, kind):  # noqa: E741
+    """The layer quantises the rows of a few pairs within its products (up to 16384 values a row): the results are those of the parts."""
+    g = gen(24)
+    up, down = experts(g, E, d, I)
+    ids, w = routing(T, k, E, 25, kind)
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        x = torch.randn(T, d + 3, generator=g, device="cuda").to(dtype)[:, 1:d + 1]
+        layer = Int8Experts(up, down, T, k, dtype)
+        rows, order = layer.outputs(x, ids)
+        assert torch.equal(layer(x, ids, w), ops.experts_to_tokens(rows, order, w)), dtype

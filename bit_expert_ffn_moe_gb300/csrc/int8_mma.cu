@@ -6,10 +6,12 @@
 //   warps 0-15   conversion: four sets of four warps, each a quarter of the tiles of 64 values
 //   warps 16-19  epilogue: accumulators (two, so that the next tile's products run meanwhile), scales, store; of the CTA's last
 //                part all twenty warps (1024 x 4096 x 8192: 76 us with four, 59 with twenty)
-//   warp 20      copies: three bulk copies a step of 128 values
-//   warp 21      products
+//   warp 20      copies of weights, one a step of 128 values; a step's place is free once it is converted
+//   warp 21      copies of activations, two a step; a step's place is free once its products are done
+//   warp 22      products
+// (Weights come from memory and activations mostly from L2, so weights have the longer ring.  With one ring for both, YYY)
 // PAIR: two CTAs share a tile of 256 weight rows (cta_group::2), each with half of the activation rows in its shared memory; the
-// leader (rank 0) issues the products of both.
+// leader (rank 0) issues the products of both, and the other's warp 22 passes on that its activations are there.
 // Work: the steps of all tiles of all experts in a row, dealt out evenly by what they cost.  A tile that several CTAs share is
 // summed by the last of them to arrive, from partial sums in memory, in the order of the CTAs.
 // Every barrier wait is bounded: on expiry the CTA records MOE_ERR_TIMEOUT, waits (bounded) for its own copies and products,
@@ -19,7 +21,8 @@
 namespace moe {
 namespace {
 
-constexpr int kSets = 4, kConvWarps = 4 * kSets, kEpiWarps = 4, kCopyWarp = kConvWarps + kEpiWarps, kMmaWarp = kCopyWarp + 1;
+constexpr int kSets = 4, kConvWarps = 4 * kSets, kEpiWarps = 4, kFinishWarps = kConvWarps + kEpiWarps;
+constexpr int kWeightWarp = kFinishWarps, kRowWarp = kWeightWarp + 1, kMmaWarp = kRowWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMostRows = 192;       // activation rows of a tile
 constexpr int kMostStages = 16;
@@ -29,9 +32,10 @@ constexpr uint32_t kTmemCols = 512, kSlotCols = 32, kSlotBase = 2 * kMostRows;
 static_assert(kSlotBase + kSets * kSlotCols == kTmemCols, "tensor memory");
 constexpr int kLeastSteps = 8;       // steps that a CTA's share of split tiles has at least, and that splitting has to save
 constexpr size_t kSmemMost = 232448;
+constexpr int kStepBytes = 2 * kInt8Tile;  // of weights
 
 struct Shared {
-    uint64_t full[kMostStages], ready[kMostStages], empty[kMostStages], acc_full[2], acc_empty[2], epilogue, all, parts, done;
+    uint64_t w_full[kMostStages], w_empty[kMostStages], x_full[kMostStages], x_empty[kMostStages], ready[kMostStages], acc_full[2], acc_empty[2], epilogue, all, parts, done;
     uint32_t tmem;
     volatile int abort;
     int last[3];  // whether this CTA is the last to arrive at a shared tile: at the one before the last, or the last
@@ -42,10 +46,13 @@ struct Shared {
 
 struct MmaArgs {
     Int8ProductArgs p;
-    int most, stages, stage_bytes, x_bytes;  // activation rows of a tile at most; the ring; its activations of a tile of weights
+    int most, x_bytes;       // activation rows of a tile at most; their bytes a tile of weights
+    int w_steps, x_steps;    // steps in the ring of weights, an even number; behind it in that of activations, at least 3
     int slot_rows;  // of partial sums, a multiple of 16
     int early;  // weights and offsets were there before the kernel in front started its dependents
 };
+
+__host__ __device__ __forceinline__ int ring_bytes(const MmaArgs& m) { return m.w_steps * kStepBytes + m.x_steps * 2 * m.x_bytes; }
 
 // An expert's rows as mt tiles of up to n rows (a multiple of 16).
 struct Rows {
@@ -228,7 +235,7 @@ __device__ __forceinline__ bool finish(const MmaArgs& args, Shared& s, unsigned 
                    (GATED ? odd * a.ldy + n / 2 : pairs ? odd * a.ldy + (n & ~1) : (int64_t)n);
     // Others' sums: in the CTA's last part (most often it is that) through the ring, which nothing uses any more, as many rows at a
     // time as fit; else straight from memory.
-    const int others = last - first, ring_rows = p.last && others > 0 ? args.stages * args.stage_bytes / (others * 512) / 16 * 16 : 0;
+    const int others = last - first, ring_rows = p.last && others > 0 ? ring_bytes(args) / (others * 512) / 16 * 16 : 0;
     uint32_t parts = 0;
     for (int begin = 0, end; begin < live; begin = end) {
         end = ring_rows > 0 ? min(begin + ring_rows, (live + 15) / 16 * 16) : (live + 15) / 16 * 16;
@@ -334,23 +341,32 @@ __device__ __forceinline__ bool finish(const MmaArgs& args, Shared& s, unsigned 
     return true;
 }
 
+// Copies in flight, the last `steps` of `it`, land before the CTA's shared memory goes.
+__device__ __forceinline__ void land(uint64_t* full, int it, int steps) {
+    volatile int never = 0;
+    for (int i = max(0, it - steps); i < it; ++i) mbar_wait(&full[i % steps], (i / steps) & 1, &never, nullptr, 100000000LL);
+}
+
 template <typename T, bool GATED, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_constant__ MmaArgs args) {
     const Int8ProductArgs& a = args.p;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Shared& s = *reinterpret_cast<Shared*>(ring + (size_t)args.stages * args.stage_bytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, S = args.stages;
+    Shared& s = *reinterpret_cast<Shared*>(ring + ring_bytes(args));
+    unsigned char* const x_ring = ring + args.w_steps * kStepBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_rank() : 0, cta = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
     const int KT = (int)((a.K + 63) / 64), KS = (KT + 1) / 2;
     const int NT128 = (int)((a.N + 127) / 128), NT = PAIR ? (NT128 + 1) / 2 : NT128;
     const Work<PAIR> work(s, args);
 
-    if (warp == kCopyWarp) {
-        if (lane < S) {
-            mbar_init(&s.full[lane], 1);
-            mbar_init(&s.ready[lane], PAIR ? 16 : 8);
-            mbar_init(&s.empty[lane], 1);
+    if (warp == kWeightWarp) {
+        if (lane < kMostStages) {
+            mbar_init(&s.w_full[lane], 1);
+            mbar_init(&s.w_empty[lane], 8);
+            mbar_init(&s.x_full[lane], 1);
+            mbar_init(&s.x_empty[lane], 1);
+            mbar_init(&s.ready[lane], PAIR ? 17 : 8);
         }
         if (lane < 2) {
             mbar_init(&s.acc_full[lane], 1);
@@ -360,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
     }
     if (threadIdx.x == 0) {
         mbar_init(&s.epilogue, kEpiWarps);
-        mbar_init(&s.all, kCopyWarp);
+        mbar_init(&s.all, kFinishWarps);
         mbar_init(&s.parts, 1);
         mbar_init(&s.done, 1);
         s.abort = 0;
@@ -415,70 +431,62 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
     const uint32_t tmem = s.tmem;
     int* const status = &a.ctrl->status;
 
-    if (warp == kCopyWarp) {
+    if (warp == kWeightWarp) {
         if (elect_one()) {
-            const uint32_t full0 = smem_u32(s.full), ring0 = smem_u32(ring);
-            const int64_t x_step = a.room * 128;
-            Turn t(S);
-            // where a tile's weights and activations of step k begin, and the activations' bytes a tile of weights
-            auto sources = [&](const Part& p, const uint8_t*& w, const uint8_t*& x) {
-                const int nt = min(PAIR ? 2 * p.nt + rank : p.nt, NT128 - 1), n = tile_rows(p) / (PAIR ? 2 : 1);
-                const int64_t row = (a.offsets ? int8_first_row(s.offset[p.e], p.e) : 0) + (int64_t)p.mt * p.r.n + (PAIR ? rank * n : 0);
-                w = a.w + (((int64_t)p.e * NT128 + nt) * KT + 2 * p.k) * kInt8Tile;
-                x = reinterpret_cast<const uint8_t*>(a.x) + 2 * p.k * x_step + row * 128;
-                return n * 128;
-            };
-            int head = 0, tail = 0;  // steps whose weights are on their way, and whose activations are too
-            bool ok = true;
-            if (args.early) {  // the first steps' weights, before the activations are there
-                const uint8_t* x0 = nullptr;  // of the first part
-                int bytes0 = 0, k0 = 0, steps0 = 0;
-                work.each(cta, [&](const Part& p) {
-                    const uint8_t *w, *x;
-                    const int bytes = sources(p, w, x);
-                    if (head == 0) x0 = x, bytes0 = bytes, k0 = p.k, steps0 = p.k1 - p.k;
-                    for (int k = p.k; k < p.k1; ++k, w += 2 * kInt8Tile, ++head) {
-                        if (head == S) return false;
-                        const int tiles = min(2, KT - 2 * k);
-                        expect_bytes(full0 + 8 * head, tiles * (kInt8Tile + bytes));
-                        bulk_copy(ring0 + head * args.stage_bytes + 2 * args.x_bytes, w, tiles * kInt8Tile, full0 + 8 * head);
-                    }
-                    return true;
-                });
-                pdl_wait();
-                for (; tail < min(head, steps0); ++tail, x0 += 2 * x_step) {
-                    const uint32_t to = ring0 + tail * args.stage_bytes;
-                    bulk_copy(to, x0, bytes0, full0 + 8 * tail);
-                    if (2 * (k0 + tail) + 1 < KT) bulk_copy(to + args.x_bytes, x0 + x_step, bytes0, full0 + 8 * tail);
-                }
-            }
+            Turn t(args.w_steps);
             int it = 0;
+            bool ok = true;
             work.each(cta, [&](const Part& p) {
-                const uint8_t *w, *x;
-                const int bytes = sources(p, w, x);
-                for (int k = p.k; k < p.k1; ++k, w += 2 * kInt8Tile, x += 2 * x_step, ++it, t.next()) {
-                    const uint32_t bar = full0 + 8 * t.at, to = ring0 + t.at * args.stage_bytes;
-                    const int tiles = min(2, KT - 2 * k);
-                    if (it >= head) {
-                        if (!mbar_wait(&s.empty[t.at], t.parity ^ 1, &s.abort, status)) return ok = false;
-                        expect_bytes(bar, tiles * (kInt8Tile + bytes));
-                        bulk_copy(to + 2 * args.x_bytes, w, tiles * kInt8Tile, bar);
-                    }
-                    if (it < tail) continue;
-                    bulk_copy(to, x, bytes, bar);
-                    if (tiles == 2) bulk_copy(to + args.x_bytes, x + x_step, bytes, bar);
+                const int nt = min(PAIR ? 2 * p.nt + rank : p.nt, NT128 - 1);
+                const uint8_t* w = a.w + (((int64_t)p.e * NT128 + nt) * KT + 2 * p.k) * kInt8Tile;
+                for (int k = p.k; k < p.k1; ++k, w += kStepBytes, ++it, t.next()) {
+                    if (!mbar_wait(&s.w_empty[t.at], t.parity ^ 1, &s.abort, status)) return ok = false;
+                    const uint32_t bar = smem_u32(&s.w_full[t.at]), bytes = min(2, KT - 2 * k) * kInt8Tile;
+                    expect_bytes(bar, bytes);
+                    bulk_copy(smem_u32(ring) + t.at * kStepBytes, w, bytes, bar);
                 }
                 return true;
             });
-            if (!ok) {  // copies in flight land before the CTA's shared memory goes
-                volatile int never = 0;
-                for (int i = max(0, it - S); i < it; ++i) mbar_wait(&s.full[i % S], (i / S) & 1, &never, nullptr, 100000000LL);
-            }
+            if (!ok) land(s.w_full, it, args.w_steps);
+        }
+    } else if (warp == kRowWarp) {
+        if (elect_one()) {
+            if (args.early) pdl_wait();
+            const int64_t x_step = a.room * 128;
+            Turn t(args.x_steps);
+            int it = 0;
+            bool ok = true;
+            work.each(cta, [&](const Part& p) {
+                const int n = tile_rows(p) / (PAIR ? 2 : 1), bytes = n * 128;
+                const int64_t row = (a.offsets ? int8_first_row(s.offset[p.e], p.e) : 0) + (int64_t)p.mt * p.r.n + (PAIR ? rank * n : 0);
+                const uint8_t* x = reinterpret_cast<const uint8_t*>(a.x) + 2 * p.k * x_step + row * 128;
+                for (int k = p.k; k < p.k1; ++k, x += 2 * x_step, ++it, t.next()) {
+                    if (!mbar_wait(&s.x_empty[t.at], t.parity ^ 1, &s.abort, status)) return ok = false;
+                    const uint32_t bar = smem_u32(&s.x_full[t.at]), to = smem_u32(x_ring) + t.at * 2 * args.x_bytes;
+                    const bool two = 2 * k + 1 < KT;
+                    expect_bytes(bar, two ? 2 * bytes : bytes);
+                    bulk_copy(to, x, bytes, bar);
+                    if (two) bulk_copy(to + args.x_bytes, x + x_step, bytes, bar);
+                }
+                return true;
+            });
+            if (!ok) land(s.x_full, it, args.x_steps);
         }
     } else if (warp == kMmaWarp) {
-        if (rank == 0 && elect_one()) {
-            const uint32_t base = smem_u32(ring);
-            Turn t(S);
+        if (PAIR && rank != 0) {
+            if (elect_one()) {
+                Turn t(args.x_steps);
+                work.each(cta, [&](const Part& p) {
+                    for (int k = p.k; k < p.k1; ++k, t.next()) {
+                        if (!mbar_wait(&s.x_full[t.at], t.parity, &s.abort, status)) return false;
+                        arrive<PAIR>(&s.ready[t.at]);
+                    }
+                    return true;
+                });
+            }
+        } else if (elect_one()) {
+            const uint32_t base = smem_u32(x_ring);
+            Turn t(args.x_steps);
             int tile = 0;
             uint32_t slot = tmem + kSlotBase;
             work.each(cta, [&](const Part& p) {
@@ -488,12 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
                 if (!mbar_wait(&s.acc_empty[b], ((tile >> 1) & 1) ^ 1, &s.abort, status)) return false;
                 tc_fence_after();
                 for (int k = p.k; k < p.k1; ++k, t.next(), slot ^= 2 * kSlotCols) {
+                    if (!mbar_wait(&s.x_full[t.at], t.parity, &s.abort, status)) return false;
                     if (!mbar_wait(&s.ready[t.at], t.parity, &s.abort, status)) return false;
                     tc_fence_after();
-                    const uint32_t x = ((base + t.at * args.stage_bytes) >> 4) | (1u << 16);
+                    const uint32_t x = ((base + t.at * 2 * args.x_bytes) >> 4) | (1u << 16);
                     step_products<PAIR>(acc, slot, x, idesc, k > p.k ? 1u : 0u);
                     if (2 * k + 1 < KT) step_products<PAIR>(acc, slot + kSlotCols, x + (args.x_bytes >> 4), idesc, 1u);
-                    commit<PAIR>(&s.empty[t.at]);
+                    commit<PAIR>(&s.x_empty[t.at]);
                 }
                 commit<PAIR>(&s.acc_full[b]);
                 ++tile;
@@ -503,32 +512,35 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
         }
     } else if (warp < kConvWarps) {
         const int set = warp >> 2, q = warp & 3;
-        const unsigned char* w0 = ring + 2 * args.x_bytes + (set & 1) * kInt8Tile + (32 * q + lane) * 16;
+        const unsigned char* w0 = ring + (set & 1) * kInt8Tile + (32 * q + lane) * 16;
         const uint32_t slot = tmem + ((uint32_t)(32 * q) << 16) + kSlotBase + set * kSlotCols;
-        Turn t(S), old(S);  // the step; the one before the last
+        // places in the rings: of the step's weights and activations, and of the activations of the step before the last
+        Turn t(args.w_steps), x(args.x_steps), old(args.x_steps);
         int it = 0, tile = 0;
         work.each(cta, [&](const Part& p) {
             // (of every tile but the last two: below, a phase that nobody waited for could be taken for the last part's)
             if (tile >= 2 && !mbar_wait_warp(&s.acc_full[tile & 1], ((tile >> 1) - 1) & 1, &s.abort, status)) return false;
             ++tile;
-            for (int k = p.k; k < p.k1; ++k, ++it, t.next()) {
+            for (int k = p.k; k < p.k1; ++k, ++it, t.next(), x.next()) {
                 if (it >= 3) old.next();
-                // (of every step: a barrier's phase that nobody waits for could be taken for the one after the next)
-                if (!mbar_wait_warp(&s.full[t.at], t.parity, &s.abort, status)) return false;
                 if ((it & 1) != set >> 1) continue;
-                if (2 * k + (set & 1) < KT) {
-                    uint32_t h[32];
-                    convert_row(w0 + (size_t)t.at * args.stage_bytes, h);
-                    // the products of the step before the last have read this slot (its phase is not mistaken: this step was copied
-                    // after the products of the step S before had completed)
-                    if (it >= 2 && !mbar_wait_warp(&s.empty[old.at], old.parity, &s.abort, status)) return false;
+                // (The ring has an even number of steps, so that a set waits for every phase of its own places, and not for others': 649 us
+                // instead of 676 for the gate and up products of 256 tokens by 8 of 128 experts.)
+                if (!mbar_wait_warp(&s.w_full[t.at], t.parity, &s.abort, status)) return false;
+                const bool there = 2 * k + (set & 1) < KT;
+                uint32_t h[32];
+                if (there) convert_row(w0 + t.at * kStepBytes, h);
+                // The products of the step before the last have read this slot.  (The phase is not mistaken: this set has waited for the
+                // products of the step two before that one, and those of the steps before it come in order.)
+                if (it >= 2 && !mbar_wait_warp(&s.x_empty[old.at], old.parity, &s.abort, status)) return false;
+                if (there) {
                     tc_fence_after();
                     tmem_st32(slot, h);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
                 }
                 __syncwarp();
-                if (lane == 0) arrive<PAIR>(&s.ready[t.at]);
+                if (lane == 0) mbar_arrive(&s.w_empty[t.at]), arrive<PAIR>(&s.ready[x.at]);
             }
             return true;
         });
@@ -553,14 +565,14 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
         });
     }
     // The CTA's last part is finished by the converting warps too, which have nothing else to do then: five warps a lane quarter.
-    if (warp < kCopyWarp) {
+    if (warp < kFinishWarps) {
         __syncwarp();
         // (Everything it needs is found again from here: what lives on until here costs the loops above registers.)
         const MmaArgs* args2 = &args;
         unsigned char* raw2 = smem_raw;
         asm volatile("" : "+l"(args2), "+l"(raw2));
         unsigned char* const ring2 = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw2) + 1023) & ~uintptr_t(1023));
-        Shared& s2 = *reinterpret_cast<Shared*>(ring2 + (size_t)args2->stages * args2->stage_bytes);
+        Shared& s2 = *reinterpret_cast<Shared*>(ring2 + ring_bytes(*args2));
         const Work<PAIR> work2(s2, *args2);
         Part p;
         const int tile = work2.last(PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, p), part = (int)threadIdx.x >> 7;
@@ -573,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
                 return mbar_wait_warp(&s2.all, turn++ & 1, &s2.abort, &args2->p.ctrl->status);
             };
             // (the epilogue's warps, which have been waiting for the accumulators, take the first rows)
-            finish<T, GATED, PAIR>(*args2, s2, ring2, work2, s2.tmem, p, tile, (part + 1) % (kCopyWarp / 4), kCopyWarp / 4, s2.sx[4], &s2.last[2],
+            finish<T, GATED, PAIR>(*args2, s2, ring2, work2, s2.tmem, p, tile, (part + 1) % (kFinishWarps / 4), kFinishWarps / 4, s2.sx[4], &s2.last[2],
                                    sync);
             tc_fence_before();
         }
@@ -616,11 +628,15 @@ cudaError_t launch_int8_mma(const Int8ProductArgs& a, moe_dtype dtype, bool gate
     m.most = (int)(rows > kMostRows ? kMostRows : (rows + 15) / 16 * 16);
     m.x_bytes = m.most * 128 / (pair ? 2 : 1);
     m.x_bytes = (m.x_bytes + 1023) / 1024 * 1024;
-    m.stage_bytes = 2 * (m.x_bytes + kInt8Tile);
-    const int fit = (int)((kSmemMost - 1024 - sizeof(Shared)) / m.stage_bytes);
-    m.stages = fit < kMostStages ? fit : kMostStages;
+    // Steps of activations: 5, but 4 or 3 where that would leave fewer than 6 or 4 of weights; and what the even number of these leaves.
+    const int fit = (int)(kSmemMost - 1024 - sizeof(Shared)) / 1024 * 1024, x_step = 2 * m.x_bytes;
+    m.x_steps = fit - 5 * x_step >= 6 * kStepBytes ? 5 : fit - 4 * x_step >= 4 * kStepBytes ? 4 : 3;
+    m.w_steps = (fit - m.x_steps * x_step) / kStepBytes / 2 * 2;
+    if (m.w_steps > kMostStages) m.w_steps = kMostStages;
+    m.x_steps = (fit - m.w_steps * kStepBytes) / x_step;
+    if (m.x_steps > kMostStages) m.x_steps = kMostStages;
     // (more than half of the SM's shared memory, so that one CTA per SM owns its tensor memory)
-    size_t smem = (size_t)m.stages * m.stage_bytes + sizeof(Shared) + 1024;
+    size_t smem = (size_t)ring_bytes(m) + sizeof(Shared) + 1024;
     if (smem < 120 * 1024) smem = 120 * 1024;
     int ctas = sm_count() < kInt8Ctas ? sm_count() : kInt8Ctas;
     if (pair) ctas = ctas / 2 * 2;

@@ -305,3 +305,41 @@ def test_no_rows():
     x = torch.randn(3, 64, device="cuda").bfloat16()
     assert (ops.int8_experts(x, ids, torch.rand(3, 2, device="cuda"), up, down, ws) == 0).all()
     assert ops.int8_experts(x[:0], ids[:0], torch.rand(0, 2, device="cuda"), up, down, ws).shape == (0, 64)
+
+
+# long rows, whose last tiles several CTAs share: two of them, four and more, with whole tiles in front of them and without
+@pytest.mark.parametrize("M,N,K", [(512, 8192, 8192), (700, 4100, 8300), (300, 19300, 16400), (40, 19100, 8257), (1300, 2100, 40000), (257, 9800, 131072),
+                                   (150, 19000, 131072)])
+def test_tiles_of_several_ctas(M, N, K):
+    """Whole numbers of at most 63 or 20 beside activations of a scale of 1: sums stay below 2^24 (127 * 20 sqrt(131072 * 1.3) is far from it)."""
+    g = gen(M + N + K)
+    most = 63 if K < 20000 else 20
+    x = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    wq, ws = torch.randint(-most, most + 1, (N, K), generator=g, device="cuda", dtype=torch.int8), scales(g, N)
+    W, space = ops.int8_weights(wq, ws), ops.int8_workspace(M, N, K)
+    rows = torch.cat((torch.arange(0, M, max(1, M // 40), device="cuda"), torch.arange(M - 3, M, device="cuda")))
+    q, s = R.numbers(x[rows])
+    want = torch.cat([R.product(q, s, wq[n:n + 2000], ws[n:n + 2000], torch.float32) for n in range(0, N, 2000)], 1)
+    y = ops.int8_linear(x, W, space)
+    for _ in range(2):
+        assert torch.equal(ops.int8_linear(x, W, space), y)
+    assert torch.equal(y[rows], want.to(y.dtype))
+    if N % 2 == 0:
+        out, bound = R.gated_bound(want, torch.bfloat16)
+        assert ((ops.int8_linear(x, W, space, gated=True)[rows].double() - out).abs() <= bound).all()
+
+
+def test_experts_tiles_of_several_ctas():
+    g = gen(12)
+    E, N, K = 5, 1500, 17000
+    wq, s = torch.randint(-63, 64, (E, N, K), generator=g, device="cuda", dtype=torch.int8), scales(g, E, N)
+    W = ops.int8_weights(wq, s)
+    for counts in ((90, 0, 300, 17, 150), (10, 9, 12, 5, 8), (0, 0, 0, 0, 400)):
+        ids = torch.cat([torch.full((n,), e) for e, n in enumerate(counts)]).int().cuda()[:, None]
+        order = ops.expert_order(ids, E)
+        x = torch.randn(len(ids), K, generator=g, device="cuda").half()
+        y = ops.int8_matmul(ops.int8_quantize(x, order), W, torch.float32, ops.int8_workspace(len(ids), N, K))
+        for e in range(E):
+            t = torch.nonzero(ids[:, 0] == e)[:, 0]
+            if len(t):
+                assert torch.equal(y[order.inv[t, 0].long()], R.product(*R.numbers(x[t]), wq[e], s[e], torch.float32)), (counts, e)

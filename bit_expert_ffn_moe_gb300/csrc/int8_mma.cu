@@ -13,8 +13,8 @@
 // products of 256 tokens by 8 of 128 experts of 8192 x 2048 took 687 us instead of 652, of 4096 tokens 1454 instead of 1396.)
 // PAIR: two CTAs share a tile of 256 weight rows (cta_group::2), each with half of the activation rows in its shared memory; the
 // leader (rank 0) issues the products of both, and the other's warp 22 passes on that its activations are there.
-// Work: the steps of all tiles of all experts in a row, dealt out evenly by what they cost.  A tile that several CTAs share is
-// summed by the last of them to arrive, from partial sums in memory, in the order of the CTAs.
+// Work: the tiles of all experts in a row, taken in turns; the last ones, where it saves enough, are dealt out by their steps.  A tile that
+// several CTAs share is summed by the last of them to arrive, from partial sums in memory, in the order of the CTAs.
 // Every barrier wait is bounded: on expiry the CTA records MOE_ERR_TIMEOUT, waits (bounded) for its own copies and products,
 // frees tensor memory and exits.
 #include "int8_mma.cuh"
@@ -81,7 +81,7 @@ struct Part {
 // neighbours work on the same weights and rows, which then come out of L2 (contiguous shares: each tile's operands from memory, 2.7
 // ms instead of 1.5 for the gate and up products of 4096 tokens).  The last `split` of them, fewer than there are CTAs, are dealt
 // out by their steps, evenly, so that all CTAs end at the same time.  (Shared tiles first, their sums made while the next
-// tile's products run: the sums' loads waited behind the copies for longer than that tile took, 94 us instead of 50 for 1024 x 4096 x 8192.)
+// tile's products run: the sums' loads waited behind the copies for longer than that tile took, 94 us instead of 59 for 1024 x 4096 x 8192.)
 template <bool PAIR>
 struct Work {
     const Shared& s;

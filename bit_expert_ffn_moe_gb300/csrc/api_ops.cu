@@ -97,6 +97,9 @@ bool matrix_ok(const void* p, moe_dtype dtype, int64_t n, int64_t ld) { return p
 
 constexpr int64_t kInt8MaxK = 131072;  // sums of K products of 127 x 127 stay below 2^31
 bool int8_ok(int64_t rows, int64_t K) { return K <= kInt8MaxK && dims_ok(rows, K); }
+// What a room has beyond the rows it is for, at most: so any room of accepted rows has bytes, and a workspace never lacks them.
+constexpr int64_t kInt8Beside = 8 * (int64_t)kMaxE + 16 + 7;
+bool int8_room_ok(int64_t room, int64_t K) { return room >= 0 && int8_ok(room > kInt8Beside ? room - kInt8Beside : 0, K); }
 bool int8_product_ok(int64_t M, int64_t N, int64_t K) { return int8_ok(M, K) && int8_ok(N, K) && dims_ok(M, N > 0 ? N : 1); }
 
 moe_status check_int8_weights(const moe_int8_weights* W) {
@@ -353,7 +356,7 @@ size_t moe_int8_weights_bytes(int64_t N, int64_t K) { return int8_ok(N, K) ? (si
 int64_t moe_int8_rows_room(int64_t M, int E) {
     return M < 0 || M > kMaxDim || E < 0 || E > kMaxE ? 0 : (M + 7) / 8 * 8 + 8 * (int64_t)E + 16;
 }
-size_t moe_int8_rows_bytes(int64_t room, int64_t K) { return int8_ok(room, K) ? (size_t)room * pad(K, 64) * 2 : 0; }
+size_t moe_int8_rows_bytes(int64_t room, int64_t K) { return int8_room_ok(room, K) ? (size_t)room * pad(K, 64) * 2 : 0; }
 
 moe_status moe_int8_weights_layout(const int8_t* w, const float* s_in, int E, int64_t rows, int64_t K, int64_t ld, int64_t first,
                                    int64_t step, int64_t N, const moe_int8_weights* W, moe_stream_t stream) {

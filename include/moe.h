@@ -607,7 +607,7 @@ typedef struct moe_int8_rows {
 } moe_int8_rows;
 
 int64_t moe_int8_rows_room(int64_t M, int E); /* for M rows, of E experts or (0) of none; 0 for an unsupported shape */
-size_t moe_int8_rows_bytes(int64_t room, int64_t K);
+size_t moe_int8_rows_bytes(int64_t room, int64_t K); /* of any room of a supported shape; else 0 */
 
 /* Rows of x [T][ldx].  offsets and inv NULL (E = 0): as they are.  offsets [E+1] (moe_expert_order's) alone: x is in expert order, rows
  * from offsets[E] on are passed over.  Both: token t goes to the rows inv[t*k .. t*k+k-1], quantised once. */

@@ -203,11 +203,11 @@ __global__ void __launch_bounds__(kThreads, SLOTS <= 8 ? 3 : SLOTS <= 16 ? 2 : 1
         acc[j] = 0.f;
     }
     if (live)
-        for (int e0 = first * P::N; e0 < d; e0 += PIECES * step) {
+        for (uint32_t e0 = first * P::N; e0 < (uint32_t)d; e0 += PIECES * step) {  // (unsigned: rows of up to 2^31 - 1 elements)
             P a[PIECES], b[PIECES][SLOTS];
 #pragma unroll
             for (int q = 0; q < PIECES; ++q) {
-                const int e = min(e0 + q * step, (d - 1) / P::N * P::N);  // (behind the end: the last piece again)
+                const int e = (int)min(e0 + q * step, (uint32_t)((d - 1) / P::N * P::N));  // (behind the end: the last piece again)
                 if (SPREAD || DW) a[q].load(arow, e, d);
                 if (!SPREAD || DW)
 #pragma unroll
@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(kThreads, SLOTS <= 8 ? 3 : SLOTS <= 16 ? 2 : 1
             }
 #pragma unroll
             for (int q = 0; q < PIECES; ++q) {
-                const int e = e0 + q * step;
-                if (PIECES > 1 && e >= d) break;
+                if (PIECES > 1 && e0 + q * step >= (uint32_t)d) break;
+                const int e = (int)(e0 + q * step);
                 float fa[P::N], sum[P::N] = {};
                 if (SPREAD || DW) a[q].settle(a_shift), a[q].get(fa);
 #pragma unroll
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, SLOTS <= 8 ? 3 : SLOTS <= 16 ? 2 : 1
 
 template <typename T, int WORDS, bool SPREAD, bool DW, int SLOTS, int PIECES>
 cudaError_t launch_token(MoveArgs m, cudaStream_t st) {
-    const int pieces = (m.d + Piece<T, WORDS>::N * PIECES - 1) / (Piece<T, WORDS>::N * PIECES);
+    const int64_t pieces = ((int64_t)m.d + Piece<T, WORDS>::N * PIECES - 1) / (Piece<T, WORDS>::N * PIECES);
     int warps = 1;
     while (warps < kThreads / 32 && warps * 32 < pieces) warps *= 2;
     const int tokens = kThreads / 32 / warps;

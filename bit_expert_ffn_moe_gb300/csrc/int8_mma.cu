@@ -195,7 +195,10 @@ __device__ __forceinline__ bool finish(const MmaArgs& args, Shared& s, unsigned 
         for (int c0 = 0; c0 < kMostRows; c0 += 32)
             if (c0 + lane < live) sx[c0 + lane] = __ldcg(from + c0 + lane);
     }
-    if (!mbar_wait_warp(&s.acc_full[b], (tile >> 1) & 1, &s.abort, status)) return false;
+    // The CTA's last part: all of its products are done.  (Not its accumulators' phase: the converting warps have not waited for all the
+    // phases before it, and a parity does not tell a phase from the one before the last.)
+    if (!mbar_wait_warp(p.last ? &s.done : &s.acc_full[b], p.last ? 0 : (tile >> 1) & 1, &s.abort, status)) return false;
+    if (p.last && __any_sync(0xffffffffu, s.abort)) return false;
     tc_fence_after();
     int first = cta, last = cta;  // the CTAs that share the tile
     // The partial sums of a CTA, [16 activation rows][4][128][4]: of the tile that it begins, or (1) goes on with.
@@ -519,11 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
         const uint32_t slot = tmem + ((uint32_t)(32 * q) << 16) + kSlotBase + set * kSlotCols;
         // places in the rings: of the step's weights and activations, and of the activations of the step before the last
         Turn t(args.w_steps), x(args.x_steps), old(args.x_steps);
-        int it = 0, tile = 0;
+        int it = 0;
         work.each(cta, [&](const Part& p) {
-            // (of every tile but the last two: below, a phase that nobody waited for could be taken for the last part's)
-            if (tile >= 2 && !mbar_wait_warp(&s.acc_full[tile & 1], ((tile >> 1) - 1) & 1, &s.abort, status)) return false;
-            ++tile;
             for (int k = p.k; k < p.k1; ++k, ++it, t.next(), x.next()) {
                 if (it >= 3) old.next();
                 if ((it & 1) != set >> 1) continue;

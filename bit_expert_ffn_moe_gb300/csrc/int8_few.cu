@@ -156,9 +156,11 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const __grid_cons
         Turn t(S), old(S);  // the step; the one before the last
         for (int k = 0; k < steps; ++k, t.next()) {
             if (k >= 3) old.next();
-            // (of every step: a barrier's phase that nobody waits for could be taken for the one after the next)
-            if (!mbar_wait_warp(&s.full[t.at], t.parity, &s.abort, status)) break;
             if ((k & 1) != set >> 1) continue;
+            // (Of the set's own steps alone: the copies of another's can be followed by the next ones in their place before this set looks.  Own
+            // phases are not mistaken: the step that had the place before, S >= 4 steps ago, had been multiplied when this set's
+            // last step took its slot; and the step that has it next waits for this one's products.)
+            if (!mbar_wait_warp(&s.full[t.at], t.parity, &s.abort, status)) break;
             if (2 * (k0 + k) + (set & 1) < KT) {
                 uint32_t h[32];
                 convert_row(w0 + (size_t)t.at * args.stage_bytes, h);
@@ -264,7 +266,7 @@ cudaError_t launch_int8_few(const Int8ProductArgs& a, moe_dtype dtype, bool gate
     f.x_bytes = (f.n * 128 + 1023) / 1024 * 1024;
     f.stage_bytes = 2 * (f.x_bytes + kInt8Tile);
     const int fit = (int)((232448 - 1024 - sizeof(Shared)) / f.stage_bytes);
-    f.stages = fit < kMostStages ? fit : kMostStages;
+    f.stages = fit < kMostStages ? fit : kMostStages;  // (4 at least)
     // (more than half of the SM's shared memory, so that CTAs do not share its tensor memory)
     size_t smem = (size_t)f.stages * f.stage_bytes + sizeof(Shared) + 1024;
     if (smem < 120 * 1024) smem = 120 * 1024;

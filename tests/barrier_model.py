@@ -48,12 +48,12 @@ def run(roles, rng):
         waits[i] = next(roles[i], "end")
 
 
-def arrivals(queue, n):
-    """The n arrivals that copies or products make when they are done, in order."""
+def arrivals(queue, n, rng=None):
+    """The n arrivals that copies (in any order) or products (in theirs) make when they are done."""
     for _ in range(n):
         while not queue:
             yield queue
-        queue.pop(0).arrive()
+        queue.pop(rng.randrange(len(queue)) if rng else 0).arrive()
         yield None
 
 
@@ -62,7 +62,7 @@ def land(full, steps, places):
         yield full[i % places], i // places
 
 
-def persistent(parts, w_steps, x_steps, last_by_accumulators=False):
+def persistent(rng, parts, w_steps, x_steps, last_by_accumulators=False):
     """parts: the steps of each of a CTA's parts.  last_by_accumulators: the converting warps wait for the accumulators of the last part, and
     on the way for those of the part before the last one, instead of for all products."""
     w_full, w_empty = barriers(w_steps, 1), barriers(w_steps, 8)
@@ -114,5 +114,37 @@ def persistent(parts, w_steps, x_steps, last_by_accumulators=False):
             yield None
             acc_empty[t % 2].arrive()
         yield from finish()
-    return [copier(w_full, w_empty, w_steps), copier(x_full, x_empty, x_steps), multiplier(), arrivals(copies, 2 * sum(parts)),
+    return [copier(w_full, w_empty, w_steps), copier(x_full, x_empty, x_steps), multiplier(), arrivals(copies, 2 * sum(parts), rng),
             arrivals(products, sum(parts) + len(parts) + 1)] + [converter(w // 8) for w in range(16)] + [epilogue() for _ in range(4)]
+
+
+def cluster(rng, steps, places, waits_for_all=False):
+    """A CTA's steps of a tile that a cluster shares.  waits_for_all: each converting warp waits for the copies of every step, not of its own."""
+    full, ready, empty, done = barriers(places, 1), barriers(places, 8), barriers(places, 1), Barrier(1)
+    copies, products = [], []
+
+    def copier():
+        for i in range(steps):
+            if i >= places:
+                yield empty[i % places], i // places - 1
+            copies.append(full[i % places])
+            yield None
+
+    def multiplier():
+        for i in range(steps):
+            yield ready[i % places], i // places
+            products.append(empty[i % places])
+            yield None
+        products.append(done)
+
+    def converter(turn):
+        for i in range(steps):
+            if waits_for_all or i % 2 == turn:
+                yield full[i % places], i // places
+            if i % 2 == turn:
+                if i >= 2:
+                    yield empty[(i - 2) % places], (i - 2) // places
+                ready[i % places].arrive()
+                yield None
+        yield done, 0
+    return [copier(), multiplier(), arrivals(copies, steps, rng), arrivals(products, steps + 1)] + [converter(w // 8) for w in range(16)]

@@ -13,7 +13,7 @@ def parts(rng):
 def test_the_persistent_kernel():
     for seed in range(120):
         rng = random.Random(seed)
-        M.run(M.persistent(parts(rng), rng.choice([2, 4, 6, 10]), rng.choice([2, 4, 6])), rng)
+        M.run(M.persistent(rng, parts(rng), rng.choice([2, 4, 6, 10]), rng.choice([2, 4, 6])), rng)
 
 
 def test_tiles_of_one_step_need_the_barrier_of_all_products():
@@ -21,4 +21,18 @@ def test_tiles_of_one_step_need_the_barrier_of_all_products():
     with pytest.raises(M.Stuck):
         for seed in range(200):
             rng = random.Random(seed)
-            M.run(M.persistent([1] * 5, 10, 12, last_by_accumulators=True), rng)
+            M.run(M.persistent(rng, [1] * 5, 10, 12, last_by_accumulators=True), rng)
+
+
+def test_the_kernel_of_clusters():
+    for seed in range(200):
+        rng = random.Random(seed)
+        M.run(M.cluster(rng, rng.randint(1, 30), rng.randint(4, 10)), rng)
+
+
+def test_converting_warps_wait_for_their_own_steps_alone():
+    """The copies of another's step can be followed by the next ones in their place before a warp looks."""
+    with pytest.raises(M.Stuck):
+        for seed in range(200):
+            rng = random.Random(seed)
+            M.run(M.cluster(rng, 30, rng.choice([4, 5]), waits_for_all=True), rng)

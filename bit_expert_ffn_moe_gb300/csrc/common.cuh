@@ -456,6 +456,16 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// What a thread that copies into a ring of `stages` places, `issued` steps of them, does when it is done, aborting or not: waits (bounded)
+// until the last ones have landed.  No CTA's shared memory goes, or is used for something else, while a copy is still on its way,
+// also where another thread gives up after this one has issued everything.  A step's copies complete a phase of its place's barrier.
+// (Out of line, so that it costs the loops around it no registers.)
+static __device__ __noinline__ void land(uint64_t* full, int issued, int stages) {
+    volatile int never = 0;
+    for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+        mbar_wait(&full[i % stages], (i / stages) & 1, &never, nullptr, 100000000LL);
+}
+
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      smem_u32(dst)),

@@ -113,15 +113,11 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const __grid_cons
             Turn t(S);
             w = a.w + ((int64_t)nt * KT + 2 * (k0 + head)) * kInt8Tile;
             int it = 0;
-            bool ok = true;
             for (; it < steps; ++it, x += 2 * x_step, t.next()) {
                 const uint32_t bar = full0 + 8 * t.at, to = ring0 + t.at * args.stage_bytes;
                 const int tiles = min(2, KT - 2 * (k0 + it));
                 if (it >= head) {
-                    if (!mbar_wait(&s.empty[t.at], t.parity ^ 1, &s.abort, status)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!mbar_wait(&s.empty[t.at], t.parity ^ 1, &s.abort, status)) break;
                     expect_bytes(bar, tiles * (kInt8Tile + bytes));
                     bulk_copy(to + 2 * args.x_bytes, w, tiles * kInt8Tile, bar);
                     w += 2 * kInt8Tile;
@@ -129,10 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const __grid_cons
                 bulk_copy(to, x, bytes, bar);
                 if (tiles == 2) bulk_copy(to + args.x_bytes, x + x_step, bytes, bar);
             }
-            if (!ok) {  // copies in flight land before the CTA's shared memory goes
-                volatile int never = 0;
-                for (int i = max(0, it - S); i < it; ++i) mbar_wait(&s.full[i % S], (i / S) & 1, &never, nullptr, 100000000LL);
-            }
+            land(s.full, it, S);
         }
     } else if (warp == kMmaWarp) {
         if (elect_one()) {
@@ -192,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_few_kernel(const __grid_cons
         mbar_wait(&s.done, 0, &never, status);
     }
     tc_fence_after();
-    __syncthreads();  // and no copy is in flight: every stage was consumed (or drained when aborting)
+    __syncthreads();  // and no copy is in flight: they have landed, or (bounded) been waited for
 
     // Results go through shared memory, [activation row][128 weight rows], on the ring.
     float* part = reinterpret_cast<float*>(ring);

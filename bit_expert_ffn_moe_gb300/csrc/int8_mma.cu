@@ -256,7 +256,10 @@ __device__ __forceinline__ bool finish(const MmaArgs& args, Shared& s, unsigned 
                     if (c != cta) bulk_copy(to, slot(c) + begin * 32, bytes, smem_u32(&s.parts)), to += bytes;
             }
             __syncwarp();
-            if (!mbar_wait_warp(&s.parts, parts++ & 1, &s.abort, status)) return false;
+            if (!mbar_wait_warp(&s.parts, parts++ & 1, &s.abort, status)) {
+                if (speaker) land(&s.parts, (int)parts, 1);
+                return false;
+            }
         }
 #pragma unroll 1
         for (int c0 = begin + 16 * unit0; c0 < end; c0 += 16 * stride) {
@@ -347,12 +350,6 @@ __device__ __forceinline__ bool finish(const MmaArgs& args, Shared& s, unsigned 
     return true;
 }
 
-// Copies in flight, the last `steps` of `it`, land before the CTA's shared memory goes.
-__device__ __forceinline__ void land(uint64_t* full, int it, int steps) {
-    volatile int never = 0;
-    for (int i = max(0, it - steps); i < it; ++i) mbar_wait(&full[i % steps], (i / steps) & 1, &never, nullptr, 100000000LL);
-}
-
 template <typename T, bool GATED, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_constant__ MmaArgs args) {
     const Int8ProductArgs& a = args.p;
@@ -441,19 +438,18 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
         if (elect_one()) {
             Turn t(args.w_steps);
             int it = 0;
-            bool ok = true;
             work.each(cta, [&](const Part& p) {
                 const int nt = min(PAIR ? 2 * p.nt + rank : p.nt, NT128 - 1);
                 const uint8_t* w = a.w + (((int64_t)p.e * NT128 + nt) * KT + 2 * p.k) * kInt8Tile;
                 for (int k = p.k; k < p.k1; ++k, w += kStepBytes, ++it, t.next()) {
-                    if (!mbar_wait(&s.w_empty[t.at], t.parity ^ 1, &s.abort, status)) return ok = false;
+                    if (!mbar_wait(&s.w_empty[t.at], t.parity ^ 1, &s.abort, status)) return false;
                     const uint32_t bar = smem_u32(&s.w_full[t.at]), bytes = min(2, KT - 2 * k) * kInt8Tile;
                     expect_bytes(bar, bytes);
                     bulk_copy(smem_u32(ring) + t.at * kStepBytes, w, bytes, bar);
                 }
                 return true;
             });
-            if (!ok) land(s.w_full, it, args.w_steps);
+            land(s.w_full, it, args.w_steps);
         }
     } else if (warp == kRowWarp) {
         if (elect_one()) {
@@ -461,13 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
             const int64_t x_step = a.room * 128;
             Turn t(args.x_steps);
             int it = 0;
-            bool ok = true;
             work.each(cta, [&](const Part& p) {
                 const int n = tile_rows(p) / (PAIR ? 2 : 1), bytes = n * 128;
                 const int64_t row = (a.offsets ? int8_first_row(s.offset[p.e], p.e) : 0) + (int64_t)p.mt * p.r.n + (PAIR ? rank * n : 0);
                 const uint8_t* x = reinterpret_cast<const uint8_t*>(a.x) + 2 * p.k * x_step + row * 128;
                 for (int k = p.k; k < p.k1; ++k, x += 2 * x_step, ++it, t.next()) {
-                    if (!mbar_wait(&s.x_empty[t.at], t.parity ^ 1, &s.abort, status)) return ok = false;
+                    if (!mbar_wait(&s.x_empty[t.at], t.parity ^ 1, &s.abort, status)) return false;
                     const uint32_t bar = smem_u32(&s.x_full[t.at]), to = smem_u32(x_ring) + t.at * 2 * args.x_bytes;
                     const bool two = 2 * k + 1 < KT;
                     expect_bytes(bar, two ? 2 * bytes : bytes);
@@ -476,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
                 }
                 return true;
             });
-            if (!ok) land(s.x_full, it, args.x_steps);
+            land(s.x_full, it, args.x_steps);
         }
     } else if (warp == kMmaWarp) {
         if (PAIR && rank != 0) {

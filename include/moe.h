@@ -641,8 +641,9 @@ moe_status moe_int8_experts(const void* x, moe_dtype dtype, int64_t ldx, const i
  * the kernel records MOE_ERR_TIMEOUT in the workspace status word and finishes, so a lost copy or
  * signal is reported by moe_get_device_status instead of hanging the GPU.  This call runs that
  * path on purpose: one kernel thread waits up to limit_us microseconds (1 .. 1000000) on an
- * mbarrier phase that nothing completes, then records MOE_ERR_TIMEOUT and returns normally.  The
- * CUDA context stays usable.  ws: an initialised workspace (only its control block is used). */
+ * mbarrier phase that nothing completes, then records MOE_ERR_TIMEOUT and returns normally.  Another
+ * thread has issued copies and lets them land before the kernel ends (MOE_ERR_CUDA instead, if they have
+ * not).  The CUDA context stays usable.  ws: an initialised workspace (only its control block is used). */
 moe_status moe_selftest_wait_timeout(void* ws, size_t ws_bytes, int limit_us, moe_stream_t stream);
 
 /* ---------------------------------------------------------------- synthetic inputs

@@ -58,6 +58,7 @@ def arrivals(queue, n, rng=None):
 
 
 def land(full, steps, places):
+    """What a copier does when it has issued everything."""
     for i in range(max(0, steps - places), steps):
         yield full[i % places], i // places
 
@@ -75,6 +76,7 @@ def persistent(rng, parts, w_steps, x_steps, last_by_accumulators=False):
             yield empty[i % places], i // places - 1
             copies.append(full[i % places])
             yield None
+        yield from land(full, sum(parts), places)
 
     def multiplier():
         i = 0
@@ -129,6 +131,7 @@ def cluster(rng, steps, places, waits_for_all=False):
                 yield empty[i % places], i // places - 1
             copies.append(full[i % places])
             yield None
+        yield from land(full, steps, places)
 
     def multiplier():
         for i in range(steps):

@@ -798,13 +798,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) umma_decode_layer_kernel(con
                 }
                 if (!ok) break;
             }
-            if (*abort_flag) {  // let the copies already issued land before shared memory is released
-                volatile int never = 0;
-                for (int i = 0; i < kStages && i < kiter; ++i) {
-                    const int it = kiter - 1 - i;
-                    mbar_wait(&full_b[it % kStages], (it / kStages) & 1, &never, nullptr, 100000000LL);
-                }
-            }
+            land(full_b, kiter, kStages);
         }
     } else if (warp == kThreads / 32) {
         // ---------------------------------------------------------- A operand copies
@@ -851,13 +845,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) umma_decode_layer_kernel(con
                 }
                 if (!ok) break;
             }
-            if (*abort_flag) {
-                volatile int never = 0;
-                for (int i = 0; i < kStages && i < kiter; ++i) {
-                    const int it = kiter - 1 - i;
-                    mbar_wait(&full_a[it % kStages], (it / kStages) & 1, &never, nullptr, 100000000LL);
-                }
-            }
+            land(full_a, kiter, kStages);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer (whole warp)

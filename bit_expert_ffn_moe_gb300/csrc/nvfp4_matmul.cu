@@ -288,11 +288,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
                 load_w(s, k0 + it);
                 load_x(s, k0 + it);
             }
-            if (*abort_flag) {
-                volatile int never = 0;
-                for (int i = max(0, it - kStages); i < it; ++i)
-                    mbar_wait(&full[i % kStages], (i / kStages) & 1, &never, nullptr, 100000000LL);
-            }
+            land(full, it, kStages);
         }
     } else if (warp == 1) {
         const uint32_t idesc = idesc_mxf4nvf4_ue4m3(128, NT);
@@ -314,7 +310,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     volatile int never = 0;
     mbar_wait(acc_full, 0, &never, args.status);  // the commit always comes; bounded all the same
     tc_fence_after();
-    __syncthreads();  // and no copy is in flight: every stage was consumed (or drained when aborting)
+    __syncthreads();  // and no copy is in flight: they have landed, or (bounded) been waited for
 
     // Results go through shared memory, [activation row][128 weight rows], on the stages; activation row c of the tile is
     // then summed over the cluster's CTAs, in rank order, scaled and stored by a warp of CTA c % splits.
@@ -528,13 +524,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     pair_load(p + 2 * kTile + 8 * kAtom, &pair.sb, (kb1 + kt) * kAtoms * kAtom, bar);
                 }
             }
-            // Copies still in flight land before the CTA's shared memory goes: after the last commit every stage has been
-            // consumed; when aborting, the leader gives the outstanding ones of both CTAs a bounded time.
-            if (*abort_flag && rank == 0) {
-                volatile int never = 0;
-                for (int i = max(0, it - kPairStages); i < it; ++i)
-                    mbar_wait(&full[i % kPairStages], (i / kPairStages) & 1, &never, nullptr, 100000000LL);
-            }
+            // The leader's barriers count the copies of both CTAs.
+            if (rank == 0) land(full, it, kPairStages);
         }
     } else if (warp == 1 && rank == 0) {
         if (elect_one()) {

@@ -193,13 +193,7 @@ __global__ void __launch_bounds__(kScrThreads, 1) router_screen_kernel(const __g
                 bulk_load(stage(s) + kScrTile, a.bhi + tile, kScrTile, &full[s]);
                 bulk_load(stage(s) + 2 * kScrTile, a.blo + tile, kScrTile, &full[s]);
             }
-            if (*abort_flag) {  // let the issued copies land before shared memory is released
-                volatile int never = 0;
-                for (int q = 0; q < kScrStages && q < i; ++q) {
-                    const int it = i - 1 - q;
-                    mbar_wait(&full[it % kScrStages], (it / kScrStages) & 1, &never, nullptr, 100000000LL);
-                }
-            }
+            land(full, i, kScrStages);
         }
     } else if (warp == 1) {
         const uint32_t idesc = idesc_f16_bf16(128, 256);

@@ -254,15 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) umma_grouped_kernel(const __grid_
                               kStageAtoms * kAtom, &full[s]);
                 }
             }
-            if (*abort_flag) {
-                // let the copies already issued land before the CTA's shared memory is released
-                // (bounded waits that the abort flag does not cut short)
-                volatile int never = 0;
-                for (int q = 0; q < kStages && q < kiter; ++q) {
-                    const int it = kiter - 1 - q;
-                    mbar_wait(&full[it % kStages], (it / kStages) & 1, &never, nullptr, 100000000LL);
-                }
-            }
+            land(full, kiter, kStages);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer (whole warp)

@@ -1,8 +1,11 @@
 // int8_matmul.cu -- products of 8-bit rows and 8-bit weights, of all rows with one matrix or of each expert's rows with its own:
 //   y[m][n] = (sum_k qx[m][k] qw[n][k]) sx[m] sw[n]
 // or gated, for rows 2 i and 2 i + 1 of the weights (gate and up of channel i):  y[m][i] = silu(gate) up.
-// The sum of whole numbers is exact up to 2^24 and rounded to fp32 beyond; the two products with the scales are in fp32, in this
-// order, and the result is rounded once to y's type.
+// The sum of whole numbers is exact where it stays within 2^24 on its way (K <= 1032 always does).  Beyond, mma and few round their fp32
+// accumulators as they add, 16 terms at a time: an adder that keeps at least 24 bits of the largest addend is off by less than 18 steps of
+// 2^-23 of it, K / 16 times; so by less than K 2^-22 of the largest sum on the way.  (Accumulators taken out every 1024 values and added as
+// whole numbers would be exact, but have no room beside the next tile's in tensor memory.)  dot adds whole numbers and rounds once.  The
+// two products with the scales are in fp32, in this order, and the result is rounded once to y's type.
 //
 //   mma     (int8_mma.cu) the tensor cores, on fp16 that holds the whole numbers
 //   few     (int8_few.cu) the same for one matrix and so few rows that there are no more tiles than SMs

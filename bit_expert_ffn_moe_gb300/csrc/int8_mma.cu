@@ -1,5 +1,5 @@
 // int8_mma.cu -- the 8-bit products on the tensor cores.  sm_103a's have no 8-bit whole numbers, but numbers up to 2048 are exact in fp16,
-// their products and sums up to 2^24 exact in the fp32 accumulators: so kind::f16, at the rate of bf16.
+// their products exact and sums too as long as they stay within 2^24: so kind::f16, at the rate of bf16.
 //   The weights are the MMA's M side (128 weight rows a CTA) and come from tensor memory: read as bytes, turned into fp16 in
 // registers by sixteen warps, stored to tensor memory, so that they cost one byte of memory traffic and shared memory sees them
 // once.  The activations are the N side (16 .. 192 rows), fp16 already, copied as they lie.

@@ -344,7 +344,8 @@ def int8_workspace(M: int, N: int, K: int, device="cuda") -> torch.Tensor:
 def int8_matmul(rows: Int8Rows, W: Int8Weights, dtype: torch.dtype, workspace: torch.Tensor, gated: bool = False,
                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """rows [M, K] times W [N, K] transposed, or each expert's rows times its matrix: [M, N] of dtype, gated [M, N / 2] (rows behind the last
-    pair with an expert are not written)."""
+    pair with an expert are not written).  Sums are exact where they stay within 2^24 on their way, always for K <= 1032, and beyond that
+    fp32 sums: a row's last bits can then depend on how many rows there are."""
     code = _SCALAR_TYPES.get(dtype)
     if code is None:
         raise TypeError("fp32, bf16 or fp16 expected, got %s" % (dtype,))

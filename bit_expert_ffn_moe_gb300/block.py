@@ -138,7 +138,6 @@ class Int8Experts:
         self._check(x, ids)
         return ops.int8_experts(x, ids, w, self.up, self.down, self.workspace)
 
-    @torch.no_grad()
     def outputs(self, x: torch.Tensor, ids: torch.Tensor) -> Tuple[torch.Tensor, ops.ExpertOrder]:
         """The experts' outputs [T k, d] in expert order, and that order: the layer without its weighted sum, for the gradient of the
         routing weights (ops.experts_to_tokens_backward)."""

@@ -3,7 +3,8 @@
 Each function checks its tensors, allocates its results and makes one call of the library, in an extension module; the work is
 the library's kernels, on torch's current stream.  None of them synchronises.  Tensors of another device than the current one are
 refused (`with torch.cuda.device(...)` makes theirs the current one).  None of them takes part in autograd: gradients come from the
-calls that compute them, and backward() through a result raises an error rather than leave its gradient out.
+calls that compute them, and backward() through a result raises an error rather than leave its gradient out.  Results in tensors that
+were given, and weights of int8_weights, are constants.
 """
 from __future__ import annotations
 
@@ -309,6 +310,7 @@ class Int8Rows:
         self.M, self.K, self.order = M, K, order
         self.q, self.s, q, s, self.room = (_module or _calls()).int8_room(M, order.E if order else 0, K, device)
         self.struct = B.moe_int8_rows(q, s, self.room)
+        self.of: Optional[torch.Tensor] = None  # the tensor that they were made of, where it requires a gradient
 
     def values(self) -> torch.Tensor:
         """The numbers they stand for, fp32 [room, K] (rows that no row was put into: anything)."""
@@ -328,6 +330,8 @@ def int8_quantize(x: torch.Tensor, order: Optional[ExpertOrder] = None, ordered:
     rows = Int8Rows(M, x.shape[1], order, x.get_device())
     inv, offsets, E = (None, None, 0) if order is None else (None if ordered else order.inv, order.offsets, order.E)
     (_module or _calls()).int8_quantize(x, inv, offsets, E, rows.struct)
+    if x.requires_grad and torch.is_grad_enabled():
+        rows.of = x
     return rows
 
 
@@ -350,7 +354,10 @@ def int8_matmul(rows: Int8Rows, W: Int8Weights, dtype: torch.dtype, workspace: t
     if code is None:
         raise TypeError("fp32, bf16 or fp16 expected, got %s" % (dtype,))
     offsets, E = (None, 0) if rows.order is None else (rows.order.offsets, rows.order.E)
-    return (_module or _calls()).int8_matmul(rows.struct, rows.s, rows.M, rows.K, offsets, E, *W.args, code, workspace, gated, out)
+    y = (_module or _calls()).int8_matmul(rows.struct, rows.s, rows.M, rows.K, offsets, E, *W.args, code, workspace, gated, out)
+    if out is None and rows.of is not None:
+        y = tied("int8_matmul's input gradient is a product with the transposed weights", y, rows.of)
+    return y
 
 
 def int8_linear(x: torch.Tensor, W: Int8Weights, workspace: torch.Tensor, gated: bool = False,

@@ -4,7 +4,7 @@ Each function checks its tensors, allocates its results and makes one call of th
 the library's kernels, on torch's current stream.  None of them synchronises.  Tensors of another device than the current one are
 refused (`with torch.cuda.device(...)` makes theirs the current one).  None of them takes part in autograd: gradients come from the
 calls that compute them, and backward() through a result raises an error rather than leave its gradient out.  Results in tensors that
-were given, and weights of int8_weights, are constants.
+were given, weights of int8_weights and the operand of nvfp4_linear are constants.
 """
 from __future__ import annotations
 
@@ -137,6 +137,7 @@ class Nvfp4Operand:
         _need(gs.numel() in (1, rows), "gs: one scale per row, or one")
         self.rows, self.K, self.q, self.s, self.gs = rows, K, q, s, gs
         self.device = q.get_device()
+        self.of: Optional[torch.Tensor] = None  # the tensor that it was made of, where it requires a gradient
         self.struct = B.moe_nvfp4_operand(q.data_ptr(), s.data_ptr(), gs.data_ptr(), int(gs.numel() == rows))
 
     def values(self) -> torch.Tensor:
@@ -154,7 +155,7 @@ def nvfp4_operand(rows: int, K: int, device="cuda") -> Nvfp4Operand:
     index = on.index if on.index is not None else torch.cuda.current_device()
     op = object.__new__(Nvfp4Operand)  # (its tensors are right as they come)
     op.q, op.s, op.gs, q, s, gs = (_module or _calls()).nvfp4_room(rows, K, index)
-    op.rows, op.K, op.device = rows, K, index
+    op.rows, op.K, op.device, op.of = rows, K, index, None
     op.struct = B.moe_nvfp4_operand(q, s, gs, 1)
     return op
 
@@ -176,6 +177,11 @@ def nvfp4_quantize(x: torch.Tensor, rows: Optional[Nvfp4Operand] = None, cols: O
     r = (None, 0, 0, 0) if rows is None else (rows.struct, rows.rows, rows.K, rows.device)
     c = (None, 0, 0, 0) if cols is None else (cols.struct, cols.rows, cols.K, cols.device)
     (_module or _calls()).nvfp4_quantize(x, *r, *c, workspace, scales_given)
+    of = x if x.requires_grad and torch.is_grad_enabled() else None
+    if rows is not None:
+        rows.of = of
+    if cols is not None:
+        cols.of = of
 
 
 def nvfp4_matmul(a: Nvfp4Operand, b: Nvfp4Operand, dtype: torch.dtype, workspace: torch.Tensor,
@@ -184,7 +190,10 @@ def nvfp4_matmul(a: Nvfp4Operand, b: Nvfp4Operand, dtype: torch.dtype, workspace
     code = _SCALAR_TYPES.get(dtype)
     if code is None:
         raise TypeError("fp32, bf16 or fp16 expected, got %s" % (dtype,))
-    return (_module or _calls()).nvfp4_matmul(a.struct, a.rows, a.K, a.device, b.struct, b.rows, b.K, b.device, a.q, code, workspace, out)
+    y = (_module or _calls()).nvfp4_matmul(a.struct, a.rows, a.K, a.device, b.struct, b.rows, b.K, b.device, a.q, code, workspace, out)
+    if out is None and (a.of is not None or b.of is not None):
+        y = tied("nvfp4_matmul's gradients are nvfp4_matmul of transposed operands", y, a.of, b.of)
+    return y
 
 
 def nvfp4_linear(x: torch.Tensor, W: Nvfp4Operand, workspace: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:

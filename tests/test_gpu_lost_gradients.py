@@ -29,6 +29,21 @@ def int8_forms():
     yield "their sum", x, lambda t: ops.experts_to_tokens(layer.outputs(t, ids)[0], order, w)
 
 
+def nvfp4_operand_of(t, columns=False):
+    op, ws = ops.nvfp4_operand(*(t.t() if columns else t).shape), ops.nvfp4_workspace(*t.shape, 1)
+    ops.nvfp4_quantize(t, None if columns else op, op if columns else None, ws)
+    return op
+
+
+def nvfp4_forms():
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, y = torch.randn(6, 64, generator=g, device="cuda"), torch.randn(40, 64, generator=g, device="cuda")
+    ws = ops.nvfp4_workspace(64, 64, 64)
+    yield "first", x, lambda t: ops.nvfp4_matmul(nvfp4_operand_of(t), nvfp4_operand_of(y), torch.float32, ws)
+    yield "second", y, lambda t: ops.nvfp4_matmul(nvfp4_operand_of(x), nvfp4_operand_of(t), torch.float32, ws)
+    yield "of columns", x, lambda t: ops.nvfp4_matmul(nvfp4_operand_of(t, True), nvfp4_operand_of(x, True), torch.float32, ws)
+
+
 def check(forms):
     for name, x, f in forms:
         plain = f(x)
@@ -56,3 +71,17 @@ def test_int8_operands_made_without_a_graph_are_constants():
     out = torch.empty(6, 40, device="cuda")
     y = ops.int8_matmul(ops.int8_quantize(x), W, torch.float32, ws, out=out)
     assert y.data_ptr() == out.data_ptr() and not y.requires_grad and not out.requires_grad
+
+
+def test_nvfp4_operands():
+    check(nvfp4_forms())
+
+
+def test_an_nvfp4_operand_is_what_it_was_last_made_of():
+    x, ws = torch.randn(6, 64, device="cuda", requires_grad=True), ops.nvfp4_workspace(64, 64, 64)
+    op, other = nvfp4_operand_of(x), nvfp4_operand_of(torch.randn(8, 64, device="cuda"))
+    assert ops.nvfp4_matmul(op, other, torch.float32, ws).requires_grad
+    ops.nvfp4_quantize(x.detach(), op)
+    assert not ops.nvfp4_matmul(op, other, torch.float32, ws).requires_grad
+    out = torch.empty(6, 8, device="cuda")
+    assert not ops.nvfp4_matmul(nvfp4_operand_of(x), other, torch.float32, ws, out).requires_grad and not out.requires_grad

@@ -52,7 +52,6 @@ struct MmaArgs {
     int most, x_bytes;       // activation rows of a tile at most; their bytes a tile of weights
     int w_steps, x_steps;    // steps in the ring of weights, and behind it in that of activations; even numbers
     int slot_rows;  // of partial sums, a multiple of 16
-    int early;  // weights and offsets were there before the kernel in front started its dependents
 };
 
 __host__ __device__ __forceinline__ int ring_bytes(const MmaArgs& m) { return m.w_steps * kStepBytes + m.x_steps * 2 * m.x_bytes; }
@@ -394,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
     }
-    if (!args.early) pdl_wait();
+    if (!a.early) pdl_wait();
     if (warp == 0) {  // the table of the experts' tiles
         int sum = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
@@ -453,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
         }
     } else if (warp == kRowWarp) {
         if (elect_one()) {
-            if (args.early) pdl_wait();
+            if (a.early) pdl_wait();
             const int64_t x_step = a.room * 128;
             Turn t(args.x_steps);
             int it = 0;
@@ -543,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
             return true;
         });
     } else {
-        if (args.early) pdl_wait();
+        if (a.early) pdl_wait();
         pdl_launch_dependents();
         uint32_t turn = 0;
         auto sync = [&] {  // of the epilogue's warps; bounded, like every wait
@@ -575,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_mma_kernel(const __grid_cons
         Part p;
         const int tile = work2.last(PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x, p), part = (int)threadIdx.x >> 7;
         if (tile >= 0 && !s2.abort) {
-            if (args2->early && part < kSets) pdl_wait();
+            if (args2->p.early && part < kSets) pdl_wait();
             uint32_t turn = 0;
             auto sync = [&] {
                 __syncwarp();
@@ -618,7 +617,6 @@ const void* mma_kernel(bool gated, bool pair) {
 cudaError_t launch_int8_mma(const Int8ProductArgs& a, moe_dtype dtype, bool gated, bool pair, cudaStream_t st) {
     MmaArgs m = {};
     m.p = a;
-    m.early = a.early;
     m.slot_rows = (int)(a.M > kMostRows ? kMostRows : (a.M + 15) / 16 * 16);
     // By expert the ring has room for tiles of four times the mean, or 64 rows above it (more of an expert's rows are several tiles): small
     // ones leave room for more steps of weights on their way.

@@ -48,8 +48,8 @@ struct Piece {
         else return 0;
     }
 
-    // (Loads are volatile and have no branches between them, so that several are in flight instead of each waiting next to its use: 297
-    // -> 97 us for the gather of 4096 tokens of 8 slots of 8192 features.)
+    // (All slots' loads stand in front of their uses, so that several are in flight instead of each waiting next to its use: 90 us for the
+    // gather of 4096 tokens of 8 slots of 8192 features, where loads in a loop with their uses took 297.)
     __device__ __forceinline__ void load(const T* row, int e, int d) {
         const T* p = row + e;
         if constexpr (WORDS == 4) {
@@ -287,7 +287,7 @@ cudaError_t launch_type(MoveArgs m, cudaStream_t st) {
     const bool pieces = m.d % N == 0 && wide(m.a, m.lda) && wide(m.b, m.ldb) && wide(m.out, m.ldo);
     if (m.dw) return pieces ? launch_slots<T, 4, SPREAD, true>(m, st) : launch_slots<T, 1, SPREAD, true>(m, st);
     if (!pieces) return launch_slots<T, 1, SPREAD, false>(m, st);
-    // (4096 x 8 x 8192: 118 us with a thread per piece, 107 with warps per token; 4 x 8 x 8192: 2.6 and 5)
+    // (4096 x 8 x 8192: 116 us with a thread per piece, 90 with warps per token; 4 x 8 x 8192: 2.6 and 5)
     if (!SPREAD && m.T >= 2 * sm_count() && m.d / N >= 64) return launch_slots<T, 4, SPREAD, false>(m, st);
     const int64_t blocks = ((int64_t)m.T * (m.d / N) + kThreads - 1) / kThreads;
     void* args[] = {&m};

@@ -4,7 +4,7 @@
 // start before anything else, and there is one tile a CTA, so that nothing has to be found out about the work first.
 //   warps 0-15  conversion of the weights (int8_mma.cu), then results out of tensor memory
 //   warp 16     copies            warp 17     products
-// 16 x 4096 x 8192 (33.6 MB): 12.0 us, 777 x 1001 x 1543: 9.0.
+// 16 x 4096 x 8192 (33.6 MB): 11.7 us, 777 x 1001 x 1543: 9.0.
 // Every barrier wait is bounded: on expiry the CTA records MOE_ERR_TIMEOUT, waits (bounded) for its own copies and products,
 // frees tensor memory and exits.
 #include "int8_mma.cuh"

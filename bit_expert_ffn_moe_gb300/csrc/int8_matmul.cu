@@ -24,7 +24,7 @@ bool few_by_expert(const Int8ProductArgs& a) { return a.M <= kDotExpertRows && a
 cudaError_t launch_int8_product(const Int8ProductArgs& a, moe_dtype dtype, bool gated, cudaStream_t st) {
     if (a.M == 0 || a.N == 0) return cudaSuccess;
     // us for 4096 x 8192 weights, dot / few / mma with one CTA a tile / with pairs: 1 row 10.2 / 12.0 / 17.4 / 18.6, 2: 10.9 / 12.0, 4: 12.5 / 12.0,
-    // 16: 36 / 12.0 / 17.2 / 18.6, 128: - / 15.0 / 28.8 / 29.6, 512: - / 34.4 / 44.5 / 40.9, 4096: - / - / 220 / 160.  By expert, 128 of 4096 x 8192: 32 rows 147 / - / 155,
+    // 16: 36 / 11.7 / 17.2 / 18.6, 128: - / 14.8 / 28.8 / 29.6, 512: - / 34.4 / 44.5 / 40.9, 4096: - / - / 220 / 160.  By expert, 128 of 4096 x 8192: 32 rows 147 / - / 155,
     // 64: 264 / - / 246; 2 of 2048 x 4096: 4 rows each 11.0 / - / 16.3, 15: 27.0 / - / 16.1; one CTA
     // a tile / pairs, 128 experts and a mean of 4 rows 593 / 592, 16: 704 / 647, 64: 1041 / 805.
     if (a.offsets ? few_by_expert(a) : a.M <= (int8_few_fits(a) ? 2 : kDotRows)) return launch_int8_dot(a, dtype, gated, nullptr, MOE_F32, 0, nullptr, 1, st);
@@ -35,6 +35,10 @@ cudaError_t launch_int8_product(const Int8ProductArgs& a, moe_dtype dtype, bool 
 cudaError_t launch_int8_linear(const void* x, moe_dtype x_dtype, int64_t ldx, uint16_t* q, float* s, const Int8ProductArgs& a, moe_dtype dtype,
                                bool gated, cudaStream_t st) {
     if (a.M == 0 || a.N == 0) return cudaSuccess;
+    // Every CTA quantises all of x for itself while its first weights arrive, which pays as long as x is short.  us of a call, x quantised by
+    // the dot products / by the rows' kernel in front: 4096 x 8192 weights, 3 rows 14.4 / 13.5, 4: 14.8 / 13.5; x 5504, 3 rows 11.6 / 11.4, 4:
+    // 11.9 / 11.4; 16384 x 8192, 3 rows 32.0 / 27.5; 4096 x 16384, 2 rows 19.7 / 21.1, 4: 24.0 / 19.1.  (2 rows of more than 8192 values lose by
+    // it.  The dot products' room is for 4 rows of 16384.)
     if (a.M <= kDotRows && a.M * a.K <= kInt8DotK) return launch_int8_dot(a, dtype, gated, x, x_dtype, ldx, nullptr, 1, st);
     const cudaError_t e = launch_int8_rows({x, ldx, a.M, a.K, nullptr, 1, nullptr, 0, a.room, q, s}, x_dtype, st);
     if (e != cudaSuccess) return e;

@@ -15,6 +15,8 @@
 // leader (rank 0) issues the products of both, and the other's warp 22 passes on that its activations are there.
 // Work: the tiles of all experts in a row, taken in turns; the last ones, where it saves enough, are dealt out by their steps.  A tile that
 // several CTAs share is summed by the last of them to arrive, from partial sums in memory, in the order of the CTAs.
+// 736 threads leave 80 registers each, and some 50 words are spilled -- none in the loops over the steps: a launch of 4096 x 4096 x 2048, 4096
+// or 8192 makes the same 82536 local loads of a warp, 24 of each.
 // Every barrier wait is bounded: on expiry the CTA records MOE_ERR_TIMEOUT, waits (bounded) for its own copies and products,
 // frees tensor memory and exits.
 #include "int8_mma.cuh"
